@@ -86,6 +86,10 @@ typedef enum kvx_status {
 #define KVX_DEV_WAIT_TIMEOUT 0x2u       /* a bulk copy, or the store a round-trip load
                                            waits for, did not complete within ~1 s; the
                                            kernel skipped work (output incomplete) */
+#define KVX_DEV_NO_FREE_PAGE 0x4u       /* a fork needed more pages than are free; it did
+                                           nothing */
+#define KVX_DEV_PAGE_NOT_HELD 0x8u      /* a page table named a page nobody holds (its count
+                                           is 0); that entry was skipped */
 
 typedef enum kvx_chunk_layout {
     KVX_CHUNK_LAYER_MAJOR = 0,
@@ -369,6 +373,165 @@ kvx_status kvx_dma_baseline(kvx_ctx *ctx, int dir, const kvx_pool *pool,
                             const kvx_request *reqs, int n_req, const kvx_chunk *chunks,
                             int n_chunks, int layer_begin, int layer_end,
                             kvx_stream_t stream, int64_t *n_copies);
+
+/* ---------------------------------------------------------------- page upkeep */
+
+/* Sharing, copying, freeing and compacting the pages of a pool, on the device, so that an
+ * engine that forks requests (parallel sampling, beam search, a shared prompt) neither reads
+ * its page tables back nor copies pages one by one.
+ *
+ * refs is a device array [num_pages]: how many page-table entries hold each page; 0 means
+ * free.  The caller owns it and the tables; these calls keep them in step.  Free pages are
+ * always handed out in ascending order of page id, so results do not depend on how the GPU
+ * schedules the work.  Full pages are shared and never written again by the library's own
+ * calls that follow (kvx_append_tokens writes only past a request's earlier tokens); a partly
+ * filled last page is never shared, so it may be appended to.
+ *
+ * Each call is one kernel launch on `stream`, asynchronous like the transfers; small batches
+ * travel in the launch itself, larger ones through the context's descriptor slots.  A page id
+ * outside the pool sets KVX_DEV_PAGE_OUT_OF_RANGE, a page nobody holds
+ * KVX_DEV_PAGE_NOT_HELD; such an entry is skipped.  Pools of up to KVX_MAX_UPKEEP_PAGES pages
+ * (KVX_ERR_CAPACITY above).  Calls on one pool's counts and tables must not overlap in time:
+ * issue them on one stream or order them with events. */
+#define KVX_MAX_UPKEEP_PAGES (1 << 20)
+
+/* A page table that a call may rewrite. */
+typedef struct kvx_table {
+    int32_t *pages;       /* device array [n_pages] of page ids */
+    int32_t n_pages;      /* entries, >= 0 */
+    int32_t reserved;     /* set to 0 */
+} kvx_table;
+
+/* One request forked from another. */
+typedef struct kvx_fork {
+    const int32_t *parent;   /* device page table of the parent; NULL if shared_tokens is 0.
+                                The same pointer as `child` grows a request in place: its
+                                first ceil(shared_tokens / page_size) entries stay */
+    int32_t *child;          /* device page table that is written
+                                [ceil(child_tokens / page_size)] */
+    int32_t shared_tokens;   /* tokens the child takes over from the parent, >= 0 */
+    int32_t child_tokens;    /* tokens the child has room for, >= shared_tokens */
+    int32_t copy;            /* 0: full pages are shared, a partly filled last page is copied.
+                                1: every page is copied (not when growing in place) */
+    int32_t reserved;        /* set to 0 */
+} kvx_fork;
+
+/* Fork: for each entry, the child's table gets the parent's full pages (their counts go up
+ * by one) and free pages for the rest (their counts become 1); the tokens of a page that is
+ * not shared are copied in every layer, K and V, and the slots after them are left as they
+ * are.  An entry with shared_tokens 0 allocates a new request, one with child == parent grows
+ * one.  If fewer pages are free than the whole batch needs, nothing is changed and
+ * KVX_DEV_NO_FREE_PAGE is set.  A child's table is no other entry's child or parent (checked
+ * at validation level 2); one parent may serve any number of entries.  A shared
+ * page's entry that was skipped is -1 in the child; a copy that was skipped leaves the
+ * child's page as it was. */
+kvx_status kvx_fork_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                          const kvx_fork *forks, int n_forks, kvx_stream_t stream);
+
+/* Free: every entry of every table gives its page back (its count goes down by one; at 0 the
+ * page is free) and becomes -1. */
+kvx_status kvx_free_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                          const kvx_table *tables, int n_tables, kvx_stream_t stream);
+
+/* Compact: with n pages live, move every live page with an id of n or more into a free page
+ * below n (the i-th such page, ascending, into the i-th free one) in every layer, K and V,
+ * and rewrite counts and tables, so that pages [n, num_pages) are all free.  `tables` must
+ * hold every table that names a page of the pool.  The bytes of moved pages also stay where
+ * they were until the page is used again.  n_live (device word, may be NULL) receives n;
+ * remap (device array [num_pages], may be NULL) receives each live page's new id and -1 for
+ * free pages, for the caller's other copies of the tables. */
+kvx_status kvx_compact_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                             const kvx_table *tables, int n_tables, int32_t *n_live,
+                             int32_t *remap, kvx_stream_t stream);
+
+/* The host checks of the three calls above (forks or tables may be NULL with a count of 0):
+ * sizes and pointers at level 0 and 1, tables that meet at level 2. */
+kvx_status kvx_upkeep_validate(const kvx_pool *pool, const int32_t *refs,
+                               const kvx_fork *forks, int n_forks, const kvx_table *tables,
+                               int n_tables, int level, char *msg, size_t msg_len);
+
+/* ---------------------------------------------------------------- attention over the pages */
+
+/* Element types of the operators below. */
+#define KVX_TYPE_HALF 0        /* IEEE half precision */
+#define KVX_TYPE_BFLOAT 1      /* bfloat16 */
+#define KVX_TYPE_FP_EIGHT 2    /* e4m3 (finite, 8 bits), cache only */
+
+/* What stays the same for every layer and step of a model. */
+typedef struct kvx_attn_cfg {
+    int32_t q_heads;       /* query heads, a multiple of kv_heads */
+    int32_t kv_heads;      /* heads of the cache: token_bytes = kv_heads x head_dim x bytes of
+                              kv_type */
+    int32_t head_dim;      /* 64 or 128 */
+    int32_t type;          /* KVX_TYPE_HALF or KVX_TYPE_BFLOAT: q, new K and V, output */
+    int32_t kv_type;       /* the cache: the same as `type`, or KVX_TYPE_FP_EIGHT */
+    int32_t window;        /* > 0: a row at position i sees positions j with i - j < window;
+                              0: no window */
+    float scale;           /* factor of q.k; 0 = 1 / sqrt(head_dim) */
+    float softcap;         /* > 0: scores become softcap * tanh(score / softcap); 0 = off */
+    const float *slopes;   /* device array [q_heads]: head h adds -slopes[h] * |i - j| to the
+                              (capped) score; NULL = off */
+} kvx_attn_cfg;
+
+/* The attention of one step: a batch of requests, each with n_new tokens at the end of its
+ * n_tokens (their K and V are in the pages, by kvx_append_tokens), over one layer's pages.
+ * Row i of request r, at position p = n_tokens - n_new + i, sees
+ *     j <= p and (no window or p - j < window),   or   j < prefix[r]
+ * (a prefix that every row sees: a prompt attended both ways, or tokens kept for all time
+ * under a window), and gets, for each of its query heads h over KV head
+ * h / (q_heads / kv_heads),
+ *     s_j = softcap * tanh(scale * k_scale * q.k_j / softcap) - slopes[h] * |p - j|,
+ *     out = v_scale * sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j).
+ * Every row sees its own position, so no row is empty.  Scores, the softmax statistics and
+ * the sums are held in 32 bits; the weights are rounded to `type` for the product with V, and
+ * the result once more to `type`.  The weight of a hidden key is exactly 0, but keys that some
+ * row of the request sees must be finite: pages, slots past n_tokens and positions that no
+ * row sees are never used, whatever they hold (page-table entries for them may be anything).
+ *
+ * A plan holds a step's batch on the device, for every layer of the step and any number of
+ * launches: it is made once (kvx_attn_plan_create allocates), refilled for the next step with
+ * kvx_attn_plan_update (which does not), and its launches may be captured into a CUDA graph.
+ * It keeps the addresses of page tables and slopes and a copy of the pool's pointers.  Its
+ * workspace serves one launch at a time: launches of one plan must not overlap in time.
+ * n_new and prefix are HOST arrays [n_req]; prefix may be NULL (all 0).  Rows of the step are
+ * packed: request r's new tokens follow those of request r - 1 in q, out, lse, k and v. */
+typedef struct kvx_attn_plan kvx_attn_plan;
+
+kvx_status kvx_attn_plan_create(kvx_ctx *ctx, const kvx_pool *pool, const kvx_request *reqs,
+                                int n_req, const int32_t *n_new, const int32_t *prefix,
+                                const kvx_attn_cfg *cfg, kvx_stream_t stream,
+                                kvx_attn_plan **out);
+/* The next step's batch: up to as many requests as the plan was made with
+ * (KVX_ERR_CAPACITY above).  Allocates nothing; copies the batch on `stream`, where the
+ * plan's earlier launches must be done or ahead of it. */
+kvx_status kvx_attn_plan_update(kvx_attn_plan *plan, const kvx_request *reqs, int n_req,
+                                const int32_t *n_new, const int32_t *prefix,
+                                kvx_stream_t stream);
+/* Synchronize the device, then free the plan (before its context). */
+void kvx_attn_plan_destroy(kvx_attn_plan *plan);
+
+/* Write the step's new K and V, [rows][kv_heads][head_dim] of `type` with k_stride and
+ * v_stride elements from token to token (0 = packed), into layer `layer`'s pages.  For an
+ * e4m3 cache the values are divided by k_scale / v_scale and rounded to the nearest code,
+ * beyond +-448 to +-448 (NaN stays NaN); otherwise the bytes are copied and the scales are
+ * not used.  Pointers 16-byte aligned, strides multiples of 8 elements. */
+kvx_status kvx_append_tokens(const kvx_attn_plan *plan, int layer, const void *k, const void *v,
+                             int64_t k_stride, int64_t v_stride, float k_scale, float v_scale,
+                             kvx_stream_t stream);
+
+/* out [rows][q_heads][head_dim] = attention of q over layer `layer`, both of `type`, with
+ * q_stride and out_stride elements from token to token (0 = packed).  lse: device array
+ * [rows][q_heads] of float, may be NULL.  k_scale and v_scale: the values of a cache element
+ * are its element times these (any finite value; 1 for a cache of `type`).  Pointers of q and
+ * out 16-byte aligned, strides multiples of 8 elements. */
+kvx_status kvx_attend(const kvx_attn_plan *plan, int layer, const void *q, int64_t q_stride,
+                      void *out, int64_t out_stride, float *lse, float k_scale, float v_scale,
+                      kvx_stream_t stream);
+
+/* The host checks of kvx_attn_plan_create. */
+kvx_status kvx_attn_validate(const kvx_pool *pool, const kvx_request *reqs, int n_req,
+                             const int32_t *n_new, const int32_t *prefix,
+                             const kvx_attn_cfg *cfg, int level, char *msg, size_t msg_len);
 
 /* Read the device status word (after synchronizing `stream`), clear it, and return
  * KVX_ERR_DEVICE_STATUS if any bit was set.  flags may be NULL. */

@@ -1,8 +1,9 @@
 """Build libkvx.so (the C-ABI library) in-tree for sm_103a with nvcc.
 
-Three translation units, compiled in parallel: the CUDA kernels + entry points (kvx.cu, by
-nvcc), the host logic (kvx_host.cpp) and the SM partitioning (kvx_partition.cpp), the last
-two by the host C++ compiler.  The CUDA runtime is
+One object per translation unit, compiled in parallel: the transfer kernels (kvx.cu), page
+upkeep (kvx_pages.cu) and attention (kvx_attend.cu) by nvcc, the host logic (kvx_host.cpp,
+kvx_cache_host.cpp) and the SM partitioning (kvx_partition.cpp) by the host C++ compiler.
+The CUDA runtime is
 linked statically so the library loads on machines without a GPU (its host logic and
 exported symbols stay usable there).
 """
@@ -20,8 +21,10 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkvx.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = [os.path.join(CSRC, f) for f in ("kvx.cu", "kvx_kernels.cuh", "kvx_host.cpp",
-                                             "kvx_partition.cpp", "kvx_internal.h")]
+CUDA_UNITS = ("kvx.cu", "kvx_pages.cu", "kvx_attend.cu")
+HOST_UNITS = ("kvx_host.cpp", "kvx_cache_host.cpp", "kvx_partition.cpp")
+SOURCES = [os.path.join(CSRC, f) for f in CUDA_UNITS + HOST_UNITS + (
+    "kvx_kernels.cuh", "kvx_internal.h", "kvx_rules.h", "kvx_ctx.h", "kvx_cache.h")]
 HEADER = os.path.join(ROOT, "include", "kvx.h")
 
 
@@ -58,13 +61,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     inc = os.path.join(home, "include")
     os.makedirs(BUILD_DIR, exist_ok=True)
     tag = f"{os.getpid()}"
-    obj_cu = os.path.join(BUILD_DIR, f"kvx.{tag}.o")
-    cu = [nvcc, "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xptxas", "-v", "-Xcompiler", "-fPIC",
-          "-c", os.path.join(CSRC, "kvx.cu"), "-o", obj_cu]
     cxx = shutil.which("g++") or shutil.which("c++")
-    objs = [obj_cu]
-    cmds = [cu]
-    for src in ("kvx_host.cpp", "kvx_partition.cpp"):
+    objs, cmds = [], []
+    for src in CUDA_UNITS:
+        obj = os.path.join(BUILD_DIR, f"{src[:-3]}.{tag}.o")
+        objs.append(obj)
+        cmds.append([nvcc, "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xptxas", "-v", "-Xcompiler",
+                     "-fPIC", "-c", os.path.join(CSRC, src), "-o", obj])
+    for src in HOST_UNITS:
         obj = os.path.join(BUILD_DIR, f"{src[:-4]}.{tag}.o")
         objs.append(obj)
         cmds.append([cxx, "-O2", "-std=c++17", "-fPIC", f"-I{inc}", "-c",
@@ -77,7 +81,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for o in objs:
         os.remove(o)
     if verbose:
-        sys.stdout.write(logs[0])
+        sys.stdout.write("".join(logs[:len(CUDA_UNITS)]))
     return LIB
 
 

@@ -1,0 +1,70 @@
+// kvx_cache.h -- descriptors and host logic of the operators that work on the page pools in
+// place: page upkeep (kvx_pages.cu), token append and attention (kvx_attend.cu).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/kvx.h"
+
+namespace kvx {
+
+// ---------------------------------------------------------------------------- page upkeep
+
+// One fork.  Child pages [0, full) are the parent's, [full, total) are free pages; of the
+// parent's pages that hold shared tokens, [full, ceil(shared / page_size)) are copied unless
+// the entry grows in place.  The *_begin fields are running totals over the entries, and one
+// entry past the last holds the batch's totals.
+struct ForkEntry {
+    const int32_t *parent;
+    int32_t *child;
+    int32_t full;
+    int32_t total;
+    int32_t shared;      // tokens
+    int32_t grow;        // child == parent: the shared entries stay as they are
+    int32_t page_begin;  // child pages
+    int32_t fresh_begin; // pages taken from the free ones
+    int32_t copy_begin;  // pages copied
+    int32_t pad;
+};
+static_assert(sizeof(ForkEntry) == 48, "descriptor layout");
+
+struct TableEntry {
+    int32_t *pages;
+    int32_t n_pages;
+    int32_t page_begin;
+};
+static_assert(sizeof(TableEntry) == 16, "descriptor layout");
+
+kvx_status validate_upkeep(const kvx_pool *pool, const int32_t *refs, const kvx_fork *forks,
+                           int n_forks, const kvx_table *tables, int n_tables, int level,
+                           bool have_gpu, char *msg, size_t len);
+
+// Fill out[n + 1]; KVX_ERR_CAPACITY when a total passes 2^31 - 1.
+kvx_status pack_forks(const kvx_pool *pool, const kvx_fork *forks, int n, ForkEntry *out,
+                      char *msg, size_t len);
+kvx_status pack_tables(const kvx_table *tables, int n, TableEntry *out, char *msg, size_t len);
+
+// Pool pointers as the kernels index them: out[slab], slab = layer * kv_factor + kv.
+void pack_slabs(const kvx_pool *pool, char **out);
+
+// ---------------------------------------------------------------------------- attention
+
+// One request of a step, as the kernels read it.
+struct AttnReq {
+    const int32_t *table;
+    int32_t n_tokens;
+    int32_t n_new;
+    int32_t prefix;
+    int32_t row_begin;   // first row of the request in q, out, lse, k and v
+    int32_t pad[2];
+};
+static_assert(sizeof(AttnReq) == 32, "descriptor layout");
+
+kvx_status validate_attn(const kvx_pool *pool, const kvx_request *reqs, int n_req,
+                         const int32_t *n_new, const int32_t *prefix, const kvx_attn_cfg *cfg,
+                         int level, bool have_gpu, char *msg, size_t len);
+
+inline int type_bytes(int type) { return type == KVX_TYPE_FP_EIGHT ? 1 : 2; }
+
+}  // namespace kvx

@@ -1,0 +1,608 @@
+// kvx_pages.cu -- page upkeep of a paged KV cache on the device: fork (share by count, copy),
+// free and compact.  Entry points and kernels; the checks and packing are in
+// kvx_cache_host.cpp.
+//
+// The one question these operators ask is "which pages are free": fork needs the i-th free
+// page, compaction pairs the i-th live page past the front with the i-th free one in it.  Both
+// are rank and select on the bitmap refs[p] > 0.  Every CTA builds that bitmap in its own
+// shared memory (one pass over refs, which stays in L2; a fork stops as soon as it has seen
+// enough free pages) and answers its own queries there, so a call is one launch with no
+// device-wide wait, no list in global memory and no order-dependent atomics.  Nothing may
+// change a page between free and live while another CTA still scans: such writes are left to
+// the last CTA that arrives at a counter.  Until then counts of live pages only go up, which
+// no bitmap sees.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "kvx_cache.h"
+#include "kvx_ctx.h"
+
+using kvx::ForkEntry;
+using kvx::TableEntry;
+
+namespace {
+
+// Descriptors up to this size travel as a kernel parameter (the parameter space of a launch
+// was 4 KB before CUDA 12.1 and a call stays within it); larger batches take a descriptor slot.
+const int kInlineBytes = 3840;
+const int kThreads = 1024;
+const int kWarps = kThreads / 32;
+const int kGranWords = 8;                // bitmap words per granule
+const int kGranPages = 32 * kGranWords;  // pages per granule: one warp scans one at a time
+const int kUnits = 8;                    // 16-byte loads in flight per lane
+
+struct Inline {
+    uint4 bytes[kInlineBytes / 16];
+};
+
+struct Args {
+    const char *ext;         // descriptors in device memory, or NULL: in the Inline parameter
+    int32_t *refs;
+    unsigned int *status;
+    unsigned int *counter;   // CTAs that have finished scanning
+    int32_t *n_live;         // compact
+    int32_t *remap;          // compact
+    int64_t token_bytes;
+    int64_t slice;           // bytes a warp copies per job
+    int32_t off_entries;     // of the entries, after the slab pointers
+    int32_t n_entries;
+    int32_t n_slabs;
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t slices;          // jobs per (page, slab)
+};
+
+// -------------------------------------------------------------------------------- device
+
+__device__ __forceinline__ int ld_ref(const int32_t *p)
+{
+    return __ldcg(p);  // L2: another CTA's atomics change counts while this launch runs
+}
+
+// The bitmap of one kind of page (free or live) with running totals per granule.
+struct Bits {
+    unsigned *words;   // [granules * kGranWords]
+    int *before;       // [granules + 1]: set bits in earlier granules
+    int granules;      // scanned
+    int total;         // set bits found
+
+    // Page of the i-th set bit, i < total.
+    __device__ int select(int i) const
+    {
+        int lo = 0, hi = granules;  // before[lo] <= i < before[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] <= i)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        int k = i - before[lo], w = lo * kGranWords;
+        for (int n; k >= (n = __popc(words[w])); ++w)
+            k -= n;
+        unsigned m = words[w];
+        int bit = 0;
+#pragma unroll
+        for (int half = 16; half; half >>= 1) {
+            const int n = __popc(m & ((1u << half) - 1));
+            if (k >= n) {
+                k -= n;
+                m >>= half;
+                bit += half;
+            } else {
+                m &= (1u << half) - 1;
+            }
+        }
+        return w * 32 + bit;
+    }
+
+    // Set bits below page p, p <= 32 * kGranWords * granules.
+    __device__ int rank(int p) const
+    {
+        int w = p >> 5, r = before[w / kGranWords];
+        for (int i = w / kGranWords * kGranWords; i < w; ++i)
+            r += __popc(words[i]);
+        if (p & 31)
+            r += __popc(words[w] & ((1u << (p & 31)) - 1));
+        return r;
+    }
+
+    __device__ bool test(int p) const { return words[p >> 5] >> (p & 31) & 1; }
+};
+
+// Build the bitmap of pages whose (refs > 0) equals `live`, in rounds of one granule per warp,
+// until `enough` bits are set or the pool ends.  All threads; ends with a barrier.
+__device__ Bits scan_pages(const Args &a, bool live, int enough, unsigned *smem)
+{
+    __shared__ int round_count[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int all = (a.num_pages + kGranPages - 1) / kGranPages;
+    Bits b;
+    b.words = smem;
+    b.before = reinterpret_cast<int *>(smem + all * kGranWords);
+    int found = 0, g0 = 0;
+    for (; g0 < all && found < enough; g0 += kWarps) {
+        const int g = g0 + warp;
+        int n = 0;
+        if (g < all) {
+            int v[kGranWords];
+#pragma unroll
+            for (int i = 0; i < kGranWords; ++i) {
+                const int p = g * kGranPages + i * 32 + lane;
+                v[i] = p < a.num_pages ? ld_ref(a.refs + p) : (live ? 0 : 1);
+            }
+#pragma unroll
+            for (int i = 0; i < kGranWords; ++i) {
+                const unsigned m = __ballot_sync(0xffffffffu, (v[i] > 0) == live);
+                if (lane == i)
+                    b.words[g * kGranWords + i] = m;
+                n += __popc(m);
+            }
+        }
+        if (lane == 0)
+            round_count[warp] = n;
+        __syncthreads();
+        const int c = round_count[lane];
+        int incl = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d)
+                incl += x;
+        }
+        if (warp == 0 && g0 + lane <= all)
+            b.before[g0 + lane] = found + incl - c;
+        found += __shfl_sync(0xffffffffu, incl, 31);
+        __syncthreads();
+    }
+    b.granules = g0 < all ? g0 : all;
+    b.total = found;
+    if (threadIdx.x == 0)
+        b.before[b.granules] = found;
+    __syncthreads();
+    return b;
+}
+
+// True in exactly one CTA, for all its threads, once every CTA has called it; that CTA sees
+// what the others wrote before.  Leaves the counter at zero.
+__device__ bool last_to_arrive(unsigned int *counter)
+{
+    __shared__ int last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicInc(counter, gridDim.x - 1) == gridDim.x - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    return last;
+}
+
+// Entry that owns flat index i: the last e with begin(e) <= i, begin of the sentinel > i.
+template <class E, class F>
+__device__ __forceinline__ int find_entry(const E *entries, int n, int i, F begin)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (begin(entries[mid]) <= i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// One warp copies `bytes` (a multiple of 16) with kUnits 16-byte loads in flight per lane.
+__device__ __forceinline__ void warp_copy(const char *src, char *dst, int64_t bytes, int lane)
+{
+    const uint4 *s = reinterpret_cast<const uint4 *>(src) + lane;
+    uint4 *d = reinterpret_cast<uint4 *>(dst) + lane;
+    int64_t rem = bytes / 16 - lane;
+    for (; rem > 32 * (kUnits - 1); rem -= 32 * kUnits, s += 32 * kUnits, d += 32 * kUnits) {
+        uint4 r[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+            r[u] = __ldcs(s + 32 * u);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+            __stcs(d + 32 * u, r[u]);
+    }
+    if (rem > 0) {
+        uint4 r[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+            if (32 * u < rem)
+                r[u] = __ldcs(s + 32 * u);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+            if (32 * u < rem)
+                __stcs(d + 32 * u, r[u]);
+    }
+}
+
+// Copy slice `slice` of `tokens` tokens from page `from` to page `to` in slab `slab`.
+__device__ __forceinline__ void copy_slice(const Args &a, const char *desc, int slab, int slice,
+                                           int from, int to, int tokens, int lane)
+{
+    const int64_t bytes = int64_t(tokens) * a.token_bytes, at = slice * a.slice;
+    if (at >= bytes)
+        return;
+    char *base = reinterpret_cast<char *const *>(desc)[slab];
+    const int64_t page = int64_t(a.page_size) * a.token_bytes;
+    const int64_t n = bytes - at < a.slice ? bytes - at : a.slice;
+    warp_copy(base + from * page + at, base + to * page + at, n, lane);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
+{
+    extern __shared__ unsigned smem[];
+    const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
+    const ForkEntry *e = reinterpret_cast<const ForkEntry *>(desc + a.off_entries);
+    const ForkEntry &end = e[a.n_entries];
+    const int lane = threadIdx.x & 31;
+    const Bits free = scan_pages(a, false, end.fresh_begin, smem);
+    if (free.total < end.fresh_begin) {  // the same in every CTA: counts of live pages only grow
+        if (last_to_arrive(a.counter) && threadIdx.x == 0)
+            atomicOr(a.status, KVX_DEV_NO_FREE_PAGE);
+        return;
+    }
+
+    // Tables, and the counts of shared pages.
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < end.page_begin;
+         i += gridDim.x * kThreads) {
+        const int x = find_entry(e, a.n_entries, i, [](const ForkEntry &f) { return f.page_begin; });
+        const int j = i - e[x].page_begin;
+        if (j >= e[x].full) {
+            e[x].child[j] = free.select(e[x].fresh_begin + j - e[x].full);
+        } else if (!e[x].grow) {
+            int p = e[x].parent[j];
+            unsigned bad = 0;
+            if (unsigned(p) >= unsigned(a.num_pages))
+                bad = KVX_DEV_PAGE_OUT_OF_RANGE;
+            else if (ld_ref(a.refs + p) <= 0)
+                bad = KVX_DEV_PAGE_NOT_HELD;
+            if (bad) {
+                atomicOr(a.status, bad);
+                p = -1;
+            } else {
+                atomicAdd(a.refs + p, 1);
+            }
+            e[x].child[j] = p;
+        }
+    }
+    if (last_to_arrive(a.counter))
+        for (int i = threadIdx.x; i < end.fresh_begin; i += kThreads)
+            a.refs[free.select(i)] = 1;
+
+    // Copies: jobs in the order (page, slab, slice).
+    const int64_t jobs = int64_t(end.copy_begin) * a.n_slabs * a.slices;
+    for (int64_t job = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); job < jobs;
+         job += int64_t(gridDim.x) * kWarps) {
+        const unsigned t = unsigned(job) / unsigned(a.slices);  // jobs < 2^31 (host)
+        const int slice = int(unsigned(job) - t * a.slices);
+        const int c = int(t / unsigned(a.n_slabs)), slab = int(t - unsigned(c) * a.n_slabs);
+        const int x = find_entry(e, a.n_entries, c, [](const ForkEntry &f) { return f.copy_begin; });
+        const int j = e[x].full + c - e[x].copy_begin;
+        const int from = e[x].parent[j];
+        unsigned bad = 0;
+        if (unsigned(from) >= unsigned(a.num_pages))
+            bad = KVX_DEV_PAGE_OUT_OF_RANGE;
+        else if (from < free.granules * kGranPages ? free.test(from) : ld_ref(a.refs + from) <= 0)
+            bad = KVX_DEV_PAGE_NOT_HELD;  // pages past the scan never turn live in this launch
+        if (bad) {
+            if (lane == 0)
+                atomicOr(a.status, bad);
+            continue;
+        }
+        const int to = free.select(e[x].fresh_begin + j - e[x].full);
+        copy_slice(a, desc, slab, slice, from, to,
+                   min(a.page_size, e[x].shared - j * a.page_size), lane);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+kvx_free_kernel(const Args a, const __grid_constant__ Inline in)
+{
+    const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
+    const TableEntry *e = reinterpret_cast<const TableEntry *>(desc + a.off_entries);
+    const int total = e[a.n_entries].page_begin;
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
+        const int x = find_entry(e, a.n_entries, i, [](const TableEntry &t) { return t.page_begin; });
+        int32_t *at = e[x].pages + (i - e[x].page_begin);
+        const int p = *at;
+        unsigned bad = 0;
+        if (unsigned(p) >= unsigned(a.num_pages)) {
+            bad = KVX_DEV_PAGE_OUT_OF_RANGE;
+        } else if (atomicSub(a.refs + p, 1) <= 0) {
+            // Not held: taken back, so that however such entries interleave the count ends
+            // at zero.
+            atomicAdd(a.refs + p, 1);
+            bad = KVX_DEV_PAGE_NOT_HELD;
+        }
+        if (bad)
+            atomicOr(a.status, bad);
+        *at = -1;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
+{
+    extern __shared__ unsigned smem[];
+    const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
+    const TableEntry *e = reinterpret_cast<const TableEntry *>(desc + a.off_entries);
+    const int lane = threadIdx.x & 31;
+    const Bits live = scan_pages(a, true, a.num_pages + 1, smem);
+    const int n = live.total, front = live.rank(n), moves = n - front;
+    // Page of the i-th free page below n: the smallest p with (p - rank(p)) pages free before
+    // it and p free, by bisection over pages.
+    auto hole = [&](int i) {
+        int lo = 0, hi = live.granules;  // free before granule lo <= i
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (mid * kGranPages - live.before[mid] <= i)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        int k = i - (lo * kGranPages - live.before[lo]), w = lo * kGranWords;
+        for (int z; k >= (z = 32 - __popc(live.words[w])); ++w)
+            k -= z;
+        unsigned m = ~live.words[w];
+        int bit = 0;
+#pragma unroll
+        for (int half = 16; half; half >>= 1) {
+            const int z = __popc(m & ((1u << half) - 1));
+            if (k >= z) {
+                k -= z;
+                m >>= half;
+                bit += half;
+            } else {
+                m &= (1u << half) - 1;
+            }
+        }
+        return w * 32 + bit;
+    };
+
+    const int total = e[a.n_entries].page_begin;
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
+        const int x = find_entry(e, a.n_entries, i, [](const TableEntry &t) { return t.page_begin; });
+        int32_t *at = e[x].pages + (i - e[x].page_begin);
+        const int p = *at;
+        if (unsigned(p) >= unsigned(a.num_pages))
+            atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+        else if (!live.test(p))
+            atomicOr(a.status, KVX_DEV_PAGE_NOT_HELD);
+        else if (p >= n)
+            *at = hole(live.rank(p) - front);
+    }
+    if (a.remap)
+        for (int p = blockIdx.x * kThreads + threadIdx.x; p < a.num_pages;
+             p += gridDim.x * kThreads)
+            a.remap[p] = !live.test(p) ? -1 : p < n ? p : hole(live.rank(p) - front);
+    if (last_to_arrive(a.counter)) {
+        for (int i = threadIdx.x; i < moves; i += kThreads) {
+            const int from = live.select(front + i);
+            a.refs[hole(i)] = ld_ref(a.refs + from);
+            a.refs[from] = 0;
+        }
+        if (a.n_live && threadIdx.x == 0)
+            *a.n_live = n;
+    }
+
+    const int64_t jobs = int64_t(moves) * a.n_slabs * a.slices;
+    for (int64_t job = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); job < jobs;
+         job += int64_t(gridDim.x) * kWarps) {
+        const unsigned t = unsigned(job) / unsigned(a.slices);
+        const int slice = int(unsigned(job) - t * a.slices);
+        const int c = int(t / unsigned(a.n_slabs)), slab = int(t - unsigned(c) * a.n_slabs);
+        copy_slice(a, desc, slab, slice, live.select(front + c), hole(c), a.page_size, lane);
+    }
+}
+
+// ---------------------------------------------------------------------------------- host
+
+size_t bitmap_bytes(int num_pages)
+{
+    const size_t granules = (size_t(num_pages) + kGranPages - 1) / kGranPages;
+    return granules * kGranWords * 4 + (granules + kWarps + 1) * 4;
+}
+
+// Cut pages of up to `page` bytes into slices so that `units` of them give every warp of the
+// grid a job, each slice at least 1 KiB and at most 8 KiB (two passes of a warp).
+void choose_slices(const kvx_ctx *ctx, int64_t units, int64_t page, Args *a)
+{
+    const int64_t warps = int64_t(ctx->num_sms) * kWarps;
+    int64_t slice = units > 0 ? units * page / warps : page;
+    slice = std::min<int64_t>(std::max<int64_t>(slice, 1024), 8192) / 16 * 16;
+    a->slice = slice;
+    a->slices = int32_t((page + slice - 1) / slice);
+}
+
+struct Batch {
+    Inline in;
+    kvx::Slot *slot = nullptr;
+    char *host = nullptr;
+    size_t bytes = 0;
+};
+
+// Where a call's descriptors are packed: the launch's own parameter, or a context slot.
+kvx_status begin_batch(kvx_ctx *ctx, size_t bytes, Batch *b)
+{
+    b->bytes = bytes;
+    if (bytes <= size_t(kInlineBytes)) {
+        b->host = reinterpret_cast<char *>(&b->in);
+        return KVX_OK;
+    }
+    kvx_status st = kvx::acquire_slot(ctx, bytes, &b->slot);
+    if (st == KVX_OK)
+        b->host = b->slot->host;
+    return st;
+}
+
+kvx_status launch_batch(kvx_ctx *ctx, void (*fn)(Args, Inline), Args a, Batch *b, int64_t ctas,
+                        size_t smem, int64_t items, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    if (b->slot) {
+        a.ext = b->slot->dev;
+        e = kvx::stage(ctx, *b->slot, b->bytes, 0, 0, s);
+    }
+    if (e != cudaSuccess)
+        return kvx::cuda_err(ctx, e, "descriptor copy");
+    if (smem > 48 * 1024 - 256)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e == cudaSuccess) {
+        void *args[] = {&a, &b->in};
+        e = cudaLaunchKernel(reinterpret_cast<const void *>(fn), dim3(unsigned(ctas)),
+                             dim3(kThreads), args, smem, s);
+    }
+    if (e != cudaSuccess)
+        return kvx::cuda_err(ctx, e, "kernel launch");
+    if (b->slot)
+        return kvx::finish_call(ctx, *b->slot, s, items, ctas, kThreads, b->bytes);
+    ctx->last_items = items;
+    ctx->last_ctas = int32_t(ctas);
+    ctx->last_threads = kThreads;
+    ctx->last_desc_bytes = int64_t(b->bytes);
+    return KVX_OK;
+}
+
+Args common_args(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs, int n)
+{
+    Args a = {};
+    a.refs = refs;
+    a.status = ctx->status_dev;
+    a.token_bytes = pool->token_bytes;
+    a.n_entries = n;
+    a.n_slabs = pool->num_layers * pool->kv_factor;
+    a.off_entries = int32_t((size_t(a.n_slabs) * sizeof(char *) + 15) / 16 * 16);
+    a.page_size = pool->page_size;
+    a.num_pages = pool->num_pages;
+    return a;
+}
+
+kvx_status too_many_jobs(kvx_ctx *ctx, int64_t pages, const Args &a)
+{
+    return pages > INT32_MAX / (int64_t(a.n_slabs) * a.slices)
+               ? kvx::set_err(ctx, KVX_ERR_CAPACITY, "%lld pages x %d slabs x %d slices exceed "
+                              "2^31 copies", (long long)pages, a.n_slabs, a.slices)
+               : KVX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvx_status kvx_fork_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                          const kvx_fork *forks, int n_forks, kvx_stream_t stream)
+{
+    if (!ctx)
+        return KVX_ERR_INVALID_ARG;
+    kvx::begin_call(ctx);
+    kvx_status st = kvx::validate_upkeep(pool, refs, forks, n_forks, nullptr, 0, ctx->validation,
+                                         true, ctx->err, sizeof ctx->err);
+    if (st != KVX_OK)
+        return st;
+    kvx::DeviceGuard guard(ctx->device);
+    if (!guard.ok)
+        return kvx::set_err(ctx, KVX_ERR_CUDA, "cannot make device %d current", ctx->device);
+    Args a = common_args(ctx, pool, refs, n_forks);
+    Batch b;
+    st = begin_batch(ctx, a.off_entries + (size_t(n_forks) + 1) * sizeof(ForkEntry), &b);
+    if (st != KVX_OK)
+        return st;
+    kvx::pack_slabs(pool, reinterpret_cast<char **>(b.host));
+    ForkEntry *e = reinterpret_cast<ForkEntry *>(b.host + a.off_entries);
+    st = kvx::pack_forks(pool, forks, n_forks, e, ctx->err, sizeof ctx->err);
+    if (st != KVX_OK)
+        return st;
+    const ForkEntry &end = e[n_forks];
+    if (end.page_begin == 0)
+        return KVX_OK;
+    int64_t longest = 0;  // tokens of a page that is copied
+    for (int i = 0; i < n_forks; ++i)
+        if (e[i + 1].copy_begin > e[i].copy_begin)
+            longest = std::max<int64_t>(longest, std::min(e[i].shared - e[i].full *
+                                                          pool->page_size, pool->page_size));
+    choose_slices(ctx, int64_t(end.copy_begin) * a.n_slabs,
+                  std::max<int64_t>(longest, 1) * pool->token_bytes, &a);
+    if ((st = too_many_jobs(ctx, end.copy_begin, a)) != KVX_OK)
+        return st;
+    a.counter = kvx::take_counter(ctx);
+    const int64_t jobs = int64_t(end.copy_begin) * a.n_slabs * a.slices;
+    const int64_t ctas = std::min<int64_t>(
+        ctx->num_sms, std::max((jobs + kWarps - 1) / kWarps,
+                               (int64_t(end.page_begin) + kThreads - 1) / kThreads));
+    return launch_batch(ctx, kvx_fork_kernel, a, &b, ctas, bitmap_bytes(pool->num_pages), jobs,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+static kvx_status tables_call(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                              const kvx_table *tables, int n_tables, int32_t *n_live,
+                              int32_t *remap, bool compact, kvx_stream_t stream)
+{
+    if (!ctx)
+        return KVX_ERR_INVALID_ARG;
+    kvx::begin_call(ctx);
+    kvx_status st = kvx::validate_upkeep(pool, refs, nullptr, 0, tables, n_tables,
+                                         ctx->validation, true, ctx->err, sizeof ctx->err);
+    if (st != KVX_OK)
+        return st;
+    if ((reinterpret_cast<uintptr_t>(n_live) | reinterpret_cast<uintptr_t>(remap)) & 3)
+        return kvx::set_err(ctx, KVX_ERR_ALIGNMENT, "n_live or remap not 4-byte aligned");
+    kvx::DeviceGuard guard(ctx->device);
+    if (!guard.ok)
+        return kvx::set_err(ctx, KVX_ERR_CUDA, "cannot make device %d current", ctx->device);
+    Args a = common_args(ctx, pool, refs, n_tables);
+    if (!compact)
+        a.off_entries = a.n_slabs = 0;
+    Batch b;
+    st = begin_batch(ctx, a.off_entries + (size_t(n_tables) + 1) * sizeof(TableEntry), &b);
+    if (st != KVX_OK)
+        return st;
+    if (compact)
+        kvx::pack_slabs(pool, reinterpret_cast<char **>(b.host));
+    TableEntry *e = reinterpret_cast<TableEntry *>(b.host + a.off_entries);
+    st = kvx::pack_tables(tables, n_tables, e, ctx->err, sizeof ctx->err);
+    if (st != KVX_OK)
+        return st;
+    const int64_t entries = e[n_tables].page_begin;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!compact) {
+        if (entries == 0)
+            return KVX_OK;
+        const int64_t ctas = std::min<int64_t>(ctx->num_sms, (entries + kThreads - 1) / kThreads);
+        return launch_batch(ctx, kvx_free_kernel, a, &b, ctas, 0, entries, s);
+    }
+    a.n_live = n_live;
+    a.remap = remap;
+    // How many pages move is known on the device only: at most half the pool.
+    choose_slices(ctx, int64_t(pool->num_pages) * a.n_slabs / 4,
+                  int64_t(pool->page_size) * pool->token_bytes, &a);
+    if ((st = too_many_jobs(ctx, pool->num_pages / 2, a)) != KVX_OK)
+        return st;
+    a.counter = kvx::take_counter(ctx);
+    return launch_batch(ctx, kvx_compact_kernel, a, &b, ctx->num_sms,
+                        bitmap_bytes(pool->num_pages), entries, s);
+}
+
+kvx_status kvx_free_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                          const kvx_table *tables, int n_tables, kvx_stream_t stream)
+{
+    return tables_call(ctx, pool, refs, tables, n_tables, nullptr, nullptr, false, stream);
+}
+
+kvx_status kvx_compact_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                             const kvx_table *tables, int n_tables, int32_t *n_live,
+                             int32_t *remap, kvx_stream_t stream)
+{
+    return tables_call(ctx, pool, refs, tables, n_tables, n_live, remap, true, stream);
+}
+
+}  // extern "C"

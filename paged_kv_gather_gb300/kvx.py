@@ -40,6 +40,14 @@ KVX_ERR_CAPACITY = 8
 
 KVX_DEV_PAGE_OUT_OF_RANGE = 0x1
 KVX_DEV_WAIT_TIMEOUT = 0x2
+KVX_DEV_NO_FREE_PAGE = 0x4
+KVX_DEV_PAGE_NOT_HELD = 0x8
+
+KVX_MAX_UPKEEP_PAGES = 1 << 20
+
+KVX_TYPE_HALF = 0
+KVX_TYPE_BFLOAT = 1
+KVX_TYPE_FP_EIGHT = 2
 
 KVX_CHUNK_LAYER_MAJOR = 0
 KVX_CHUNK_TOKEN_MAJOR = 1
@@ -105,13 +113,37 @@ class kvx_link_model(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class kvx_table(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class kvx_fork(ctypes.Structure):
+    _fields_ = [("parent", ctypes.c_void_p), ("child", ctypes.c_void_p),
+                ("shared_tokens", ctypes.c_int32), ("child_tokens", ctypes.c_int32),
+                ("copy", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class kvx_attn_cfg(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("kv_type", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p)]
+
+
 CHUNK_DTYPE = np.dtype([("request", "<i4"), ("token_begin", "<i4"), ("n_tokens", "<i4"),
                         ("layer_begin", "<i4"), ("n_layers", "<i4"), ("layout", "<i4"),
                         ("ptr", "<u8")])
 REQUEST_DTYPE = np.dtype([("page_table", "<u8"), ("page_table_host", "<u8"),
                           ("n_tokens", "<i4"), ("reserved", "<i4")])
+TABLE_DTYPE = np.dtype([("pages", "<u8"), ("n_pages", "<i4"), ("reserved", "<i4")])
+FORK_DTYPE = np.dtype([("parent", "<u8"), ("child", "<u8"), ("shared_tokens", "<i4"),
+                       ("child_tokens", "<i4"), ("copy", "<i4"), ("reserved", "<i4")])
 assert CHUNK_DTYPE.itemsize == ctypes.sizeof(kvx_chunk)
 assert REQUEST_DTYPE.itemsize == ctypes.sizeof(kvx_request)
+assert TABLE_DTYPE.itemsize == ctypes.sizeof(kvx_table)
+assert FORK_DTYPE.itemsize == ctypes.sizeof(kvx_fork)
 
 # ---------------------------------------------------------------------------- prototypes
 
@@ -189,6 +221,26 @@ _proto("kvx_partition_info", _c.c_int, [_c.c_void_p, _c.c_int, _P(_c.c_void_p),
 _proto("kvx_partition_destroy", None, [_c.c_void_p])
 _proto("kvx_load_chunks_noalloc", _c.c_int, [*_batch, _P(kvx_launch_cfg), _c.c_void_p,
                                              _c.c_void_p])
+_upkeep = [_ctx_t, _P(kvx_pool), _c.c_void_p, _c.c_void_p, _c.c_int]
+_proto("kvx_fork_pages", _c.c_int, [*_upkeep, _c.c_void_p])
+_proto("kvx_free_pages", _c.c_int, [*_upkeep, _c.c_void_p])
+_proto("kvx_compact_pages", _c.c_int, [*_upkeep, _c.c_void_p, _c.c_void_p, _c.c_void_p])
+_proto("kvx_upkeep_validate", _c.c_int,
+       [_P(kvx_pool), _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_int, _c.c_int,
+        _c.c_char_p, _c.c_size_t])
+_step = [_c.c_void_p, _c.c_int, _c.c_void_p, _c.c_void_p]
+_proto("kvx_attn_plan_create", _c.c_int,
+       [_ctx_t, _P(kvx_pool), *_step, _P(kvx_attn_cfg), _c.c_void_p, _P(_c.c_void_p)])
+_proto("kvx_attn_plan_update", _c.c_int, [_c.c_void_p, *_step, _c.c_void_p])
+_proto("kvx_attn_plan_destroy", None, [_c.c_void_p])
+_proto("kvx_append_tokens", _c.c_int,
+       [_c.c_void_p, _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_float,
+        _c.c_float, _c.c_void_p])
+_proto("kvx_attend", _c.c_int,
+       [_c.c_void_p, _c.c_int, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p,
+        _c.c_float, _c.c_float, _c.c_void_p])
+_proto("kvx_attn_validate", _c.c_int,
+       [_P(kvx_pool), *_step, _P(kvx_attn_cfg), _c.c_int, _c.c_char_p, _c.c_size_t])
 
 EXPORTED = ["kvx_create", "kvx_destroy", "kvx_set_validation", "kvx_default_launch_cfg",
             "kvx_store_chunks", "kvx_load_chunks", "kvx_exchange_chunks", "kvx_roundtrip_chunks",
@@ -200,7 +252,9 @@ EXPORTED = ["kvx_create", "kvx_destroy", "kvx_set_validation", "kvx_default_laun
             "kvx_load_chunks_noalloc", "kvx_default_link_model", "kvx_estimate_us",
             "kvx_estimate_pair_us", "kvx_estimate_stream_us", "kvx_partition_create",
             "kvx_partition_info", "kvx_partition_destroy", "kvx_test_roundtrip_timeout",
-            "kvx_roundtrip_unit"]
+            "kvx_roundtrip_unit", "kvx_fork_pages", "kvx_free_pages", "kvx_compact_pages",
+            "kvx_upkeep_validate", "kvx_attn_plan_create", "kvx_attn_plan_update",
+            "kvx_attn_plan_destroy", "kvx_append_tokens", "kvx_attend", "kvx_attn_validate"]
 
 KVX_NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -305,6 +359,36 @@ def chunks_array(specs, base_ptr: int) -> np.ndarray:
         a["layout"] = [c.layout for c in specs]
         a["ptr"] = np.asarray([c.offset for c in specs], np.uint64) + np.uint64(base_ptr)
     return a
+
+
+def tables_array(entries) -> np.ndarray:
+    """entries: iterable of (page_table_ptr, n_pages) of tables a call may rewrite."""
+    entries = list(entries)
+    a = np.zeros(len(entries), TABLE_DTYPE)
+    for i, (ptr, n) in enumerate(entries):
+        a[i]["pages"] = ptr
+        a[i]["n_pages"] = n
+    return a
+
+
+def forks_array(entries) -> np.ndarray:
+    """entries: iterable of (parent_ptr, child_ptr, shared_tokens, child_tokens, copy)."""
+    entries = list(entries)
+    a = np.zeros(len(entries), FORK_DTYPE)
+    for i, (parent, child, shared, total, copy) in enumerate(entries):
+        a[i] = (parent, child, shared, total, int(copy), 0)
+    return a
+
+
+_TYPES = {"fp16": KVX_TYPE_HALF, "bf16": KVX_TYPE_BFLOAT, "fp8": KVX_TYPE_FP_EIGHT}
+
+
+def attn_config(q_heads: int, kv_heads: int, head_dim: int, dtype: str = "bf16",
+                kv_dtype: Optional[str] = None, window: int = 0, scale: float = 0.0,
+                softcap: float = 0.0, slopes: int = 0) -> kvx_attn_cfg:
+    """A kvx_attn_cfg; dtype "fp16" or "bf16", kv_dtype the same (default) or "fp8" (e4m3)."""
+    return kvx_attn_cfg(q_heads, kv_heads, head_dim, _TYPES[dtype], _TYPES[kv_dtype or dtype],
+                        window, scale, softcap, slopes or None)
 
 
 def _arr_ptr(a: Optional[np.ndarray], dtype) -> Tuple[int, int]:
@@ -511,6 +595,97 @@ def kvx_load_chunks_noalloc(pool: Pool, reqs, chunks, layer_begin: int = 0,
                                       _cfg_ptr(cfg), stream, device_flags or None)
     if st != KVX_OK:
         raise KvxError(st, "kvx_load_chunks_noalloc")
+
+
+def kvx_fork_pages(ctx, pool: Pool, refs: int, forks, stream: int = 0) -> None:
+    """Fork requests (forks_array): share full pages, copy the rest into free ones."""
+    p, n = _arr_ptr(forks, FORK_DTYPE)
+    _check(ctx, _lib.kvx_fork_pages(ctx, ctypes.byref(pool.c), refs, p, n, stream))
+
+
+def kvx_free_pages(ctx, pool: Pool, refs: int, tables, stream: int = 0) -> None:
+    """Give back every page of the tables (tables_array); their entries become -1."""
+    p, n = _arr_ptr(tables, TABLE_DTYPE)
+    _check(ctx, _lib.kvx_free_pages(ctx, ctypes.byref(pool.c), refs, p, n, stream))
+
+
+def kvx_compact_pages(ctx, pool: Pool, refs: int, tables, n_live: int = 0, remap: int = 0,
+                      stream: int = 0) -> None:
+    """Move the live pages to the front of the pool and rewrite counts and tables."""
+    p, n = _arr_ptr(tables, TABLE_DTYPE)
+    _check(ctx, _lib.kvx_compact_pages(ctx, ctypes.byref(pool.c), refs, p, n, n_live or None,
+                                       remap or None, stream))
+
+
+def kvx_upkeep_validate(pool: Pool, refs: int, forks=None, tables=None,
+                        level: int = 1) -> Tuple[int, str]:
+    """Host checks of the page upkeep calls alone: (status, message)."""
+    fp, nf = _arr_ptr(forks, FORK_DTYPE)
+    tp, nt = _arr_ptr(tables, TABLE_DTYPE)
+    buf = ctypes.create_string_buffer(512)
+    st = _lib.kvx_upkeep_validate(ctypes.byref(pool.c), refs or None, fp, nf, tp, nt, level, buf,
+                                  len(buf))
+    return st, buf.value.decode()
+
+
+def _step_args(reqs, n_new, prefix):
+    """reqs, n_req, n_new and prefix of a step, and the arrays that must outlive the call."""
+    rp, nr = _arr_ptr(reqs, REQUEST_DTYPE)
+    new = np.ascontiguousarray(n_new, dtype=np.int32)
+    pre = None if prefix is None else np.ascontiguousarray(prefix, dtype=np.int32)
+    if len(new) != nr or (pre is not None and len(pre) != nr):
+        raise ValueError("n_new and prefix need one entry per request")
+    return [rp, nr, new.ctypes.data, None if pre is None else pre.ctypes.data], (new, pre)
+
+
+def kvx_attn_plan_create(ctx, pool: Pool, reqs, n_new, cfg: kvx_attn_cfg, prefix=None,
+                         stream: int = 0):
+    """A plan of one step's batch for kvx_append_tokens and kvx_attend; returns its handle."""
+    args, keep = _step_args(reqs, n_new, prefix)
+    h = ctypes.c_void_p()
+    _check(ctx, _lib.kvx_attn_plan_create(ctx, ctypes.byref(pool.c), *args, ctypes.byref(cfg),
+                                          stream, ctypes.byref(h)))
+    h.ctx = ctx  # for error messages; the context must outlive the plan
+    return h
+
+
+def kvx_attn_plan_update(plan, reqs, n_new, prefix=None, stream: int = 0) -> None:
+    """Refill a plan with the next step's batch (no more requests than it was made with)."""
+    args, keep = _step_args(reqs, n_new, prefix)
+    _check(plan.ctx, _lib.kvx_attn_plan_update(plan, *args, stream))
+
+
+def kvx_attn_plan_destroy(plan) -> None:
+    """Wait for the device, then free an attention plan (before its context)."""
+    _lib.kvx_attn_plan_destroy(plan)
+
+
+def kvx_append_tokens(plan, layer: int, k: int, v: int, k_stride: int = 0, v_stride: int = 0,
+                      k_scale: float = 1.0, v_scale: float = 1.0, stream: int = 0) -> None:
+    """Write the step's new K and V (device addresses, strides in elements) into the pages."""
+    st = _lib.kvx_append_tokens(plan, layer, k, v, k_stride, v_stride, k_scale, v_scale, stream)
+    if st != KVX_OK:
+        raise KvxError(st, kvx_last_error(plan.ctx))
+
+
+def kvx_attend(plan, layer: int, q: int, out: int, q_stride: int = 0, out_stride: int = 0,
+               lse: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+               stream: int = 0) -> None:
+    """Attention of the step's rows over the pages of `layer` (device addresses)."""
+    st = _lib.kvx_attend(plan, layer, q, q_stride, out, out_stride, lse or None, k_scale, v_scale,
+                         stream)
+    if st != KVX_OK:
+        raise KvxError(st, kvx_last_error(plan.ctx))
+
+
+def kvx_attn_validate(pool: Pool, reqs, n_new, cfg: kvx_attn_cfg, prefix=None,
+                      level: int = 1) -> Tuple[int, str]:
+    """Host checks of kvx_attn_plan_create alone: (status, message)."""
+    args, keep = _step_args(reqs, n_new, prefix)
+    buf = ctypes.create_string_buffer(512)
+    st = _lib.kvx_attn_validate(ctypes.byref(pool.c), *args, ctypes.byref(cfg), level, buf,
+                                len(buf))
+    return st, buf.value.decode()
 
 
 def kvx_dma_baseline(ctx, direction: int, pool: Pool, reqs, chunks, layer_begin: int = 0,
