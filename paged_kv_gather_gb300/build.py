@@ -24,7 +24,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_UNITS = ("kvx.cu", "kvx_pages.cu", "kvx_attend.cu")
 HOST_UNITS = ("kvx_host.cpp", "kvx_cache_host.cpp", "kvx_partition.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in CUDA_UNITS + HOST_UNITS + (
-    "kvx_kernels.cuh", "kvx_internal.h", "kvx_rules.h", "kvx_ctx.h", "kvx_cache.h")]
+    "kvx_kernels.cuh", "kvx_internal.h", "kvx_rules.h", "kvx_ctx.h", "kvx_cache.h",
+    "kvx_attend.cuh", "kvx_attend_rows.cuh", "kvx_attend_tiles.cuh")]
 HEADER = os.path.join(ROOT, "include", "kvx.h")
 
 

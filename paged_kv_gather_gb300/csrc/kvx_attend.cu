@@ -1,8 +1,6 @@
 // kvx_attend.cu -- append and attention over the pages of a paged KV cache: plans, entry
-// points and kernels.  The checks are in kvx_cache_host.cpp.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+// points and the append kernel.  The attention kernels are in kvx_attend_rows.cuh and
+// kvx_attend_tiles.cuh, the checks in kvx_cache_host.cpp.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -10,10 +8,20 @@
 #include <cstring>
 #include <new>
 
+#include "kvx_attend.cuh"
+#include "kvx_attend_rows.cuh"
+#include "kvx_attend_tiles.cuh"
 #include "kvx_cache.h"
 #include "kvx_ctx.h"
 
-using kvx::AttnReq;
+// One of the two attention kernels: requests of at most kRowMax rows per KV head, and the rest.
+enum { kRows = 0, kTiles = 1 };
+
+struct Schedule {
+    int n_req = 0;
+    int64_t tiles = 0;
+    int ctas = 0;
+};
 
 struct kvx_attn_plan {
     kvx_ctx *ctx = nullptr;
@@ -24,10 +32,20 @@ struct kvx_attn_plan {
     int capacity = 0;          // requests
     int n_req = 0;
     int64_t rows = 0;
-    char *host = nullptr;      // pinned image of the device descriptors
-    char *dev = nullptr;
-    size_t bytes = 0;
-    cudaEvent_t copied = nullptr;  // the last update's copy
+    Schedule kind[2];
+    // Descriptors: [AttnStart of each kind][AttnReq of all, of each kind]; a pinned image, and
+    // the device's copy.
+    char *host = nullptr, *dev = nullptr;
+    unsigned int *counters = nullptr;  // [kind][2 * SMs], zero between launches
+    float *partial = nullptr;          // of both kinds, one after the other's launch
+    cudaEvent_t copied = nullptr;      // the last update's copy
+
+    size_t starts_at(int k) const { return size_t(k) * ctx->num_sms * sizeof(kvx::AttnStart); }
+    size_t reqs_at(int k) const  // k = 2: all requests, for append
+    {
+        return starts_at(2) + size_t(k) * capacity * sizeof(AttnReq);
+    }
+    size_t bytes() const { return reqs_at(3); }
 };
 
 namespace {
@@ -39,26 +57,6 @@ struct Step {
     int32_t rows;
     int32_t page_size;
     int32_t num_pages;
-};
-
-template <int TYPE>
-struct Elem;
-template <>
-struct Elem<KVX_TYPE_HALF> {
-    typedef __half T;
-    static __device__ float load(T x) { return __half2float(x); }
-    static __device__ T store(float x) { return __float2half_rn(x); }
-};
-template <>
-struct Elem<KVX_TYPE_BFLOAT> {
-    typedef __nv_bfloat16 T;
-    static __device__ float load(T x) { return __bfloat162float(x); }
-    static __device__ T store(float x) { return __float2bfloat16_rn(x); }
-};
-template <>
-struct Elem<KVX_TYPE_FP_EIGHT> {
-    typedef __nv_fp8_e4m3 T;
-    static __device__ float load(T x) { return float(x); }
 };
 
 // Request of a row: the last r with row_begin <= row that has rows.  Requests without new
@@ -128,84 +126,45 @@ kvx_append_kernel(const Append a)
     }
 }
 
-// ------------------------------------------------------------------------------- attend
-
-struct Attend {
-    Step step;
-    const char *q;
-    char *out;
-    float *lse;
-    int64_t q_stride, out_stride;  // bytes between tokens
-    const char *k, *v;             // layer's pools
-    int64_t token_bytes;
-    const float *slopes;
-    int32_t q_heads, kv_heads, window;
-    float scale;                   // of q . k, with k_scale
-    float softcap, v_scale;
-};
-
-// A warp per (row, query head), one key at a time.
-template <int TYPE, int KV, int D>
-__global__ void __launch_bounds__(128)
-kvx_attend_kernel(const Attend a)
-{
-    typedef Elem<TYPE> E;
-    typedef Elem<KV> C;
-    const int lane = threadIdx.x & 31;
-    const int64_t job = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (job >= int64_t(a.step.rows) * a.q_heads)
-        return;
-    const int row = int(job / a.q_heads), h = int(job % a.q_heads);
-    const int kvh = h / (a.q_heads / a.kv_heads);
-    const AttnReq r = a.step.reqs[request_of_row(a.step.reqs, a.step.n_req, row, lane)];
-    const int pos = r.n_tokens - r.n_new + row - r.row_begin;
-    const int low = a.window ? max(0, pos - a.window + 1) : 0;
-    float q[D / 32], o[D / 32];
-    const typename E::T *qp = reinterpret_cast<const typename E::T *>(a.q + row * a.q_stride) + h * D;
-    for (int i = 0; i < D / 32; ++i) {
-        q[i] = E::load(qp[lane + 32 * i]);
-        o[i] = 0.0f;
-    }
-    float m = -INFINITY, l = 0.0f;
-    const int end = max(pos + 1, r.prefix);
-    for (int j = 0; j < end; ++j) {
-        if (j >= r.prefix && j < low) {
-            j = low - 1;
-            continue;
-        }
-        const int page = r.table[j / a.step.page_size];
-        if (unsigned(page) >= unsigned(a.step.num_pages)) {
-            if (lane == 0)
-                atomicOr(a.step.status, KVX_DEV_PAGE_OUT_OF_RANGE);
-            continue;
-        }
-        const int64_t at = (int64_t(page) * a.step.page_size + j % a.step.page_size) * a.token_bytes;
-        const typename C::T *k = reinterpret_cast<const typename C::T *>(a.k + at) + kvh * D;
-        const typename C::T *v = reinterpret_cast<const typename C::T *>(a.v + at) + kvh * D;
-        float s = 0.0f;
-        for (int i = 0; i < D / 32; ++i)
-            s += q[i] * C::load(k[lane + 32 * i]);
-        for (int d = 16; d; d >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= a.scale;
-        if (a.softcap > 0.0f)
-            s = a.softcap * tanhf(s / a.softcap);
-        if (a.slopes)
-            s -= a.slopes[h] * fabsf(float(pos - j));
-        const float m2 = fmaxf(m, s), keep = expf(m - m2), p = expf(s - m2);
-        l = l * keep + p;
-        for (int i = 0; i < D / 32; ++i)
-            o[i] = o[i] * keep + p * C::load(v[lane + 32 * i]);
-        m = m2;
-    }
-    typename E::T *op = reinterpret_cast<typename E::T *>(a.out + row * a.out_stride) + h * D;
-    for (int i = 0; i < D / 32; ++i)
-        op[lane + 32 * i] = E::store(o[i] / l * a.v_scale);
-    if (a.lse && lane == 0)
-        a.lse[job] = m + logf(l);
-}
-
 // ---------------------------------------------------------------------------------- host
+
+// Lay the units of one kind end to end and give every CTA its share (struct Work).
+void schedule(kvx_attn_plan *p, int kind, const AttnReq *reqs, int n_req)
+{
+    const int group = p->cfg.q_heads / p->cfg.kv_heads;
+    const int T = kind == kRows ? kRowTile : kTileKeys;
+    const int block_rows = kind == kRows ? kRowMax : kBlockRows;
+    auto blocks = [&](const AttnReq &r) {
+        return int((int64_t(r.n_new) * group + block_rows - 1) / block_rows);
+    };
+    auto tiles_of = [&](const AttnReq &r, int block) {
+        const int64_t row0 = int64_t(block) * block_rows;
+        const int64_t row1 = std::min<int64_t>(row0 + block_rows, int64_t(r.n_new) * group) - 1;
+        const int pmin = r.n_tokens - r.n_new + int(row0 / group);
+        const int pmax = r.n_tokens - r.n_new + int(row1 / group);
+        int first, skip, tiles;
+        kvx::key_tiles(r.prefix, p->cfg.window ? std::max(0, pmin - p->cfg.window + 1) : 0,
+                       pmax + 1, T, &first, &skip, &tiles);
+        return tiles;
+    };
+    Schedule &s = p->kind[kind];
+    s.n_req = n_req;
+    s.tiles = 0;
+    for (int r = 0; r < n_req; ++r)
+        for (int b = 0, n = blocks(reqs[r]); b < n; ++b)
+            s.tiles += int64_t(tiles_of(reqs[r], b)) * p->cfg.kv_heads;
+    s.ctas = int(std::min<int64_t>(p->ctx->num_sms, s.tiles));
+    kvx::AttnStart *out = reinterpret_cast<kvx::AttnStart *>(p->host + p->starts_at(kind));
+    int64_t line = 0;
+    int c = 0;
+    for (int r = 0; r < n_req; ++r)
+        for (int b = 0, n = blocks(reqs[r]); b < n; ++b) {
+            const int64_t tiles = tiles_of(reqs[r], b), all = tiles * p->cfg.kv_heads;
+            for (int64_t at; c < s.ctas && (at = c * s.tiles / s.ctas) < line + all; ++c)
+                out[c] = {r, b, int32_t((at - line) / tiles), int32_t((at - line) % tiles)};
+            line += all;
+        }
+}
 
 kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const int32_t *n_new,
                      const int32_t *prefix, cudaStream_t s)
@@ -214,17 +173,28 @@ kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const
     cudaError_t e = cudaEventSynchronize(p->copied);  // the image may still be being read
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "waiting for the plan's last copy");
-    AttnReq *out = reinterpret_cast<AttnReq *>(p->host);
+    const int group = p->cfg.q_heads / p->cfg.kv_heads;
+    AttnReq *lists[3];
+    for (int k = 0; k < 3; ++k)
+        lists[k] = reinterpret_cast<AttnReq *>(p->host + p->reqs_at(k));
+    int counts[2] = {0, 0};
     int64_t rows = 0;
     for (int r = 0; r < n_req; ++r) {
-        out[r] = {reqs[r].page_table, reqs[r].n_tokens, n_new[r], prefix ? prefix[r] : 0,
-                  int32_t(rows), {0, 0}};
+        const AttnReq x = {reqs[r].page_table, reqs[r].n_tokens, n_new[r], prefix ? prefix[r] : 0,
+                           int32_t(rows), {0, 0}};
+        lists[2][r] = x;
+        if (n_new[r] > 0) {
+            const int k = int64_t(n_new[r]) * group <= kRowMax ? kRows : kTiles;
+            lists[k][counts[k]++] = x;
+        }
         rows += n_new[r];
     }
     p->n_req = n_req;
     p->rows = rows;
+    for (int k = 0; k < 2; ++k)
+        schedule(p, k, lists[k], counts[k]);
     if (n_req) {
-        e = cudaMemcpyAsync(p->dev, p->host, n_req * sizeof(AttnReq), cudaMemcpyHostToDevice, s);
+        e = cudaMemcpyAsync(p->dev, p->host, p->bytes(), cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess)
             e = cudaEventRecord(p->copied, s);
     }
@@ -254,22 +224,37 @@ kvx_status io_check(const kvx_attn_plan *p, int layer, const void *x, int64_t *s
 
 Step step_of(const kvx_attn_plan *p)
 {
-    return {reinterpret_cast<const AttnReq *>(p->dev), p->ctx->status_dev, p->n_req,
+    return {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(2)), p->ctx->status_dev, p->n_req,
             int32_t(p->rows), p->page_size, p->num_pages};
 }
 
-const void *attend_kernel(const kvx_attn_cfg &c)
+// Kernel of a kind, with its shared memory and the floats of a partial result.
+struct Kernel {
+    const void *fn;
+    int threads;
+    size_t smem;
+    int slot_floats;
+};
+
+template <int TYPE, int KV, int D>
+Kernel kernel_of(int kind)
 {
-#define PICK(T, K)                                                                    \
-    if (c.type == T && c.kv_type == K)                                                \
-        return c.head_dim == 64 ? reinterpret_cast<const void *>(kvx_attend_kernel<T, K, 64>) \
-                                : reinterpret_cast<const void *>(kvx_attend_kernel<T, K, 128>);
-    PICK(KVX_TYPE_HALF, KVX_TYPE_HALF)
-    PICK(KVX_TYPE_HALF, KVX_TYPE_FP_EIGHT)
-    PICK(KVX_TYPE_BFLOAT, KVX_TYPE_BFLOAT)
-    PICK(KVX_TYPE_BFLOAT, KVX_TYPE_FP_EIGHT)
-#undef PICK
-    return nullptr;
+    if (kind == kRows)
+        return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D>), kRowThreads,
+                row_smem(), row_slot_floats<D>()};
+    return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KV, D>), kTileThreads,
+            size_t(TileShape<D>::kBytes), TileShape<D>::kSlotFloats};
+}
+
+Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
+{
+    const bool half = c.type == KVX_TYPE_HALF, eight = c.kv_type == KVX_TYPE_FP_EIGHT;
+    const int H = KVX_TYPE_HALF, B = KVX_TYPE_BFLOAT, F = KVX_TYPE_FP_EIGHT;
+    if (c.head_dim == 64)
+        return half ? eight ? kernel_of<H, F, 64>(kind) : kernel_of<H, H, 64>(kind)
+                    : eight ? kernel_of<B, F, 64>(kind) : kernel_of<B, B, 64>(kind);
+    return half ? eight ? kernel_of<H, F, 128>(kind) : kernel_of<H, H, 128>(kind)
+                : eight ? kernel_of<B, F, 128>(kind) : kernel_of<B, B, 128>(kind);
 }
 
 }  // namespace
@@ -303,17 +288,30 @@ kvx_status kvx_attn_plan_create(kvx_ctx *ctx, const kvx_pool *pool, const kvx_re
     p->num_layers = pool->num_layers;
     p->token_bytes = pool->token_bytes;
     p->capacity = n_req;
-    p->bytes = std::max<size_t>(1, n_req) * sizeof(AttnReq);
     p->pools = new (std::nothrow) char *[2 * size_t(pool->num_layers)];
     if (!p->pools) {
         kvx_attn_plan_destroy(p);
         return kvx::set_err(ctx, KVX_ERR_CAPACITY, "out of host memory");
     }
     kvx::pack_slabs(pool, p->pools);
-    cudaError_t e = cudaHostAlloc(reinterpret_cast<void **>(&p->host), p->bytes,
-                                  cudaHostAllocDefault);
+    size_t partial = 0;
+    cudaError_t e = cudaSuccess;
+    for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
+        const Kernel kn = pick_kernel(p->cfg, k);
+        partial = std::max(partial, 2 * size_t(ctx->num_sms) * kn.slot_floats * sizeof(float));
+        e = cudaFuncSetAttribute(kn.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kn.smem));
+    }
     if (e == cudaSuccess)
-        e = cudaMalloc(reinterpret_cast<void **>(&p->dev), p->bytes);
+        e = cudaHostAlloc(reinterpret_cast<void **>(&p->host), p->bytes(), cudaHostAllocDefault);
+    if (e == cudaSuccess)
+        e = cudaMalloc(reinterpret_cast<void **>(&p->dev), p->bytes());
+    if (e == cudaSuccess)
+        e = cudaMalloc(reinterpret_cast<void **>(&p->partial), partial);
+    const size_t counters = 4 * size_t(ctx->num_sms) * sizeof(unsigned int);
+    if (e == cudaSuccess)
+        e = cudaMalloc(reinterpret_cast<void **>(&p->counters), counters);
+    if (e == cudaSuccess)
+        e = cudaMemsetAsync(p->counters, 0, counters, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess)
         e = cudaEventCreateWithFlags(&p->copied, cudaEventDisableTiming);
     if (e != cudaSuccess) {
@@ -364,8 +362,10 @@ void kvx_attn_plan_destroy(kvx_attn_plan *p)
         cudaDeviceSynchronize();
         if (p->copied)
             cudaEventDestroy(p->copied);
-        if (p->dev)
-            cudaFree(p->dev);
+        for (void *d : {static_cast<void *>(p->dev), static_cast<void *>(p->counters),
+                        static_cast<void *>(p->partial)})
+            if (d)
+                cudaFree(d);
         if (p->host)
             cudaFreeHost(p->host);
     }
@@ -435,16 +435,27 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
     if (!guard.ok)
         return kvx::set_err(p->ctx, KVX_ERR_CUDA, "cannot make device %d current",
                             p->ctx->device);
-    Attend a = {step_of(p), static_cast<const char *>(q), static_cast<char *>(out), lse, q_stride,
-                out_stride, p->pools[2 * layer], p->pools[2 * layer + 1], p->token_bytes,
-                p->cfg.slopes, p->cfg.q_heads, p->cfg.kv_heads, p->cfg.window,
-                p->cfg.scale * k_scale, p->cfg.softcap, v_scale};
-    void *args[] = {&a};
-    const int64_t jobs = p->rows * p->cfg.q_heads;
-    const cudaError_t e = cudaLaunchKernel(attend_kernel(p->cfg), dim3(unsigned((jobs + 3) / 4)),
-                                           dim3(128), args, 0,
-                                           reinterpret_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? KVX_OK : kvx::cuda_err(p->ctx, e, "attention launch");
+    const Attend a = {static_cast<const char *>(q), static_cast<char *>(out), lse, q_stride,
+                      out_stride, p->pools[2 * layer], p->pools[2 * layer + 1], p->token_bytes,
+                      p->cfg.slopes, p->ctx->status_dev, p->cfg.q_heads, p->cfg.kv_heads,
+                      p->cfg.q_heads / p->cfg.kv_heads, p->cfg.window, p->page_size, p->num_pages,
+                      p->cfg.scale * k_scale, p->cfg.softcap, v_scale};
+    for (int k = 0; k < 2; ++k) {
+        const Schedule &s = p->kind[k];
+        if (s.ctas == 0)
+            continue;
+        const Kernel kn = pick_kernel(p->cfg, k);
+        const Work w = {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(k)),
+                        reinterpret_cast<const kvx::AttnStart *>(p->dev + p->starts_at(k)),
+                        p->counters + 2 * k * p->ctx->num_sms, p->partial, s.tiles, s.ctas};
+        void *args[] = {const_cast<Attend *>(&a), const_cast<Work *>(&w)};
+        const cudaError_t e = cudaLaunchKernel(kn.fn, dim3(unsigned(s.ctas)),
+                                               dim3(unsigned(kn.threads)), args, kn.smem,
+                                               reinterpret_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return kvx::cuda_err(p->ctx, e, "attention launch");
+    }
+    return KVX_OK;
 }
 
 }  // extern "C"

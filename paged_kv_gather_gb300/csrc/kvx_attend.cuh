@@ -1,0 +1,157 @@
+// kvx_attend.cuh -- what the attention kernels share: element types, a step's schedule,
+// visibility of keys, and the scores' arithmetic.  Included by kvx_attend.cu only.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kvx_cache.h"
+
+using kvx::AttnReq;
+using kvx::AttnStart;
+
+namespace {
+
+const float kLog2e = 1.4426950408889634f;
+const float kLn2 = 0.6931471805599453f;
+
+struct Attend {
+    const char *q;
+    char *out;
+    float *lse;
+    int64_t q_stride, out_stride;  // bytes between tokens
+    const char *k, *v;             // the layer's pools
+    int64_t token_bytes;
+    const float *slopes;
+    unsigned int *status;
+    int32_t q_heads, kv_heads, group, window;
+    int32_t page_size, num_pages;
+    float scale;                   // of q . k, with k_scale
+    float softcap, v_scale;
+};
+
+// The schedule of one kernel.  The keys that each unit of rows visits, cut into tiles, are
+// laid end to end over all units; CTA c takes tiles [c * tiles / ctas, (c + 1) * tiles / ctas)
+// of that line, so every CTA has the same work to within a tile whatever the lengths.  A unit
+// that one CTA does not finish alone is joined from partial results: CTA c keeps one it began
+// and did not finish in slot 2 c + 1, and one it took over from CTA c - 1 in slot 2 c.
+struct Work {
+    const AttnReq *reqs;       // of this kernel, those with rows
+    const AttnStart *starts;   // [ctas]
+    unsigned int *counters;    // [ctas]: arrivals at the unit that CTA c began, zero between launches
+    float *partial;
+    int64_t tiles;
+    int32_t ctas;
+};
+
+// CTA that takes tile x of the line.
+__device__ __forceinline__ int cta_of(const Work &w, int64_t x)
+{
+    return int(((x + 1) * w.ctas - 1) / w.tiles);
+}
+
+// Keys that some row of a unit sees: [0, prefix) and [low, end); positions of its first and
+// last row.  Tiles of T keys: tile i holds keys from T * (i < first ? i : i + skip), so that
+// keys between prefix and low are passed over in whole tiles.
+struct Keys {
+    int prefix, low, end, pmin, pmax;
+    int first, skip, tiles;
+
+    template <int T>
+    __device__ __forceinline__ void set(const AttnReq &r, int window, int row_lo, int row_hi)
+    {
+        prefix = r.prefix;
+        pmin = r.n_tokens - r.n_new + row_lo;
+        pmax = r.n_tokens - r.n_new + row_hi;
+        low = window ? max(0, pmin - window + 1) : 0;
+        end = pmax + 1;
+        kvx::key_tiles(prefix, low, end, T, &first, &skip, &tiles);
+    }
+    __device__ __forceinline__ bool used(int j) const
+    {
+        return j < prefix || (j >= low && j < end);
+    }
+};
+
+__device__ __forceinline__ float exp2_(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh by its definition, 1 - 2 / (exp(2 x) + 1): off by a few 2^-24 of 1 whatever x, where
+// the hardware's approximate tanh is off by 2^-11.
+__device__ __forceinline__ float tanh_(float x)
+{
+    return 1.0f - __fdividef(2.0f, exp2_(x * (2.0f * kLog2e)) + 1.0f);
+}
+
+// What turns q . k into a score in units of log 2.
+struct Score {
+    float factor;      // without a cap: scale * log2 e
+    float cap, inner;  // with one: cap * log2 e, scale / softcap
+
+    __device__ __forceinline__ explicit Score(const Attend &a)
+        : factor(a.scale * kLog2e), cap(a.softcap * kLog2e),
+          inner(a.softcap > 0.0f ? a.scale / a.softcap : 0.0f)
+    {
+    }
+    __device__ __forceinline__ float capped(float dot) const { return cap * tanh_(dot * inner); }
+};
+
+// 2^-e and 2^e with 2^e the power of two above `top` >= 0; e is kept to what leaves both
+// normal numbers.
+__device__ __forceinline__ void unit_scale(float top, float *down, float *up)
+{
+    const int e = min(max(int(__float_as_uint(top) >> 23) - 126, -60), 126);
+    *down = __uint_as_float(unsigned(127 - e) << 23);
+    *up = __uint_as_float(unsigned(127 + e) << 23);
+}
+
+template <int TYPE>
+struct Elem;
+template <>
+struct Elem<KVX_TYPE_HALF> {
+    typedef __half T;
+    static __device__ __forceinline__ float load(T x) { return __half2float(x); }
+    static __device__ __forceinline__ unsigned pack(float lo, float hi)
+    {
+        unsigned r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+};
+template <>
+struct Elem<KVX_TYPE_BFLOAT> {
+    typedef __nv_bfloat16 T;
+    static __device__ __forceinline__ float load(T x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ unsigned pack(float lo, float hi)
+    {
+        unsigned r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+};
+
+// All of a kernel's dynamic shared memory; the matrix tiles in it start on 1024 bytes.
+extern __shared__ __align__(1024) char attend_smem[];
+
+__device__ __forceinline__ unsigned smem_u32(const void *p)
+{
+    return unsigned(__cvta_generic_to_shared(p));
+}
+
+// 16 bytes into shared memory, zeros if !valid.
+__device__ __forceinline__ void cp_async16(unsigned dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+
+}  // namespace

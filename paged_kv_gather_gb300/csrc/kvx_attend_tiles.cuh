@@ -1,0 +1,824 @@
+// kvx_attend_tiles.cuh -- attention of more than 16 rows per KV head (prefill chunks, many
+// drafted tokens): every key meets enough rows that the tensor cores bound the kernel.
+// Included by kvx_attend.cu only.
+#pragma once
+
+#include "kvx_attend.cuh"
+
+namespace {
+
+// A CTA takes a block of 256 rows (new tokens x the heads that share a KV head, packed) of one
+// KV head as two tiles of 128, 128 keys at a time.  Tensor memory holds, per tile, the scores
+// S (128 columns) and the output O (D columns), 512 columns in all at D = 128; the weights P
+// go back into the columns of S as the first operand of P V, so they never pass through
+// shared memory.  Two warpgroups turn the scores of one tile each into weights, a thread per
+// row, while the tensor cores work on the other tile: S0 -> P0 beside P1 V, S1 and so on.
+// One warp issues the products; three warps bring K and V from the pages into a ring of
+// shared-memory slots (K0, V0, K1, V1, ...).
+//
+// Shared-memory tiles are [D / 64][128 rows][64 elements] with the 16-byte chunks of a
+// 128-byte line permuted by the row's low three bits, the layout the matrix instructions
+// call 128-byte swizzle.  K and q are read along it, V across it (its rows are the summed
+// index), so the same copy serves both.
+const int kTileThreads = 384;
+const int kTileRows = 128;
+const int kTileKeys = 128;
+const int kBlockRows = 2 * kTileRows;
+const int kLoaders = 96;
+const int kLoaderLag = 2;          // slots a loader fills before it announces the first
+
+template <int D>
+struct TileShape {
+    static const int kTile = kTileRows * D * 2;              // bytes of a q, K or V tile
+    static const int kSlots = D == 128 ? 5 : 10;
+    static const int kOffRing = 2 * kTile;
+    static const int kOffKeys = kOffRing + kSlots * kTile;   // int64 [2][kTileKeys]
+    static const int kOffBars = kOffKeys + 2 * kTileKeys * 8;
+    static const int kOffMisc = kOffBars + 256;              // int[4]
+    static const int kBytes = kOffMisc + 16;
+    static const int kSlotFloats = kBlockRows * (D + 2);     // a partial result: O, m, l
+};
+
+// Barriers, by index: of the two tiles of rows first, then loader's, the ring's, the end's.
+enum {
+    kBarQ = 0,      // q is in shared memory
+    kBarS = 2,      // S is complete, and every product before it
+    kBarP = 4,      // P is in tensor memory
+    kBarO = 6,      // O is complete
+    kBarJoin = 8,   // the threads of the tile among themselves
+    kBarKeys = 10,  // the loaders among themselves
+    kBarFull = 11,
+    kBarEmpty = 21,
+    kBarEnd = 31,
+    kBars = 32
+};
+
+__device__ __forceinline__ void mbar_init(unsigned bar, unsigned count)
+{
+    asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(unsigned bar)
+{
+    asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(unsigned bar, unsigned phase)
+{
+    unsigned ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared.b64 p, [%1], %2; "
+                 "selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(phase)
+                 : "memory");
+    return ok;
+}
+
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Wait for a phase of a barrier, for about a second at most; then, or once another wait of
+// the CTA has run out, false.  The answer is the same for a whole warp.  No thread of the
+// kernel waits in any other way than this before its last barrier, so a wait that runs out
+// ends the launch.
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned phase, volatile int *gave_up,
+                                          unsigned *status)
+{
+    bool ok = mbar_try(bar, phase);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const uint64_t t0 = now_ns();
+        for (;;) {
+            for (int i = 0; i < 64 && !ok; ++i)
+                ok = mbar_try(bar, phase);
+            if (__all_sync(0xffffffffu, ok))
+                return true;
+            if (__any_sync(0xffffffffu, *gave_up != 0))
+                return false;
+            if (__any_sync(0xffffffffu, now_ns() - t0 > 1000000000ull)) {
+                *gave_up = 1;
+                atomicOr(status, KVX_DEV_WAIT_TIMEOUT);
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void fence_async_shared()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tc_fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tc_commit(unsigned bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::
+                     "r"(bar)
+                 : "memory");
+}
+
+// D (tensor memory) = A B, or += with `add`; A in shared or tensor memory, B in shared.
+__device__ __forceinline__ void tc_mma_ss(unsigned d, uint64_t a, uint64_t b, unsigned idesc,
+                                          bool add)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; "
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
+                 "l"(b), "r"(idesc), "r"(unsigned(add))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_ts(unsigned d, unsigned a, uint64_t b, unsigned idesc,
+                                          bool add)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; "
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
+                 "l"(b), "r"(idesc), "r"(unsigned(add))
+                 : "memory");
+}
+
+// 32 (16) consecutive columns of this thread's lane of tensor memory.
+__device__ __forceinline__ void tc_ld32(float (&r)[32], unsigned addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+          "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]),
+          "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]),
+          "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_st32(unsigned addr, const float (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31, %32};" ::"r"(addr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
+        "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]),
+        "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]), "f"(r[19]), "f"(r[20]), "f"(r[21]),
+        "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]), "f"(r[28]),
+        "f"(r[29]), "f"(r[30]), "f"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_st16(unsigned addr, const unsigned (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+// The loads into r are complete; keeps uses of r behind the wait.
+__device__ __forceinline__ void tc_wait_ld(float (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        asm volatile("" : "+f"(r[i]));
+}
+
+// Two 32-bit numbers at a time.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ float2 halves_of(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ void tc_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory operand with 128-byte swizzle: 8-row groups 1024 bytes apart; `lead` bytes
+// between 64-element blocks where the operand is read across its lines.
+__device__ __forceinline__ uint64_t tile_desc(unsigned addr, unsigned lead)
+{
+    return uint64_t((addr & 0x3ffff) >> 4) | uint64_t(lead >> 4) << 16 | uint64_t(1024 >> 4) << 32 |
+           uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+
+// kind::f16 with 32-bit accumulators, M = 128.
+__host__ __device__ constexpr unsigned mma_idesc(int type, int n, bool b_across)
+{
+    return 1u << 4 | unsigned(type == KVX_TYPE_BFLOAT) << 7 | unsigned(type == KVX_TYPE_BFLOAT) << 10 |
+           unsigned(b_across) << 16 | unsigned(n / 8) << 17 | unsigned(128 / 16) << 24;
+}
+
+// Byte offset of 16-byte chunk c of row r in a shared-memory tile.
+__device__ __forceinline__ int tile_at(int r, int c)
+{
+    return (c >> 3) * (kTileRows * 128) + r * 128 + (((c ^ r) & 7) << 4);
+}
+
+// Walks a CTA's share of the line; every role of the CTA steps through the same units.
+struct Walk {
+    const Attend &a;
+    const Work &w;
+    int64_t line, line1;
+    AttnStart at;
+    AttnReq r;
+    Keys keys;
+    int row0, rows, todo;   // of the block; tiles of keys to do
+
+    __device__ __forceinline__ Walk(const Attend &a_, const Work &w_) : a(a_), w(w_)
+    {
+        line = int64_t(blockIdx.x) * w.tiles / w.ctas;
+        line1 = (int64_t(blockIdx.x) + 1) * w.tiles / w.ctas;
+        at = w.starts[blockIdx.x];
+        if (line < line1)
+            enter();
+    }
+    __device__ __forceinline__ bool done() const { return line >= line1; }
+    __device__ __forceinline__ int key_of(int i) const
+    {
+        const int t = at.tile + i;
+        return (t < keys.first ? t : t + keys.skip) * kTileKeys;
+    }
+    __device__ __forceinline__ void enter()
+    {
+        r = w.reqs[at.request];
+        const int all = r.n_new * a.group;
+        row0 = at.block * kBlockRows;
+        rows = min(kBlockRows, all - row0);
+        keys.set<kTileKeys>(r, a.window, row0 / a.group, (row0 + rows - 1) / a.group);
+        todo = int(min(int64_t(keys.tiles - at.tile), line1 - line));
+    }
+    __device__ __forceinline__ void next()
+    {
+        line += todo;
+        if (done())
+            return;
+        at.tile = 0;
+        if (++at.head == a.kv_heads) {
+            at.head = 0;
+            if ((++at.block) * kBlockRows >= r.n_new * a.group) {
+                at.block = 0;
+                ++at.request;
+            }
+        }
+        enter();
+    }
+};
+
+template <int TYPE, int KV, int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+kvx_attend_tiles_kernel(const Attend a, const Work w)
+{
+    typedef TileShape<D> T;
+    typedef Elem<TYPE> E;
+    constexpr bool kEight = KV == KVX_TYPE_FP_EIGHT;
+    constexpr int kMath = kEight ? KVX_TYPE_HALF : TYPE;
+    typedef Elem<kMath> P;
+    char *smem = attend_smem;
+    int *misc = reinterpret_cast<int *>(smem + T::kOffMisc);
+    int &gave_up = misc[0];
+    unsigned &tmem_base = reinterpret_cast<unsigned &>(misc[1]);
+    int *last_cta = misc + 2;
+    const unsigned sm = smem_u32(smem);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto bar = [&](int i) { return sm + T::kOffBars + 8 * i; };
+    auto wait = [&](int i, unsigned phase) { return mbar_wait(bar(i), phase, &gave_up, a.status); };
+
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar(kBarQ + x), kTileRows);
+            mbar_init(bar(kBarJoin + x), kTileRows);
+            mbar_init(bar(kBarS + x), 1);
+            mbar_init(bar(kBarP + x), kTileRows);
+            mbar_init(bar(kBarO + x), 1);
+        }
+        mbar_init(bar(kBarKeys), kLoaders);
+        mbar_init(bar(kBarEnd), 1);
+        for (int i = 0; i < T::kSlots; ++i) {
+            mbar_init(bar(kBarFull + i), kLoaders);
+            mbar_init(bar(kBarEmpty + i), 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const unsigned tmem = tmem_base;
+
+    if (warp == 8) {
+        // ------------------------------------------------------------- matrix products
+        constexpr unsigned kDescS = mma_idesc(kMath, kTileKeys, false);
+        constexpr unsigned kDescO = mma_idesc(kMath, D, true);
+        unsigned slot = 0, turn = 0;  // ring position and its phase
+        unsigned q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        bool ok = true;
+        auto scores = [&](int x, unsigned s) {
+            const uint64_t q = tile_desc(sm + x * T::kTile, 16);
+            const uint64_t k = tile_desc(sm + T::kOffRing + s * T::kTile, 16);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint64_t step = ((i >> 2) * (kTileRows * 128) + (i & 3) * 32) >> 4;
+                tc_mma_ss(tmem + x * kTileKeys, q + step, k + step, kDescS, i > 0);
+            }
+            tc_commit(bar(kBarS + x));
+        };
+        auto advance = [&]() {
+            if (++slot == T::kSlots) {
+                slot = 0;
+                turn ^= 1;
+            }
+        };
+        for (Walk u(a, w); ok && !u.done(); u.next()) {
+            const int tiles = u.rows > kTileRows ? 2 : 1;
+            for (int x = 0; ok && x < tiles; ++x) {
+                ok = wait(kBarQ + x, q_phase[x]);
+                q_phase[x] ^= 1;
+            }
+            if (!ok || !(ok = wait(kBarFull + slot, turn)))
+                break;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int x = 0; x < tiles; ++x)
+                    scores(x, slot);
+                tc_commit(bar(kBarEmpty + slot));
+            }
+            __syncwarp();
+            advance();
+            for (int i = 0; i < u.todo; ++i) {
+                const unsigned v_slot = slot;
+                ok = wait(kBarFull + slot, turn);
+                if (!ok)
+                    break;
+                advance();
+                const bool more = i + 1 < u.todo;
+                if (more && !(ok = wait(kBarFull + slot, turn)))
+                    break;
+                for (int x = 0; x < tiles; ++x) {
+                    ok = wait(kBarP + x, p_phase[x]);
+                    if (!ok)
+                        break;
+                    p_phase[x] ^= 1;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t v = tile_desc(sm + T::kOffRing + v_slot * T::kTile,
+                                                     kTileRows * 128);
+#pragma unroll
+                        for (int k = 0; k < kTileKeys / 16; ++k)
+                            tc_mma_ts(tmem + 2 * kTileKeys + x * D, tmem + x * kTileKeys + 8 * k,
+                                      v + (k * 2048 >> 4), kDescO, i > 0 || k > 0);
+                        if (more)
+                            scores(x, slot);
+                        else
+                            tc_commit(bar(kBarO + x));
+                    }
+                    __syncwarp();
+                }
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    tc_commit(bar(kBarEmpty + v_slot));
+                    if (more)
+                        tc_commit(bar(kBarEmpty + slot));
+                }
+                __syncwarp();
+                if (more)
+                    advance();
+            }
+        }
+        if (!ok) {
+            // Let what was issued run out before the memory it works on goes away.
+            if (lane == 0)
+                tc_commit(bar(kBarEnd));
+            const uint64_t t0 = now_ns();
+            while (!__all_sync(0xffffffffu, mbar_try(bar(kBarEnd), 0)) &&
+                   !__any_sync(0xffffffffu, now_ns() - t0 > 1000000000ull)) {
+            }
+        }
+    } else if (warp > 8) {
+        // ------------------------------------------------------------- K and V
+        const int lt = threadIdx.x - (kTileThreads - kLoaders);
+        int64_t *offs = reinterpret_cast<int64_t *>(smem + T::kOffKeys);  // [2][kTileKeys]
+        constexpr int kRow = D * (kEight ? 1 : 2), kChunks = kRow / 16;
+        unsigned slot = 0, turn = 0, filled = 0;  // filled: slots issued so far
+        bool ok = true;
+        auto announce = [&](unsigned n) {  // slot number n of the stream is complete
+            fence_async_shared();
+            mbar_arrive(bar(kBarFull + n % T::kSlots));
+        };
+        unsigned parity = 0;
+        for (Walk u(a, w); ok && !u.done(); u.next()) {
+            const int64_t head_at = int64_t(u.at.head) * kRow;
+            for (int i = 0; ok && i < u.todo; ++i) {
+                // Where each key of the tile lies; -1: not used.
+                int64_t *off = offs + parity * kTileKeys;
+                parity ^= 1;
+                const int j0 = u.key_of(i);
+                for (int t = lt; t < kTileKeys; t += kLoaders) {
+                    const int j = j0 + t;
+                    int64_t o = -1;
+                    if (u.keys.used(j)) {
+                        const int page = __ldg(u.r.table + j / a.page_size);
+                        if (unsigned(page) < unsigned(a.num_pages))
+                            o = (int64_t(page) * a.page_size + j % a.page_size) * a.token_bytes +
+                                head_at;
+                        else
+                            atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+                    }
+                    off[t] = o;
+                }
+                mbar_arrive(bar(kBarKeys));
+                ok = wait(kBarKeys, parity ^ 1);
+                for (int side = 0; ok && side < 2; ++side) {
+                    if (!(ok = wait(kBarEmpty + slot, turn ^ 1)))
+                        break;
+                    const char *base = side ? a.v : a.k;
+                    char *dst = smem + T::kOffRing + slot * T::kTile;
+                    if (!kEight) {
+                        const unsigned d = smem_u32(dst);
+#pragma unroll 4
+                        for (int x = lt; x < kTileKeys * kChunks; x += kLoaders) {
+                            const int t = x / kChunks, c = x % kChunks;
+                            const int64_t o = off[t];
+                            cp_async16(d + tile_at(t, c), base + (o >= 0 ? o : 0) + c * 16, o >= 0);
+                        }
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        if (filled >= kLoaderLag) {
+                            asm volatile("cp.async.wait_group %0;" ::"n"(kLoaderLag) : "memory");
+                            announce(filled - kLoaderLag);
+                        }
+                    } else {
+                        constexpr int kBatch = 6;
+                        for (int x0 = lt; x0 < kTileKeys * kChunks; x0 += kBatch * kLoaders) {
+                            uint4 in[kBatch];
+#pragma unroll
+                            for (int b = 0; b < kBatch; ++b) {
+                                const int x = x0 + b * kLoaders;
+                                in[b] = make_uint4(0, 0, 0, 0);
+                                if (x < kTileKeys * kChunks) {
+                                    const int64_t o = off[x / kChunks];
+                                    if (o >= 0)
+                                        in[b] = __ldg(reinterpret_cast<const uint4 *>(
+                                            base + o + x % kChunks * 16));
+                                }
+                            }
+#pragma unroll
+                            for (int b = 0; b < kBatch; ++b) {
+                                const int x = x0 + b * kLoaders;
+                                if (x < kTileKeys * kChunks) {
+                                    const int t = x / kChunks, c = x % kChunks;
+                                    const unsigned y[4] = {in[b].x, in[b].y, in[b].z, in[b].w};
+                                    unsigned h[8];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        h[2 * k] = half2_of_e4m3(y[k] & 0xffffu);
+                                        h[2 * k + 1] = half2_of_e4m3(y[k] >> 16);
+                                    }
+                                    *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c)) =
+                                        make_uint4(h[0], h[1], h[2], h[3]);
+                                    *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c + 1)) =
+                                        make_uint4(h[4], h[5], h[6], h[7]);
+                                }
+                            }
+                        }
+                        announce(filled);
+                    }
+                    ++filled;
+                    if (++slot == T::kSlots) {
+                        slot = 0;
+                        turn ^= 1;
+                    }
+                }
+            }
+        }
+        if (!kEight) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            for (unsigned n = filled > kLoaderLag ? filled - kLoaderLag : 0; ok && n < filled; ++n)
+                announce(n);
+        }
+    } else {
+        // ------------------------------------------------------------- weights
+        const int x = warp >> 2;                        // tile of rows
+        const int row = threadIdx.x & (kTileRows - 1);  // and row in it
+        const unsigned lanes = unsigned(warp & 3) << 21;
+        const unsigned ts = tmem + lanes + x * kTileKeys;
+        const unsigned to = tmem + lanes + 2 * kTileKeys + x * D;
+        const Score score(a);
+        unsigned s_phase = 0, o_phase = 0;
+        bool ok = true;
+        for (Walk u(a, w); ok && !u.done(); u.next()) {
+            const bool mine = x == 0 || u.rows > kTileRows;  // the tile has rows
+            const bool have = x * kTileRows + row < u.rows;
+            const int packed = u.row0 + (have ? x * kTileRows + row : 0);
+            const int tok = packed / a.group, head = u.at.head * a.group + packed - tok * a.group;
+            const int pos = u.r.n_tokens - u.r.n_new + tok;
+            const int64_t orow = u.r.row_begin + tok;
+            const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.0f;
+            float row_factor = 1.0f;
+            if (mine) {
+                // q into shared memory, a row per thread.
+                const uint4 *q = reinterpret_cast<const uint4 *>(a.q + orow * a.q_stride +
+                                                                 head * (D * 2));
+                char *dst = smem + x * T::kTile;
+                float down = 1.0f;
+                if (kEight) {  // scaled by a power of two into half precision
+                    float top = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 v = have ? q[c] : make_uint4(0, 0, 0, 0);
+                        const typename E::T *e = reinterpret_cast<const typename E::T *>(&v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            top = fmaxf(top, fabsf(E::load(e[i])));
+                    }
+                    unit_scale(top, &down, &row_factor);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 v = have ? q[c] : make_uint4(0, 0, 0, 0);
+                    if (kEight) {
+                        const typename E::T *e = reinterpret_cast<const typename E::T *>(&v);
+                        uint4 h;
+                        h.x = P::pack(E::load(e[0]) * down, E::load(e[1]) * down);
+                        h.y = P::pack(E::load(e[2]) * down, E::load(e[3]) * down);
+                        h.z = P::pack(E::load(e[4]) * down, E::load(e[5]) * down);
+                        h.w = P::pack(E::load(e[6]) * down, E::load(e[7]) * down);
+                        v = h;
+                    }
+                    *reinterpret_cast<uint4 *>(dst + tile_at(row, c)) = v;
+                }
+                fence_async_shared();
+                mbar_arrive(bar(kBarQ + x));
+            }
+            float m = -INFINITY, l = 0.0f;
+            if (mine) {
+                // Scores stay products of q and k, with one factor to units of log 2, where
+                // that factor is all there is to them.  The same for a whole warp: the loads
+                // and stores of tensor memory below must not diverge.
+                const float factor = score.factor * row_factor;
+                const bool plain = !(a.softcap > 0.0f) && !a.slopes && a.scale > 1e-10f;
+                for (int i = 0; i < u.todo; ++i) {
+                    const int j0 = u.key_of(i);
+                    ok = wait(kBarS + x, s_phase);
+                    if (!ok)
+                        break;
+                    s_phase ^= 1;
+                    tc_fence_after();
+                    const bool all_seen = j0 + kTileKeys <= u.keys.prefix ||
+                                          (j0 + kTileKeys - 1 <= u.keys.pmin &&
+                                           (!a.window || j0 > u.keys.pmax - a.window));
+                    // First pass: the largest score.  Scores that need more than one factor,
+                    // or have hidden ones among them, are written back as they are to be used.
+                    // Reading S twice costs less than the 128 registers of holding it.
+                    const float unit = plain ? factor : 1.0f;
+                    float top = -INFINITY;
+                    if (plain && all_seen) {
+                        float s[2][32], t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        tc_ld32(s[0], ts);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            float(&z)[32] = s[b & 1];
+                            tc_wait_ld(z);
+                            if (b < 3)
+                                tc_ld32(s[(b + 1) & 1], ts + 32 * (b + 1));
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                t4[k & 3] = fmaxf(t4[k & 3], z[k]);
+                        }
+                        top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    } else {
+                        const int lo = a.window ? pos - a.window + 1 - j0 : -j0;
+                        const int hi = pos - j0, pre = u.keys.prefix - j0;
+#pragma unroll 1
+                        for (int b = 0; b < 4; ++b) {
+                            float z[32];
+                            tc_ld32(z, ts + 32 * b);
+                            tc_wait_ld(z);
+                            if (!plain) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) {
+                                    z[k] = a.softcap > 0.0f ? score.capped(z[k] * row_factor)
+                                                            : z[k] * factor;
+                                    z[k] -= slope * fabsf(float(hi - 32 * b - k));
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int j = 32 * b + k;
+                                if (!(j < pre || (j >= lo && j <= hi)))
+                                    z[k] = -INFINITY;
+                                top = fmaxf(top, z[k]);
+                            }
+                            tc_st32(ts + 32 * b, z);
+                        }
+                        tc_wait_st();
+                    }
+                    top *= unit;
+                    // The subtracted maximum may lag by up to 2^8; O is rescaled only past
+                    // that.  S of this step is complete, so P V of the last one is too.
+                    const bool lift = top > m + 8.0f;
+                    if (__any_sync(0xffffffffu, lift)) {
+                        const float next = lift ? top : m;
+                        const float keep = lift ? exp2_(m - next) : 1.0f;
+                        m = next;
+                        l *= keep;
+                        if (i > 0) {
+#pragma unroll 1
+                            for (int b = 0; b < D / 32; ++b) {
+                                float o[32];
+                                tc_ld32(o, to + 32 * b);
+                                tc_wait_ld(o);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    o[k] *= keep;
+                                tc_st32(to + 32 * b, o);
+                            }
+                        }
+                    }
+                    // Second pass: weights.  P of columns 32 b .. + 31 takes columns 16 b .. + 15,
+                    // which held scores that have been read.
+                    const float base = m == -INFINITY ? 0.0f : m;
+                    const uint64_t unit2 = pair_of(unit, unit), base2 = pair_of(-base, -base);
+                    uint64_t sum[2] = {0, 0};
+                    {
+                        float s[2][32];
+                        tc_ld32(s[0], ts);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            float(&z)[32] = s[b & 1];
+                            tc_wait_ld(z);
+                            if (b < 3)
+                                tc_ld32(s[(b + 1) & 1], ts + 32 * (b + 1));
+                            unsigned p[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                float2 e = halves_of(
+                                    fma_pair(pair_of(z[2 * k], z[2 * k + 1]), unit2, base2));
+                                e.x = exp2_(e.x);
+                                e.y = exp2_(e.y);
+                                sum[k & 1] = add_pair(sum[k & 1], pair_of(e.x, e.y));
+                                p[k] = P::pack(e.x, e.y);
+                            }
+                            tc_st16(ts + 16 * b, p);
+                        }
+                    }
+                    const float2 sums = halves_of(add_pair(sum[0], sum[1]));
+                    l += sums.x + sums.y;
+                    tc_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bar(kBarP + x));
+                }
+                if (!ok)
+                    break;
+                ok = wait(kBarO + x, o_phase);
+                if (!ok)
+                    break;
+                o_phase ^= 1;
+                tc_fence_after();
+            }
+
+            // The result, or this CTA's part of it.
+            const int64_t unit_at = u.line - u.at.tile;
+            const int c0 = cta_of(w, unit_at), c1 = cta_of(w, unit_at + u.keys.tiles - 1);
+            auto write = [&](int b, const float(&o)[32], float ll) {
+                const float f = a.v_scale / ll;
+                uint4 *out = reinterpret_cast<uint4 *>(a.out + orow * a.out_stride +
+                                                       (head * D + 32 * b) * 2);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    out[k] = make_uint4(E::pack(o[8 * k] * f, o[8 * k + 1] * f),
+                                        E::pack(o[8 * k + 2] * f, o[8 * k + 3] * f),
+                                        E::pack(o[8 * k + 4] * f, o[8 * k + 5] * f),
+                                        E::pack(o[8 * k + 6] * f, o[8 * k + 7] * f));
+            };
+            // A part: [D / 4][256 rows][4] of O, then [256][m, l].
+            const int prow = x * kTileRows + row;
+            auto part = [&](int c) {
+                return w.partial + (2 * int64_t(c) + (c == c0)) * T::kSlotFloats;
+            };
+            if (mine) {
+                float *slot = part(blockIdx.x);
+#pragma unroll 1
+                for (int b = 0; b < D / 32; ++b) {
+                    float o[32];
+                    tc_ld32(o, to + 32 * b);
+                    tc_wait_ld(o);
+                    if (c0 == c1) {
+                        if (have)
+                            write(b, o, l);
+                    } else if (have) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<float4 *>(slot + ((8 * b + k) * kBlockRows + prow) * 4) =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+                if (c0 == c1 && have && a.lse)
+                    a.lse[orow * a.q_heads + head] = m * kLn2 + logf(l);
+                if (c0 != c1 && have)
+                    *reinterpret_cast<float2 *>(slot + kBlockRows * D + 2 * prow) = make_float2(m, l);
+            }
+            if (mine && c0 != c1) {
+                // The last CTA to arrive joins the tile's parts, in order.
+                __threadfence();
+                mbar_arrive(bar(kBarJoin + x));
+                if (!(ok = wait(kBarJoin + x, 0)))
+                    break;
+                if (row == 0) {
+                    unsigned *counter = w.counters + 2 * c0 + x;
+                    const unsigned n = atomicAdd(counter, 1);
+                    last_cta[x] = n == unsigned(c1 - c0);
+                    if (n == unsigned(c1 - c0))
+                        *counter = 0;
+                    __threadfence();
+                }
+                mbar_arrive(bar(kBarJoin + x));
+                if (!(ok = wait(kBarJoin + x, 1)))
+                    break;
+                if (last_cta[x] && have) {
+                    float mm = -INFINITY, ll = 0.0f;
+                    for (int c = c0; c <= c1; ++c)
+                        mm = fmaxf(mm, __ldcg(part(c) + kBlockRows * D + 2 * prow));
+                    for (int c = c0; c <= c1; ++c) {
+                        const float2 p = __ldcg(reinterpret_cast<const float2 *>(
+                            part(c) + kBlockRows * D + 2 * prow));
+                        ll += p.x == -INFINITY ? 0.0f : exp2_(p.x - mm) * p.y;
+                    }
+#pragma unroll 1
+                    for (int b = 0; b < D / 32; ++b) {
+                        float o[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = 0.0f;
+                        for (int c = c0; c <= c1; ++c) {
+                            const float pm = __ldcg(part(c) + kBlockRows * D + 2 * prow);
+                            const float f = pm == -INFINITY ? 0.0f : exp2_(pm - mm);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                                    part(c) + ((8 * b + k) * kBlockRows + prow) * 4));
+                                o[4 * k] += f * v.x;
+                                o[4 * k + 1] += f * v.y;
+                                o[4 * k + 2] += f * v.z;
+                                o[4 * k + 3] += f * v.w;
+                            }
+                        }
+                        write(b, o, ll);
+                    }
+                    if (a.lse)
+                        a.lse[orow * a.q_heads + head] = mm * kLn2 + logf(ll);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+}  // namespace

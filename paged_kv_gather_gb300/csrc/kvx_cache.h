@@ -61,6 +61,34 @@ struct AttnReq {
 };
 static_assert(sizeof(AttnReq) == 32, "descriptor layout");
 
+// Where a CTA begins: unit (request, block of rows, KV head) and tile within it.
+struct AttnStart {
+    int32_t request;
+    int32_t block;
+    int32_t head;
+    int32_t tile;
+};
+static_assert(sizeof(AttnStart) == 16, "descriptor layout");
+
+// Tiles of T keys that cover [0, prefix) and [low, end), in order: `first` tiles from key 0,
+// then the rest `skip` tiles further on; no tile twice.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline void key_tiles(int prefix, int low, int end, int T, int *first, int *skip, int *tiles)
+{
+    const int f = (prefix + T - 1) / T, l = low / T;
+    if (f < l) {
+        *first = f;
+        *skip = l - f;
+        *tiles = f + (end + T - 1) / T - l;
+    } else {
+        *first = 0;
+        *skip = 0;
+        *tiles = ((end > prefix ? end : prefix) + T - 1) / T;
+    }
+}
+
 kvx_status validate_attn(const kvx_pool *pool, const kvx_request *reqs, int n_req,
                          const int32_t *n_new, const int32_t *prefix, const kvx_attn_cfg *cfg,
                          int level, bool have_gpu, char *msg, size_t len);
