@@ -14,8 +14,9 @@
 #include "kvx_cache.h"
 #include "kvx_ctx.h"
 
-// One of the two attention kernels: requests of at most kRowMax rows per KV head, and the rest.
-enum { kRows = 0, kTiles = 1 };
+// The attention kernels by the rows (new tokens x heads that share a KV head) of a request:
+// up to 8, up to 16, more.
+enum { kRows = 0, kMoreRows = 1, kTiles = 2, kKinds = 3 };
 
 struct Schedule {
     int n_req = 0;
@@ -32,20 +33,21 @@ struct kvx_attn_plan {
     int capacity = 0;          // requests
     int n_req = 0;
     int64_t rows = 0;
-    Schedule kind[2];
+    Schedule kind[kKinds];
     // Descriptors: [AttnStart of each kind][AttnReq of all, of each kind]; a pinned image, and
     // the device's copy.
     char *host = nullptr, *dev = nullptr;
-    unsigned int *counters = nullptr;  // [kind][2 * SMs], zero between launches
-    float *partial = nullptr;          // of both kinds, one after the other's launch
+    unsigned int *counters = nullptr;  // [2 * most_ctas()], zero between launches
+    float *partial = nullptr;          // serves one kind's launch after the other
     cudaEvent_t copied = nullptr;      // the last update's copy
 
-    size_t starts_at(int k) const { return size_t(k) * ctx->num_sms * sizeof(kvx::AttnStart); }
-    size_t reqs_at(int k) const  // k = 2: all requests, for append
+    int most_ctas() const { return 2 * ctx->num_sms; }  // of a launch
+    size_t starts_at(int k) const { return size_t(k) * most_ctas() * sizeof(kvx::AttnStart); }
+    size_t reqs_at(int k) const  // k = kKinds: all requests, for append
     {
-        return starts_at(2) + size_t(k) * capacity * sizeof(AttnReq);
+        return starts_at(kKinds) + size_t(k) * capacity * sizeof(AttnReq);
     }
-    size_t bytes() const { return reqs_at(3); }
+    size_t bytes() const { return reqs_at(kKinds + 1); }
 };
 
 namespace {
@@ -128,12 +130,46 @@ kvx_append_kernel(const Append a)
 
 // ---------------------------------------------------------------------------------- host
 
+// Kernel of a kind, with its shared memory and the floats of a partial result.
+struct Kernel {
+    const void *fn;
+    int threads, ctas_per_sm;
+    size_t smem;
+    int slot_floats;
+};
+
+template <int TYPE, int KV, int D>
+Kernel kernel_of(int kind)
+{
+    if (kind == kRows)
+        return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D, 1>),
+                kRowThreads, row_ctas_per_sm<KV, D, 1>(), row_smem<KV, D, 1>(),
+                row_slot_floats<D, 1>()};
+    if (kind == kMoreRows)
+        return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D, 2>),
+                kRowThreads, row_ctas_per_sm<KV, D, 2>(), row_smem<KV, D, 2>(),
+                row_slot_floats<D, 2>()};
+    return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KV, D>), kTileThreads, 1,
+            size_t(TileShape<D>::kBytes), TileShape<D>::kSlotFloats};
+}
+
+Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
+{
+    const bool half = c.type == KVX_TYPE_HALF, eight = c.kv_type == KVX_TYPE_FP_EIGHT;
+    const int H = KVX_TYPE_HALF, B = KVX_TYPE_BFLOAT, F = KVX_TYPE_FP_EIGHT;
+    if (c.head_dim == 64)
+        return half ? eight ? kernel_of<H, F, 64>(kind) : kernel_of<H, H, 64>(kind)
+                    : eight ? kernel_of<B, F, 64>(kind) : kernel_of<B, B, 64>(kind);
+    return half ? eight ? kernel_of<H, F, 128>(kind) : kernel_of<H, H, 128>(kind)
+                : eight ? kernel_of<B, F, 128>(kind) : kernel_of<B, B, 128>(kind);
+}
+
 // Lay the units of one kind end to end and give every CTA its share (struct Work).
 void schedule(kvx_attn_plan *p, int kind, const AttnReq *reqs, int n_req)
 {
     const int group = p->cfg.q_heads / p->cfg.kv_heads;
-    const int T = kind == kRows ? kRowTile : kTileKeys;
-    const int block_rows = kind == kRows ? kRowMax : kBlockRows;
+    const int T = kind == kTiles ? kTileKeys : kRowTile;
+    const int block_rows = kind == kTiles ? kBlockRows : kRowMax;
     auto blocks = [&](const AttnReq &r) {
         return int((int64_t(r.n_new) * group + block_rows - 1) / block_rows);
     };
@@ -153,7 +189,8 @@ void schedule(kvx_attn_plan *p, int kind, const AttnReq *reqs, int n_req)
     for (int r = 0; r < n_req; ++r)
         for (int b = 0, n = blocks(reqs[r]); b < n; ++b)
             s.tiles += int64_t(tiles_of(reqs[r], b)) * p->cfg.kv_heads;
-    s.ctas = int(std::min<int64_t>(p->ctx->num_sms, s.tiles));
+    s.ctas = int(std::min<int64_t>(
+        int64_t(p->ctx->num_sms) * pick_kernel(p->cfg, kind).ctas_per_sm, s.tiles));
     kvx::AttnStart *out = reinterpret_cast<kvx::AttnStart *>(p->host + p->starts_at(kind));
     int64_t line = 0;
     int c = 0;
@@ -174,24 +211,25 @@ kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "waiting for the plan's last copy");
     const int group = p->cfg.q_heads / p->cfg.kv_heads;
-    AttnReq *lists[3];
-    for (int k = 0; k < 3; ++k)
+    AttnReq *lists[kKinds + 1];
+    for (int k = 0; k <= kKinds; ++k)
         lists[k] = reinterpret_cast<AttnReq *>(p->host + p->reqs_at(k));
-    int counts[2] = {0, 0};
+    int counts[kKinds] = {};
     int64_t rows = 0;
     for (int r = 0; r < n_req; ++r) {
         const AttnReq x = {reqs[r].page_table, reqs[r].n_tokens, n_new[r], prefix ? prefix[r] : 0,
                            int32_t(rows), {0, 0}};
-        lists[2][r] = x;
+        lists[kKinds][r] = x;
         if (n_new[r] > 0) {
-            const int k = int64_t(n_new[r]) * group <= kRowMax ? kRows : kTiles;
+            const int64_t n = int64_t(n_new[r]) * group;
+            const int k = n <= 8 ? kRows : n <= kRowMax ? kMoreRows : kTiles;
             lists[k][counts[k]++] = x;
         }
         rows += n_new[r];
     }
     p->n_req = n_req;
     p->rows = rows;
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < kKinds; ++k)
         schedule(p, k, lists[k], counts[k]);
     if (n_req) {
         e = cudaMemcpyAsync(p->dev, p->host, p->bytes(), cudaMemcpyHostToDevice, s);
@@ -224,37 +262,8 @@ kvx_status io_check(const kvx_attn_plan *p, int layer, const void *x, int64_t *s
 
 Step step_of(const kvx_attn_plan *p)
 {
-    return {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(2)), p->ctx->status_dev, p->n_req,
+    return {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(kKinds)), p->ctx->status_dev, p->n_req,
             int32_t(p->rows), p->page_size, p->num_pages};
-}
-
-// Kernel of a kind, with its shared memory and the floats of a partial result.
-struct Kernel {
-    const void *fn;
-    int threads;
-    size_t smem;
-    int slot_floats;
-};
-
-template <int TYPE, int KV, int D>
-Kernel kernel_of(int kind)
-{
-    if (kind == kRows)
-        return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D>), kRowThreads,
-                row_smem(), row_slot_floats<D>()};
-    return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KV, D>), kTileThreads,
-            size_t(TileShape<D>::kBytes), TileShape<D>::kSlotFloats};
-}
-
-Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
-{
-    const bool half = c.type == KVX_TYPE_HALF, eight = c.kv_type == KVX_TYPE_FP_EIGHT;
-    const int H = KVX_TYPE_HALF, B = KVX_TYPE_BFLOAT, F = KVX_TYPE_FP_EIGHT;
-    if (c.head_dim == 64)
-        return half ? eight ? kernel_of<H, F, 64>(kind) : kernel_of<H, H, 64>(kind)
-                    : eight ? kernel_of<B, F, 64>(kind) : kernel_of<B, B, 64>(kind);
-    return half ? eight ? kernel_of<H, F, 128>(kind) : kernel_of<H, H, 128>(kind)
-                : eight ? kernel_of<B, F, 128>(kind) : kernel_of<B, B, 128>(kind);
 }
 
 }  // namespace
@@ -296,9 +305,10 @@ kvx_status kvx_attn_plan_create(kvx_ctx *ctx, const kvx_pool *pool, const kvx_re
     kvx::pack_slabs(pool, p->pools);
     size_t partial = 0;
     cudaError_t e = cudaSuccess;
-    for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
+    for (int k = 0; k < kKinds && e == cudaSuccess; ++k) {
         const Kernel kn = pick_kernel(p->cfg, k);
-        partial = std::max(partial, 2 * size_t(ctx->num_sms) * kn.slot_floats * sizeof(float));
+        partial = std::max(partial, 2 * size_t(ctx->num_sms) * kn.ctas_per_sm * kn.slot_floats *
+                                        sizeof(float));
         e = cudaFuncSetAttribute(kn.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kn.smem));
     }
     if (e == cudaSuccess)
@@ -307,7 +317,7 @@ kvx_status kvx_attn_plan_create(kvx_ctx *ctx, const kvx_pool *pool, const kvx_re
         e = cudaMalloc(reinterpret_cast<void **>(&p->dev), p->bytes());
     if (e == cudaSuccess)
         e = cudaMalloc(reinterpret_cast<void **>(&p->partial), partial);
-    const size_t counters = 4 * size_t(ctx->num_sms) * sizeof(unsigned int);
+    const size_t counters = 2 * size_t(p->most_ctas()) * sizeof(unsigned int);
     if (e == cudaSuccess)
         e = cudaMalloc(reinterpret_cast<void **>(&p->counters), counters);
     if (e == cudaSuccess)
@@ -439,15 +449,15 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
                       out_stride, p->pools[2 * layer], p->pools[2 * layer + 1], p->token_bytes,
                       p->cfg.slopes, p->ctx->status_dev, p->cfg.q_heads, p->cfg.kv_heads,
                       p->cfg.q_heads / p->cfg.kv_heads, p->cfg.window, p->page_size, p->num_pages,
-                      p->cfg.scale * k_scale, p->cfg.softcap, v_scale};
-    for (int k = 0; k < 2; ++k) {
+                      Divisor::of(p->page_size), p->cfg.scale * k_scale, p->cfg.softcap, v_scale};
+    for (int k = 0; k < kKinds; ++k) {
         const Schedule &s = p->kind[k];
         if (s.ctas == 0)
             continue;
         const Kernel kn = pick_kernel(p->cfg, k);
         const Work w = {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(k)),
                         reinterpret_cast<const kvx::AttnStart *>(p->dev + p->starts_at(k)),
-                        p->counters + 2 * k * p->ctx->num_sms, p->partial, s.tiles, s.ctas};
+                        p->counters, p->partial, s.tiles, s.ctas};
         void *args[] = {const_cast<Attend *>(&a), const_cast<Work *>(&w)};
         const cudaError_t e = cudaLaunchKernel(kn.fn, dim3(unsigned(s.ctas)),
                                                dim3(unsigned(kn.threads)), args, kn.smem,

@@ -19,6 +19,25 @@ namespace {
 const float kLog2e = 1.4426950408889634f;
 const float kLn2 = 0.6931471805599453f;
 
+// Division of 0 <= n < 2^31 by a number fixed on the host: with L = ceil(log2 d), n / d =
+// n m >> (31 + L) for m = floor(2^(31 + L) / d) + 1, whose error n (m - 2^(31+L) / d) stays
+// below 2^31, less than what reaches the next multiple.
+struct Divisor {
+    uint32_t m, shift;
+
+    static Divisor of(int d)
+    {
+        int L = 0;
+        while ((int64_t(1) << L) < d)
+            ++L;
+        return {uint32_t((uint64_t(1) << (31 + L)) / uint64_t(d) + 1), uint32_t(31 + L)};
+    }
+    __device__ __forceinline__ int div(int n) const
+    {
+        return int(uint64_t(uint32_t(n)) * m >> shift);
+    }
+};
+
 struct Attend {
     const char *q;
     char *out;
@@ -30,6 +49,7 @@ struct Attend {
     unsigned int *status;
     int32_t q_heads, kv_heads, group, window;
     int32_t page_size, num_pages;
+    Divisor page;
     float scale;                   // of q . k, with k_scale
     float softcap, v_scale;
 };

@@ -10,29 +10,50 @@ namespace {
 // A CTA of eight warps takes a unit (request, KV head) 128 keys at a time, 16 to a warp.  Each
 // warp streams its own keys through a private ring of shared-memory stages with asynchronous
 // copies and keeps its own running maximum, sum and output in registers, so warps wait for
-// nobody until the unit ends; then the eight results are joined in shared memory.  Products
-// run on m16n8k16 matrix instructions whose 16 rows hold the heads that share the KV head
-// times the new tokens: rows left over cost nothing that is scarce here.
+// nobody until the unit ends; then the eight results are joined in shared memory.
+//
+// The products are taken transposed, S' = K Q' and O' = V' P', on m16n8k16 matrix instructions:
+// keys and head elements fill the 16 rows and the unit's rows (new tokens x heads that share
+// the KV head) are the 8 columns, NT times.  With the unit's rows as the 16 instead, half of
+// the work and of the accumulators went to rows that do not exist.  P' changes from result to
+// operand by a transposition of 8 x 8 blocks between lanes.
 //
 // An e4m3 cache is multiplied in half precision, which holds every code exactly, whatever the
 // type of q: q is first scaled by a power of two per row to at most 1, which is exact for
 // bfloat16 down to 2^-24 of the row's largest element.  The order of the 16 elements a matrix
-// instruction sums over is free as long as both operands share it; K's is chosen so that a
-// thread's operands are 16 consecutive bytes, and V's columns likewise.
+// instruction sums over is free as long as both operands share it, and so is that of O's
+// columns; they are chosen so that a thread's operands are 16 consecutive bytes of a key.
 const int kRowWarps = 8;
 const int kRowThreads = 32 * kRowWarps;
 const int kRowKeys = 16;                      // keys per warp and step
 const int kRowTile = kRowKeys * kRowWarps;
-const int kRowRing = 24 << 10;                // bytes of a warp's ring
-const int kRowMax = 16;                       // rows of a unit
+const int kRowMax = 16;                       // rows of a unit, NT = 2
 const int kRowStages = 6;                     // at most
 
-template <int D>
-__host__ __device__ constexpr int row_slot_floats() { return kRowMax * (D + 2); }  // a partial result: O, m, l
+// Two CTAs share an SM where a stage of 16 keys is small enough that both rings, and the
+// registers of NT = 1, leave them room: their joins then hide behind each other's streaming.
+template <int KV, int D, int NT>
+__host__ __device__ constexpr int row_ctas_per_sm()
+{
+    return NT == 1 && D * (KV == KVX_TYPE_FP_EIGHT ? 1 : 2) <= 128 ? 2 : 1;
+}
 
+template <int KV, int D, int NT>
+__host__ __device__ constexpr int row_ring()  // bytes of a warp's ring
+{
+    return (24 << 10) / row_ctas_per_sm<KV, D, NT>();
+}
+
+template <int D, int NT>
+__host__ __device__ constexpr int row_slot_floats()  // a partial result: O, m, l
+{
+    return 8 * NT * (D + 2);
+}
+
+template <int KV, int D, int NT>
 constexpr size_t row_smem()
 {
-    return size_t(kRowWarps) * kRowRing + kRowWarps * kRowMax * 2 * 4;
+    return size_t(kRowWarps) * row_ring<KV, D, NT>() + kRowWarps * 8 * NT * 2 * 4;
 }
 
 __device__ __forceinline__ void ldmatrix4(unsigned (&r)[4], unsigned addr)
@@ -67,11 +88,19 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const unsigned (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes (low byte first) as two half-precision numbers.
-__device__ __forceinline__ unsigned half2_of_e4m3(unsigned two)
+// Four e4m3 codes (low byte first) as two pairs of half-precision numbers.
+__device__ __forceinline__ void half4_of_e4m3(unsigned four, unsigned &lo, unsigned &hi)
+{
+    asm("{ .reg .b16 x, y; mov.b32 {x, y}, %2; cvt.rn.f16x2.e4m3x2 %0, x; "
+        "cvt.rn.f16x2.e4m3x2 %1, y; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+
+__device__ __forceinline__ unsigned transpose8x8(unsigned x)
 {
     unsigned r;
-    asm("{ .reg .b16 x; cvt.u16.u32 x, %1; cvt.rn.f16x2.e4m3x2 %0, x; }" : "=r"(r) : "r"(two));
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
@@ -95,14 +124,15 @@ __device__ __forceinline__ uint2 lds8(unsigned addr)
 // Layout of a stage and of the matrix operands taken from it.  Rows of D elements lie back to
 // back; 16-byte chunks are permuted within 128-byte lines so that the reads of a warp spread
 // over all banks.
-template <int KV, int D>
+template <int KV, int D, int NT>
 struct RowLayout {
     static const int kItem = KV == KVX_TYPE_FP_EIGHT ? 1 : 2;
     static const int kRow = D * kItem;                 // bytes of a key
     static const int kChunks = kRow / 16;
     static const int kSide = kRowKeys * kRow;          // bytes of K (or V) in a stage
     static const int kStage = 2 * kSide;
-    static const int kNumStages = kRowRing / kStage < kRowStages ? kRowRing / kStage : kRowStages;
+    static const int kRing = row_ring<KV, D, NT>();
+    static const int kNumStages = kRing / kStage < kRowStages ? kRing / kStage : kRowStages;
     static const bool kEight = KV == KVX_TYPE_FP_EIGHT;
 
     // Byte offset of chunk c of key t.
@@ -121,31 +151,33 @@ struct RowLayout {
         const int x = t * kChunks + c;  // one or two chunks of every second key
         return ((x & ~7) | ((x & 7) ^ ((t >> 1 & 3) << 1))) << 4;
     }
-    // Output column held in element e (0, 1) of accumulator nt by quad thread c.
-    static __device__ __forceinline__ int column(int nt, int e, int c)
+    // Element of the head in row quad + 8 * half of block mt of O'.
+    static __device__ __forceinline__ int element(int mt, int half, int quad)
     {
-        return kEight ? (2 * c + e) * (D / 8) + nt : nt * 8 + 2 * c + e;
+        return kEight ? quad * (D / 8) + 2 * mt + half : 16 * mt + 8 * half + quad;
     }
 };
 
-template <int TYPE, int KV, int D>
-__global__ void __launch_bounds__(kRowThreads, 1)
+template <int TYPE, int KV, int D, int NT>
+__global__ void __launch_bounds__(kRowThreads, row_ctas_per_sm<KV, D, NT>())
 kvx_attend_rows_kernel(const Attend a, const Work w)
 {
-    typedef RowLayout<KV, D> L;
+    typedef RowLayout<KV, D, NT> L;
     typedef Elem<TYPE> E;
     constexpr bool kEight = L::kEight;
     constexpr int kMath = kEight ? KVX_TYPE_HALF : TYPE;  // of the matrix products
-    constexpr int kSteps = D / 16, kCols = D / 8;
+    constexpr int kSteps = D / 16, kRowsMax = 8 * NT;
+    constexpr int kSlot = row_slot_floats<D, NT>();
     char *smem = attend_smem;
-    float *ml = reinterpret_cast<float *>(smem + kRowWarps * kRowRing);  // [warp][row][m, l]
+    float *ml = reinterpret_cast<float *>(smem + kRowWarps * L::kRing);  // [warp][row][m, l]
     __shared__ int flag;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quad = lane >> 2, c = lane & 3;
-    const unsigned ring = smem_u32(smem) + warp * kRowRing;
+    const unsigned ring = smem_u32(smem) + warp * L::kRing;
     const int64_t line0 = int64_t(blockIdx.x) * w.tiles / w.ctas;
     const int64_t line1 = (int64_t(blockIdx.x) + 1) * w.tiles / w.ctas;
     const Score score(a);
+    const bool plain = !(a.softcap > 0.0f) && !a.slopes;
 
     AttnStart at = w.starts[blockIdx.x];
     int64_t line = line0;
@@ -157,71 +189,6 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
         const int64_t unit = line - at.tile;                   // the unit's first tile
         const int todo = int(min(int64_t(keys.tiles - at.tile), line1 - line));
 
-        // q as matrix operands, zero in rows that are left over.
-        unsigned qa[kSteps][4];
-        float row_factor[2] = {1.0f, 1.0f}, slope[2] = {0.0f, 0.0f};
-        int pos[2];
-        {
-            const char *qp[2];
-            bool have[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int row = quad + 8 * x, tok = row / a.group, h = row - tok * a.group;
-                have[x] = row < rows;
-                pos[x] = keys.pmin + (have[x] ? tok : 0);
-                const int head = at.head * a.group + (have[x] ? h : 0);
-                qp[x] = a.q + int64_t(r.row_begin + (have[x] ? tok : 0)) * a.q_stride + head * D * 2;
-                if (a.slopes)
-                    slope[x] = a.slopes[head] * kLog2e;
-            }
-            if (!kEight) {
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        qa[s][i] = have[i & 1] ? *reinterpret_cast<const unsigned *>(
-                                                     qp[i & 1] + 2 * (16 * s + 8 * (i >> 1) + 2 * c))
-                                               : 0u;
-            } else {
-                // Step s, quad thread c: elements 64 (s / 4) + 16 c + 4 (s % 4) .. + 3, as the
-                // bytes of chunk 4 (s / 4) + c of a key.
-                float f[kSteps][2][4], top[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint2 u = make_uint2(0, 0);
-                        if (have[x])
-                            u = *reinterpret_cast<const uint2 *>(
-                                qp[x] + 2 * (64 * (s >> 2) + 16 * c + 4 * (s & 3)));
-                        const typename E::T *e = reinterpret_cast<const typename E::T *>(&u);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f[s][x][i] = E::load(e[i]);
-                            top[x] = fmaxf(top[x], fabsf(f[s][x][i]));
-                        }
-                    }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-                    float down;
-                    unit_scale(top[x], &down, &row_factor[x]);
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        qa[s][x] = Elem<kMath>::pack(f[s][x][0] * down, f[s][x][1] * down);
-                        qa[s][2 + x] = Elem<kMath>::pack(f[s][x][2] * down, f[s][x][3] * down);
-                    }
-                }
-            }
-        }
-
-        float o[kCols][4];
-#pragma unroll
-        for (int n = 0; n < kCols; ++n)
-            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
         // The warp's keys in step i of the unit's share.
         auto first_key = [&](int i) {
             const int t = at.tile + i;
@@ -231,18 +198,19 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
         // Page of key `lane` of step i, or -1; loaded one step before it is used.
         auto page_of = [&](int i) {
             const int j = first_key(i) + (lane & (kRowKeys - 1));
-            return i < todo && keys.used(j) ? __ldg(r.table + j / a.page_size) : -1;
+            return i < todo && keys.used(j) ? __ldg(r.table + a.page.div(j)) : -1;
         };
         auto issue = [&](int i, int page) {
-            const int j = first_key(i) + (lane & (kRowKeys - 1));
-            int64_t off = -1;
-            if (i < todo && keys.used(j)) {
-                if (unsigned(page) < unsigned(a.num_pages))
-                    off = (int64_t(page) * a.page_size + j % a.page_size) * a.token_bytes + head_at;
-                else
-                    atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
-            }
             if (i < todo) {
+                const int j = first_key(i) + (lane & (kRowKeys - 1));
+                int64_t off = -1;
+                if (keys.used(j)) {
+                    if (unsigned(page) < unsigned(a.num_pages))
+                        off = (int64_t(page) * a.page_size + j - a.page.div(j) * a.page_size) *
+                                  a.token_bytes + head_at;
+                    else
+                        atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+                }
                 const unsigned stage = ring + (i % L::kNumStages) * L::kStage;
 #pragma unroll
                 for (int x = 0; x < kRowKeys * L::kChunks / 32; ++x) {
@@ -264,6 +232,73 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
             issue(i, page);
             page = next;
         }
+
+        // q as the second operand: row quad + 8 n in column quad, zero past the unit's rows.
+        // Of the scores and O', a thread has columns 2 c and 2 c + 1.
+        unsigned qb[NT][kSteps][2];
+        float factor[NT][2], slope[NT][2];
+        int pos[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const bool have = quad + 8 * n < rows;
+            const int row = have ? quad + 8 * n : 0, tok = row / a.group;
+            const char *qp = a.q + int64_t(r.row_begin + tok) * a.q_stride +
+                             (at.head * a.group + row - tok * a.group) * (D * 2);
+            float up = 1.0f;
+            if (!kEight) {
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qb[n][s][i] = have ? *reinterpret_cast<const unsigned *>(
+                                                 qp + 2 * (16 * s + 8 * i + 2 * c)) : 0u;
+            } else {
+                // Step s, quad thread c: elements 64 (s / 4) + 16 c + 4 (s % 4) .. + 3, as the
+                // bytes of chunk 4 (s / 4) + c of a key.
+                uint2 u[kSteps];
+                float top = 0.0f, down;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    u[s] = have ? *reinterpret_cast<const uint2 *>(
+                                      qp + 2 * (64 * (s >> 2) + 16 * c + 4 * (s & 3)))
+                                : make_uint2(0, 0);
+                    const typename E::T *e = reinterpret_cast<const typename E::T *>(&u[s]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        top = fmaxf(top, fabsf(E::load(e[i])));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                unit_scale(top, &down, &up);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    const typename E::T *e = reinterpret_cast<const typename E::T *>(&u[s]);
+                    qb[n][s][0] = Elem<kMath>::pack(E::load(e[0]) * down, E::load(e[1]) * down);
+                    qb[n][s][1] = Elem<kMath>::pack(E::load(e[2]) * down, E::load(e[3]) * down);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int mine = 2 * c + e + 8 * n, t = mine < rows ? mine / a.group : 0;
+                pos[n][e] = keys.pmin + t;
+                factor[n][e] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * e) *
+                               (a.softcap > 0.0f ? score.inner : score.factor);
+                slope[n][e] = a.slopes && mine < rows
+                                  ? a.slopes[at.head * a.group + mine - t * a.group] * kLog2e
+                                  : 0.0f;
+            }
+        }
+
+        float o[NT][kSteps][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t)
+                o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.0f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+
 #pragma unroll 1
         for (int i = 0; i < todo; ++i) {
             asm volatile("cp.async.wait_group %0;" ::"n"(L::kNumStages - 2) : "memory");
@@ -276,93 +311,116 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
             const int j0 = first_key(i);
             const unsigned ks = ring + (i % L::kNumStages) * L::kStage, vs = ks + L::kSide;
 
-            // Scores: s[n][2 x + e] is row quad + 8 x, key j0 + 8 n + 2 c + e.
-            float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+            // Scores: s[n][2 x + e] is key j0 + quad + 8 x, row 8 n + 2 c + e.
+            float s[NT][4], odd[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                s[n][0] = s[n][1] = s[n][2] = s[n][3] = odd[n][0] = odd[n][1] = odd[n][2] =
+                    odd[n][3] = 0.0f;
             if (!kEight) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int t = 0; t < kSteps; t += 2) {
+                    unsigned k0[4], k1[4];
+                    ldmatrix4(k0, ks + L::k_at(lane & 15, 2 * t + (lane >> 4)));
+                    ldmatrix4(k1, ks + L::k_at(lane & 15, 2 * t + 2 + (lane >> 4)));
 #pragma unroll
-                    for (int t = 0; t < kSteps; t += 2) {
-                        unsigned b[4];
-                        ldmatrix4(b, ks + L::k_at(8 * n + (lane & 7), 2 * t + (lane >> 3)));
-                        mma16816<kMath>(s[n], qa[t], b[0], b[1]);
-                        mma16816<kMath>(s[n], qa[t + 1], b[2], b[3]);
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816<kMath>(s[n], k0, qb[n][t][0], qb[n][t][1]);
+                        mma16816<kMath>(odd[n], k1, qb[n][t + 1][0], qb[n][t + 1][1]);
                     }
+                }
             } else {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int t = 0; t < kSteps / 4; ++t) {
+                    const uint4 u0 = lds16(ks + L::k_at(quad, 4 * t + c));
+                    const uint4 u1 = lds16(ks + L::k_at(quad + 8, 4 * t + c));
+                    const unsigned x0[4] = {u0.x, u0.y, u0.z, u0.w};
+                    const unsigned x1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-                    for (int t = 0; t < kSteps / 4; ++t) {
-                        const uint4 u = lds16(ks + L::k_at(8 * n + quad, 4 * t + c));
-                        const unsigned x[4] = {u.x, u.y, u.z, u.w};
+                    for (int y = 0; y < 4; ++y) {
+                        unsigned k[4];
+                        half4_of_e4m3(x0[y], k[0], k[2]);
+                        half4_of_e4m3(x1[y], k[1], k[3]);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            mma16816<kMath>(s[n], qa[4 * t + y], half2_of_e4m3(x[y] & 0xffffu),
-                                            half2_of_e4m3(x[y] >> 16));
+                        for (int n = 0; n < NT; ++n)
+                            mma16816<kMath>(y & 1 ? odd[n] : s[n], k, qb[n][4 * t + y][0],
+                                            qb[n][4 * t + y][1]);
                     }
+                }
             }
 
             const bool all_seen = j0 + kRowKeys <= keys.prefix ||
                                   (j0 + kRowKeys - 1 <= keys.pmin &&
                                    (!a.window || j0 > keys.pmax - a.window));
-            float top[2] = {-INFINITY, -INFINITY};
+            bool lift = false;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int x = 0; x < 4; ++x) {
+                    const int e = x & 1;
+                    float z = (s[n][x] + odd[n][x]) * factor[n][e];
+                    if (!plain) {
+                        if (a.softcap > 0.0f)
+                            z = score.cap * tanh_(z);
+                        z -= slope[n][e] * fabsf(float(pos[n][e] - j0 - quad - 8 * (x >> 1)));
+                    }
+                    if (!all_seen) {
+                        const int j = j0 + quad + 8 * (x >> 1);
+                        if (!(j < keys.prefix || (j <= pos[n][e] &&
+                                                  (!a.window || pos[n][e] - j < a.window))))
+                            z = -INFINITY;
+                    }
+                    s[n][x] = z;
+                    lift |= z > m[n][e] + 8.0f;
+                }
+            // What is subtracted need not be the maximum: it may lag by up to 2^8, which
+            // neither a 32-bit sum nor a weight in either 16-bit type minds.  So lanes compare
+            // notes, and the output is rescaled, only past that.
+            if (__any_sync(0xffffffffu, lift)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float z = s[n][2 * x + e] * row_factor[x];
-                        z = a.softcap > 0.0f ? score.capped(z) : z * score.factor;
-                        const int j = j0 + 8 * n + 2 * c + e;
-                        if (a.slopes)
-                            z -= slope[x] * fabsf(float(pos[x] - j));
-                        if (!all_seen && !(j < keys.prefix ||
-                                           (j <= pos[x] && (!a.window || pos[x] - j < a.window))))
-                            z = -INFINITY;
-                        s[n][2 * x + e] = z;
-                        top[x] = fmaxf(top[x], z);
+                        float top = fmaxf(s[n][e], s[n][2 + e]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const float next = fmaxf(m[n][e], top);
+                        const float keep = next == -INFINITY ? 1.0f : exp2_(m[n][e] - next);
+                        m[n][e] = next;
+                        l[n][e] *= keep;
+#pragma unroll
+                        for (int t = 0; t < kSteps; ++t) {
+                            o[n][t][e] *= keep;
+                            o[n][t][2 + e] *= keep;
+                        }
                     }
-                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
             }
-            // The subtracted maximum may lag by up to 2^8, which neither a 32-bit sum nor a
-            // weight in either 16-bit type minds; the output is rescaled only past that.
-            if (__any_sync(0xffffffffu, top[0] > m[0] + 8.0f || top[1] > m[1] + 8.0f)) {
+            unsigned p[NT][2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float next = fmaxf(m[x], top[x]);
-                    const float keep = next == -INFINITY ? 1.0f : exp2_(m[x] - next);
-                    m[x] = next;
-                    l[x] *= keep;
+            for (int n = 0; n < NT; ++n) {
+                float z[4];
 #pragma unroll
-                    for (int n = 0; n < kCols; ++n) {
-                        o[n][2 * x] *= keep;
-                        o[n][2 * x + 1] *= keep;
-                    }
+                for (int x = 0; x < 4; ++x) {
+                    const int e = x & 1;
+                    z[x] = exp2_(s[n][x] - (m[n][e] == -INFINITY ? 0.0f : m[n][e]));
+                    l[n][e] += z[x];
                 }
-            }
-            unsigned p[4];  // the weights as the first operand: keys are its columns
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float base = m[x] == -INFINITY ? 0.0f : m[x];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float p0 = exp2_(s[n][2 * x] - base), p1 = exp2_(s[n][2 * x + 1] - base);
-                    l[x] += p0 + p1;
-                    p[2 * n + x] = Elem<kMath>::pack(p0, p1);
-                }
+                p[n][0] = transpose8x8(Elem<kMath>::pack(z[0], z[1]));
+                p[n][1] = transpose8x8(Elem<kMath>::pack(z[2], z[3]));
             }
             if (!kEight) {
 #pragma unroll
-                for (int n = 0; n < kCols; n += 2) {
-                    unsigned b[4];
-                    ldmatrix4_trans(b, vs + L::v_at(lane & 15, n + (lane >> 4)));
-                    mma16816<kMath>(o[n], p, b[0], b[1]);
-                    mma16816<kMath>(o[n + 1], p, b[2], b[3]);
+                for (int t = 0; t < kSteps; ++t) {
+                    unsigned v[4];
+                    ldmatrix4_trans(v, vs + L::v_at((lane & 7) + 8 * (lane >> 4),
+                                                    2 * t + (lane >> 3 & 1)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16816<kMath>(o[n][t], v, p[n][0], p[n][1]);
                 }
             } else {
-                // Keys 2c, 2c + 1, 2c + 8, 2c + 9, columns quad * D / 8 and on.
+                // Keys 2c, 2c + 1, 2c + 8, 2c + 9, elements quad * D / 8 and on.
                 unsigned v[4][D / 32];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
@@ -380,13 +438,12 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const unsigned sel = half ? 0x7362 : 0x5140;  // x0 y0 x1 y1
-                        const unsigned lo = __byte_perm(v[0][g], v[1][g], sel);
-                        const unsigned hi = __byte_perm(v[2][g], v[3][g], sel);
-                        const int n = 4 * g + 2 * half;
-                        mma16816<kMath>(o[n], p, half2_of_e4m3(lo & 0xffffu),
-                                        half2_of_e4m3(hi & 0xffffu));
-                        mma16816<kMath>(o[n + 1], p, half2_of_e4m3(lo >> 16),
-                                        half2_of_e4m3(hi >> 16));
+                        unsigned k[4];
+                        half4_of_e4m3(__byte_perm(v[0][g], v[1][g], sel), k[0], k[1]);
+                        half4_of_e4m3(__byte_perm(v[2][g], v[3][g], sel), k[2], k[3]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816<kMath>(o[n][2 * g + half], k, p[n][0], p[n][1]);
                     }
             }
         }
@@ -394,32 +451,34 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
 
         // Join the warps' results in the rings' memory: [warp][row][D + 8].
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-            if (c == 0) {
-                float *p = ml + (warp * kRowMax + quad + 8 * x) * 2;
-                p[0] = m[x];
-                p[1] = l[x];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+                if (quad == 0)
+                    *reinterpret_cast<float2 *>(ml + (warp * kRowsMax + 8 * n + 2 * c + e) * 2) =
+                        make_float2(m[n][e], l[n][e]);
             }
-        }
         __syncthreads();
         float *join = reinterpret_cast<float *>(smem);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-            if (quad + 8 * x < rows) {
-                float *p = join + (warp * kRowMax + quad + 8 * x) * (D + 8);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < kCols; ++n) {
-                    p[L::column(n, 0, c)] = o[n][2 * x];
-                    p[L::column(n, 1, c)] = o[n][2 * x + 1];
+            for (int e = 0; e < 2; ++e)
+                if (8 * n + 2 * c + e < rows) {
+                    float *p = join + (warp * kRowsMax + 8 * n + 2 * c + e) * (D + 8);
+#pragma unroll
+                    for (int t = 0; t < kSteps; ++t) {
+                        p[L::element(t, 0, quad)] = o[n][t][e];
+                        p[L::element(t, 1, quad)] = o[n][t][2 + e];
+                    }
                 }
-            }
         __syncthreads();
 
         const int c0 = cta_of(w, unit), c1 = cta_of(w, unit + keys.tiles - 1);
-        float *slot = w.partial + (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) *
-                                      row_slot_floats<D>();
+        float *slot = w.partial + (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) * kSlot;
         auto write = [&](int row, int d, float4 v, float mm, float ll) {
             const int tok = row / a.group, head = at.head * a.group + row - tok * a.group;
             const int64_t orow = r.row_begin + tok;
@@ -434,14 +493,14 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
             float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
             for (int k = 0; k < kRowWarps; ++k)
-                mm = fmaxf(mm, ml[(k * kRowMax + row) * 2]);
+                mm = fmaxf(mm, ml[(k * kRowsMax + row) * 2]);
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < kRowWarps; ++k) {
-                const float *p = ml + (k * kRowMax + row) * 2;
+                const float *p = ml + (k * kRowsMax + row) * 2;
                 const float f = p[0] == -INFINITY ? 0.0f : exp2_(p[0] - mm);
                 const float4 u = *reinterpret_cast<const float4 *>(
-                    join + (k * kRowMax + row) * (D + 8) + d);
+                    join + (k * kRowsMax + row) * (D + 8) + d);
                 ll += f * p[1];
                 v.x += f * u.x;
                 v.y += f * u.y;
@@ -452,10 +511,9 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
                 write(row, d, v, mm, ll);
             } else {
                 *reinterpret_cast<float4 *>(slot + row * D + d) = v;
-                if (d == 0) {
-                    slot[kRowMax * D + 2 * row] = mm;
-                    slot[kRowMax * D + 2 * row + 1] = ll;
-                }
+                if (d == 0)
+                    *reinterpret_cast<float2 *>(slot + kRowsMax * D + 2 * row) =
+                        make_float2(mm, ll);
             }
         }
         if (c0 != c1) {
@@ -473,19 +531,19 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
             if (flag) {
                 const int parts = c1 - c0 + 1;
                 auto part = [&](int k) {
-                    return w.partial + (2 * int64_t(c0 + k) + (k == 0)) * row_slot_floats<D>();
+                    return w.partial + (2 * int64_t(c0 + k) + (k == 0)) * kSlot;
                 };
                 for (int i = threadIdx.x; i < rows * (D / 4); i += kRowThreads) {
                     const int row = i / (D / 4), d = i % (D / 4) * 4;
                     float mm = -INFINITY, ll = 0.0f;
 #pragma unroll 8
                     for (int k = 0; k < parts; ++k)
-                        mm = fmaxf(mm, __ldcg(part(k) + kRowMax * D + 2 * row));
+                        mm = fmaxf(mm, __ldcg(part(k) + kRowsMax * D + 2 * row));
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
                     for (int k = 0; k < parts; ++k) {
                         const float2 p = __ldcg(reinterpret_cast<const float2 *>(
-                            part(k) + kRowMax * D + 2 * row));
+                            part(k) + kRowsMax * D + 2 * row));
                         const float4 u = __ldcg(reinterpret_cast<const float4 *>(
                             part(k) + row * D + d));
                         const float f = p.x == -INFINITY ? 0.0f : exp2_(p.x - mm);

@@ -463,10 +463,10 @@ kvx_attend_tiles_kernel(const Attend a, const Work w)
                     const int j = j0 + t;
                     int64_t o = -1;
                     if (u.keys.used(j)) {
-                        const int page = __ldg(u.r.table + j / a.page_size);
+                        const int nth = a.page.div(j), page = __ldg(u.r.table + nth);
                         if (unsigned(page) < unsigned(a.num_pages))
-                            o = (int64_t(page) * a.page_size + j % a.page_size) * a.token_bytes +
-                                head_at;
+                            o = (int64_t(page) * a.page_size + j - nth * a.page_size) *
+                                    a.token_bytes + head_at;
                         else
                             atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
                     }
@@ -515,10 +515,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w)
                                     const unsigned y[4] = {in[b].x, in[b].y, in[b].z, in[b].w};
                                     unsigned h[8];
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        h[2 * k] = half2_of_e4m3(y[k] & 0xffffu);
-                                        h[2 * k + 1] = half2_of_e4m3(y[k] >> 16);
-                                    }
+                                    for (int k = 0; k < 4; ++k)
+                                        half4_of_e4m3(y[k], h[2 * k], h[2 * k + 1]);
                                     *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c)) =
                                         make_uint4(h[0], h[1], h[2], h[3]);
                                     *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c + 1)) =
