@@ -37,6 +37,8 @@ struct kvx_attn_plan {
     // Descriptors: [AttnStart of each kind][AttnReq of all, of each kind]; a pinned image, and
     // the device's copy.
     char *host = nullptr, *dev = nullptr;
+    CUtensorMap *maps = nullptr;       // host: as pools, where the cache is copied by tensor copies
+    int32_t box = 0;                   // keys per copy, 0: it is not
     unsigned int *counters = nullptr;  // [2 * most_ctas()], zero between launches
     float *partial = nullptr;          // serves one kind's launch after the other
     cudaEvent_t copied = nullptr;      // the last update's copy
@@ -150,7 +152,7 @@ Kernel kernel_of(int kind)
                 kRowThreads, row_ctas_per_sm<KV, D, 2>(), row_smem<KV, D, 2>(),
                 row_slot_floats<D, 2>()};
     return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KV, D>), kTileThreads, 1,
-            size_t(TileShape<D>::kBytes), TileShape<D>::kSlotFloats};
+            size_t(TileShape<KV, D>::kBytes), TileShape<KV, D>::kSlotFloats};
 }
 
 Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
@@ -239,6 +241,51 @@ kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const
     return e == cudaSuccess ? KVX_OK : kvx::cuda_err(ctx, e, "plan copy");
 }
 
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Describe each layer's K and V as a matrix [slots][heads x head_dim] for tensor copies of
+// runs of keys: the largest power of two that divides the page size, up to a tile, so that a
+// run never crosses pages.  Runs below eight keys, an e4m3 cache (converted on the way) and
+// slots past the copies' 32-bit coordinates stay with plain copies (box 0).
+kvx_status make_maps(kvx_attn_plan *p)
+{
+    int box = 1;
+    while (box < kTileKeys && p->page_size % (2 * box) == 0)
+        box *= 2;
+    const int64_t slots = int64_t(p->num_pages) * p->page_size;
+    if (p->cfg.kv_type == KVX_TYPE_FP_EIGHT || box < 8 || slots > INT32_MAX)
+        return KVX_OK;
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                     cudaEnableDefault, &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn)
+        return kvx::set_err(p->ctx, KVX_ERR_CUDA, "cuTensorMapEncodeTiled not found");
+    p->maps = new (std::nothrow) CUtensorMap[2 * size_t(p->num_layers)];
+    if (!p->maps)
+        return kvx::set_err(p->ctx, KVX_ERR_CAPACITY, "out of host memory");
+    for (int i = 0; i < 2 * p->num_layers; ++i) {
+        const cuuint64_t dims[2] = {cuuint64_t(p->cfg.kv_heads) * p->cfg.head_dim,
+                                    cuuint64_t(slots)};
+        const cuuint64_t stride[1] = {cuuint64_t(p->token_bytes)};
+        const cuuint32_t shape[2] = {64, cuuint32_t(box)}, step[2] = {1, 1};
+        const CUresult r = reinterpret_cast<EncodeTiled>(fn)(
+            p->maps + i,
+            p->cfg.kv_type == KVX_TYPE_HALF ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            2, p->pools[i], dims, stride, shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS)
+            return kvx::set_err(p->ctx, KVX_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", int(r));
+    }
+    p->box = box;
+    return KVX_OK;
+}
+
 kvx_status io_check(const kvx_attn_plan *p, int layer, const void *x, int64_t *stride,
                     int64_t heads, const char *what)
 {
@@ -303,6 +350,10 @@ kvx_status kvx_attn_plan_create(kvx_ctx *ctx, const kvx_pool *pool, const kvx_re
         return kvx::set_err(ctx, KVX_ERR_CAPACITY, "out of host memory");
     }
     kvx::pack_slabs(pool, p->pools);
+    if ((st = make_maps(p)) != KVX_OK) {
+        kvx_attn_plan_destroy(p);
+        return st;
+    }
     size_t partial = 0;
     cudaError_t e = cudaSuccess;
     for (int k = 0; k < kKinds && e == cudaSuccess; ++k) {
@@ -379,6 +430,7 @@ void kvx_attn_plan_destroy(kvx_attn_plan *p)
         if (p->host)
             cudaFreeHost(p->host);
     }
+    delete[] p->maps;
     delete[] p->pools;
     delete p;
 }
@@ -449,7 +501,7 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
                       out_stride, p->pools[2 * layer], p->pools[2 * layer + 1], p->token_bytes,
                       p->cfg.slopes, p->ctx->status_dev, p->cfg.q_heads, p->cfg.kv_heads,
                       p->cfg.q_heads / p->cfg.kv_heads, p->cfg.window, p->page_size, p->num_pages,
-                      Divisor::of(p->page_size), p->cfg.scale * k_scale, p->cfg.softcap, v_scale};
+                      Divisor::of(p->page_size), p->box, p->cfg.scale * k_scale, p->cfg.softcap, v_scale};
     for (int k = 0; k < kKinds; ++k) {
         const Schedule &s = p->kind[k];
         if (s.ctas == 0)
@@ -458,7 +510,11 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
         const Work w = {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(k)),
                         reinterpret_cast<const kvx::AttnStart *>(p->dev + p->starts_at(k)),
                         p->counters, p->partial, s.tiles, s.ctas};
-        void *args[] = {const_cast<Attend *>(&a), const_cast<Work *>(&w)};
+        CUtensorMap none = {};
+        CUtensorMap *maps[2] = {p->box ? p->maps + 2 * layer : &none,
+                                p->box ? p->maps + 2 * layer + 1 : &none};
+        // The kernels of few rows take the first two.
+        void *args[] = {const_cast<Attend *>(&a), const_cast<Work *>(&w), maps[0], maps[1]};
         const cudaError_t e = cudaLaunchKernel(kn.fn, dim3(unsigned(s.ctas)),
                                                dim3(unsigned(kn.threads)), args, kn.smem,
                                                reinterpret_cast<cudaStream_t>(stream));

@@ -2,6 +2,7 @@
 // visibility of keys, and the scores' arithmetic.  Included by kvx_attend.cu only.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -50,6 +51,7 @@ struct Attend {
     int32_t q_heads, kv_heads, group, window;
     int32_t page_size, num_pages;
     Divisor page;
+    int32_t box;                   // keys per tensor copy, 0: the cache is not copied that way
     float scale;                   // of q . k, with k_scale
     float softcap, v_scale;
 };
@@ -94,6 +96,13 @@ struct Keys {
     __device__ __forceinline__ bool used(int j) const
     {
         return j < prefix || (j >= low && j < end);
+    }
+    // Keys j .. j + T - 1 are all used.
+    template <int T>
+    __device__ __forceinline__ bool whole(int j) const
+    {
+        return j + T <= prefix || (j >= low && j + T <= end) ||
+               (low <= prefix && j + T <= max(prefix, end));
     }
 };
 

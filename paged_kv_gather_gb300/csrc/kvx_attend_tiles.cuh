@@ -14,7 +14,11 @@ namespace {
 // shared memory.  Two warpgroups turn the scores of one tile each into weights, a thread per
 // row, while the tensor cores work on the other tile: S0 -> P0 beside P1 V, S1 and so on.
 // One warp issues the products; three warps bring K and V from the pages into a ring of
-// shared-memory slots (K0, V0, K1, V1, ...).
+// shared-memory slots (K0, V0, K1, V1, ...).  Where a tile of keys is whole and a page holds
+// eight keys or a power of two more, one of them fetches it with tensor copies, a run of keys
+// inside a page each: with 16-byte copies by the threads of all three, the only way for other
+// pages and ragged ends, the ring was what the kernel waited for.  An e4m3 cache is copied as
+// it is into a stage of its own and from there converted to half precision in the ring.
 //
 // Shared-memory tiles are [D / 64][128 rows][64 elements] with the 16-byte chunks of a
 // 128-byte line permuted by the row's low three bits, the layout the matrix instructions
@@ -25,14 +29,17 @@ const int kTileRows = 128;
 const int kTileKeys = 128;
 const int kBlockRows = 2 * kTileRows;
 const int kLoaders = 96;
-const int kLoaderLag = 2;          // slots a loader fills before it announces the first
+const int kLoaderWarps = kLoaders / 32;
+const int kLoaderLag = 2;          // slots filled by 16-byte copies before the first is announced
 
-template <int D>
+template <int KV, int D>
 struct TileShape {
+    static const bool kEight = KV == KVX_TYPE_FP_EIGHT;
     static const int kTile = kTileRows * D * 2;              // bytes of a q, K or V tile
-    static const int kSlots = D == 128 ? 5 : 10;
+    static const int kSlots = (D == 128 ? 5 : 10) - kEight;
     static const int kOffRing = 2 * kTile;
-    static const int kOffKeys = kOffRing + kSlots * kTile;   // int64 [2][kTileKeys]
+    static const int kOffStage = kOffRing + kSlots * kTile;  // e4m3: [2][kTile / 2]
+    static const int kOffKeys = kOffStage + kEight * kTile;  // int64 [2][kTileKeys]
     static const int kOffBars = kOffKeys + 2 * kTileKeys * 8;
     static const int kOffMisc = kOffBars + 256;              // int[4]
     static const int kBytes = kOffMisc + 16;
@@ -254,6 +261,21 @@ __device__ __forceinline__ int tile_at(int r, int c)
     return (c >> 3) * (kTileRows * 128) + r * 128 + (((c ^ r) & 7) << 4);
 }
 
+// A box of a matrix in global memory into shared memory; completes on a barrier.
+__device__ __forceinline__ void tensor_copy(unsigned dst, const CUtensorMap *map, int x, int y,
+                                            unsigned bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
 // Walks a CTA's share of the line; every role of the CTA steps through the same units.
 struct Walk {
     const Attend &a;
@@ -306,9 +328,10 @@ struct Walk {
 
 template <int TYPE, int KV, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
-kvx_attend_tiles_kernel(const Attend a, const Work w)
+kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CUtensorMap k_map,
+                        const __grid_constant__ CUtensorMap v_map)
 {
-    typedef TileShape<D> T;
+    typedef TileShape<KV, D> T;
     typedef Elem<TYPE> E;
     constexpr bool kEight = KV == KVX_TYPE_FP_EIGHT;
     constexpr int kMath = kEight ? KVX_TYPE_HALF : TYPE;
@@ -341,7 +364,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w)
         mbar_init(bar(kBarKeys), kLoaders);
         mbar_init(bar(kBarEnd), 1);
         for (int i = 0; i < T::kSlots; ++i) {
-            mbar_init(bar(kBarFull + i), kLoaders);
+            mbar_init(bar(kBarFull + i), kLoaderWarps);
             mbar_init(bar(kBarEmpty + i), 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -445,20 +468,108 @@ kvx_attend_tiles_kernel(const Attend a, const Work w)
         const int lt = threadIdx.x - (kTileThreads - kLoaders);
         int64_t *offs = reinterpret_cast<int64_t *>(smem + T::kOffKeys);  // [2][kTileKeys]
         constexpr int kRow = D * (kEight ? 1 : 2), kChunks = kRow / 16;
-        unsigned slot = 0, turn = 0, filled = 0;  // filled: slots issued so far
+        constexpr int kCopies = (kTileKeys * kChunks + kLoaders - 1) / kLoaders;  // per thread
+        constexpr unsigned kPerTile = D / 64;  // tensor copies side by side
+        unsigned slot = 0, turn = 0;
+        unsigned filled = 0, announced = 0;    // slots of the stream so far
         bool ok = true;
-        auto announce = [&](unsigned n) {  // slot number n of the stream is complete
+        // This warp's part of slot number `announced` is in place.
+        auto announce = [&]() {
             fence_async_shared();
-            mbar_arrive(bar(kBarFull + n % T::kSlots));
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(kBarFull + announced % T::kSlots));
+            ++announced;
         };
-        unsigned parity = 0;
+        auto advance = [&]() {
+            ++filled;
+            if (++slot == T::kSlots) {
+                slot = 0;
+                turn ^= 1;
+            }
+        };
+        // Copy this thread's chunks of 16 bytes of a tile, where each key lies at off[key].
+        auto copy = [&](const char *base, const int64_t *off, unsigned dst) {
+#pragma unroll 4
+            for (int b = 0; b < kCopies; ++b) {
+                const int x = lt + b * kLoaders, t = x / kChunks, c = x % kChunks;
+                if (x < kTileKeys * kChunks) {
+                    const int64_t o = off[t];
+                    cp_async16(dst + (kEight ? x * 16 : tile_at(t, c)),
+                               base + (o >= 0 ? o : 0) + c * 16, o >= 0);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        unsigned key_phase = 0;
+        // e4m3: tile sides (K, V, K, V, ...) are copied one ahead of their conversion.
+        bool staged = false;
+        auto convert = [&]() {  // the staged side, number `filled` of the stream
+            const char *src = smem + T::kOffStage + (filled & 1) * (T::kTile / 2);
+            char *dst = smem + T::kOffRing + slot * T::kTile;
+#pragma unroll
+            for (int b = 0; b < kCopies; ++b) {
+                const int x = lt + b * kLoaders, t = x / kChunks, c = x % kChunks;
+                if (x < kTileKeys * kChunks) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(src + x * 16);
+                    uint4 h0, h1;
+                    half4_of_e4m3(u.x, h0.x, h0.y);
+                    half4_of_e4m3(u.y, h0.z, h0.w);
+                    half4_of_e4m3(u.z, h1.x, h1.y);
+                    half4_of_e4m3(u.w, h1.z, h1.w);
+                    *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c)) = h0;
+                    *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c + 1)) = h1;
+                }
+            }
+            announce();
+            advance();
+        };
         for (Walk u(a, w); ok && !u.done(); u.next()) {
             const int64_t head_at = int64_t(u.at.head) * kRow;
+            // A lane per tensor copy of a tile: run of keys `lane / kPerTile` and 64-element
+            // block of the head `lane % kPerTile`; its page is looked up a tile ahead.
+            const int run = a.box ? int(unsigned(lane) / kPerTile) * a.box : kTileKeys;
+            auto page_of = [&](int i) {
+                const int j = i < u.todo ? u.key_of(i) + run : 0;
+                return i < u.todo && run < kTileKeys && u.keys.used(j)
+                           ? __ldg(u.r.table + a.page.div(j)) : -1;
+            };
+            int next = kEight ? -1 : page_of(0);
             for (int i = 0; ok && i < u.todo; ++i) {
-                // Where each key of the tile lies; -1: not used.
-                int64_t *off = offs + parity * kTileKeys;
-                parity ^= 1;
                 const int j0 = u.key_of(i);
+                if (!kEight) {
+                    const int page = next;
+                    next = page_of(i + 1);
+                    if (a.box && u.keys.whole<kTileKeys>(j0) &&
+                        __all_sync(0xffffffffu, run >= kTileKeys ||
+                                                    unsigned(page) < unsigned(a.num_pages))) {
+                        const int j = j0 + run;
+                        const int y = page * a.page_size + j - a.page.div(j) * a.page_size;
+                        for (int side = 0; side < 2; ++side) {
+                            if (!(ok = wait(kBarEmpty + slot, turn ^ 1)))
+                                break;
+                            if (lane == 0) {
+                                if (warp == 9)
+                                    mbar_expect(bar(kBarFull + slot), T::kTile);
+                                else
+                                    mbar_arrive(bar(kBarFull + slot));
+                            }
+                            __syncwarp();
+                            if (warp == 9 && run < kTileKeys) {
+                                const int block = int(unsigned(lane) % kPerTile);
+                                tensor_copy(sm + T::kOffRing + slot * T::kTile +
+                                                block * (kTileRows * 128) + run * 128,
+                                            side ? &v_map : &k_map, u.at.head * D + block * 64, y,
+                                            bar(kBarFull + slot));
+                            }
+                            ++announced;
+                            advance();
+                        }
+                        continue;
+                    }
+                }
+                // Where each key of the tile lies; -1: not used.
+                int64_t *off = offs + key_phase * kTileKeys;
                 for (int t = lt; t < kTileKeys; t += kLoaders) {
                     const int j = j0 + t;
                     int64_t o = -1;
@@ -473,71 +584,49 @@ kvx_attend_tiles_kernel(const Attend a, const Work w)
                     off[t] = o;
                 }
                 mbar_arrive(bar(kBarKeys));
-                ok = wait(kBarKeys, parity ^ 1);
+                ok = wait(kBarKeys, key_phase);
+                key_phase ^= 1;
                 for (int side = 0; ok && side < 2; ++side) {
+                    const char *base = side ? a.v : a.k;
+                    if (kEight) {
+                        // The stage that this side takes was converted two sides ago.
+                        copy(base, off, sm + T::kOffStage +
+                                            ((filled + staged) & 1) * (T::kTile / 2));
+                        if (staged) {
+                            asm volatile("cp.async.wait_group 1;" ::: "memory");
+                            if ((ok = wait(kBarEmpty + slot, turn ^ 1)))
+                                convert();
+                        }
+                        staged = true;
+                        continue;
+                    }
                     if (!(ok = wait(kBarEmpty + slot, turn ^ 1)))
                         break;
-                    const char *base = side ? a.v : a.k;
-                    char *dst = smem + T::kOffRing + slot * T::kTile;
-                    if (!kEight) {
-                        const unsigned d = smem_u32(dst);
-#pragma unroll 4
-                        for (int x = lt; x < kTileKeys * kChunks; x += kLoaders) {
-                            const int t = x / kChunks, c = x % kChunks;
-                            const int64_t o = off[t];
-                            cp_async16(d + tile_at(t, c), base + (o >= 0 ? o : 0) + c * 16, o >= 0);
-                        }
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                        if (filled >= kLoaderLag) {
-                            asm volatile("cp.async.wait_group %0;" ::"n"(kLoaderLag) : "memory");
-                            announce(filled - kLoaderLag);
-                        }
-                    } else {
-                        constexpr int kBatch = 6;
-                        for (int x0 = lt; x0 < kTileKeys * kChunks; x0 += kBatch * kLoaders) {
-                            uint4 in[kBatch];
-#pragma unroll
-                            for (int b = 0; b < kBatch; ++b) {
-                                const int x = x0 + b * kLoaders;
-                                in[b] = make_uint4(0, 0, 0, 0);
-                                if (x < kTileKeys * kChunks) {
-                                    const int64_t o = off[x / kChunks];
-                                    if (o >= 0)
-                                        in[b] = __ldg(reinterpret_cast<const uint4 *>(
-                                            base + o + x % kChunks * 16));
-                                }
-                            }
-#pragma unroll
-                            for (int b = 0; b < kBatch; ++b) {
-                                const int x = x0 + b * kLoaders;
-                                if (x < kTileKeys * kChunks) {
-                                    const int t = x / kChunks, c = x % kChunks;
-                                    const unsigned y[4] = {in[b].x, in[b].y, in[b].z, in[b].w};
-                                    unsigned h[8];
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        half4_of_e4m3(y[k], h[2 * k], h[2 * k + 1]);
-                                    *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c)) =
-                                        make_uint4(h[0], h[1], h[2], h[3]);
-                                    *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c + 1)) =
-                                        make_uint4(h[4], h[5], h[6], h[7]);
-                                }
-                            }
-                        }
-                        announce(filled);
-                    }
-                    ++filled;
-                    if (++slot == T::kSlots) {
-                        slot = 0;
-                        turn ^= 1;
+                    copy(base, off, sm + T::kOffRing + slot * T::kTile);
+                    advance();
+                    if (a.box) {  // alone between tiles that come by tensor copies
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        announce();
+                    } else if (filled - announced > kLoaderLag) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(kLoaderLag) : "memory");
+                        announce();
                     }
                 }
             }
         }
-        if (!kEight) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            for (unsigned n = filled > kLoaderLag ? filled - kLoaderLag : 0; ok && n < filled; ++n)
-                announce(n);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (ok && staged && (ok = wait(kBarEmpty + slot, turn ^ 1)))
+            convert();
+        while (ok && announced < filled)
+            announce();
+        if (!ok && warp == 9) {
+            // Tensor copies may still be under way: see the slots filled last complete.
+            const uint64_t t0 = now_ns();
+            for (unsigned n = filled > T::kSlots ? filled - T::kSlots : 0; n < filled; ++n)
+                while (!__all_sync(0xffffffffu,
+                                   mbar_try(bar(kBarFull + n % T::kSlots), n / T::kSlots & 1)) &&
+                       !__any_sync(0xffffffffu, now_ns() - t0 > 1000000000ull)) {
+                }
         }
     } else {
         // ------------------------------------------------------------- weights
