@@ -115,6 +115,36 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned phase, volatile
     return true;
 }
 
+// The same for a thread on its own.
+__device__ __forceinline__ bool mbar_wait_one(unsigned bar, unsigned phase, volatile int *gave_up,
+                                              unsigned *status)
+{
+    if (mbar_try(bar, phase))
+        return true;
+    const uint64_t t0 = now_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try(bar, phase))
+                return true;
+        if (*gave_up)
+            return false;
+        if (now_ns() - t0 > 1000000000ull) {
+            *gave_up = 1;
+            atomicOr(status, KVX_DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    unsigned one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(one)::"memory");
+    return one;
+}
+
 __device__ __forceinline__ void fence_async_shared()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -204,6 +234,13 @@ __device__ __forceinline__ void tc_wait_ld(float (&r)[32])
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         asm volatile("" : "+f"(r[i]));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Two 32-bit numbers at a time.
@@ -342,7 +379,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
     unsigned &tmem_base = reinterpret_cast<unsigned &>(misc[1]);
     int *last_cta = misc + 2;
     const unsigned sm = smem_u32(smem);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     auto bar = [&](int i) { return sm + T::kOffBars + 8 * i; };
     auto wait = [&](int i, unsigned phase) { return mbar_wait(bar(i), phase, &gave_up, a.status); };
 
@@ -376,93 +413,93 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
 
     if (warp == 8) {
         // ------------------------------------------------------------- matrix products
-        constexpr unsigned kDescS = mma_idesc(kMath, kTileKeys, false);
-        constexpr unsigned kDescO = mma_idesc(kMath, D, true);
-        unsigned slot = 0, turn = 0;  // ring position and its phase
-        unsigned q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-        bool ok = true;
-        auto scores = [&](int x, unsigned s) {
-            const uint64_t q = tile_desc(sm + x * T::kTile, 16);
-            const uint64_t k = tile_desc(sm + T::kOffRing + s * T::kTile, 16);
+        // One thread does it all: the queue of products is a few deep, so every instruction
+        // between the last of one batch and the first of the next shows once the weights of
+        // the other tile are there in time.
+        if (elect_one()) {
+            constexpr unsigned kDescS = mma_idesc(kMath, kTileKeys, false);
+            constexpr unsigned kDescO = mma_idesc(kMath, D, true);
+            const uint64_t q_desc = tile_desc(sm, 16);
+            const uint64_t k_desc = tile_desc(sm + T::kOffRing, 16);
+            const uint64_t v_desc = tile_desc(sm + T::kOffRing, kTileRows * 128);
+            unsigned slot = 0, turn = 0;  // ring position and its phase
+            unsigned q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            bool ok = true;
+            auto wait1 = [&](int i, unsigned phase) {
+                return mbar_wait_one(bar(i), phase, &gave_up, a.status);
+            };
+            auto scores = [&](int x, unsigned s) {
+                const uint64_t q = q_desc + x * (T::kTile >> 4), k = k_desc + s * (T::kTile >> 4);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint64_t step = ((i >> 2) * (kTileRows * 128) + (i & 3) * 32) >> 4;
-                tc_mma_ss(tmem + x * kTileKeys, q + step, k + step, kDescS, i > 0);
-            }
-            tc_commit(bar(kBarS + x));
-        };
-        auto advance = [&]() {
-            if (++slot == T::kSlots) {
-                slot = 0;
-                turn ^= 1;
-            }
-        };
-        for (Walk u(a, w); ok && !u.done(); u.next()) {
-            const int tiles = u.rows > kTileRows ? 2 : 1;
-            for (int x = 0; ok && x < tiles; ++x) {
-                ok = wait(kBarQ + x, q_phase[x]);
-                q_phase[x] ^= 1;
-            }
-            if (!ok || !(ok = wait(kBarFull + slot, turn)))
-                break;
-            tc_fence_after();
-            if (lane == 0) {
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t step = ((i >> 2) * (kTileRows * 128) + (i & 3) * 32) >> 4;
+                    tc_mma_ss(tmem + x * kTileKeys, q + step, k + step, kDescS, i > 0);
+                }
+                tc_commit(bar(kBarS + x));
+            };
+            auto advance = [&]() {
+                if (++slot == T::kSlots) {
+                    slot = 0;
+                    turn ^= 1;
+                }
+            };
+            for (Walk u(a, w); ok && !u.done(); u.next()) {
+                const int tiles = u.rows > kTileRows ? 2 : 1;
+                for (int x = 0; ok && x < tiles; ++x) {
+                    ok = wait1(kBarQ + x, q_phase[x]);
+                    q_phase[x] ^= 1;
+                }
+                if (!ok || !(ok = wait1(kBarFull + slot, turn)))
+                    break;
+                tc_fence_after();
                 for (int x = 0; x < tiles; ++x)
                     scores(x, slot);
                 tc_commit(bar(kBarEmpty + slot));
-            }
-            __syncwarp();
-            advance();
-            for (int i = 0; i < u.todo; ++i) {
-                const unsigned v_slot = slot;
-                ok = wait(kBarFull + slot, turn);
-                if (!ok)
-                    break;
                 advance();
-                const bool more = i + 1 < u.todo;
-                if (more && !(ok = wait(kBarFull + slot, turn)))
-                    break;
-                for (int x = 0; x < tiles; ++x) {
-                    ok = wait(kBarP + x, p_phase[x]);
-                    if (!ok)
+                for (int i = 0; i < u.todo; ++i) {
+                    const unsigned v_slot = slot;
+                    if (!(ok = wait1(kBarFull + slot, turn)))
                         break;
-                    p_phase[x] ^= 1;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t v = tile_desc(sm + T::kOffRing + v_slot * T::kTile,
-                                                     kTileRows * 128);
+                    advance();
+                    const bool more = i + 1 < u.todo;
+                    if (more && !(ok = wait1(kBarFull + slot, turn)))
+                        break;
+                    const uint64_t v = v_desc + v_slot * (T::kTile >> 4);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (x >= tiles)
+                            break;
+                        if (!(ok = wait1(kBarP + x, p_phase[x])))
+                            break;
+                        p_phase[x] ^= 1;
+                        tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < kTileKeys / 16; ++k)
                             tc_mma_ts(tmem + 2 * kTileKeys + x * D, tmem + x * kTileKeys + 8 * k,
-                                      v + (k * 2048 >> 4), kDescO, i > 0 || k > 0);
+                                      v + (k * 2048 >> 4), kDescO, k > 0 || i > 0);
                         if (more)
                             scores(x, slot);
                         else
                             tc_commit(bar(kBarO + x));
                     }
-                    __syncwarp();
-                }
-                if (!ok)
-                    break;
-                if (lane == 0) {
+                    if (!ok)
+                        break;
                     tc_commit(bar(kBarEmpty + v_slot));
-                    if (more)
+                    if (more) {
                         tc_commit(bar(kBarEmpty + slot));
+                        advance();
+                    }
                 }
-                __syncwarp();
-                if (more)
-                    advance();
             }
-        }
-        if (!ok) {
-            // Let what was issued run out before the memory it works on goes away.
-            if (lane == 0)
+            if (!ok) {
+                // Let what was issued run out before the memory it works on goes away.
                 tc_commit(bar(kBarEnd));
-            const uint64_t t0 = now_ns();
-            while (!__all_sync(0xffffffffu, mbar_try(bar(kBarEnd), 0)) &&
-                   !__any_sync(0xffffffffu, now_ns() - t0 > 1000000000ull)) {
+                const uint64_t t0 = now_ns();
+                while (!mbar_try(bar(kBarEnd), 0) && now_ns() - t0 < 1000000000ull) {
+                }
             }
         }
+        __syncwarp();
     } else if (warp > 8) {
         // ------------------------------------------------------------- K and V
         const int lt = threadIdx.x - (kTileThreads - kLoaders);
@@ -714,8 +751,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                             if (b < 3)
                                 tc_ld32(s[(b + 1) & 1], ts + 32 * (b + 1));
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                t4[k & 3] = fmaxf(t4[k & 3], z[k]);
+                            for (int k = 0; k < 32; k += 2)
+                                t4[k >> 1 & 3] = max3(t4[k >> 1 & 3], z[k], z[k + 1]);
                         }
                         top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     } else {
