@@ -18,9 +18,13 @@
 // up to 8, up to 16, more.
 enum { kRows = 0, kMoreRows = 1, kTiles = 2, kKinds = 3 };
 
+// What joining the parts of a cut unit is worth in keys read, and what a unit costs beyond
+// its tiles (by bytes of K and V for the kernels of few rows, by tiles for the other).
+const int64_t kLeastBytes = 160 << 10, kUnitBytes = 64 << 10;
+const int kLeastTiles = 4, kUnitTiles = 2;
+
 struct Schedule {
     int n_req = 0;
-    int64_t tiles = 0;
     int ctas = 0;
 };
 
@@ -61,6 +65,7 @@ struct Step {
     int32_t rows;
     int32_t page_size;
     int32_t num_pages;
+    Divisor page;
 };
 
 // Request of a row: the last r with row_begin <= row that has rows.  Requests without new
@@ -91,42 +96,78 @@ struct Append {
     int32_t units;           // 16-byte units of a cache token
 };
 
-// A warp per (new token, K or V).
+// 16 bytes of the cache from the new token's elements.
+template <int TYPE, int KV>
+struct Unit {
+    uint4 in[KV == TYPE ? 1 : 2];
+
+    __device__ __forceinline__ void load(const char *src, int u)
+    {
+#pragma unroll
+        for (int i = 0; i < (KV == TYPE ? 1 : 2); ++i)
+            in[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + (KV == TYPE ? u : 2 * u + i));
+    }
+    __device__ __forceinline__ uint4 value(float scale) const
+    {
+        if (KV == TYPE)
+            return in[0];
+        typedef typename Elem<TYPE>::T T;
+        const T *x = reinterpret_cast<const T *>(in);
+        unsigned r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            unsigned two[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 f = make_float2(Elem<TYPE>::load(x[4 * i + 2 * k]) / scale,
+                                             Elem<TYPE>::load(x[4 * i + 2 * k + 1]) / scale);
+                two[k] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+            }
+            r[i] = two[0] | two[1] << 16;
+        }
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    }
+};
+
+// A warp per (new token, K or V), four 16-byte units of the cache in flight per lane.  The
+// copy is bound by memory; where few tokens are new, by the latency of table and data.
 template <int TYPE, int KV>
 __global__ void __launch_bounds__(256)
 kvx_append_kernel(const Append a)
 {
     const int lane = threadIdx.x & 31;
     const int64_t job = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (job >= 2 * int64_t(a.step.rows))
-        return;
     const int row = int(job >> 1), kv = int(job & 1);
+    wait_for_earlier_work();
+    if (row >= a.step.rows)
+        return;
+    const char *src = a.src[kv] + row * a.stride[kv];
+    Unit<TYPE, KV> x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (lane + 32 * i < a.units)
+            x[i].load(src, lane + 32 * i);
     const AttnReq q = a.step.reqs[request_of_row(a.step.reqs, a.step.n_req, row, lane)];
-    const int pos = q.n_tokens - q.n_new + row - q.row_begin;
-    const int page = q.table[pos / a.step.page_size];
+    const int pos = q.n_tokens - q.n_new + row - q.row_begin, nth = a.step.page.div(pos);
+    const int page = __ldg(q.table + nth);
     if (unsigned(page) >= unsigned(a.step.num_pages)) {
         if (lane == 0)
             atomicOr(a.step.status, KVX_DEV_PAGE_OUT_OF_RANGE);
         return;
     }
-    const char *src = a.src[kv] + row * a.stride[kv];
-    char *dst = a.pool[kv] +
-                (int64_t(page) * a.step.page_size + pos % a.step.page_size) * a.token_bytes;
-    for (int u = lane; u < a.units; u += 32) {
-        if (KV == TYPE) {
-            reinterpret_cast<uint4 *>(dst)[u] = reinterpret_cast<const uint4 *>(src)[u];
-        } else {
-            typedef typename Elem<TYPE>::T T;
-            alignas(16) T in[16];
-            reinterpret_cast<uint4 *>(in)[0] = reinterpret_cast<const uint4 *>(src)[2 * u];
-            reinterpret_cast<uint4 *>(in)[1] = reinterpret_cast<const uint4 *>(src)[2 * u + 1];
-            alignas(16) unsigned char out[16];
+    uint4 *dst = reinterpret_cast<uint4 *>(
+        a.pool[kv] +
+        (int64_t(page) * a.step.page_size + pos - nth * a.step.page_size) * a.token_bytes);
+#pragma unroll 1
+    for (int u0 = lane; u0 < a.units; u0 += 128) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                out[i] = __nv_cvt_float_to_fp8(Elem<TYPE>::load(in[i]) / a.scale[kv],
-                                               __NV_SATFINITE, __NV_E4M3);
-            reinterpret_cast<uint4 *>(dst)[u] = *reinterpret_cast<uint4 *>(out);
-        }
+        for (int i = 0; i < 4; ++i)
+            if (u0 + 32 * i < a.units)
+                dst[u0 + 32 * i] = x[i].value(a.scale[kv]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (u0 + 128 + 32 * i < a.units)
+                x[i].load(src, u0 + 128 + 32 * i);
     }
 }
 
@@ -166,12 +207,20 @@ Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
                 : eight ? kernel_of<B, F, 128>(kind) : kernel_of<B, B, 128>(kind);
 }
 
-// Lay the units of one kind end to end and give every CTA its share (struct Work).
+// Lay the units of one kind end to end and give every CTA its share (struct Work).  Shares
+// are equal in tiles plus `extra` per unit, for what a unit costs besides its tiles.  No share
+// is below `least` tiles on average and no unit is cut closer than that to its ends: joining
+// parts costs about as much as reading so many tiles.
 void schedule(kvx_attn_plan *p, int kind, const AttnReq *reqs, int n_req)
 {
-    const int group = p->cfg.q_heads / p->cfg.kv_heads;
+    const int group = p->cfg.q_heads / p->cfg.kv_heads, heads = p->cfg.kv_heads;
     const int T = kind == kTiles ? kTileKeys : kRowTile;
     const int block_rows = kind == kTiles ? kBlockRows : kRowMax;
+    const int64_t tile_bytes = 2 * int64_t(T) * p->cfg.head_dim * kvx::type_bytes(p->cfg.kv_type);
+    const int least = kind == kTiles ? kLeastTiles
+                                     : int(std::max<int64_t>(1, kLeastBytes / tile_bytes));
+    const int extra = kind == kTiles ? kUnitTiles
+                                     : int(std::max<int64_t>(1, kUnitBytes / tile_bytes));
     auto blocks = [&](const AttnReq &r) {
         return int((int64_t(r.n_new) * group + block_rows - 1) / block_rows);
     };
@@ -185,24 +234,60 @@ void schedule(kvx_attn_plan *p, int kind, const AttnReq *reqs, int n_req)
                        pmax + 1, T, &first, &skip, &tiles);
         return tiles;
     };
-    Schedule &s = p->kind[kind];
-    s.n_req = n_req;
-    s.tiles = 0;
-    for (int r = 0; r < n_req; ++r)
-        for (int b = 0, n = blocks(reqs[r]); b < n; ++b)
-            s.tiles += int64_t(tiles_of(reqs[r], b)) * p->cfg.kv_heads;
-    s.ctas = int(std::min<int64_t>(
-        int64_t(p->ctx->num_sms) * pick_kernel(p->cfg, kind).ctas_per_sm, s.tiles));
-    kvx::AttnStart *out = reinterpret_cast<kvx::AttnStart *>(p->host + p->starts_at(kind));
-    int64_t line = 0;
-    int c = 0;
+    int64_t tiles = 0, cost = 0;
     for (int r = 0; r < n_req; ++r)
         for (int b = 0, n = blocks(reqs[r]); b < n; ++b) {
-            const int64_t tiles = tiles_of(reqs[r], b), all = tiles * p->cfg.kv_heads;
-            for (int64_t at; c < s.ctas && (at = c * s.tiles / s.ctas) < line + all; ++c)
-                out[c] = {r, b, int32_t((at - line) / tiles), int32_t((at - line) % tiles)};
-            line += all;
+            const int t = tiles_of(reqs[r], b);
+            tiles += int64_t(t) * heads;
+            cost += int64_t(t + extra) * heads;
         }
+    Schedule &s = p->kind[kind];
+    s.n_req = n_req;
+    s.ctas = 0;
+    if (tiles == 0)
+        return;
+    const int64_t slots = int64_t(p->ctx->num_sms) * pick_kernel(p->cfg, kind).ctas_per_sm;
+    const int64_t shares = std::min(slots, std::max<int64_t>(1, tiles / least));
+    kvx::AttnStart *out = reinterpret_cast<kvx::AttnStart *>(p->host + p->starts_at(kind));
+    int64_t at = 0, line = 0;     // of the unit, in cost and in tiles
+    int64_t share = 0;            // shares begun
+    int64_t begun = 0;            // line position where the last of them begins
+    bool carry = false;           // one begins with the next unit
+    auto place = [&](int r, int b, int h, int tile, int first) {
+        if (s.ctas > 0)
+            out[s.ctas - 1].tiles = line + tile - begun;
+        begun = line + tile;
+        out[s.ctas++] = {r, b, h, tile, first, 0, 0};
+    };
+    for (int r = 0; r < n_req; ++r)
+        for (int b = 0, n = blocks(reqs[r]); b < n; ++b) {
+            const int t = tiles_of(reqs[r], b);
+            for (int h = 0; h < heads; ++h) {
+                // Shares whose boundary falls on this unit: at its start, inside, at its end.
+                auto boundary = [&] { return share * cost / shares - at - extra; };
+                int first = s.ctas - 1, cut = 0;
+                bool start = carry;
+                for (carry = false; share < shares && boundary() < least; ++share)
+                    start = true;
+                if (start) {
+                    first = s.ctas;
+                    place(r, b, h, 0, first);
+                }
+                for (; share < shares && boundary() < t; ++share) {
+                    if (t - boundary() < least) {
+                        carry = true;
+                    } else if (boundary() > cut) {
+                        cut = int(boundary());
+                        place(r, b, h, cut, first);
+                    }
+                }
+                for (int c = first; c < s.ctas - 1; ++c)
+                    out[c].last = s.ctas - 1;
+                at += t + extra;
+                line += t;
+            }
+        }
+    out[s.ctas - 1].tiles = line - begun;
 }
 
 kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const int32_t *n_new,
@@ -286,6 +371,24 @@ kvx_status make_maps(kvx_attn_plan *p)
     return KVX_OK;
 }
 
+// A launch that may start while the kernel ahead of it on the stream drains; the kernels
+// themselves wait for that one's completion before they touch memory.
+cudaError_t launch_early(const void *fn, int64_t ctas, int threads, size_t smem, cudaStream_t s,
+                         void **args)
+{
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(ctas));
+    lc.blockDim = dim3(unsigned(threads));
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelExC(&lc, fn, args);
+}
+
 kvx_status io_check(const kvx_attn_plan *p, int layer, const void *x, int64_t *stride,
                     int64_t heads, const char *what)
 {
@@ -310,7 +413,7 @@ kvx_status io_check(const kvx_attn_plan *p, int layer, const void *x, int64_t *s
 Step step_of(const kvx_attn_plan *p)
 {
     return {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(kKinds)), p->ctx->status_dev, p->n_req,
-            int32_t(p->rows), p->page_size, p->num_pages};
+            int32_t(p->rows), p->page_size, p->num_pages, Divisor::of(p->page_size)};
 }
 
 }  // namespace
@@ -470,8 +573,8 @@ kvx_status kvx_append_tokens(const kvx_attn_plan *p, int layer, const void *k, c
             : reinterpret_cast<const void *>(
                   kvx_append_kernel<KVX_TYPE_BFLOAT, KVX_TYPE_FP_EIGHT>);
     void *args[] = {&a};
-    const cudaError_t e = cudaLaunchKernel(fn, dim3(unsigned((2 * p->rows + 7) / 8)), dim3(256),
-                                           args, 0, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_early(fn, (2 * p->rows + 7) / 8, 256, 0,
+                                       reinterpret_cast<cudaStream_t>(stream), args);
     return e == cudaSuccess ? KVX_OK : kvx::cuda_err(p->ctx, e, "append launch");
 }
 
@@ -509,15 +612,14 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
         const Kernel kn = pick_kernel(p->cfg, k);
         const Work w = {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(k)),
                         reinterpret_cast<const kvx::AttnStart *>(p->dev + p->starts_at(k)),
-                        p->counters, p->partial, s.tiles, s.ctas};
+                        p->counters, p->partial};
         CUtensorMap none = {};
         CUtensorMap *maps[2] = {p->box ? p->maps + 2 * layer : &none,
                                 p->box ? p->maps + 2 * layer + 1 : &none};
         // The kernels of few rows take the first two.
         void *args[] = {const_cast<Attend *>(&a), const_cast<Work *>(&w), maps[0], maps[1]};
-        const cudaError_t e = cudaLaunchKernel(kn.fn, dim3(unsigned(s.ctas)),
-                                               dim3(unsigned(kn.threads)), args, kn.smem,
-                                               reinterpret_cast<cudaStream_t>(stream));
+        const cudaError_t e = launch_early(kn.fn, s.ctas, kn.threads, kn.smem,
+                                           reinterpret_cast<cudaStream_t>(stream), args);
         if (e != cudaSuccess)
             return kvx::cuda_err(p->ctx, e, "attention launch");
     }

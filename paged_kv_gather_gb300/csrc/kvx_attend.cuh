@@ -57,23 +57,24 @@ struct Attend {
 };
 
 // The schedule of one kernel.  The keys that each unit of rows visits, cut into tiles, are
-// laid end to end over all units; CTA c takes tiles [c * tiles / ctas, (c + 1) * tiles / ctas)
-// of that line, so every CTA has the same work to within a tile whatever the lengths.  A unit
-// that one CTA does not finish alone is joined from partial results: CTA c keeps one it began
-// and did not finish in slot 2 c + 1, and one it took over from CTA c - 1 in slot 2 c.
+// laid end to end over all units, and every CTA takes an equal stretch of that line, whatever
+// the lengths (AttnStart).  A unit that one CTA does not finish alone is joined from partial
+// results: CTA c keeps one it began and did not finish in slot 2 c + 1, and one it took over
+// from CTA c - 1 in slot 2 c.
 struct Work {
     const AttnReq *reqs;       // of this kernel, those with rows
-    const AttnStart *starts;   // [ctas]
-    unsigned int *counters;    // [ctas]: arrivals at the unit that CTA c began, zero between launches
+    const AttnStart *starts;   // [CTAs]
+    unsigned int *counters;    // [2 * CTAs]: arrivals at the unit a CTA began, zero between launches
     float *partial;
-    int64_t tiles;
-    int32_t ctas;
 };
 
-// CTA that takes tile x of the line.
-__device__ __forceinline__ int cta_of(const Work &w, int64_t x)
+// Kernels here start while the one before them on the stream ends (programmatic dependent
+// launch): they touch memory only past this wait for its completion, and let the next one
+// start in the same way.
+__device__ __forceinline__ void wait_for_earlier_work()
 {
-    return int(((x + 1) * w.ctas - 1) / w.tiles);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Keys that some row of a unit sees: [0, prefix) and [low, end); positions of its first and

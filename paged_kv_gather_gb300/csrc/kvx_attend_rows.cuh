@@ -174,20 +174,17 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quad = lane >> 2, c = lane & 3;
     const unsigned ring = smem_u32(smem) + warp * L::kRing;
-    const int64_t line0 = int64_t(blockIdx.x) * w.tiles / w.ctas;
-    const int64_t line1 = (int64_t(blockIdx.x) + 1) * w.tiles / w.ctas;
     const Score score(a);
     const bool plain = !(a.softcap > 0.0f) && !a.slopes;
 
+    wait_for_earlier_work();
     AttnStart at = w.starts[blockIdx.x];
-    int64_t line = line0;
-    while (line < line1) {
+    while (at.tiles > 0) {
         const AttnReq r = w.reqs[at.request];
         Keys keys;
         keys.set<kRowTile>(r, a.window, 0, r.n_new - 1);
         const int rows = r.n_new * a.group;
-        const int64_t unit = line - at.tile;                   // the unit's first tile
-        const int todo = int(min(int64_t(keys.tiles - at.tile), line1 - line));
+        const int todo = int(min(int64_t(keys.tiles - at.tile), at.tiles));
 
         // The warp's keys in step i of the unit's share.
         auto first_key = [&](int i) {
@@ -477,7 +474,8 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
                 }
         __syncthreads();
 
-        const int c0 = cta_of(w, unit), c1 = cta_of(w, unit + keys.tiles - 1);
+        const int c0 = at.tile > 0 ? at.first : int(blockIdx.x);
+        const int c1 = at.tile + todo < keys.tiles ? at.last : int(blockIdx.x);
         float *slot = w.partial + (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) * kSlot;
         auto write = [&](int row, int d, float4 v, float mm, float ll) {
             const int tok = row / a.group, head = at.head * a.group + row - tok * a.group;
@@ -559,7 +557,7 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
         }
         __syncthreads();  // the rings and ml are free for the next unit
 
-        line += todo;
+        at.tiles -= todo;
         at.tile = 0;
         if (++at.head == a.kv_heads) {
             at.head = 0;

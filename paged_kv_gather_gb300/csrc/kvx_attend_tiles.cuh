@@ -317,7 +317,6 @@ __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes)
 struct Walk {
     const Attend &a;
     const Work &w;
-    int64_t line, line1;
     AttnStart at;
     AttnReq r;
     Keys keys;
@@ -325,13 +324,20 @@ struct Walk {
 
     __device__ __forceinline__ Walk(const Attend &a_, const Work &w_) : a(a_), w(w_)
     {
-        line = int64_t(blockIdx.x) * w.tiles / w.ctas;
-        line1 = (int64_t(blockIdx.x) + 1) * w.tiles / w.ctas;
         at = w.starts[blockIdx.x];
-        if (line < line1)
+        if (!done())
             enter();
     }
-    __device__ __forceinline__ bool done() const { return line >= line1; }
+    __device__ __forceinline__ bool done() const { return at.tiles <= 0; }
+    // The CTAs that begin and end the unit.
+    __device__ __forceinline__ int begun_by() const
+    {
+        return at.tile > 0 ? at.first : int(blockIdx.x);
+    }
+    __device__ __forceinline__ int ended_by() const
+    {
+        return at.tile + todo < keys.tiles ? at.last : int(blockIdx.x);
+    }
     __device__ __forceinline__ int key_of(int i) const
     {
         const int t = at.tile + i;
@@ -344,11 +350,11 @@ struct Walk {
         row0 = at.block * kBlockRows;
         rows = min(kBlockRows, all - row0);
         keys.set<kTileKeys>(r, a.window, row0 / a.group, (row0 + rows - 1) / a.group);
-        todo = int(min(int64_t(keys.tiles - at.tile), line1 - line));
+        todo = int(min(int64_t(keys.tiles - at.tile), at.tiles));
     }
     __device__ __forceinline__ void next()
     {
-        line += todo;
+        at.tiles -= todo;
         if (done())
             return;
         at.tile = 0;
@@ -410,6 +416,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const unsigned tmem = tmem_base;
+    wait_for_earlier_work();
 
     if (warp == 8) {
         // ------------------------------------------------------------- matrix products
@@ -847,8 +854,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             }
 
             // The result, or this CTA's part of it.
-            const int64_t unit_at = u.line - u.at.tile;
-            const int c0 = cta_of(w, unit_at), c1 = cta_of(w, unit_at + u.keys.tiles - 1);
+            const int c0 = u.begun_by(), c1 = u.ended_by();
             auto write = [&](int b, const float(&o)[32], float ll) {
                 const float f = a.v_scale / ll;
                 uint4 *out = reinterpret_cast<uint4 *>(a.out + orow * a.out_stride +

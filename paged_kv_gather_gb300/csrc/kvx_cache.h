@@ -61,14 +61,18 @@ struct AttnReq {
 };
 static_assert(sizeof(AttnReq) == 32, "descriptor layout");
 
-// Where a CTA begins: unit (request, block of rows, KV head) and tile within it.
+// A CTA's share of the units (request, block of rows, KV head) laid end to end: where it
+// begins, how many tiles of keys it takes, and which CTAs it meets at its ends.
 struct AttnStart {
     int32_t request;
     int32_t block;
     int32_t head;
-    int32_t tile;
+    int32_t tile;     // within the unit
+    int32_t first;    // CTA that began the unit, if tile > 0
+    int32_t last;     // CTA that ends the unit this share stops inside of, if it does
+    int64_t tiles;
 };
-static_assert(sizeof(AttnStart) == 16, "descriptor layout");
+static_assert(sizeof(AttnStart) == 32, "descriptor layout");
 
 // Tiles of T keys that cover [0, prefix) and [low, end), in order: `first` tiles from key 0,
 // then the rest `skip` tiles further on; no tile twice.

@@ -31,6 +31,7 @@ const int kThreads = 1024;
 const int kWarps = kThreads / 32;
 const int kGranWords = 8;                // bitmap words per granule
 const int kGranPages = 32 * kGranWords;  // pages per granule: one warp scans one at a time
+const int kTableWarps = 4;               // of a CTA that also copies
 const int kUnits = 8;                    // 16-byte loads in flight per lane
 
 struct Inline {
@@ -52,6 +53,7 @@ struct Args {
     int32_t page_size;
     int32_t num_pages;
     int32_t slices;          // jobs per (page, slab)
+    int32_t table_warps;     // of each CTA, for tables; the others copy
 };
 
 // -------------------------------------------------------------------------------- device
@@ -59,6 +61,15 @@ struct Args {
 __device__ __forceinline__ int ld_ref(const int32_t *p)
 {
     return __ldcg(p);  // L2: another CTA's atomics change counts while this launch runs
+}
+
+// These kernels start while the one before them on the stream ends (programmatic dependent
+// launch): they touch memory only past this wait for its completion, and let the next one
+// start in the same way.
+__device__ __forceinline__ void wait_for_earlier_work()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // The bitmap of one kind of page (free or live) with running totals per granule.
@@ -165,19 +176,14 @@ __device__ Bits scan_pages(const Args &a, bool live, int enough, unsigned *smem)
     return b;
 }
 
-// True in exactly one CTA, for all its threads, once every CTA has called it; that CTA sees
-// what the others wrote before.  Leaves the counter at zero.
-__device__ bool last_to_arrive(unsigned int *counter)
+// Arrival of this CTA's scan, by one thread, after a barrier that ends the scan; and, past a
+// later barrier, whether it was the last CTA of the launch to arrive.  The counter is left at
+// zero.
+__device__ void arrive(unsigned int *counter, int *last)
 {
-    __shared__ int last;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        last = atomicInc(counter, gridDim.x - 1) == gridDim.x - 1;
-        __threadfence();
-    }
-    __syncthreads();
-    return last;
+    __threadfence();
+    *last = atomicInc(counter, gridDim.x - 1) == gridDim.x - 1;
+    __threadfence();
 }
 
 // Entry that owns flat index i: the last e with begin(e) <= i, begin of the sentinel > i.
@@ -244,16 +250,28 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
     const ForkEntry *e = reinterpret_cast<const ForkEntry *>(desc + a.off_entries);
     const ForkEntry &end = e[a.n_entries];
     const int lane = threadIdx.x & 31;
+    __shared__ int last;
+    wait_for_earlier_work();
     const Bits free = scan_pages(a, false, end.fresh_begin, smem);
+    if (threadIdx.x == 0)
+        arrive(a.counter, &last);
     if (free.total < end.fresh_begin) {  // the same in every CTA: counts of live pages only grow
-        if (last_to_arrive(a.counter) && threadIdx.x == 0)
+        if (blockIdx.x == 0 && threadIdx.x == 0)
             atomicOr(a.status, KVX_DEV_NO_FREE_PAGE);
         return;
     }
 
-    // Tables, and the counts of shared pages.
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < end.page_begin;
-         i += gridDim.x * kThreads) {
+    // Pages past the scan do not turn live in this launch.
+    auto is_free = [&](int p) {
+        return p < free.granules * kGranPages ? free.test(p) : ld_ref(a.refs + p) <= 0;
+    };
+
+    // Tables, and the counts of shared pages, by the last warps of every CTA (by all, if there
+    // is nothing to copy) beside the copies of the others.
+    const int warp = threadIdx.x >> 5, copy_warps = kWarps - a.table_warps;
+    const int table_threads = 32 * a.table_warps;
+    for (int i = blockIdx.x * table_threads + threadIdx.x - 32 * copy_warps;
+         warp >= copy_warps && i < end.page_begin; i += gridDim.x * table_threads) {
         const int x = find_entry(e, a.n_entries, i, [](const ForkEntry &f) { return f.page_begin; });
         const int j = i - e[x].page_begin;
         if (j >= e[x].full) {
@@ -263,7 +281,7 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
             unsigned bad = 0;
             if (unsigned(p) >= unsigned(a.num_pages))
                 bad = KVX_DEV_PAGE_OUT_OF_RANGE;
-            else if (ld_ref(a.refs + p) <= 0)
+            else if (is_free(p))
                 bad = KVX_DEV_PAGE_NOT_HELD;
             if (bad) {
                 atomicOr(a.status, bad);
@@ -274,14 +292,10 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
             e[x].child[j] = p;
         }
     }
-    if (last_to_arrive(a.counter))
-        for (int i = threadIdx.x; i < end.fresh_begin; i += kThreads)
-            a.refs[free.select(i)] = 1;
-
     // Copies: jobs in the order (page, slab, slice).
     const int64_t jobs = int64_t(end.copy_begin) * a.n_slabs * a.slices;
-    for (int64_t job = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); job < jobs;
-         job += int64_t(gridDim.x) * kWarps) {
+    for (int64_t job = int64_t(blockIdx.x) * copy_warps + warp; warp < copy_warps && job < jobs;
+         job += int64_t(gridDim.x) * copy_warps) {
         const unsigned t = unsigned(job) / unsigned(a.slices);  // jobs < 2^31 (host)
         const int slice = int(unsigned(job) - t * a.slices);
         const int c = int(t / unsigned(a.n_slabs)), slab = int(t - unsigned(c) * a.n_slabs);
@@ -291,8 +305,8 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
         unsigned bad = 0;
         if (unsigned(from) >= unsigned(a.num_pages))
             bad = KVX_DEV_PAGE_OUT_OF_RANGE;
-        else if (from < free.granules * kGranPages ? free.test(from) : ld_ref(a.refs + from) <= 0)
-            bad = KVX_DEV_PAGE_NOT_HELD;  // pages past the scan never turn live in this launch
+        else if (is_free(from))
+            bad = KVX_DEV_PAGE_NOT_HELD;
         if (bad) {
             if (lane == 0)
                 atomicOr(a.status, bad);
@@ -302,6 +316,10 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
         copy_slice(a, desc, slab, slice, from, to,
                    min(a.page_size, e[x].shared - j * a.page_size), lane);
     }
+    __syncthreads();
+    if (last)
+        for (int i = threadIdx.x; i < end.fresh_begin; i += kThreads)
+            a.refs[free.select(i)] = 1;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -310,6 +328,7 @@ kvx_free_kernel(const Args a, const __grid_constant__ Inline in)
     const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
     const TableEntry *e = reinterpret_cast<const TableEntry *>(desc + a.off_entries);
     const int total = e[a.n_entries].page_begin;
+    wait_for_earlier_work();
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
         const int x = find_entry(e, a.n_entries, i, [](const TableEntry &t) { return t.page_begin; });
         int32_t *at = e[x].pages + (i - e[x].page_begin);
@@ -336,7 +355,11 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
     const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
     const TableEntry *e = reinterpret_cast<const TableEntry *>(desc + a.off_entries);
     const int lane = threadIdx.x & 31;
+    __shared__ int last;
+    wait_for_earlier_work();
     const Bits live = scan_pages(a, true, a.num_pages + 1, smem);
+    if (threadIdx.x == 0)
+        arrive(a.counter, &last);
     const int n = live.total, front = live.rank(n), moves = n - front;
     // Page of the i-th free page below n: the smallest p with (p - rank(p)) pages free before
     // it and p free, by bisection over pages.
@@ -368,8 +391,11 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
         return w * 32 + bit;
     };
 
+    const int warp = threadIdx.x >> 5, copy_warps = kWarps - a.table_warps;
+    const int table_threads = 32 * a.table_warps;
+    const int mine = blockIdx.x * table_threads + threadIdx.x - 32 * copy_warps;
     const int total = e[a.n_entries].page_begin;
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
+    for (int i = mine; warp >= copy_warps && i < total; i += gridDim.x * table_threads) {
         const int x = find_entry(e, a.n_entries, i, [](const TableEntry &t) { return t.page_begin; });
         int32_t *at = e[x].pages + (i - e[x].page_begin);
         const int p = *at;
@@ -381,10 +407,19 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
             *at = hole(live.rank(p) - front);
     }
     if (a.remap)
-        for (int p = blockIdx.x * kThreads + threadIdx.x; p < a.num_pages;
-             p += gridDim.x * kThreads)
+        for (int p = mine; warp >= copy_warps && p < a.num_pages; p += gridDim.x * table_threads)
             a.remap[p] = !live.test(p) ? -1 : p < n ? p : hole(live.rank(p) - front);
-    if (last_to_arrive(a.counter)) {
+
+    const int64_t jobs = int64_t(moves) * a.n_slabs * a.slices;
+    for (int64_t job = int64_t(blockIdx.x) * copy_warps + warp; warp < copy_warps && job < jobs;
+         job += int64_t(gridDim.x) * copy_warps) {
+        const unsigned t = unsigned(job) / unsigned(a.slices);
+        const int slice = int(unsigned(job) - t * a.slices);
+        const int c = int(t / unsigned(a.n_slabs)), slab = int(t - unsigned(c) * a.n_slabs);
+        copy_slice(a, desc, slab, slice, live.select(front + c), hole(c), a.page_size, lane);
+    }
+    __syncthreads();
+    if (last) {
         for (int i = threadIdx.x; i < moves; i += kThreads) {
             const int from = live.select(front + i);
             a.refs[hole(i)] = ld_ref(a.refs + from);
@@ -392,15 +427,6 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
         }
         if (a.n_live && threadIdx.x == 0)
             *a.n_live = n;
-    }
-
-    const int64_t jobs = int64_t(moves) * a.n_slabs * a.slices;
-    for (int64_t job = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); job < jobs;
-         job += int64_t(gridDim.x) * kWarps) {
-        const unsigned t = unsigned(job) / unsigned(a.slices);
-        const int slice = int(unsigned(job) - t * a.slices);
-        const int c = int(t / unsigned(a.n_slabs)), slab = int(t - unsigned(c) * a.n_slabs);
-        copy_slice(a, desc, slab, slice, live.select(front + c), hole(c), a.page_size, lane);
     }
 }
 
@@ -458,9 +484,18 @@ kvx_status launch_batch(kvx_ctx *ctx, void (*fn)(Args, Inline), Args a, Batch *b
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e == cudaSuccess) {
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3(unsigned(ctas));
+        lc.blockDim = dim3(kThreads);
+        lc.dynamicSmemBytes = smem;
+        lc.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
         void *args[] = {&a, &b->in};
-        e = cudaLaunchKernel(reinterpret_cast<const void *>(fn), dim3(unsigned(ctas)),
-                             dim3(kThreads), args, smem, s);
+        e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(fn), args);
     }
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "kernel launch");
@@ -535,10 +570,12 @@ kvx_status kvx_fork_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
     if ((st = too_many_jobs(ctx, end.copy_begin, a)) != KVX_OK)
         return st;
     a.counter = kvx::take_counter(ctx);
+    a.table_warps = end.copy_begin ? kTableWarps : kWarps;
     const int64_t jobs = int64_t(end.copy_begin) * a.n_slabs * a.slices;
     const int64_t ctas = std::min<int64_t>(
         ctx->num_sms, std::max((jobs + kWarps - 1) / kWarps,
-                               (int64_t(end.page_begin) + kThreads - 1) / kThreads));
+                               (int64_t(end.page_begin) + 32 * a.table_warps - 1) /
+                                   (32 * a.table_warps)));
     return launch_batch(ctx, kvx_fork_kernel, a, &b, ctas, bitmap_bytes(pool->num_pages), jobs,
                         reinterpret_cast<cudaStream_t>(stream));
 }
@@ -582,6 +619,7 @@ static kvx_status tables_call(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
     }
     a.n_live = n_live;
     a.remap = remap;
+    a.table_warps = kTableWarps;
     // How many pages move is known on the device only: at most half the pool.
     choose_slices(ctx, int64_t(pool->num_pages) * a.n_slabs / 4,
                   int64_t(pool->page_size) * pool->token_bytes, &a);
