@@ -20,7 +20,7 @@ enum { kRows = 0, kMoreRows = 1, kTiles = 2, kKinds = 3 };
 
 // What joining the parts of a cut unit is worth in keys read, and what a unit costs beyond
 // its tiles (by bytes of K and V for the kernels of few rows, by tiles for the other).
-const int64_t kLeastBytes = 160 << 10, kUnitBytes = 64 << 10;
+const int64_t kLeastBytes = 160 << 10, kUnitBytes = 128 << 10;
 const int kLeastTiles = 4, kUnitTiles = 2;
 
 struct Schedule {

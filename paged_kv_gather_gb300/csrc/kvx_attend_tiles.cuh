@@ -41,7 +41,7 @@ struct TileShape {
     static const int kOffStage = kOffRing + kSlots * kTile;  // e4m3: [2][kTile / 2]
     static const int kOffKeys = kOffStage + kEight * kTile;  // int64 [2][kTileKeys]
     static const int kOffBars = kOffKeys + 2 * kTileKeys * 8;
-    static const int kOffMisc = kOffBars + 256;              // int[4]
+    static const int kOffMisc = kOffBars + 8 * 34;              // int[4]
     static const int kBytes = kOffMisc + 16;
     static const int kSlotFloats = kBlockRows * (D + 2);     // a partial result: O, m, l
 };
@@ -50,14 +50,15 @@ struct TileShape {
 enum {
     kBarQ = 0,      // q is in shared memory
     kBarS = 2,      // S is complete, and every product before it
-    kBarP = 4,      // P is in tensor memory
-    kBarO = 6,      // O is complete
-    kBarJoin = 8,   // the threads of the tile among themselves
-    kBarKeys = 10,  // the loaders among themselves
-    kBarFull = 11,
-    kBarEmpty = 21,
-    kBarEnd = 31,
-    kBars = 32
+    kBarP = 4,      // P of the first 64 keys is in tensor memory
+    kBarP2 = 6,     // and of the others
+    kBarO = 8,      // O is complete
+    kBarJoin = 10,  // the threads of the tile among themselves
+    kBarKeys = 12,  // the loaders among themselves
+    kBarFull = 13,
+    kBarEmpty = 23,
+    kBarEnd = 33,
+    kBars = 34
 };
 
 __device__ __forceinline__ void mbar_init(unsigned bar, unsigned count)
@@ -243,6 +244,12 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+// The bits 0 .. n - 1 of 32.
+__device__ __forceinline__ unsigned bits_below(int n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1;
+}
+
 // Two 32-bit numbers at a time.
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi)
 {
@@ -402,6 +409,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             mbar_init(bar(kBarJoin + x), kTileRows);
             mbar_init(bar(kBarS + x), 1);
             mbar_init(bar(kBarP + x), kTileRows);
+            mbar_init(bar(kBarP2 + x), kTileRows);
             mbar_init(bar(kBarO + x), 1);
         }
         mbar_init(bar(kBarKeys), kLoaders);
@@ -476,14 +484,23 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                     for (int x = 0; x < 2; ++x) {
                         if (x >= tiles)
                             break;
-                        if (!(ok = wait1(kBarP + x, p_phase[x])))
+                        // P V of the first 64 keys runs while the weights of the others are
+                        // still being made.
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (!(ok = wait1((half ? kBarP2 : kBarP) + x, p_phase[x])))
+                                break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = half * (kTileKeys / 32); k < (half + 1) * (kTileKeys / 32);
+                                 ++k)
+                                tc_mma_ts(tmem + 2 * kTileKeys + x * D,
+                                          tmem + x * kTileKeys + 8 * k, v + (k * 2048 >> 4),
+                                          kDescO, k > 0 || i > 0);
+                        }
+                        if (!ok)
                             break;
                         p_phase[x] ^= 1;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < kTileKeys / 16; ++k)
-                            tc_mma_ts(tmem + 2 * kTileKeys + x * D, tmem + x * kTileKeys + 8 * k,
-                                      v + (k * 2048 >> 4), kDescO, k > 0 || i > 0);
                         if (more)
                             scores(x, slot);
                         else
@@ -534,14 +551,18 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         };
         // Copy this thread's chunks of 16 bytes of a tile, where each key lies at off[key].
         auto copy = [&](const char *base, const int64_t *off, unsigned dst) {
-#pragma unroll 4
+            int64_t o[kCopies];  // all at once: nothing moves across an asynchronous copy
+#pragma unroll
+            for (int b = 0; b < kCopies; ++b) {
+                const int x = lt + b * kLoaders;
+                o[b] = x < kTileKeys * kChunks ? off[x / kChunks] : -1;
+            }
+#pragma unroll
             for (int b = 0; b < kCopies; ++b) {
                 const int x = lt + b * kLoaders, t = x / kChunks, c = x % kChunks;
-                if (x < kTileKeys * kChunks) {
-                    const int64_t o = off[t];
+                if (x < kTileKeys * kChunks)
                     cp_async16(dst + (kEight ? x * 16 : tile_at(t, c)),
-                               base + (o >= 0 ? o : 0) + c * 16, o >= 0);
-                }
+                               base + (o[b] >= 0 ? o[b] : 0) + c * 16, o[b] >= 0);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -551,16 +572,22 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         auto convert = [&]() {  // the staged side, number `filled` of the stream
             const char *src = smem + T::kOffStage + (filled & 1) * (T::kTile / 2);
             char *dst = smem + T::kOffRing + slot * T::kTile;
+            uint4 in[kCopies];  // all at once: loads do not move up across stores
+#pragma unroll
+            for (int b = 0; b < kCopies; ++b) {
+                const int x = lt + b * kLoaders;
+                if (x < kTileKeys * kChunks)
+                    in[b] = *reinterpret_cast<const uint4 *>(src + x * 16);
+            }
 #pragma unroll
             for (int b = 0; b < kCopies; ++b) {
                 const int x = lt + b * kLoaders, t = x / kChunks, c = x % kChunks;
                 if (x < kTileKeys * kChunks) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(src + x * 16);
                     uint4 h0, h1;
-                    half4_of_e4m3(u.x, h0.x, h0.y);
-                    half4_of_e4m3(u.y, h0.z, h0.w);
-                    half4_of_e4m3(u.z, h1.x, h1.y);
-                    half4_of_e4m3(u.w, h1.z, h1.w);
+                    half4_of_e4m3(in[b].x, h0.x, h0.y);
+                    half4_of_e4m3(in[b].y, h0.z, h0.w);
+                    half4_of_e4m3(in[b].z, h1.x, h1.y);
+                    half4_of_e4m3(in[b].w, h1.z, h1.w);
                     *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c)) = h0;
                     *reinterpret_cast<uint4 *>(dst + tile_at(t, 2 * c + 1)) = h1;
                 }
@@ -579,6 +606,14 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                            ? __ldg(u.r.table + a.page.div(j)) : -1;
             };
             int next = kEight ? -1 : page_of(0);
+            // Page of key lt + b * kLoaders of tile i.
+            auto key_page = [&](int i, int b) {
+                const int t = lt + b * kLoaders;
+                const int j = i < u.todo && t < kTileKeys ? u.key_of(i) + t : 0;
+                return i < u.todo && t < kTileKeys && u.keys.used(j)
+                           ? __ldg(u.r.table + a.page.div(j)) : -1;
+            };
+            int later[2] = {-1, -1};
             for (int i = 0; ok && i < u.todo; ++i) {
                 const int j0 = u.key_of(i);
                 if (!kEight) {
@@ -614,18 +649,27 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 }
                 // Where each key of the tile lies; -1: not used.
                 int64_t *off = offs + key_phase * kTileKeys;
-                for (int t = lt; t < kTileKeys; t += kLoaders) {
-                    const int j = j0 + t;
-                    int64_t o = -1;
-                    if (u.keys.used(j)) {
-                        const int nth = a.page.div(j), page = __ldg(u.r.table + nth);
-                        if (unsigned(page) < unsigned(a.num_pages))
-                            o = (int64_t(page) * a.page_size + j - nth * a.page_size) *
-                                    a.token_bytes + head_at;
-                        else
-                            atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+                int page[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    // Looked up a tile ahead where every tile comes this way.
+                    page[b] = !a.box && i > 0 ? later[b] : key_page(i, b);
+                    later[b] = a.box ? -1 : key_page(i + 1, b);
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int t = lt + b * kLoaders, j = j0 + t;
+                    if (t < kTileKeys) {
+                        int64_t o = -1;
+                        if (u.keys.used(j)) {
+                            if (unsigned(page[b]) < unsigned(a.num_pages))
+                                o = (int64_t(page[b]) * a.page_size + j -
+                                     a.page.div(j) * a.page_size) * a.token_bytes + head_at;
+                            else
+                                atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+                        }
+                        off[t] = o;
                     }
-                    off[t] = o;
                 }
                 mbar_arrive(bar(kBarKeys));
                 ok = wait(kBarKeys, key_phase);
@@ -680,6 +724,11 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         const unsigned ts = tmem + lanes + x * kTileKeys;
         const unsigned to = tmem + lanes + 2 * kTileKeys + x * D;
         const Score score(a);
+        // Rows of q and out as a warp reads and writes them: kRowsAtOnce of its 32 at a time,
+        // kRowChunks lanes to a row.
+        constexpr int kRowChunks = D / 8, kRowsAtOnce = 32 / kRowChunks;
+        const int sub_row = lane / kRowChunks, sub_chunk = lane % kRowChunks;
+        const int warp_row = row & ~31;
         unsigned s_phase = 0, o_phase = 0;
         bool ok = true;
         for (Walk u(a, w); ok && !u.done(); u.next()) {
@@ -692,36 +741,41 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.0f;
             float row_factor = 1.0f;
             if (mine) {
-                // q into shared memory, a row per thread.
-                const uint4 *q = reinterpret_cast<const uint4 *>(a.q + orow * a.q_stride +
-                                                                 head * (D * 2));
+                // q into shared memory.  A warp reads its 32 rows a few whole rows at a time:
+                // with a row per thread, every load and store of the warp met 32 lines.
+                const int64_t off = have ? orow * a.q_stride + head * (D * 2) : -1;
                 char *dst = smem + x * T::kTile;
-                float down = 1.0f;
-                if (kEight) {  // scaled by a power of two into half precision
-                    float top = 0.0f;
+                uint4 v[kRowChunks];
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 v = have ? q[c] : make_uint4(0, 0, 0, 0);
-                        const typename E::T *e = reinterpret_cast<const typename E::T *>(&v);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            top = fmaxf(top, fabsf(E::load(e[i])));
-                    }
-                    unit_scale(top, &down, &row_factor);
+                for (int t = 0; t < kRowChunks; ++t) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off, t * kRowsAtOnce + sub_row);
+                    v[t] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.q + o) + sub_chunk)
+                                  : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 v = have ? q[c] : make_uint4(0, 0, 0, 0);
-                    if (kEight) {
-                        const typename E::T *e = reinterpret_cast<const typename E::T *>(&v);
-                        uint4 h;
-                        h.x = P::pack(E::load(e[0]) * down, E::load(e[1]) * down);
-                        h.y = P::pack(E::load(e[2]) * down, E::load(e[3]) * down);
-                        h.z = P::pack(E::load(e[4]) * down, E::load(e[5]) * down);
-                        h.w = P::pack(E::load(e[6]) * down, E::load(e[7]) * down);
-                        v = h;
+                for (int t = 0; t < kRowChunks; ++t) {
+                    if (kEight) {  // scaled by a power of two into half precision
+                        const typename E::T *e = reinterpret_cast<const typename E::T *>(&v[t]);
+                        float q[8], top = 0.0f, down, up;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            q[i] = E::load(e[i]);
+                            top = fmaxf(top, fabsf(q[i]));
+                        }
+#pragma unroll
+                        for (int d = 1; d < kRowChunks; d <<= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        unit_scale(top, &down, &up);
+                        v[t] = make_uint4(P::pack(q[0] * down, q[1] * down),
+                                          P::pack(q[2] * down, q[3] * down),
+                                          P::pack(q[4] * down, q[5] * down),
+                                          P::pack(q[6] * down, q[7] * down));
+                        up = __shfl_sync(0xffffffffu, up, lane % kRowsAtOnce * kRowChunks);
+                        if (lane / kRowsAtOnce == t)
+                            row_factor = up;
                     }
-                    *reinterpret_cast<uint4 *>(dst + tile_at(row, c)) = v;
+                    *reinterpret_cast<uint4 *>(
+                        dst + tile_at(warp_row + t * kRowsAtOnce + sub_row, sub_chunk)) = v[t];
                 }
                 fence_async_shared();
                 mbar_arrive(bar(kBarQ + x));
@@ -763,28 +817,63 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                         }
                         top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     } else {
-                        const int lo = a.window ? pos - a.window + 1 - j0 : -j0;
                         const int hi = pos - j0, pre = u.keys.prefix - j0;
+                        const int lo = a.window ? hi - a.window + 1 : -j0;
+                        // Where rows see no key after their own, -|i - j| is j - i.
+                        const bool behind = u.keys.prefix <= u.keys.pmin + 1;
 #pragma unroll 1
                         for (int b = 0; b < 4; ++b) {
                             float z[32];
                             tc_ld32(z, ts + 32 * b);
                             tc_wait_ld(z);
-                            if (!plain) {
+                            const float away = float(32 * b - hi);  // j - i of z[0]
+                            if (a.softcap > 0.0f) {
+                                const float f = score.inner * row_factor;
+                                float most = 0.0f;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
-                                    z[k] = a.softcap > 0.0f ? score.capped(z[k] * row_factor)
-                                                            : z[k] * factor;
-                                    z[k] -= slope * fabsf(float(hi - 32 * b - k));
+                                    z[k] *= f;
+                                    most = fmaxf(most, fabsf(z[k]));
+                                }
+                                if (__all_sync(0xffffffffu, most <= 1.0f)) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        z[k] = score.cap * tanh_small(z[k]);
+                                } else {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        z[k] = score.cap * tanh_(z[k]);
+                                }
+                            } else if (!plain) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    z[k] *= factor;
+                            }
+                            if (a.slopes) {
+                                if (behind) {
+                                    const float z0 = slope * away;
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        z[k] += fmaf(slope, float(k), z0);
+                                } else {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        z[k] -= slope * fabsf(away + float(k));
                                 }
                             }
+                            if (!all_seen) {
+                                const unsigned seen = (bits_below(hi + 1 - 32 * b) &
+                                                       ~bits_below(lo - 32 * b)) |
+                                                      bits_below(pre - 32 * b);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int j = 32 * b + k;
-                                if (!(j < pre || (j >= lo && j <= hi)))
-                                    z[k] = -INFINITY;
-                                top = fmaxf(top, z[k]);
+                                for (int k = 0; k < 32; ++k)
+                                    z[k] = seen >> k & 1 ? z[k] : -INFINITY;
                             }
+                            float t4[2] = {top, -INFINITY};
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2)
+                                t4[k >> 1 & 1] = max3(t4[k >> 1 & 1], z[k], z[k + 1]);
+                            top = fmaxf(t4[0], t4[1]);
                             tc_st32(ts + 32 * b, z);
                         }
                         tc_wait_st();
@@ -836,13 +925,15 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                                 p[k] = P::pack(e.x, e.y);
                             }
                             tc_st16(ts + 16 * b, p);
+                            if (b & 1) {
+                                tc_wait_st();
+                                tc_fence_before();
+                                mbar_arrive(bar((b == 1 ? kBarP : kBarP2) + x));
+                            }
                         }
                     }
                     const float2 sums = halves_of(add_pair(sum[0], sum[1]));
                     l += sums.x + sums.y;
-                    tc_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(bar(kBarP + x));
                 }
                 if (!ok)
                     break;
@@ -855,16 +946,33 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
 
             // The result, or this CTA's part of it.
             const int c0 = u.begun_by(), c1 = u.ended_by();
-            auto write = [&](int b, const float(&o)[32], float ll) {
+            // Rows go out by way of q's place in shared memory, which is free by now; each warp
+            // uses its own rows of it.
+            auto put = [&](int b, const float(&o)[32], float ll) {
                 const float f = a.v_scale / ll;
-                uint4 *out = reinterpret_cast<uint4 *>(a.out + orow * a.out_stride +
-                                                       (head * D + 32 * b) * 2);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    out[k] = make_uint4(E::pack(o[8 * k] * f, o[8 * k + 1] * f),
-                                        E::pack(o[8 * k + 2] * f, o[8 * k + 3] * f),
-                                        E::pack(o[8 * k + 4] * f, o[8 * k + 5] * f),
-                                        E::pack(o[8 * k + 6] * f, o[8 * k + 7] * f));
+                    *reinterpret_cast<uint4 *>(smem + x * T::kTile + tile_at(row, 4 * b + k)) =
+                        make_uint4(E::pack(o[8 * k] * f, o[8 * k + 1] * f),
+                                   E::pack(o[8 * k + 2] * f, o[8 * k + 3] * f),
+                                   E::pack(o[8 * k + 4] * f, o[8 * k + 5] * f),
+                                   E::pack(o[8 * k + 6] * f, o[8 * k + 7] * f));
+            };
+            auto flush = [&](float mm, float ll) {
+                const int64_t off = have ? orow * a.out_stride + head * (D * 2) : -1;
+                __syncwarp();
+#pragma unroll
+                for (int t = 0; t < kRowChunks; ++t) {
+                    const int r = t * kRowsAtOnce + sub_row;
+                    const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                    if (o >= 0)
+                        reinterpret_cast<uint4 *>(a.out + o)[sub_chunk] =
+                            *reinterpret_cast<const uint4 *>(
+                                smem + x * T::kTile + tile_at(warp_row + r, sub_chunk));
+                }
+                __syncwarp();
+                if (have && a.lse)
+                    a.lse[orow * a.q_heads + head] = mm * kLn2 + logf(ll);
             };
             // A part: [D / 4][256 rows][4] of O, then [256][m, l].
             const int prow = x * kTileRows + row;
@@ -879,8 +987,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                     tc_ld32(o, to + 32 * b);
                     tc_wait_ld(o);
                     if (c0 == c1) {
-                        if (have)
-                            write(b, o, l);
+                        put(b, o, l);
                     } else if (have) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -888,9 +995,9 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                                 make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                 }
-                if (c0 == c1 && have && a.lse)
-                    a.lse[orow * a.q_heads + head] = m * kLn2 + logf(l);
-                if (c0 != c1 && have)
+                if (c0 == c1)
+                    flush(m, l);
+                else if (have)
                     *reinterpret_cast<float2 *>(slot + kBlockRows * D + 2 * prow) = make_float2(m, l);
             }
             if (mine && c0 != c1) {
@@ -910,10 +1017,12 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 mbar_arrive(bar(kBarJoin + x));
                 if (!(ok = wait(kBarJoin + x, 1)))
                     break;
-                if (last_cta[x] && have) {
+                if (last_cta[x]) {
                     float mm = -INFINITY, ll = 0.0f;
+#pragma unroll 4
                     for (int c = c0; c <= c1; ++c)
                         mm = fmaxf(mm, __ldcg(part(c) + kBlockRows * D + 2 * prow));
+#pragma unroll 4
                     for (int c = c0; c <= c1; ++c) {
                         const float2 p = __ldcg(reinterpret_cast<const float2 *>(
                             part(c) + kBlockRows * D + 2 * prow));
@@ -925,23 +1034,26 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             o[k] = 0.0f;
+#pragma unroll 2
                         for (int c = c0; c <= c1; ++c) {
+                            float4 v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                v[k] = __ldcg(reinterpret_cast<const float4 *>(
+                                    part(c) + ((8 * b + k) * kBlockRows + prow) * 4));
                             const float pm = __ldcg(part(c) + kBlockRows * D + 2 * prow);
                             const float f = pm == -INFINITY ? 0.0f : exp2_(pm - mm);
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                                    part(c) + ((8 * b + k) * kBlockRows + prow) * 4));
-                                o[4 * k] += f * v.x;
-                                o[4 * k + 1] += f * v.y;
-                                o[4 * k + 2] += f * v.z;
-                                o[4 * k + 3] += f * v.w;
+                                o[4 * k] += f * v[k].x;
+                                o[4 * k + 1] += f * v[k].y;
+                                o[4 * k + 2] += f * v[k].z;
+                                o[4 * k + 3] += f * v[k].w;
                             }
                         }
-                        write(b, o, ll);
+                        put(b, o, ll);
                     }
-                    if (a.lse)
-                        a.lse[orow * a.q_heads + head] = mm * kLn2 + logf(ll);
+                    flush(mm, ll);
                 }
             }
         }
