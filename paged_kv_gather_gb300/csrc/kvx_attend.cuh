@@ -121,21 +121,12 @@ __device__ __forceinline__ float tanh_(float x)
     return 1.0f - __fdividef(2.0f, exp2_(x * (2.0f * kLog2e)) + 1.0f);
 }
 
-// tanh for |x| <= 1: x P(x^2), P of degree 7 with the least largest relative error there (4e-9;
-// weighted least squares iterated to it), so 1.3e-7 in 32 bits.  Scores rarely leave that range
-// under a cap, and it takes no special-function instruction.
-__device__ __forceinline__ float tanh_small(float x)
-{
-    const float u = x * x;
-    float p = -0.00035334547f;
-    p = fmaf(p, u, 0.0022822295f);
-    p = fmaf(p, u, -0.0079174442f);
-    p = fmaf(p, u, 0.021464821f);
-    p = fmaf(p, u, -0.053870913f);
-    p = fmaf(p, u, 0.13332160f);
-    p = fmaf(p, u, -0.33333278f);
-    return x * fmaf(p, u, 1.0f);
-}
+// tanh x = x P(x^2) for |x| <= 1/2: P of degree 4 with the least largest relative error there
+// (1.3e-8, by weighted least squares iterated to it).  Scores rarely leave that range under a
+// cap, and it takes no special-function instruction.  kTanh[i] goes with x^(2 i).
+const int kTanhTerms = 5;
+__device__ constexpr float kTanh[kTanhTerms] = {1.0f, -0.33333069f, 0.13324779f, -0.052986074f,
+                                                0.017135007f};
 
 // What turns q . k into a score in units of log 2.
 struct Score {

@@ -186,9 +186,10 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
         const int rows = r.n_new * a.group;
         const int todo = int(min(int64_t(keys.tiles - at.tile), at.tiles));
 
-        // The warp's keys in step i of the unit's share.
+        // The warp's keys in step i of the unit's share; last keys first, so that a bias that
+        // favours near keys does not raise the maximum step by step.
         auto first_key = [&](int i) {
-            const int t = at.tile + i;
+            const int t = keys.tiles - 1 - at.tile - i;
             return (t < keys.first ? t : t + keys.skip) * kRowTile + warp * kRowKeys;
         };
         const int64_t head_at = int64_t(at.head) * L::kRow;

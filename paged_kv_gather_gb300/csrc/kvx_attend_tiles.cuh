@@ -244,6 +244,20 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The bits 0 .. n - 1 of 32.
 __device__ __forceinline__ unsigned bits_below(int n)
 {
@@ -269,6 +283,13 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -345,9 +366,11 @@ struct Walk {
     {
         return at.tile + todo < keys.tiles ? at.last : int(blockIdx.x);
     }
+    // Key that step i begins at.  Last keys first: where a bias favours near keys, the largest
+    // score is then met early and O is hardly ever rescaled.
     __device__ __forceinline__ int key_of(int i) const
     {
-        const int t = at.tile + i;
+        const int t = keys.tiles - 1 - at.tile - i;
         return (t < keys.first ? t : t + keys.skip) * kTileKeys;
     }
     __device__ __forceinline__ void enter()
@@ -786,6 +809,18 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 // that factor is all there is to them.  The same for a whole warp: the loads
                 // and stores of tensor memory below must not diverge.
                 const float factor = score.factor * row_factor;
+                // Under a cap, the terms of cap tanh(inner x) / x in x^2.
+                const float inner = score.inner * row_factor;
+                const bool series_fits = inner > 1e-4f && inner < 1e4f;
+                uint64_t series[kTanhTerms];
+                {
+                    float t = a.softcap > 0.0f ? score.cap * inner : factor;
+#pragma unroll
+                    for (int n = 0; n < kTanhTerms; ++n) {
+                        series[n] = pair_of(t * kTanh[n], t * kTanh[n]);
+                        t *= inner * inner;
+                    }
+                }
                 const bool plain = !(a.softcap > 0.0f) && !a.slopes && a.scale > 1e-10f;
                 for (int i = 0; i < u.todo; ++i) {
                     const int j0 = u.key_of(i);
@@ -820,46 +855,70 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                         const int hi = pos - j0, pre = u.keys.prefix - j0;
                         const int lo = a.window ? hi - a.window + 1 : -j0;
                         // Where rows see no key after their own, -|i - j| is j - i.
-                        const bool behind = u.keys.prefix <= u.keys.pmin + 1;
-#pragma unroll 1
-                        for (int b = 0; b < 4; ++b) {
-                            float z[32];
-                            tc_ld32(z, ts + 32 * b);
-                            tc_wait_ld(z);
+                        const bool behind = a.slopes && u.keys.prefix <= u.keys.pmin + 1;
+                        // Scores from products, two at a time: a factor or the cap's series, and a
+                        // bias that grows by `step` from pair to pair (its rounding grows with the
+                        // bias, that is, with how little such keys weigh).  Each combination is
+                        // code of its own: as one with conditions, all of it is executed.
+                        auto shape = [&](float(&z)[32], float away, auto capped, auto biased) {
+                            const float z0 = slope * away, two = 2.0f * slope;
+                            uint64_t bias = pair_of(z0, z0 + slope);
+                            const uint64_t step = pair_of(two, two);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const uint64_t x = pair_of(z[2 * k], z[2 * k + 1]);
+                                uint64_t t = series[0];
+                                if constexpr (decltype(capped)::value) {
+                                    const uint64_t u = mul_pair(x, x);
+                                    t = series[kTanhTerms - 1];
+#pragma unroll
+                                    for (int n = kTanhTerms - 2; n >= 0; --n)
+                                        t = fma_pair(t, u, series[n]);
+                                }
+                                float2 y;
+                                if constexpr (decltype(biased)::value) {
+                                    y = halves_of(fma_pair(x, t, bias));
+                                    bias = add_pair(bias, step);
+                                } else {
+                                    y = halves_of(mul_pair(x, t));
+                                }
+                                z[2 * k] = y.x;
+                                z[2 * k + 1] = y.y;
+                            }
+                        };
+                        auto adjust = [&](float(&z)[32], int b) {
                             const float away = float(32 * b - hi);  // j - i of z[0]
                             if (a.softcap > 0.0f) {
-                                const float f = score.inner * row_factor;
-                                float most = 0.0f;
+                                float most = 0.0f, least = 0.0f;
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    z[k] *= f;
-                                    most = fmaxf(most, fabsf(z[k]));
+                                for (int k = 0; k < 32; k += 2) {
+                                    most = max3(most, z[k], z[k + 1]);
+                                    least = min3(least, z[k], z[k + 1]);
                                 }
-                                if (__all_sync(0xffffffffu, most <= 1.0f)) {
+                                const bool small = series_fits && fmaxf(most, -least) * inner <= 0.5f;
+                                if (!__all_sync(0xffffffffu, small)) {
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
-                                        z[k] = score.cap * tanh_small(z[k]);
+                                        z[k] = score.cap * tanh_(z[k] * inner);
+                                    if (behind) {
+#pragma unroll
+                                        for (int k = 0; k < 32; ++k)
+                                            z[k] += slope * (away + float(k));
+                                    }
+                                } else if (behind) {
+                                    shape(z, away, Yes(), Yes());
                                 } else {
-#pragma unroll
-                                    for (int k = 0; k < 32; ++k)
-                                        z[k] = score.cap * tanh_(z[k]);
+                                    shape(z, away, Yes(), No());
                                 }
+                            } else if (behind) {
+                                shape(z, away, No(), Yes());
                             } else if (!plain) {
+                                shape(z, away, No(), No());
+                            }
+                            if (a.slopes && !behind) {
 #pragma unroll
                                 for (int k = 0; k < 32; ++k)
-                                    z[k] *= factor;
-                            }
-                            if (a.slopes) {
-                                if (behind) {
-                                    const float z0 = slope * away;
-#pragma unroll
-                                    for (int k = 0; k < 32; ++k)
-                                        z[k] += fmaf(slope, float(k), z0);
-                                } else {
-#pragma unroll
-                                    for (int k = 0; k < 32; ++k)
-                                        z[k] -= slope * fabsf(away + float(k));
-                                }
+                                    z[k] -= slope * fabsf(away + float(k));
                             }
                             if (!all_seen) {
                                 const unsigned seen = (bits_below(hi + 1 - 32 * b) &
@@ -875,6 +934,18 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                                 t4[k >> 1 & 1] = max3(t4[k >> 1 & 1], z[k], z[k + 1]);
                             top = fmaxf(t4[0], t4[1]);
                             tc_st32(ts + 32 * b, z);
+                        };
+                        float s[2][32];
+                        tc_ld32(s[0], ts);
+#pragma unroll 1
+                        for (int b = 0; b < 4; b += 2) {
+                            tc_wait_ld(s[0]);
+                            tc_ld32(s[1], ts + 32 * (b + 1));
+                            adjust(s[0], b);
+                            tc_wait_ld(s[1]);
+                            if (b == 0)
+                                tc_ld32(s[0], ts + 64);
+                            adjust(s[1], b + 1);
                         }
                         tc_wait_st();
                     }
