@@ -889,13 +889,14 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                         auto adjust = [&](float(&z)[32], int b) {
                             const float away = float(32 * b - hi);  // j - i of z[0]
                             if (a.softcap > 0.0f) {
-                                float most = 0.0f, least = 0.0f;
+                                float most = 0.0f;
 #pragma unroll
-                                for (int k = 0; k < 32; k += 2) {
-                                    most = max3(most, z[k], z[k + 1]);
-                                    least = min3(least, z[k], z[k + 1]);
+                                for (int k = 0; k < 16; ++k) {
+                                    const uint64_t x = pair_of(z[2 * k], z[2 * k + 1]);
+                                    const float2 u = halves_of(mul_pair(x, x));
+                                    most = max3(most, u.x, u.y);
                                 }
-                                const bool small = series_fits && fmaxf(most, -least) * inner <= 0.5f;
+                                const bool small = series_fits && most * inner * inner <= 0.25f;
                                 if (!__all_sync(0xffffffffu, small)) {
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
@@ -935,17 +936,12 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                             top = fmaxf(t4[0], t4[1]);
                             tc_st32(ts + 32 * b, z);
                         };
-                        float s[2][32];
-                        tc_ld32(s[0], ts);
+                        float s0[32];
 #pragma unroll 1
-                        for (int b = 0; b < 4; b += 2) {
-                            tc_wait_ld(s[0]);
-                            tc_ld32(s[1], ts + 32 * (b + 1));
-                            adjust(s[0], b);
-                            tc_wait_ld(s[1]);
-                            if (b == 0)
-                                tc_ld32(s[0], ts + 64);
-                            adjust(s[1], b + 1);
+                        for (int b = 0; b < 4; ++b) {
+                            tc_ld32(s0, ts + 32 * b);
+                            tc_wait_ld(s0);
+                            adjust(s0, b);
                         }
                         tc_wait_st();
                     }
