@@ -18,15 +18,11 @@
 // up to 8, up to 16, more.
 enum { kRows = 0, kMoreRows = 1, kTiles = 2, kKinds = 3 };
 
-// What joining the parts of a cut unit is worth in keys read, and what a unit costs beyond
-// its tiles (by bytes of K and V for the kernels of few rows, by tiles for the other).
-const int64_t kLeastBytes = 160 << 10, kUnitBytes = 128 << 10;
-const int kLeastTiles = 4, kUnitTiles = 2;
-
-struct Schedule {
-    int n_req = 0;
-    int ctas = 0;
-};
+// What a unit costs beyond its tiles, and what each part of one costs that is cut, measured:
+// in bytes of K and V read meanwhile for the kernels of few rows, in tiles for the other
+// (half as many where a cap on the scores makes tiles take twice as long).
+const int64_t kUnitBytes = 128 << 10, kPartBytes = 48 << 10;
+const int64_t kUnitTiles = 4, kPartTiles = 2;
 
 struct kvx_attn_plan {
     kvx_ctx *ctx = nullptr;
@@ -37,13 +33,14 @@ struct kvx_attn_plan {
     int capacity = 0;          // requests
     int n_req = 0;
     int64_t rows = 0;
-    Schedule kind[kKinds];
+    int ctas[kKinds] = {};     // of each kernel's launch
+    bool cut[kKinds] = {};     // whether it cuts units
     // Descriptors: [AttnStart of each kind][AttnReq of all, of each kind]; a pinned image, and
     // the device's copy.
     char *host = nullptr, *dev = nullptr;
     CUtensorMap *maps = nullptr;       // host: as pools, where the cache is copied by tensor copies
     int32_t box = 0;                   // keys per copy, 0: it is not
-    unsigned int *counters = nullptr;  // [2 * most_ctas()], zero between launches
+    unsigned int *counters = nullptr;  // [most_ctas()], zero between launches
     float *partial = nullptr;          // serves one kind's launch after the other
     cudaEvent_t copied = nullptr;      // the last update's copy
 
@@ -179,6 +176,7 @@ struct Kernel {
     int threads, ctas_per_sm;
     size_t smem;
     int slot_floats;
+    const void *join;  // of the parts of cut units, or NULL: the kernel joins them itself
 };
 
 template <int TYPE, int KV, int D>
@@ -187,13 +185,14 @@ Kernel kernel_of(int kind)
     if (kind == kRows)
         return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D, 1>),
                 kRowThreads, row_ctas_per_sm<KV, D, 1>(), row_smem<KV, D, 1>(),
-                row_slot_floats<D, 1>()};
+                row_slot_floats<D, 1>(), nullptr};
     if (kind == kMoreRows)
         return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D, 2>),
                 kRowThreads, row_ctas_per_sm<KV, D, 2>(), row_smem<KV, D, 2>(),
-                row_slot_floats<D, 2>()};
+                row_slot_floats<D, 2>(), nullptr};
     return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KV, D>), kTileThreads, 1,
-            size_t(TileShape<KV, D>::kBytes), TileShape<KV, D>::kSlotFloats};
+            size_t(TileShape<KV, D>::kBytes), TileShape<KV, D>::kSlotFloats,
+            reinterpret_cast<const void *>(kvx_attend_join_kernel<TYPE, D>)};
 }
 
 Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
@@ -208,87 +207,127 @@ Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
 }
 
 // Lay the units of one kind end to end and give every CTA its share (struct Work).  Shares
-// are equal in tiles plus `extra` per unit, for what a unit costs besides its tiles.  No share
-// is below `least` tiles on average and no unit is cut closer than that to its ends: joining
-// parts costs about as much as reading so many tiles.
-void schedule(kvx_attn_plan *p, int kind, const AttnReq *reqs, int n_req)
-{
-    const int group = p->cfg.q_heads / p->cfg.kv_heads, heads = p->cfg.kv_heads;
-    const int T = kind == kTiles ? kTileKeys : kRowTile;
-    const int block_rows = kind == kTiles ? kBlockRows : kRowMax;
-    const int64_t tile_bytes = 2 * int64_t(T) * p->cfg.head_dim * kvx::type_bytes(p->cfg.kv_type);
-    const int least = kind == kTiles ? kLeastTiles
-                                     : int(std::max<int64_t>(1, kLeastBytes / tile_bytes));
-    const int extra = kind == kTiles ? kUnitTiles
-                                     : int(std::max<int64_t>(1, kUnitBytes / tile_bytes));
-    auto blocks = [&](const AttnReq &r) {
+// are equal in tiles plus what a unit costs besides them.  Whether units are cut at all is
+// decided by an estimate of the slowest CTA's time: cutting evens the shares out, but each
+// part of a cut unit has to be written, and joined by one of its CTAs.
+struct Scheduler {
+    const kvx_attn_plan *p;
+    const AttnReq *reqs;
+    int n_req, kind, group, heads, block_rows, tile_keys;
+    int64_t unit_cost, part_cost;   // beyond the tiles, in tiles
+
+    Scheduler(const kvx_attn_plan *p_, int kind_, const AttnReq *reqs_, int n)
+        : p(p_), reqs(reqs_), n_req(n), kind(kind_), group(p_->cfg.q_heads / p_->cfg.kv_heads),
+          heads(p_->cfg.kv_heads), block_rows(kind_ == kTiles ? kBlockRows : kRowMax),
+          tile_keys(kind_ == kTiles ? kTileKeys : kRowTile)
+    {
+        if (kind == kTiles) {
+            const bool plain = p->cfg.softcap == 0.0f;
+            unit_cost = plain ? kUnitTiles : kUnitTiles / 2;
+            part_cost = plain ? kPartTiles : kPartTiles / 2;
+        } else {
+            const int64_t tile_bytes =
+                2 * int64_t(tile_keys) * p->cfg.head_dim * kvx::type_bytes(p->cfg.kv_type);
+            unit_cost = std::max<int64_t>(1, kUnitBytes / tile_bytes);
+            part_cost = std::max<int64_t>(1, kPartBytes / tile_bytes);
+        }
+    }
+    int blocks(const AttnReq &r) const
+    {
         return int((int64_t(r.n_new) * group + block_rows - 1) / block_rows);
-    };
-    auto tiles_of = [&](const AttnReq &r, int block) {
+    }
+    int tiles_of(const AttnReq &r, int block) const
+    {
         const int64_t row0 = int64_t(block) * block_rows;
         const int64_t row1 = std::min<int64_t>(row0 + block_rows, int64_t(r.n_new) * group) - 1;
         const int pmin = r.n_tokens - r.n_new + int(row0 / group);
         const int pmax = r.n_tokens - r.n_new + int(row1 / group);
         int first, skip, tiles;
         kvx::key_tiles(r.prefix, p->cfg.window ? std::max(0, pmin - p->cfg.window + 1) : 0,
-                       pmax + 1, T, &first, &skip, &tiles);
+                       pmax + 1, tile_keys, &first, &skip, &tiles);
         return tiles;
-    };
-    int64_t tiles = 0, cost = 0;
-    for (int r = 0; r < n_req; ++r)
-        for (int b = 0, n = blocks(reqs[r]); b < n; ++b) {
-            const int t = tiles_of(reqs[r], b);
-            tiles += int64_t(t) * heads;
-            cost += int64_t(t + extra) * heads;
-        }
-    Schedule &s = p->kind[kind];
-    s.n_req = n_req;
-    s.ctas = 0;
-    if (tiles == 0)
-        return;
-    const int64_t slots = int64_t(p->ctx->num_sms) * pick_kernel(p->cfg, kind).ctas_per_sm;
-    const int64_t shares = std::min(slots, std::max<int64_t>(1, tiles / least));
-    kvx::AttnStart *out = reinterpret_cast<kvx::AttnStart *>(p->host + p->starts_at(kind));
-    int64_t at = 0, line = 0;     // of the unit, in cost and in tiles
-    int64_t share = 0;            // shares begun
-    int64_t begun = 0;            // line position where the last of them begins
-    bool carry = false;           // one begins with the next unit
-    auto place = [&](int r, int b, int h, int tile, int first) {
-        if (s.ctas > 0)
-            out[s.ctas - 1].tiles = line + tile - begun;
-        begun = line + tile;
-        out[s.ctas++] = {r, b, h, tile, first, 0, 0};
-    };
-    for (int r = 0; r < n_req; ++r)
-        for (int b = 0, n = blocks(reqs[r]); b < n; ++b) {
-            const int t = tiles_of(reqs[r], b);
-            for (int h = 0; h < heads; ++h) {
-                // Shares whose boundary falls on this unit: at its start, inside, at its end.
-                auto boundary = [&] { return share * cost / shares - at - extra; };
-                int first = s.ctas - 1, cut = 0;
-                bool start = carry;
-                for (carry = false; share < shares && boundary() < least; ++share)
-                    start = true;
-                if (start) {
-                    first = s.ctas;
-                    place(r, b, h, 0, first);
-                }
-                for (; share < shares && boundary() < t; ++share) {
-                    if (t - boundary() < least) {
-                        carry = true;
-                    } else if (boundary() > cut) {
-                        cut = int(boundary());
-                        place(r, b, h, cut, first);
+    }
+
+    // Place the shares, cutting no unit closer than `least` tiles to its ends; into `out`, if
+    // not NULL.  Returns the CTAs, and the slowest one's time in *slowest.
+    int place(int64_t shares, int64_t total, int64_t least, kvx::AttnStart *out,
+              int64_t *slowest) const
+    {
+        int64_t at = 0, line = 0;     // of the unit, in cost and in tiles
+        int64_t share = 0;            // shares begun
+        int64_t begun = 0, load = 0;  // line position where the last of them begins, its time
+        int ctas = 0;
+        bool carry = false;           // one begins with the next unit
+        *slowest = 0;
+        auto start = [&](int r, int b, int h, int64_t tile, int first) {
+            if (ctas > 0 && out)
+                out[ctas - 1].tiles = line + tile - begun;
+            begun = line + tile;
+            if (out)
+                out[ctas] = {r, b, h, int32_t(tile), first, 0, 0};
+            ++ctas;
+            *slowest = std::max(*slowest, load);
+            load = 0;
+        };
+        for (int r = 0; r < n_req; ++r)
+            for (int b = 0, n = blocks(reqs[r]); b < n; ++b) {
+                const int64_t t = tiles_of(reqs[r], b);
+                for (int h = 0; h < heads; ++h) {
+                    // Shares whose boundary falls on this unit: at its start, inside, at its end.
+                    auto boundary = [&] { return share * total / shares - at - unit_cost; };
+                    int first = ctas - 1;
+                    int64_t cut = 0;
+                    bool begin = carry;
+                    for (carry = false; share < shares && boundary() < std::min(least, t); ++share)
+                        begin = true;
+                    if (begin) {
+                        first = ctas;
+                        start(r, b, h, 0, first);
                     }
+                    for (; share < shares && boundary() < t; ++share) {
+                        if (t - boundary() < least) {
+                            carry = true;
+                        } else if (boundary() > cut) {
+                            load += boundary() - cut + unit_cost + part_cost;
+                            cut = boundary();
+                            start(r, b, h, cut, first);
+                        }
+                    }
+                    load += t - cut + unit_cost + (cut ? part_cost : 0);
+                    if (out)
+                        for (int c = first; c < ctas - 1; ++c)
+                            out[c].last = ctas - 1;
+                    at += t + unit_cost;
+                    line += t;
                 }
-                for (int c = first; c < s.ctas - 1; ++c)
-                    out[c].last = s.ctas - 1;
-                at += t + extra;
-                line += t;
             }
-        }
-    out[s.ctas - 1].tiles = line - begun;
-}
+        *slowest = std::max(*slowest, load);
+        if (out)
+            out[ctas - 1].tiles = line - begun;
+        return ctas;
+    }
+
+    int run(kvx::AttnStart *out) const
+    {
+        int64_t tiles = 0, total = 0;
+        for (int r = 0; r < n_req; ++r)
+            for (int b = 0, n = blocks(reqs[r]); b < n; ++b) {
+                const int64_t t = tiles_of(reqs[r], b);
+                tiles += t * heads;
+                total += (t + unit_cost) * heads;
+            }
+        if (tiles == 0)
+            return 0;
+        const int64_t slots = int64_t(p->ctx->num_sms) * pick_kernel(p->cfg, kind).ctas_per_sm;
+        const int64_t least = 2 * part_cost, whole = INT32_MAX;
+        const int64_t shares = std::min(slots, std::max<int64_t>(1, tiles / least));
+        int64_t cut_time, whole_time;
+        place(shares, total, least, nullptr, &cut_time);
+        place(slots, total, whole, nullptr, &whole_time);
+        return whole_time <= cut_time ? place(slots, total, whole, out, &whole_time)
+                                      : place(shares, total, least, out, &cut_time);
+    }
+};
 
 kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const int32_t *n_new,
                      const int32_t *prefix, cudaStream_t s)
@@ -316,8 +355,13 @@ kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const
     }
     p->n_req = n_req;
     p->rows = rows;
-    for (int k = 0; k < kKinds; ++k)
-        schedule(p, k, lists[k], counts[k]);
+    for (int k = 0; k < kKinds; ++k) {
+        kvx::AttnStart *starts = reinterpret_cast<kvx::AttnStart *>(p->host + p->starts_at(k));
+        p->ctas[k] = Scheduler(p, k, lists[k], counts[k]).run(starts);
+        p->cut[k] = false;
+        for (int c = 0; c < p->ctas[k]; ++c)
+            p->cut[k] |= starts[c].tile > 0;
+    }
     if (n_req) {
         e = cudaMemcpyAsync(p->dev, p->host, p->bytes(), cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess)
@@ -373,11 +417,11 @@ kvx_status make_maps(kvx_attn_plan *p)
 
 // A launch that may start while the kernel ahead of it on the stream drains; the kernels
 // themselves wait for that one's completion before they touch memory.
-cudaError_t launch_early(const void *fn, int64_t ctas, int threads, size_t smem, cudaStream_t s,
+cudaError_t launch_early(const void *fn, dim3 ctas, int threads, size_t smem, cudaStream_t s,
                          void **args)
 {
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(unsigned(ctas));
+    lc.gridDim = ctas;
     lc.blockDim = dim3(unsigned(threads));
     lc.dynamicSmemBytes = smem;
     lc.stream = s;
@@ -471,7 +515,7 @@ kvx_status kvx_attn_plan_create(kvx_ctx *ctx, const kvx_pool *pool, const kvx_re
         e = cudaMalloc(reinterpret_cast<void **>(&p->dev), p->bytes());
     if (e == cudaSuccess)
         e = cudaMalloc(reinterpret_cast<void **>(&p->partial), partial);
-    const size_t counters = 2 * size_t(p->most_ctas()) * sizeof(unsigned int);
+    const size_t counters = size_t(p->most_ctas()) * sizeof(unsigned int);
     if (e == cudaSuccess)
         e = cudaMalloc(reinterpret_cast<void **>(&p->counters), counters);
     if (e == cudaSuccess)
@@ -573,7 +617,7 @@ kvx_status kvx_append_tokens(const kvx_attn_plan *p, int layer, const void *k, c
             : reinterpret_cast<const void *>(
                   kvx_append_kernel<KVX_TYPE_BFLOAT, KVX_TYPE_FP_EIGHT>);
     void *args[] = {&a};
-    const cudaError_t e = launch_early(fn, (2 * p->rows + 7) / 8, 256, 0,
+    const cudaError_t e = launch_early(fn, dim3(unsigned((2 * p->rows + 7) / 8)), 256, 0,
                                        reinterpret_cast<cudaStream_t>(stream), args);
     return e == cudaSuccess ? KVX_OK : kvx::cuda_err(p->ctx, e, "append launch");
 }
@@ -606,8 +650,7 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
                       p->cfg.q_heads / p->cfg.kv_heads, p->cfg.window, p->page_size, p->num_pages,
                       Divisor::of(p->page_size), p->box, p->cfg.scale * k_scale, p->cfg.softcap, v_scale};
     for (int k = 0; k < kKinds; ++k) {
-        const Schedule &s = p->kind[k];
-        if (s.ctas == 0)
+        if (p->ctas[k] == 0)
             continue;
         const Kernel kn = pick_kernel(p->cfg, k);
         const Work w = {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(k)),
@@ -618,8 +661,12 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
                                 p->box ? p->maps + 2 * layer + 1 : &none};
         // The kernels of few rows take the first two.
         void *args[] = {const_cast<Attend *>(&a), const_cast<Work *>(&w), maps[0], maps[1]};
-        const cudaError_t e = launch_early(kn.fn, s.ctas, kn.threads, kn.smem,
-                                           reinterpret_cast<cudaStream_t>(stream), args);
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        cudaError_t e = launch_early(kn.fn, dim3(unsigned(p->ctas[k])), kn.threads, kn.smem, s,
+                                     args);
+        if (e == cudaSuccess && kn.join && p->cut[k])
+            e = launch_early(kn.join, dim3(unsigned(p->ctas[k] - 1), kBlockRows / kJoinRows),
+                             kJoinThreads, 0, s, args);
         if (e != cudaSuccess)
             return kvx::cuda_err(p->ctx, e, "attention launch");
     }

@@ -64,7 +64,7 @@ struct Attend {
 struct Work {
     const AttnReq *reqs;       // of this kernel, those with rows
     const AttnStart *starts;   // [CTAs]
-    unsigned int *counters;    // [2 * CTAs]: arrivals at the unit a CTA began, zero between launches
+    unsigned int *counters;    // [CTAs]: arrivals at the unit a CTA began, zero between launches
     float *partial;
 };
 

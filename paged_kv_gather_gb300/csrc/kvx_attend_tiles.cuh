@@ -41,7 +41,7 @@ struct TileShape {
     static const int kOffStage = kOffRing + kSlots * kTile;  // e4m3: [2][kTile / 2]
     static const int kOffKeys = kOffStage + kEight * kTile;  // int64 [2][kTileKeys]
     static const int kOffBars = kOffKeys + 2 * kTileKeys * 8;
-    static const int kOffMisc = kOffBars + 8 * 34;              // int[4]
+    static const int kOffMisc = kOffBars + 8 * 32;              // int[2]
     static const int kBytes = kOffMisc + 16;
     static const int kSlotFloats = kBlockRows * (D + 2);     // a partial result: O, m, l
 };
@@ -53,12 +53,11 @@ enum {
     kBarP = 4,      // P of the first 64 keys is in tensor memory
     kBarP2 = 6,     // and of the others
     kBarO = 8,      // O is complete
-    kBarJoin = 10,  // the threads of the tile among themselves
-    kBarKeys = 12,  // the loaders among themselves
-    kBarFull = 13,
-    kBarEmpty = 23,
-    kBarEnd = 33,
-    kBars = 34
+    kBarKeys = 10,  // the loaders among themselves
+    kBarFull = 11,
+    kBarEmpty = 21,
+    kBarEnd = 31,
+    kBars = 32
 };
 
 __device__ __forceinline__ void mbar_init(unsigned bar, unsigned count)
@@ -413,7 +412,6 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
     int *misc = reinterpret_cast<int *>(smem + T::kOffMisc);
     int &gave_up = misc[0];
     unsigned &tmem_base = reinterpret_cast<unsigned &>(misc[1]);
-    int *last_cta = misc + 2;
     const unsigned sm = smem_u32(smem);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     auto bar = [&](int i) { return sm + T::kOffBars + 8 * i; };
@@ -429,7 +427,6 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         gave_up = 0;
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(kBarQ + x), kTileRows);
-            mbar_init(bar(kBarJoin + x), kTileRows);
             mbar_init(bar(kBarS + x), 1);
             mbar_init(bar(kBarP + x), kTileRows);
             mbar_init(bar(kBarP2 + x), kTileRows);
@@ -1043,11 +1040,9 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             };
             // A part: [D / 4][256 rows][4] of O, then [256][m, l].
             const int prow = x * kTileRows + row;
-            auto part = [&](int c) {
-                return w.partial + (2 * int64_t(c) + (c == c0)) * T::kSlotFloats;
-            };
             if (mine) {
-                float *slot = part(blockIdx.x);
+                float *slot = w.partial +
+                              (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) * T::kSlotFloats;
 #pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
                     float o[32];
@@ -1067,67 +1062,90 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 else if (have)
                     *reinterpret_cast<float2 *>(slot + kBlockRows * D + 2 * prow) = make_float2(m, l);
             }
-            if (mine && c0 != c1) {
-                // The last CTA to arrive joins the tile's parts, in order.
-                __threadfence();
-                mbar_arrive(bar(kBarJoin + x));
-                if (!(ok = wait(kBarJoin + x, 0)))
-                    break;
-                if (row == 0) {
-                    unsigned *counter = w.counters + 2 * c0 + x;
-                    const unsigned n = atomicAdd(counter, 1);
-                    last_cta[x] = n == unsigned(c1 - c0);
-                    if (n == unsigned(c1 - c0))
-                        *counter = 0;
-                    __threadfence();
-                }
-                mbar_arrive(bar(kBarJoin + x));
-                if (!(ok = wait(kBarJoin + x, 1)))
-                    break;
-                if (last_cta[x]) {
-                    float mm = -INFINITY, ll = 0.0f;
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c)
-                        mm = fmaxf(mm, __ldcg(part(c) + kBlockRows * D + 2 * prow));
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        const float2 p = __ldcg(reinterpret_cast<const float2 *>(
-                            part(c) + kBlockRows * D + 2 * prow));
-                        ll += p.x == -INFINITY ? 0.0f : exp2_(p.x - mm) * p.y;
-                    }
-#pragma unroll 1
-                    for (int b = 0; b < D / 32; ++b) {
-                        float o[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            o[k] = 0.0f;
-#pragma unroll 2
-                        for (int c = c0; c <= c1; ++c) {
-                            float4 v[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                v[k] = __ldcg(reinterpret_cast<const float4 *>(
-                                    part(c) + ((8 * b + k) * kBlockRows + prow) * 4));
-                            const float pm = __ldcg(part(c) + kBlockRows * D + 2 * prow);
-                            const float f = pm == -INFINITY ? 0.0f : exp2_(pm - mm);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                o[4 * k] += f * v[k].x;
-                                o[4 * k + 1] += f * v[k].y;
-                                o[4 * k + 2] += f * v[k].z;
-                                o[4 * k + 3] += f * v[k].w;
-                            }
-                        }
-                        put(b, o, ll);
-                    }
-                    flush(mm, ll);
-                }
-            }
         }
     }
     __syncthreads();
     if (warp == 8)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// The results of units that were cut: block (c, slice) joins, in order, the parts of the unit
+// that CTA c began and did not end, for 32 of its rows.  A launch of its own puts every SM to
+// this, where the last CTA of a unit would have read up to 150 parts of 128 KB alone (65 us
+// against 37 for 64 new tokens behind 32k), and spares all of them a fence and a counter.
+const int kJoinThreads = 256;
+const int kJoinRows = 32;
+
+template <int TYPE, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+kvx_attend_join_kernel(const Attend a, const Work w)
+{
+    typedef Elem<TYPE> E;
+    constexpr int kSlotFloats = kBlockRows * (D + 2);
+    __shared__ uint2 out[kJoinRows][D / 4 + 1];
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const AttnStart next = w.starts[c0 + 1];
+    const int c1 = w.starts[c0].last;
+    wait_for_earlier_work();
+    if (next.tile == 0 || next.first != c0)
+        return;
+    const AttnReq r = w.reqs[next.request];
+    const int row0 = next.block * kBlockRows, rows = min(kBlockRows, r.n_new * a.group - row0);
+    const int row = blockIdx.y * kJoinRows + lane;
+    if (int(blockIdx.y) * kJoinRows >= rows)
+        return;
+    auto part = [&](int c) { return w.partial + (2 * int64_t(c) + (c == c0)) * kSlotFloats; };
+    auto ml = [&](int c) {
+        return __ldcg(reinterpret_cast<const float2 *>(part(c) + kBlockRows * D) + row);
+    };
+    float mm = -INFINITY, ll = 0.0f;
+    float4 o[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+        o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (row < rows) {
+#pragma unroll 8
+        for (int c = c0; c <= c1; ++c)
+            mm = fmaxf(mm, ml(c).x);
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            float4 v[D / 32];
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+                v[k] = __ldcg(reinterpret_cast<const float4 *>(part(c)) +
+                              (8 * k + warp) * kBlockRows + row);
+            const float2 p = ml(c);
+            const float f = p.x == -INFINITY ? 0.0f : exp2_(p.x - mm);
+            ll += f * p.y;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                o[k].x += f * v[k].x;
+                o[k].y += f * v[k].y;
+                o[k].z += f * v[k].z;
+                o[k].w += f * v[k].w;
+            }
+        }
+        const float f = a.v_scale / ll;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+            out[lane][8 * k + warp] =
+                make_uint2(E::pack(o[k].x * f, o[k].y * f), E::pack(o[k].z * f, o[k].w * f));
+    }
+    __syncthreads();
+    // Whole rows, 8 bytes to a lane.
+    for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
+        const int sub = i / (D / 4), d = i % (D / 4), packed = row0 + blockIdx.y * kJoinRows + sub;
+        if (blockIdx.y * kJoinRows + sub < rows) {
+            const int tok = packed / a.group, head = next.head * a.group + packed - tok * a.group;
+            reinterpret_cast<uint2 *>(a.out + (r.row_begin + tok) * a.out_stride +
+                                      head * (D * 2))[d] = out[sub][d];
+        }
+    }
+    if (a.lse && warp == 0 && row < rows) {
+        const int packed = row0 + row, tok = packed / a.group;
+        a.lse[int64_t(r.row_begin + tok) * a.q_heads + next.head * a.group + packed -
+              tok * a.group] = mm * kLn2 + logf(ll);
+    }
 }
 
 }  // namespace
