@@ -264,7 +264,7 @@ struct Scheduler {
                 out[ctas - 1].tiles = line + tile - begun;
             begun = line + tile;
             if (out)
-                out[ctas] = {r, b, h, int32_t(tile), first, 0, 0};
+                out[ctas] = {r, b, h, int32_t(tile), first, 0, 0, reqs[r]};
             ++ctas;
             *slowest = std::max(*slowest, load);
             load = 0;
@@ -307,7 +307,9 @@ struct Scheduler {
         return ctas;
     }
 
-    int run(kvx::AttnStart *out) const
+    // Lay out the shares into `out`, if not NULL; returns the CTAs and the slowest one's time
+    // in tiles.
+    int run(kvx::AttnStart *out, int64_t *time) const
     {
         int64_t tiles = 0, total = 0;
         for (int r = 0; r < n_req; ++r)
@@ -316,6 +318,7 @@ struct Scheduler {
                 tiles += t * heads;
                 total += (t + unit_cost) * heads;
             }
+        *time = 0;
         if (tiles == 0)
             return 0;
         const int64_t slots = int64_t(p->ctx->num_sms) * pick_kernel(p->cfg, kind).ctas_per_sm;
@@ -324,8 +327,8 @@ struct Scheduler {
         int64_t cut_time, whole_time;
         place(shares, total, least, nullptr, &cut_time);
         place(slots, total, whole, nullptr, &whole_time);
-        return whole_time <= cut_time ? place(slots, total, whole, out, &whole_time)
-                                      : place(shares, total, least, out, &cut_time);
+        return whole_time <= cut_time ? place(slots, total, whole, out, time)
+                                      : place(shares, total, least, out, time);
     }
 };
 
@@ -355,9 +358,25 @@ kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const
     }
     p->n_req = n_req;
     p->rows = rows;
+    // Few requests of few rows beside chunks go with the chunks, if that costs less than the
+    // launch they would otherwise have (about three tiles' time).
+    const int few = counts[kRows] + counts[kMoreRows];
+    if (few > 0 && counts[kTiles] > 0) {
+        AttnReq *all = lists[kTiles] + counts[kTiles];
+        std::copy(lists[kRows], lists[kRows] + counts[kRows], all);
+        std::copy(lists[kMoreRows], lists[kMoreRows] + counts[kMoreRows], all + counts[kRows]);
+        int64_t alone, together;
+        Scheduler(p, kTiles, lists[kTiles], counts[kTiles]).run(nullptr, &alone);
+        Scheduler(p, kTiles, lists[kTiles], counts[kTiles] + few).run(nullptr, &together);
+        if (together <= alone + 3) {
+            counts[kTiles] += few;
+            counts[kRows] = counts[kMoreRows] = 0;
+        }
+    }
     for (int k = 0; k < kKinds; ++k) {
         kvx::AttnStart *starts = reinterpret_cast<kvx::AttnStart *>(p->host + p->starts_at(k));
-        p->ctas[k] = Scheduler(p, k, lists[k], counts[k]).run(starts);
+        int64_t time;
+        p->ctas[k] = Scheduler(p, k, lists[k], counts[k]).run(starts, &time);
         p->cut[k] = false;
         for (int c = 0; c < p->ctas[k]; ++c)
             p->cut[k] |= starts[c].tile > 0;

@@ -69,8 +69,9 @@ struct Work {
 };
 
 // Kernels here start while the one before them on the stream ends (programmatic dependent
-// launch): they touch memory only past this wait for its completion, and let the next one
-// start in the same way.
+// launch).  Before this wait for its completion they touch nothing but the plan's descriptors,
+// which only copies write, and no kernel starts early behind a copy; after it they let the
+// next kernel start in the same way.
 __device__ __forceinline__ void wait_for_earlier_work()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -177,10 +177,10 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
     const Score score(a);
     const bool plain = !(a.softcap > 0.0f) && !a.slopes;
 
-    wait_for_earlier_work();
     AttnStart at = w.starts[blockIdx.x];
+    wait_for_earlier_work();
     while (at.tiles > 0) {
-        const AttnReq r = w.reqs[at.request];
+        const AttnReq r = at.req;
         Keys keys;
         keys.set<kRowTile>(r, a.window, 0, r.n_new - 1);
         const int rows = r.n_new * a.group;
@@ -563,6 +563,8 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
         if (++at.head == a.kv_heads) {
             at.head = 0;
             ++at.request;
+            if (at.tiles > 0)
+                at.req = w.reqs[at.request];
         }
     }
 }

@@ -349,9 +349,9 @@ struct Walk {
     Keys keys;
     int row0, rows, todo;   // of the block; tiles of keys to do
 
-    __device__ __forceinline__ Walk(const Attend &a_, const Work &w_) : a(a_), w(w_)
+    __device__ __forceinline__ Walk(const Attend &a_, const Work &w_, const AttnStart &at_)
+        : a(a_), w(w_), at(at_)
     {
-        at = w.starts[blockIdx.x];
         if (!done())
             enter();
     }
@@ -374,7 +374,7 @@ struct Walk {
     }
     __device__ __forceinline__ void enter()
     {
-        r = w.reqs[at.request];
+        r = at.req;
         const int all = r.n_new * a.group;
         row0 = at.block * kBlockRows;
         rows = min(kBlockRows, all - row0);
@@ -391,7 +391,7 @@ struct Walk {
             at.head = 0;
             if ((++at.block) * kBlockRows >= r.n_new * a.group) {
                 at.block = 0;
-                ++at.request;
+                at.req = w.reqs[++at.request];
             }
         }
         enter();
@@ -444,6 +444,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const unsigned tmem = tmem_base;
+    const AttnStart begin = w.starts[blockIdx.x];
     wait_for_earlier_work();
 
     if (warp == 8) {
@@ -478,7 +479,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                     turn ^= 1;
                 }
             };
-            for (Walk u(a, w); ok && !u.done(); u.next()) {
+            for (Walk u(a, w, begin); ok && !u.done(); u.next()) {
                 const int tiles = u.rows > kTileRows ? 2 : 1;
                 for (int x = 0; ok && x < tiles; ++x) {
                     ok = wait1(kBarQ + x, q_phase[x]);
@@ -615,7 +616,15 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             announce();
             advance();
         };
-        for (Walk u(a, w); ok && !u.done(); u.next()) {
+        for (Walk u(a, w, begin); ok && !u.done(); u.next()) {
+            // The loaders are ahead of the warps that will read this unit's rows of q.
+            for (int i = lt; i < u.rows * (D / 64); i += kLoaders) {
+                const int packed = u.row0 + i / (D / 64), tok = packed / a.group;
+                const char *q = a.q + int64_t(u.r.row_begin + tok) * a.q_stride +
+                                (u.at.head * a.group + packed - tok * a.group) * (D * 2) +
+                                i % (D / 64) * 128;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+            }
             const int64_t head_at = int64_t(u.at.head) * kRow;
             // A lane per tensor copy of a tile: run of keys `lane / kPerTile` and 64-element
             // block of the head `lane % kPerTile`; its page is looked up a tile ahead.
@@ -751,7 +760,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         const int warp_row = row & ~31;
         unsigned s_phase = 0, o_phase = 0;
         bool ok = true;
-        for (Walk u(a, w); ok && !u.done(); u.next()) {
+        for (Walk u(a, w, begin); ok && !u.done(); u.next()) {
             const bool mine = x == 0 || u.rows > kTileRows;  // the tile has rows
             const bool have = x * kTileRows + row < u.rows;
             const int packed = u.row0 + (have ? x * kTileRows + row : 0);
@@ -1089,7 +1098,7 @@ kvx_attend_join_kernel(const Attend a, const Work w)
     wait_for_earlier_work();
     if (next.tile == 0 || next.first != c0)
         return;
-    const AttnReq r = w.reqs[next.request];
+    const AttnReq &r = next.req;
     const int row0 = next.block * kBlockRows, rows = min(kBlockRows, r.n_new * a.group - row0);
     const int row = blockIdx.y * kJoinRows + lane;
     if (int(blockIdx.y) * kJoinRows >= rows)

@@ -71,8 +71,9 @@ struct AttnStart {
     int32_t first;    // CTA that began the unit, if tile > 0
     int32_t last;     // CTA that ends the unit this share stops inside of, if it does
     int64_t tiles;
+    AttnReq req;      // of `request`: one load instead of two in a row
 };
-static_assert(sizeof(AttnStart) == 32, "descriptor layout");
+static_assert(sizeof(AttnStart) == 64, "descriptor layout");
 
 // Tiles of T keys that cover [0, prefix) and [low, end), in order: `first` tiles from key 0,
 // then the rest `skip` tiles further on; no tile twice.
