@@ -27,12 +27,16 @@ namespace {
 // Descriptors up to this size travel as a kernel parameter (the parameter space of a launch
 // was 4 KB before CUDA 12.1 and a call stays within it); larger batches take a descriptor slot.
 const int kInlineBytes = 3840;
-const int kThreads = 1024;
+// 12 warps of a CTA copy, 4 see to tables: 24 KiB of loads in flight per SM and 8 KiB to a
+// job carry copies of whole requests at the rate of a device copy (6.77 TB/s); with 28 or 14
+// warps, or 16 KiB jobs, they reached 91-96 % of it.
+const int kThreads = 512;
 const int kWarps = kThreads / 32;
 const int kGranWords = 8;                // bitmap words per granule
 const int kGranPages = 32 * kGranWords;  // pages per granule: one warp scans one at a time
 const int kTableWarps = 4;               // of a CTA that also copies
-const int kUnits = 8;                    // 16-byte loads in flight per lane
+const int64_t kSliceBytes = 8192;        // of a warp's job where there are many
+const int kUnits = 8;                    // 16-byte loads in flight per lane, or half as many of 32
 
 struct Inline {
     uint4 bytes[kInlineBytes / 16];
@@ -40,6 +44,7 @@ struct Inline {
 
 struct Args {
     const char *ext;         // descriptors in device memory, or NULL: in the Inline parameter
+    int32_t inline_bytes;    // of them there
     int32_t *refs;
     unsigned int *status;
     unsigned int *counter;   // CTAs that have finished scanning
@@ -53,6 +58,7 @@ struct Args {
     int32_t page_size;
     int32_t num_pages;
     int32_t slices;          // jobs per (page, slab)
+    int32_t wide;            // everything that is copied is 32-byte aligned
     int32_t table_warps;     // of each CTA, for tables; the others copy
 };
 
@@ -70,6 +76,17 @@ __device__ __forceinline__ void wait_for_earlier_work()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The call's descriptors where searching them is cheap: inline ones are brought into shared
+// memory (at `to`; the caller's next barrier ends it).
+__device__ __forceinline__ const char *descriptors(const Args &a, const Inline &in, char *to)
+{
+    if (a.ext)
+        return a.ext;
+    for (int i = threadIdx.x; i < a.inline_bytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(to)[i] = in.bytes[i];
+    return to;
 }
 
 // The bitmap of one kind of page (free or live) with running totals per granule.
@@ -155,7 +172,7 @@ __device__ Bits scan_pages(const Args &a, bool live, int enough, unsigned *smem)
         if (lane == 0)
             round_count[warp] = n;
         __syncthreads();
-        const int c = round_count[lane];
+        const int c = lane < kWarps ? round_count[lane] : 0;
         int incl = c;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -163,7 +180,7 @@ __device__ Bits scan_pages(const Args &a, bool live, int enough, unsigned *smem)
             if (lane >= d)
                 incl += x;
         }
-        if (warp == 0 && g0 + lane <= all)
+        if (warp == 0 && lane < kWarps && g0 + lane <= all)
             b.before[g0 + lane] = found + incl - c;
         found += __shfl_sync(0xffffffffu, incl, 31);
         __syncthreads();
@@ -199,6 +216,49 @@ __device__ __forceinline__ int find_entry(const E *entries, int n, int i, F begi
             hi = mid;
     }
     return lo;
+}
+
+struct V32 {
+    unsigned r[8];
+};
+
+__device__ __forceinline__ V32 ld_32(const V32 *p)
+{
+    V32 v;
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.r[0]), "=r"(v.r[1]), "=r"(v.r[2]), "=r"(v.r[3]), "=r"(v.r[4]),
+                   "=r"(v.r[5]), "=r"(v.r[6]), "=r"(v.r[7])
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void st_32(V32 *p, const V32 &v)
+{
+    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                 "r"(v.r[0]), "r"(v.r[1]), "r"(v.r[2]), "r"(v.r[3]), "r"(v.r[4]), "r"(v.r[5]),
+                 "r"(v.r[6]), "r"(v.r[7])
+                 : "memory");
+}
+
+// One warp copies `bytes` (a multiple of 32, addresses too) with kUnits / 2 32-byte loads in
+// flight per lane.
+__device__ __forceinline__ void warp_copy_32(const char *src, char *dst, int64_t bytes, int lane)
+{
+    const int kN = kUnits / 2;
+    const V32 *s = reinterpret_cast<const V32 *>(src) + lane;
+    V32 *d = reinterpret_cast<V32 *>(dst) + lane;
+    int64_t rem = bytes / 32 - lane;
+    for (; rem > 0; rem -= 32 * kN, s += 32 * kN, d += 32 * kN) {
+        V32 r[kN];
+#pragma unroll
+        for (int u = 0; u < kN; ++u)
+            if (32 * u < rem)
+                r[u] = ld_32(s + 32 * u);
+#pragma unroll
+        for (int u = 0; u < kN; ++u)
+            if (32 * u < rem)
+                st_32(d + 32 * u, r[u]);
+    }
 }
 
 // One warp copies `bytes` (a multiple of 16) with kUnits 16-byte loads in flight per lane.
@@ -239,18 +299,23 @@ __device__ __forceinline__ void copy_slice(const Args &a, const char *desc, int 
     char *base = reinterpret_cast<char *const *>(desc)[slab];
     const int64_t page = int64_t(a.page_size) * a.token_bytes;
     const int64_t n = bytes - at < a.slice ? bytes - at : a.slice;
-    warp_copy(base + from * page + at, base + to * page + at, n, lane);
+    if (a.wide)
+        warp_copy_32(base + from * page + at, base + to * page + at, n, lane);
+    else
+        warp_copy(base + from * page + at, base + to * page + at, n, lane);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
 kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
 {
     extern __shared__ unsigned smem[];
-    const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
-    const ForkEntry *e = reinterpret_cast<const ForkEntry *>(desc + a.off_entries);
-    const ForkEntry &end = e[a.n_entries];
-    const int lane = threadIdx.x & 31;
     __shared__ int last;
+    __shared__ Inline staged;
+    const char *desc = descriptors(a, in, reinterpret_cast<char *>(&staged));
+    const ForkEntry *e = reinterpret_cast<const ForkEntry *>(desc + a.off_entries);
+    const int lane = threadIdx.x & 31;
+    __syncthreads();
+    const ForkEntry end = e[a.n_entries];
     wait_for_earlier_work();
     const Bits free = scan_pages(a, false, end.fresh_begin, smem);
     if (threadIdx.x == 0)
@@ -325,8 +390,10 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
 __global__ void __launch_bounds__(kThreads, 1)
 kvx_free_kernel(const Args a, const __grid_constant__ Inline in)
 {
-    const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
+    __shared__ Inline staged;
+    const char *desc = descriptors(a, in, reinterpret_cast<char *>(&staged));
     const TableEntry *e = reinterpret_cast<const TableEntry *>(desc + a.off_entries);
+    __syncthreads();
     const int total = e[a.n_entries].page_begin;
     wait_for_earlier_work();
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
@@ -352,10 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
 {
     extern __shared__ unsigned smem[];
-    const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
+    __shared__ int last;
+    __shared__ Inline staged;
+    const char *desc = descriptors(a, in, reinterpret_cast<char *>(&staged));
     const TableEntry *e = reinterpret_cast<const TableEntry *>(desc + a.off_entries);
     const int lane = threadIdx.x & 31;
-    __shared__ int last;
     wait_for_earlier_work();
     const Bits live = scan_pages(a, true, a.num_pages + 1, smem);
     if (threadIdx.x == 0)
@@ -438,13 +506,16 @@ size_t bitmap_bytes(int num_pages)
     return granules * kGranWords * 4 + (granules + kWarps + 1) * 4;
 }
 
-// Cut pages of up to `page` bytes into slices so that `units` of them give every warp of the
-// grid a job, each slice at least 1 KiB and at most 8 KiB (two passes of a warp).
+// Cut `units` pages of up to `page` bytes into slices so that every warp of the grid has one
+// job, or, past that, jobs of about 8 KiB; no slice below 1 KiB.
 void choose_slices(const kvx_ctx *ctx, int64_t units, int64_t page, Args *a)
 {
-    const int64_t warps = int64_t(ctx->num_sms) * kWarps;
-    int64_t slice = units > 0 ? units * page / warps : page;
-    slice = std::min<int64_t>(std::max<int64_t>(slice, 1024), 8192) / 16 * 16;
+    const int64_t warps = int64_t(ctx->num_sms) * (kWarps - kTableWarps);
+    const int64_t fill = units > 0 ? std::max<int64_t>(1, warps / units) : 1;
+    int64_t slice = std::max<int64_t>((page + fill - 1) / fill, 1024);
+    if (units * page > 2 * kSliceBytes * warps)
+        slice = std::min<int64_t>(slice, kSliceBytes);
+    slice = (slice + 31) / 32 * 32;
     a->slice = slice;
     a->slices = int32_t((page + slice - 1) / slice);
 }
@@ -474,6 +545,7 @@ kvx_status launch_batch(kvx_ctx *ctx, void (*fn)(Args, Inline), Args a, Batch *b
                         size_t smem, int64_t items, cudaStream_t s)
 {
     cudaError_t e = cudaSuccess;
+    a.inline_bytes = b->slot ? 0 : int32_t((b->bytes + 15) / 16 * 16);
     if (b->slot) {
         a.ext = b->slot->dev;
         e = kvx::stage(ctx, *b->slot, b->bytes, 0, 0, s);
@@ -519,6 +591,11 @@ Args common_args(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs, int n)
     a.off_entries = int32_t((size_t(a.n_slabs) * sizeof(char *) + 15) / 16 * 16);
     a.page_size = pool->page_size;
     a.num_pages = pool->num_pages;
+    uintptr_t bits = uintptr_t(pool->token_bytes);
+    for (int l = 0; l < pool->num_layers; ++l)
+        for (int k = 0; k < pool->kv_factor; ++k)
+            bits |= reinterpret_cast<uintptr_t>((k ? pool->v_pages : pool->k_pages)[l]);
+    a.wide = bits % 32 == 0;
     return a;
 }
 
