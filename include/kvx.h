@@ -388,7 +388,9 @@ kvx_status kvx_dma_baseline(kvx_ctx *ctx, int dir, const kvx_pool *pool,
  * filled last page is never shared, so it may be appended to.
  *
  * Each call is one kernel launch on `stream`, asynchronous like the transfers; small batches
- * travel in the launch itself, larger ones through the context's descriptor slots.  A page id
+ * (about 3.8 KB of descriptors: 8 bytes per layer and K or V, 48 per fork, 16 per table) travel
+ * in the launch itself and can be captured into a CUDA graph, larger ones go through the
+ * context's descriptor slots.  A page id
  * outside the pool sets KVX_DEV_PAGE_OUT_OF_RANGE, a page nobody holds
  * KVX_DEV_PAGE_NOT_HELD; such an entry is skipped.  Pools of up to KVX_MAX_UPKEEP_PAGES pages
  * (KVX_ERR_CAPACITY above).  Calls on one pool's counts and tables must not overlap in time:
@@ -492,7 +494,9 @@ typedef struct kvx_attn_cfg {
  * launches: it is made once (kvx_attn_plan_create allocates), refilled for the next step with
  * kvx_attn_plan_update (which does not), and its launches may be captured into a CUDA graph.
  * It keeps the addresses of page tables and slopes and a copy of the pool's pointers.  Its
- * workspace serves one launch at a time: launches of one plan must not overlap in time.
+ * workspace serves one launch at a time: launches of one plan must not overlap in time, and a
+ * graph captured from a plan must be captured again after an update.  A request has at most
+ * 2^30 tokens (KVX_ERR_CAPACITY above).
  * n_new and prefix are HOST arrays [n_req]; prefix may be NULL (all 0).  Rows of the step are
  * packed: request r's new tokens follow those of request r - 1 in q, out, lse, k and v. */
 typedef struct kvx_attn_plan kvx_attn_plan;

@@ -505,6 +505,8 @@ kvx_status kvx_attn_plan_create(kvx_ctx *ctx, const kvx_pool *pool, const kvx_re
     p->cfg = *cfg;
     if (p->cfg.scale == 0.0f)
         p->cfg.scale = 1.0f / std::sqrt(float(cfg->head_dim));
+    if (p->cfg.window > 1 << 30)  // longer than any request
+        p->cfg.window = 0;
     p->page_size = pool->page_size;
     p->num_pages = pool->num_pages;
     p->num_layers = pool->num_layers;

@@ -33,6 +33,9 @@ int64_t pages_of(int64_t tokens, int64_t page_size)
     return (tokens + page_size - 1) / page_size;
 }
 
+// Positions of a request stay below this, so that sums of two of them fit in 32 bits.
+constexpr int32_t kMaxTokens = 1 << 30;
+
 // The pool's own checks are those of a transfer without chunks.
 kvx_status validate_pool(const kvx_pool *pool, int level, bool have_gpu, char *msg, size_t len)
 {
@@ -222,6 +225,9 @@ kvx_status validate_attn(const kvx_pool *pool, const kvx_request *reqs, int n_re
         if (reqs[r].n_tokens < 0 || n_new[r] < 0 || n_new[r] > reqs[r].n_tokens)
             return fail(KVX_ERR_INVALID_ARG, msg, len, "request %d: n_tokens %d, n_new %d", r,
                         reqs[r].n_tokens, n_new[r]);
+        if (reqs[r].n_tokens > kMaxTokens)
+            return fail(KVX_ERR_CAPACITY, msg, len, "request %d: n_tokens %d exceeds 2^30", r,
+                        reqs[r].n_tokens);
         if (p < 0 || p > reqs[r].n_tokens)
             return fail(KVX_ERR_INVALID_ARG, msg, len, "request %d: prefix %d of %d tokens", r,
                         p, reqs[r].n_tokens);

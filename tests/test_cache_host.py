@@ -118,6 +118,9 @@ def attn(n_tokens=(100, 50), n_new=(1, 50), prefix=None, p=None, table=A, level=
     ({"scale": float("nan")}, INV),
     ({"slopes": A + 2}, ALIGN),
     ({"n_tokens": (2 ** 31 - 1,) * 2, "n_new": (2 ** 27, 2 ** 27)}, kvx.KVX_ERR_CAPACITY),
+    ({"n_tokens": (2 ** 30,) * 2, "n_new": (2 ** 27, 2 ** 27)}, kvx.KVX_ERR_CAPACITY),
+    ({"n_tokens": (2 ** 30 + 1, 1), "n_new": (1, 1)}, kvx.KVX_ERR_CAPACITY),
+    ({"n_tokens": (2 ** 30, 1), "n_new": (1, 1), "window": 2 ** 31 - 1}, OK),
 ])
 def test_attention_arguments(kw, status):
     kw = dict(kw)
