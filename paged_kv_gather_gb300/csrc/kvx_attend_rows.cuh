@@ -178,7 +178,7 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
     const bool plain = !(a.softcap > 0.0f) && !a.slopes;
 
     AttnStart at = w.starts[blockIdx.x];
-    wait_for_earlier_work();
+    bool waited = false;  // for earlier work: the first unit's arithmetic goes before it
     while (at.tiles > 0) {
         const AttnReq r = at.req;
         Keys keys;
@@ -223,12 +223,19 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
 
-        int page = page_of(0);
-#pragma unroll 1
-        for (int i = 0; i < L::kNumStages - 1; ++i) {
-            const int next = page_of(i + 1);
-            issue(i, page);
-            page = next;
+        if (!waited)
+            wait_for_earlier_work();
+        waited = true;
+        int page;
+        {
+            int first[L::kNumStages];  // pages of the first steps, looked up together
+#pragma unroll
+            for (int i = 0; i < L::kNumStages; ++i)
+                first[i] = page_of(i);
+#pragma unroll
+            for (int i = 0; i < L::kNumStages - 1; ++i)
+                issue(i, first[i]);
+            page = first[L::kNumStages - 1];
         }
 
         // q as the second operand: row quad + 8 n in column quad, zero past the unit's rows.
@@ -517,9 +524,9 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
         }
         if (c0 != c1) {
             // The last CTA to arrive joins the parts, in order.
-            __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
+                __threadfence();  // with the barrier before it, for all the CTA has written
                 const unsigned n = atomicAdd(w.counters + c0, 1);
                 flag = n == unsigned(c1 - c0);
                 if (n == unsigned(c1 - c0))

@@ -445,7 +445,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
     tc_fence_after();
     const unsigned tmem = tmem_base;
     const AttnStart begin = w.starts[blockIdx.x];
-    wait_for_earlier_work();
+    bool waited = false;  // for earlier work: the first unit's arithmetic goes before it
 
     if (warp == 8) {
         // ------------------------------------------------------------- matrix products
@@ -617,6 +617,9 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             advance();
         };
         for (Walk u(a, w, begin); ok && !u.done(); u.next()) {
+            if (!waited)
+                wait_for_earlier_work();
+            waited = true;
             // The loaders are ahead of the warps that will read this unit's rows of q.
             for (int i = lt; i < u.rows * (D / 64); i += kLoaders) {
                 const int packed = u.row0 + i / (D / 64), tok = packed / a.group;
@@ -767,6 +770,9 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             const int tok = packed / a.group, head = u.at.head * a.group + packed - tok * a.group;
             const int pos = u.r.n_tokens - u.r.n_new + tok;
             const int64_t orow = u.r.row_begin + tok;
+            if (!waited)
+                wait_for_earlier_work();
+            waited = true;
             const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.0f;
             float row_factor = 1.0f;
             if (mine) {
