@@ -23,6 +23,12 @@ namespace {
 // bfloat16 down to 2^-24 of the row's largest element.  The order of the 16 elements a matrix
 // instruction sums over is free as long as both operands share it, and so is that of O's
 // columns; they are chosen so that a thread's operands are 16 consecutive bytes of a key.
+//
+// Measured: 64 bf16 requests of 1k to 32k tokens, 8 KV heads, 321 us (2.2 GB, 6.9 TB/s; a copy
+// reaches 6.8); 64 e4m3 requests, 4 KV heads, 92 us (552 MB, 5.9 TB/s, where the heads' runs
+// of 128 bytes are what memory serves less well: neither more bytes in flight nor more warps
+// change it); one request of 32k tokens 28 us (134 MB), of 512 tokens 5.4 us, of which three
+// are a launch and the rest the chain page id, keys, products, join.
 const int kRowWarps = 8;
 const int kRowThreads = 32 * kRowWarps;
 const int kRowKeys = 16;                      // keys per warp and step
