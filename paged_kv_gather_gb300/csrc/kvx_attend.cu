@@ -147,7 +147,7 @@ kvx_append_kernel(const Append a)
             x[i].load(src, lane + 32 * i);
     const AttnReq q = a.step.reqs[request_of_row(a.step.reqs, a.step.n_req, row, lane)];
     const int pos = q.n_tokens - q.n_new + row - q.row_begin, nth = a.step.page.div(pos);
-    const int page = __ldg(q.table + nth);
+    const int page = q.table[nth];
     if (unsigned(page) >= unsigned(a.step.num_pages)) {
         if (lane == 0)
             atomicOr(a.step.status, KVX_DEV_PAGE_OUT_OF_RANGE);

@@ -71,7 +71,8 @@ struct Work {
 // Kernels here start while the one before them on the stream ends (programmatic dependent
 // launch).  Before this wait for its completion they touch nothing but the plan's descriptors,
 // which only copies write, and no kernel starts early behind a copy; after it they let the
-// next kernel start in the same way.
+// next kernel start in the same way.  What an earlier kernel may have written (tables, q, new K
+// and V, the pages) is never read through the read-only path: it may change while they run.
 __device__ __forceinline__ void wait_for_earlier_work()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -203,7 +203,7 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
         // Page of key `lane` of step i, or -1; loaded one step before it is used.
         auto page_of = [&](int i) {
             const int j = first_key(i) + (lane & (kRowKeys - 1));
-            return i < todo && keys.used(j) ? __ldg(r.table + a.page.div(j)) : -1;
+            return i < todo && keys.used(j) ? r.table[a.page.div(j)] : -1;
         };
         auto issue = [&](int i, int page) {
             if (i < todo) {

@@ -40,21 +40,7 @@ const int kLoaders = 96;
 const int kLoaderWarps = kLoaders / 32;
 const int kLoaderLag = 2;          // slots filled by 16-byte copies before the first is announced
 
-template <int KV, int D>
-struct TileShape {
-    static const bool kEight = KV == KVX_TYPE_FP_EIGHT;
-    static const int kTile = kTileRows * D * 2;              // bytes of a q, K or V tile
-    static const int kSlots = (D == 128 ? 5 : 10) - kEight;
-    static const int kOffRing = 2 * kTile;
-    static const int kOffStage = kOffRing + kSlots * kTile;  // e4m3: [2][kTile / 2]
-    static const int kOffKeys = kOffStage + kEight * kTile;  // int64 [2][kTileKeys]
-    static const int kOffBars = kOffKeys + 2 * kTileKeys * 8;
-    static const int kOffMisc = kOffBars + 8 * 32;              // int[2]
-    static const int kBytes = kOffMisc + 16;
-    static const int kSlotFloats = kBlockRows * (D + 2);     // a partial result: O, m, l
-};
-
-// Barriers, by index: of the two tiles of rows first, then loader's, the ring's, the end's.
+// Barriers, by index: of the two tiles of rows first, then the loaders', the ring's, the end's.
 enum {
     kBarQ = 0,      // q is in shared memory
     kBarS = 2,      // S is complete, and every product before it
@@ -66,6 +52,21 @@ enum {
     kBarEmpty = 21,
     kBarEnd = 31,
     kBars = 32
+};
+
+template <int KV, int D>
+struct TileShape {
+    static const bool kEight = KV == KVX_TYPE_FP_EIGHT;
+    static const int kTile = kTileRows * D * 2;              // bytes of a q, K or V tile
+    static const int kSlots = (D == 128 ? 5 : 10) - kEight;
+    static const int kOffRing = 2 * kTile;
+    static const int kOffStage = kOffRing + kSlots * kTile;  // e4m3: [2][kTile / 2]
+    static const int kOffKeys = kOffStage + kEight * kTile;  // int64 [2][kTileKeys]
+    static const int kOffBars = kOffKeys + 2 * kTileKeys * 8;
+    static const int kOffMisc = kOffBars + 8 * kBars;        // int[2]
+    static const int kBytes = kOffMisc + 16;
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+    static const int kSlotFloats = kBlockRows * (D + 2);     // a partial result: O, m, l
 };
 
 __device__ __forceinline__ void mbar_init(unsigned bar, unsigned count)
@@ -643,7 +644,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             auto page_of = [&](int i) {
                 const int j = i < u.todo ? u.key_of(i) + run : 0;
                 return i < u.todo && run < kTileKeys && u.keys.used(j)
-                           ? __ldg(u.r.table + a.page.div(j)) : -1;
+                           ? u.r.table[a.page.div(j)] : -1;
             };
             int next = kEight ? -1 : page_of(0);
             // Page of key lt + b * kLoaders of tile i.
@@ -651,7 +652,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 const int t = lt + b * kLoaders;
                 const int j = i < u.todo && t < kTileKeys ? u.key_of(i) + t : 0;
                 return i < u.todo && t < kTileKeys && u.keys.used(j)
-                           ? __ldg(u.r.table + a.page.div(j)) : -1;
+                           ? u.r.table[a.page.div(j)] : -1;
             };
             int later[2] = {-1, -1};
             for (int i = 0; ok && i < u.todo; ++i) {
@@ -792,7 +793,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
 #pragma unroll
                 for (int t = 0; t < kRowChunks; ++t) {
                     const int64_t o = __shfl_sync(0xffffffffu, off, t * kRowsAtOnce + sub_row);
-                    v[t] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.q + o) + sub_chunk)
+                    v[t] = o >= 0 ? reinterpret_cast<const uint4 *>(a.q + o)[sub_chunk]
                                   : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll

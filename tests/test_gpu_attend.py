@@ -389,3 +389,69 @@ def test_append_reports_pages_out_of_range(ctx, bad):
     assert torch.equal(flat[0, 0, slot], k[0].view(torch.uint8))
     flat[:, 0, slot] = was[:, 0, slot]
     assert torch.equal(flat, was) and int(kept[2]) >= 0
+
+
+def _steps(ctx, synchronize, steps=40):
+    """Grow, append, attend, shrink the life of two requests again and again; every output."""
+    page, heads, dim, group = 16, 2, 64, 8
+    pages = torch.zeros((2, 1, 64, page, heads * dim * 2), dtype=torch.uint8, device="cuda")
+    pool = kvx.Pool.from_tensor(pages, page)
+    refs = torch.zeros(64, dtype=torch.int32, device="cuda")
+    tables = torch.full((2, 64), -1, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.randn((steps, 2 * 24, (group + 2) * heads * dim), device="cuda",
+                    generator=g).bfloat16()
+    cfg = kvx.attn_config(heads * group, heads, dim)
+    outs, now = [], [0, 0]
+    plan = None
+
+    def settle():
+        if synchronize:
+            torch.cuda.synchronize()
+
+    for i in range(steps):
+        new = [(1, 1), (20, 1), (3, 17)][i % 3]
+        then = [n + m for n, m in zip(now, new)]
+        rows = tables.data_ptr(), tables[1].data_ptr()
+        kvx.kvx_fork_pages(ctx, pool, refs.data_ptr(), kvx.forks_array(
+            [(p, p, n, t, False) for p, n, t in zip(rows, now, then)]))
+        settle()
+        reqs = kvx.requests_array([(p, None, t) for p, t in zip(rows, then)])
+        if plan is None:
+            plan = kvx.kvx_attn_plan_create(ctx, pool, reqs, new, cfg)
+        else:
+            kvx.kvx_attn_plan_update(plan, reqs, new)
+        settle()
+        # A copy first, then kernels that start while the one before them ends: what append
+        # and attend read is written just ahead of them, on the same few pages every time.
+        y = (x[i, :sum(new)] * 1.0).contiguous()
+        width = heads * dim * 2
+        at = y.data_ptr()
+        stride = y.stride(0)
+        out = torch.empty((sum(new), heads * group, dim), dtype=torch.bfloat16, device="cuda")
+        settle()
+        kvx.kvx_append_tokens(plan, 0, at + group * width, at + (group + 1) * width, stride, stride)
+        settle()
+        kvx.kvx_attend(plan, 0, at, out.data_ptr(), stride)
+        settle()
+        outs.append(out)
+        now = then
+        if i % 8 == 7:  # both end and begin anew on the pages they free
+            kvx.kvx_free_pages(ctx, pool, refs.data_ptr(), kvx.tables_array(
+                [(p, -(-n // page)) for p, n in zip(rows, now)]))
+            now = [0, 0]
+            settle()
+    torch.cuda.synchronize()
+    kvx.kvx_attn_plan_destroy(plan)
+    assert kvx.kvx_get_status(ctx) == 0
+    return outs
+
+
+def test_back_to_back_calls_see_each_others_work(ctx):
+    """The calls of a step, which may start while the one before them drains, give the same
+    outputs as with the GPU idle between them."""
+    want = _steps(ctx, True)
+    for _ in range(3):
+        for a, b in zip(_steps(ctx, False), want):
+            assert torch.equal(a, b)
