@@ -31,7 +31,7 @@ namespace {
 // Measured: 2048 rows x 8 heads behind 32k tokens (2.13 TFLOP) 1.37 ms on its own and 1.45-1.5
 // ms in long runs under the power cap (cuBLAS sustains 1.70 PFLOP/s there); the tensor pipe is
 // active 68 % of the cycles.  A unit costs about 9000 cycles beside its steps (q in, first
-// scores, O out), which is what short prompts pay: 2k tokens 51 us, 8k 380 us.
+// scores, O out), which is what short prompts pay: 2k tokens 36 us, 8k 375 us.
 const int kTileThreads = 384;
 const int kTileRows = 128;
 const int kTileKeys = 128;
@@ -349,7 +349,7 @@ __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes)
                  : "memory");
 }
 
-// Walks a CTA's share of the line; every role of the CTA steps through the same units.
+// Walks a CTA's share of the line, or the units dealt to it; every role of the CTA steps through the same units.
 struct Walk {
     const Attend &a;
     const Work &w;
@@ -393,8 +393,13 @@ struct Walk {
     __device__ __forceinline__ void next()
     {
         at.tiles -= todo;
-        if (done())
+        if (done()) {
+            if (at.last == 0 || at.tile + todo < keys.tiles)
+                return;
+            at = w.starts[at.last];
+            enter();
             return;
+        }
         at.tile = 0;
         if (++at.head == a.kv_heads) {
             at.head = 0;

@@ -69,7 +69,8 @@ struct AttnStart {
     int32_t head;
     int32_t tile;     // within the unit
     int32_t first;    // CTA that began the unit, if tile > 0
-    int32_t last;     // CTA that ends the unit this share stops inside of, if it does
+    int32_t last;     // CTA that ends the unit this share stops inside of, if it does; else the
+                      // share that the CTA takes next, 0: none
     int64_t tiles;
     AttnReq req;      // of `request`: one load instead of two in a row
 };

@@ -455,3 +455,39 @@ def test_back_to_back_calls_see_each_others_work(ctx):
     for _ in range(3):
         for a, b in zip(_steps(ctx, False), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tokens,new,heads,group", [
+    ([700, 1, 450, 333, 90], [700, 1, 450, 333, 90], 8, 4),        # prompts
+    ([900, 40, 260, 2000, 5], [300, 40, 130, 500, 5], 8, 5),       # chunks
+    ([1 + 37 * r % 400 for r in range(38)], [1] * 38, 64, 17),     # many units, short
+    ([1 + 37 * r % 400 for r in range(39)], [1] * 39, 64, 17)])    # and some more
+def test_more_units_than_sms(ctx, tokens, new, heads, group):
+    """Several units of unequal length for every SM, whole or cut."""
+    run_case(ctx, tokens, new, heads, group, 64, 16)
+
+
+def test_update_between_schedules(ctx):
+    """A plan refilled with batches of few long and many short units gives what it gave."""
+    tokens = [3000, 520, 300, 700, 64, 900]
+    cache = Cache(tokens, 8, 128, 16)
+    cfg = kvx.attn_config(32, 8, 128)
+    news = [[3000, 520, 300, 700, 64, 900], [1, 0, 64, 0, 0, 1], [64, 0, 0, 0, 0, 0], [1] * 6]
+    q = make_q(sum(tokens), 32, 128, "bf16", 5)
+    plan = kvx.kvx_attn_plan_create(ctx, cache.kvx_pool, cache.requests(), news[0], cfg)
+    outs = []
+    for i in (0, 1, 2, 0, 3, 1, 0, 2, 3):
+        if outs:
+            kvx.kvx_attn_plan_update(plan, cache.requests(), news[i])
+        out = torch.zeros((sum(news[i]), 32, 128), dtype=torch.bfloat16, device="cuda")
+        kvx.kvx_attend(plan, LAYER, q.data_ptr(), out.data_ptr())
+        outs.append((i, out))
+    torch.cuda.synchronize()
+    kvx.kvx_attn_plan_destroy(plan)
+    assert kvx.kvx_get_status(ctx) == 0
+    first = {}
+    for i, out in outs:
+        assert torch.equal(first.setdefault(i, out), out)
+    for i, out in first.items():
+        if i:
+            check(cache, q[:sum(news[i])].unflatten(1, (32, 128)), out, None, news[i], 4, 128 ** -0.5)
