@@ -252,19 +252,19 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
+{
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 struct Yes {
     static constexpr bool value = true;
 };
 struct No {
     static constexpr bool value = false;
 };
-
-__device__ __forceinline__ float min3(float a, float b, float c)
-{
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 
 // The bits 0 .. n - 1 of 32.
 __device__ __forceinline__ unsigned bits_below(int n)
@@ -915,14 +915,14 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                         auto adjust = [&](float(&z)[32], int b) {
                             const float away = float(32 * b - hi);  // j - i of z[0]
                             if (a.softcap > 0.0f) {
-                                float most = 0.0f;
+                                float most = 0.0f, more = 0.0f;
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    const uint64_t x = pair_of(z[2 * k], z[2 * k + 1]);
-                                    const float2 u = halves_of(mul_pair(x, x));
-                                    most = max3(most, u.x, u.y);
+                                for (int k = 0; k < 32; k += 4) {
+                                    most = max3_abs(most, z[k], z[k + 1]);
+                                    more = max3_abs(more, z[k + 2], z[k + 3]);
                                 }
-                                const bool small = series_fits && most * inner * inner <= 0.25f;
+                                most = fmaxf(most, more);
+                                const bool small = series_fits && most * inner <= 0.5f;
                                 if (!__all_sync(0xffffffffu, small)) {
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
