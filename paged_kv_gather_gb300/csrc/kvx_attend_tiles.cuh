@@ -840,7 +840,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 const bool series_fits = inner > 1e-4f && inner < 1e4f;
                 uint64_t series[kTanhTerms];
                 {
-                    float t = a.softcap > 0.0f ? score.cap * inner : factor;
+                    // Without a cap the first term alone is used, and is the factor itself.
+                    float t = a.softcap > 0.0f ? score.cap * inner : factor * (1.0f / kTanh[0]);
 #pragma unroll
                     for (int n = 0; n < kTanhTerms; ++n) {
                         series[n] = pair_of(t * kTanh[n], t * kTanh[n]);
