@@ -921,6 +921,8 @@ kvx_status kvx_create(kvx_ctx **out, int device, size_t max_descriptor_bytes)
         e = cudaMemset(ctx->status_dev, 0, 256);
     if (e == cudaSuccess)
         e = cudaHostAlloc(reinterpret_cast<void **>(&ctx->status_host), 64, cudaHostAllocDefault);
+    if (e == cudaSuccess)
+        e = kvx::prepare_upkeep();
     if (e != cudaSuccess) {
         kvx_destroy(ctx);
         return KVX_ERR_CUDA;

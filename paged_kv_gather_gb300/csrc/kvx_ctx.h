@@ -124,6 +124,11 @@ inline void begin_call(kvx_ctx *ctx)
     ctx->last_desc_bytes = 0;
 }
 
+// Allow the page upkeep kernels the shared memory of the largest pool, on the current device:
+// once, for every call of every context after it, so that no call lowers it under another
+// thread's launch.
+cudaError_t prepare_upkeep();
+
 // The context's next descriptor slot, once the launch that last used it has finished.
 inline kvx_status acquire_slot(kvx_ctx *ctx, size_t bytes, Slot **out)
 {

@@ -557,23 +557,18 @@ kvx_status launch_batch(kvx_ctx *ctx, void (*fn)(Args, Inline), Args a, Batch *b
     }
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "descriptor copy");
-    if (smem > 48 * 1024 - 256)
-        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e == cudaSuccess) {
-        cudaLaunchConfig_t lc = {};
-        lc.gridDim = dim3(unsigned(ctas));
-        lc.blockDim = dim3(kThreads);
-        lc.dynamicSmemBytes = smem;
-        lc.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        lc.attrs = attr;
-        lc.numAttrs = 1;
-        void *args[] = {&a, &b->in};
-        e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(fn), args);
-    }
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(ctas));
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = smem;  // up to what prepare_upkeep asked for
+    lc.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    void *args[] = {&a, &b->in};
+    e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(fn), args);
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "kernel launch");
     if (b->slot)
@@ -613,6 +608,17 @@ kvx_status too_many_jobs(kvx_ctx *ctx, int64_t pages, const Args &a)
 }
 
 }  // namespace
+
+cudaError_t kvx::prepare_upkeep()
+{
+    const int smem = int(bitmap_bytes(KVX_MAX_UPKEEP_PAGES));
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kvx_fork_kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kvx_compact_kernel),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e;
+}
 
 extern "C" {
 
