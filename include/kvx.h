@@ -381,7 +381,8 @@ kvx_status kvx_dma_baseline(kvx_ctx *ctx, int dir, const kvx_pool *pool,
  * its page tables back nor copies pages one by one.
  *
  * refs is a device array [num_pages]: how many page-table entries hold each page; 0 means
- * free.  The caller owns it and the tables; these calls keep them in step.  Free pages are
+ * free.  The caller owns it and the tables; these calls keep them in step.  (While a fork or
+ * a compaction runs, the count of one free page may be below 0.)  Free pages are
  * always handed out in ascending order of page id, so results do not depend on how the GPU
  * schedules the work.  Full pages are shared and never written again by the library's own
  * calls that follow (kvx_append_tokens writes only past a request's earlier tokens); a partly
@@ -394,7 +395,8 @@ kvx_status kvx_dma_baseline(kvx_ctx *ctx, int dir, const kvx_pool *pool,
  * outside the pool sets KVX_DEV_PAGE_OUT_OF_RANGE, a page nobody holds
  * KVX_DEV_PAGE_NOT_HELD; such an entry is skipped.  Pools of up to KVX_MAX_UPKEEP_PAGES pages
  * (KVX_ERR_CAPACITY above).  Calls on one pool's counts and tables must not overlap in time:
- * issue them on one stream or order them with events. */
+ * issue them on one stream or order them with events.  Calls on different pools, replays of
+ * captured ones among them, may. */
 #define KVX_MAX_UPKEEP_PAGES (1 << 20)
 
 /* A page table that a call may rewrite. */

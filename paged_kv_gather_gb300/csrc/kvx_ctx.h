@@ -13,11 +13,6 @@
 namespace kvx {
 
 const int kSlots = 4;
-// Words of the status allocation (256 bytes) that count a launch's CTAs.  Each call takes the
-// next one; the last CTA to arrive leaves it at zero again, so a call finds it clean as long
-// as fewer than kCounters of them are on the GPU at once.
-const int kCounterFirst = 16;
-const int kCounters = 48;
 
 struct Slot {
     char *host = nullptr;
@@ -39,9 +34,8 @@ struct kvx_ctx {
     // Descriptor copies run here, beside the caller's stream, so that a call's copy overlaps
     // the previous call's kernel instead of sitting between two kernels.
     cudaStream_t copy_stream = nullptr;
-    unsigned int *status_dev = nullptr;  // word 0: status; words from kCounterFirst: counters
+    unsigned int *status_dev = nullptr;
     unsigned int *status_host = nullptr;
-    int next_counter = 0;
     int64_t last_items = 0;
     int32_t last_ctas = 0;
     int32_t last_threads = 0;
@@ -160,13 +154,6 @@ inline kvx_status finish_call(kvx_ctx *ctx, Slot &slot, cudaStream_t s, int64_t 
     ctx->last_threads = threads;
     ctx->last_desc_bytes = int64_t(desc_bytes);
     return KVX_OK;
-}
-
-inline unsigned int *take_counter(kvx_ctx *ctx)
-{
-    unsigned int *c = ctx->status_dev + kCounterFirst + ctx->next_counter;
-    ctx->next_counter = (ctx->next_counter + 1) % kCounters;
-    return c;
 }
 
 }  // namespace kvx

@@ -9,8 +9,10 @@
 // enough free pages) and answers its own queries there, so a call is one launch with no
 // device-wide wait, no list in global memory and no order-dependent atomics.  Nothing may
 // change a page between free and live while another CTA still scans: such writes are left to
-// the last CTA that arrives at a counter.  Until then counts of live pages only go up, which
-// no bitmap sees.
+// the last CTA that has scanned.  Until then counts of live pages only go up, which no bitmap
+// sees.  CTAs count themselves in refs, below zero at the first page that will turn live: a
+// page whose count is not positive is free, so no bitmap sees that either, the last CTA's
+// writes leave no trace of it, and calls share nothing but the pool they work on.
 //
 // Measured: copies of whole requests (6.7 GB read and written) 991 us and compaction (4.1 GB)
 // 620 us, the rate of a device copy; one request forked into four (256 tails of 18 KB) 4 us
@@ -52,7 +54,6 @@ struct Args {
     int32_t inline_bytes;    // of them there
     int32_t *refs;
     unsigned int *status;
-    unsigned int *counter;   // CTAs that have finished scanning
     int32_t *n_live;         // compact
     int32_t *remap;          // compact
     int64_t token_bytes;
@@ -199,12 +200,12 @@ __device__ Bits scan_pages(const Args &a, bool live, int enough, unsigned *smem)
 }
 
 // Arrival of this CTA's scan, by one thread, after a barrier that ends the scan; and, past a
-// later barrier, whether it was the last CTA of the launch to arrive.  The counter is left at
-// zero.
-__device__ void arrive(unsigned int *counter, int *last)
+// later barrier, whether it was the last CTA of the launch to arrive.  `count` is that of a
+// free page, 0 before the launch.
+__device__ void arrive(int32_t *count, int *last)
 {
     __threadfence();
-    *last = atomicInc(counter, gridDim.x - 1) == gridDim.x - 1;
+    *last = atomicSub(count, 1) == 1 - int(gridDim.x);
     __threadfence();
 }
 
@@ -323,13 +324,13 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
     const ForkEntry end = e[a.n_entries];
     wait_for_earlier_work();
     const Bits free = scan_pages(a, false, end.fresh_begin, smem);
-    if (threadIdx.x == 0)
-        arrive(a.counter, &last);
     if (free.total < end.fresh_begin) {  // the same in every CTA: counts of live pages only grow
         if (blockIdx.x == 0 && threadIdx.x == 0)
             atomicOr(a.status, KVX_DEV_NO_FREE_PAGE);
         return;
     }
+    if (end.fresh_begin > 0 && threadIdx.x == 0)
+        arrive(a.refs + free.select(0), &last);
 
     // Pages past the scan do not turn live in this launch.
     auto is_free = [&](int p) {
@@ -387,7 +388,7 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
                    min(a.page_size, e[x].shared - j * a.page_size), lane);
     }
     __syncthreads();
-    if (last)
+    if (end.fresh_begin > 0 && last)
         for (int i = threadIdx.x; i < end.fresh_begin; i += kThreads)
             a.refs[free.select(i)] = 1;
 }
@@ -431,8 +432,6 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
     const int lane = threadIdx.x & 31;
     wait_for_earlier_work();
     const Bits live = scan_pages(a, true, a.num_pages + 1, smem);
-    if (threadIdx.x == 0)
-        arrive(a.counter, &last);
     const int n = live.total, front = live.rank(n), moves = n - front;
     // Page of the i-th free page below n: the smallest p with (p - rank(p)) pages free before
     // it and p free, by bisection over pages.
@@ -463,6 +462,10 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
         }
         return w * 32 + bit;
     };
+    if (moves > 0 && threadIdx.x == 0)
+        arrive(a.refs + hole(0), &last);
+    if (a.n_live && blockIdx.x == 0 && threadIdx.x == 0)
+        *a.n_live = n;
 
     const int warp = threadIdx.x >> 5, copy_warps = kWarps - a.table_warps;
     const int table_threads = 32 * a.table_warps;
@@ -492,15 +495,12 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
         copy_slice(a, desc, slab, slice, live.select(front + c), hole(c), a.page_size, lane);
     }
     __syncthreads();
-    if (last) {
+    if (moves > 0 && last)
         for (int i = threadIdx.x; i < moves; i += kThreads) {
             const int from = live.select(front + i);
             a.refs[hole(i)] = ld_ref(a.refs + from);
             a.refs[from] = 0;
         }
-        if (a.n_live && threadIdx.x == 0)
-            *a.n_live = n;
-    }
 }
 
 // ---------------------------------------------------------------------------------- host
@@ -657,7 +657,6 @@ kvx_status kvx_fork_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
                   std::max<int64_t>(longest, 1) * pool->token_bytes, &a);
     if ((st = too_many_jobs(ctx, end.copy_begin, a)) != KVX_OK)
         return st;
-    a.counter = kvx::take_counter(ctx);
     a.table_warps = end.copy_begin ? kTableWarps : kWarps;
     const int64_t jobs = int64_t(end.copy_begin) * a.n_slabs * a.slices;
     const int64_t ctas = std::min<int64_t>(
@@ -713,7 +712,6 @@ static kvx_status tables_call(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
                   int64_t(pool->page_size) * pool->token_bytes, &a);
     if ((st = too_many_jobs(ctx, pool->num_pages / 2, a)) != KVX_OK)
         return st;
-    a.counter = kvx::take_counter(ctx);
     return launch_batch(ctx, kvx_compact_kernel, a, &b, ctx->num_sms,
                         bitmap_bytes(pool->num_pages), entries, s);
 }

@@ -1,4 +1,5 @@
-"""Page upkeep where its limits lie: pool sizes about the default limit of shared memory."""
+"""Page upkeep where its limits lie: pool sizes about the default limit of shared memory, and
+calls on several pools of one context at a time."""
 import os
 import subprocess
 import sys
@@ -15,6 +16,7 @@ if not torch.cuda.is_available():
 from paged_kv_gather_gb300.build import build  # noqa: E402
 
 build()
+from paged_kv_gather_gb300 import kvx  # noqa: E402
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -54,3 +56,66 @@ def test_pools_about_the_default_limit_of_shared_memory():
     r = subprocess.run([sys.executable, "-c", ABOUT_THE_DEFAULT], cwd=ROOT, timeout=300,
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+class Copier:
+    """A pool whose parent request is copied whole into a child and the child freed again:
+    every round finds the pool as the one before it did."""
+
+    def __init__(self, n_pages, pages, seed):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        self.bytes = torch.randint(0, 256, (2, 3, n_pages, 4, 64), dtype=torch.uint8, device="cuda",
+                                   generator=g)
+        self.pool = kvx.Pool.from_tensor(self.bytes, 4)
+        order = torch.randperm(n_pages, device="cuda", generator=g).int()
+        self.parent = order[:pages].contiguous()
+        self.refs = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+        self.refs[self.parent.long()] = 1
+        self.before = self.refs.clone()
+        self.want = (self.refs == 0).nonzero()[:pages, 0].int()
+        self.child = torch.full_like(self.parent, -1)
+        self.forks = kvx.forks_array([(self.parent.data_ptr(), self.child.data_ptr(), 4 * pages,
+                                       4 * pages, True)])
+        self.tables = kvx.tables_array([(self.child.data_ptr(), pages)])
+
+    def round(self, ctx, stream):
+        """Returns the child's table and the counts after the copy, taken on the stream."""
+        kvx.kvx_fork_pages(ctx, self.pool, self.refs.data_ptr(), self.forks,
+                           stream=stream.cuda_stream)
+        seen = self.child.clone(), self.refs.clone()
+        kvx.kvx_free_pages(ctx, self.pool, self.refs.data_ptr(), self.tables,
+                           stream=stream.cuda_stream)
+        return seen
+
+    def check(self, seen):
+        held = self.before.clone()
+        held[self.want.long()] = 1
+        for child, refs in seen:
+            assert torch.equal(child, self.want) and torch.equal(refs, held)
+        assert torch.equal(self.refs, self.before)
+        assert torch.equal(self.bytes[:, :, self.want.long()], self.bytes[:, :, self.parent.long()])
+
+
+def test_calls_on_different_pools_at_the_same_time():
+    """A captured call replayed on one stream beside more direct calls on another than a
+    context keeps anything for, on one context: neither sees the other."""
+    ctx = kvx.kvx_create(0)
+    a, b = Copier(60000, 300, 1), Copier(20000, 37, 2)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=sa):
+        last = a.round(ctx, sa)
+    got_a, got_b = [], []
+    for _ in range(150):
+        with torch.cuda.stream(sa):
+            graph.replay()
+            got_a.append([x.clone() for x in last])
+        with torch.cuda.stream(sb):
+            got_b.append(b.round(ctx, sb))
+    torch.cuda.synchronize()
+    a.check(got_a)
+    b.check(got_b)
+    assert kvx.kvx_get_status(ctx) == 0
+    kvx.kvx_destroy(ctx)
