@@ -98,9 +98,10 @@ __device__ __forceinline__ uint64_t now_ns()
 }
 
 // Wait for a phase of a barrier, for about a second at most; then, or once another wait of
-// the CTA has run out, false.  The answer is the same for a whole warp.  No thread of the
-// kernel waits in any other way than this before its last barrier, so a wait that runs out
-// ends the launch.
+// the CTA has run out, false.  The answer is the same for a whole warp.  Past the wait for
+// earlier work, which every role of the CTA does before its first barrier, so that the second
+// is this kernel's own, no thread waits in any other way before the last barrier: a wait that
+// runs out ends the launch.
 __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned phase, volatile int *gave_up,
                                           unsigned *status)
 {
@@ -467,6 +468,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         // between the last of one batch and the first of the next shows once the weights of
         // the other tile are there in time.
         if (elect_one()) {
+            wait_for_earlier_work();
             constexpr unsigned kDescS = mma_idesc(kMath, kTileKeys, false);
             constexpr unsigned kDescO = mma_idesc(kMath, D, true);
             const uint64_t q_desc = tile_desc(sm, 16);
