@@ -338,11 +338,12 @@ kvx_fork_kernel(const Args a, const __grid_constant__ Inline in)
     };
 
     // Tables, and the counts of shared pages, by the last warps of every CTA (by all, if there
-    // is nothing to copy) beside the copies of the others.
+    // is nothing to copy) beside the copies of the others.  There are up to 2^31 - 1 entries;
+    // the step past the last of them fits in 32 bits without a sign.
     const int warp = threadIdx.x >> 5, copy_warps = kWarps - a.table_warps;
     const int table_threads = 32 * a.table_warps;
-    for (int i = blockIdx.x * table_threads + threadIdx.x - 32 * copy_warps;
-         warp >= copy_warps && i < end.page_begin; i += gridDim.x * table_threads) {
+    for (unsigned i = blockIdx.x * table_threads + threadIdx.x - 32 * copy_warps;
+         warp >= copy_warps && i < unsigned(end.page_begin); i += gridDim.x * table_threads) {
         const int x = find_entry(e, a.n_entries, i, [](const ForkEntry &f) { return f.page_begin; });
         const int j = i - e[x].page_begin;
         if (j >= e[x].full) {
@@ -400,9 +401,9 @@ kvx_free_kernel(const Args a, const __grid_constant__ Inline in)
     const char *desc = descriptors(a, in, reinterpret_cast<char *>(&staged));
     const TableEntry *e = reinterpret_cast<const TableEntry *>(desc + a.off_entries);
     __syncthreads();
-    const int total = e[a.n_entries].page_begin;
+    const unsigned total = e[a.n_entries].page_begin;
     wait_for_earlier_work();
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
+    for (unsigned i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
         const int x = find_entry(e, a.n_entries, i, [](const TableEntry &t) { return t.page_begin; });
         int32_t *at = e[x].pages + (i - e[x].page_begin);
         const int p = *at;
@@ -469,9 +470,9 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
 
     const int warp = threadIdx.x >> 5, copy_warps = kWarps - a.table_warps;
     const int table_threads = 32 * a.table_warps;
-    const int mine = blockIdx.x * table_threads + threadIdx.x - 32 * copy_warps;
-    const int total = e[a.n_entries].page_begin;
-    for (int i = mine; warp >= copy_warps && i < total; i += gridDim.x * table_threads) {
+    const unsigned mine = blockIdx.x * table_threads + threadIdx.x - 32 * copy_warps;
+    const unsigned total = e[a.n_entries].page_begin;
+    for (unsigned i = mine; warp >= copy_warps && i < total; i += gridDim.x * table_threads) {
         const int x = find_entry(e, a.n_entries, i, [](const TableEntry &t) { return t.page_begin; });
         int32_t *at = e[x].pages + (i - e[x].page_begin);
         const int p = *at;
@@ -483,7 +484,8 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
             *at = hole(live.rank(p) - front);
     }
     if (a.remap)
-        for (int p = mine; warp >= copy_warps && p < a.num_pages; p += gridDim.x * table_threads)
+        for (int p = int(mine); warp >= copy_warps && p < a.num_pages;
+             p += gridDim.x * table_threads)
             a.remap[p] = !live.test(p) ? -1 : p < n ? p : hole(live.rank(p) - front);
 
     const int64_t jobs = int64_t(moves) * a.n_slabs * a.slices;

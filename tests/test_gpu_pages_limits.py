@@ -1,5 +1,5 @@
-"""Page upkeep where its limits lie: pool sizes about the default limit of shared memory, and
-calls on several pools of one context at a time."""
+"""Page upkeep where its limits lie: pool sizes about the default limit of shared memory,
+calls on several pools of one context at a time, and as many table entries as there may be."""
 import os
 import subprocess
 import sys
@@ -118,4 +118,51 @@ def test_calls_on_different_pools_at_the_same_time():
     a.check(got_a)
     b.check(got_b)
     assert kvx.kvx_get_status(ctx) == 0
+    kvx.kvx_destroy(ctx)
+
+
+def test_as_many_entries_as_a_call_takes():
+    """2^31 - 1 table entries in a call: a fork that shares them, a compaction that rewrites
+    them and a free that gives them back."""
+    total, n = 2 ** 31 - 1, 1 << 20
+    ctx = kvx.kvx_create(0)
+    pool = torch.zeros((1, 1, n, 1, 16), dtype=torch.uint8, device="cuda")
+    p = kvx.Pool.from_tensor(pool, 1)
+    parent = torch.arange(1, n, dtype=torch.int32, device="cuda")   # page 0 is free
+    refs = torch.ones(n, dtype=torch.int32, device="cuda")
+    refs[0] = 0
+    table = torch.full((total + 1,), -7, dtype=torch.int32, device="cuda")
+    n_live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    whole, rest = divmod(total, n - 1)
+    at = [(i * (n - 1), n - 1) for i in range(whole)] + [(whole * (n - 1), rest)]
+
+    def is_parent(last):
+        for begin, m in at:
+            want = parent[:m].clone()
+            want[parent[:m] == n - 1] = last
+            assert torch.equal(table[begin:begin + m], want)
+        assert int(table[total]) == -7
+
+    torch.cuda.synchronize()
+    kvx.kvx_fork_pages(ctx, p, refs.data_ptr(), kvx.forks_array(
+        [(parent.data_ptr(), table.data_ptr() + 4 * begin, m, m, False) for begin, m in at]))
+    torch.cuda.synchronize()
+    assert kvx.kvx_get_status(ctx) == 0
+    is_parent(n - 1)
+    held = torch.full_like(refs, 1 + whole)
+    held[1:1 + rest] += 1
+    held[0] = 0
+    assert torch.equal(refs, held)
+    tables = kvx.tables_array([(table.data_ptr(), total)])
+    kvx.kvx_compact_pages(ctx, p, refs.data_ptr(), tables, n_live.data_ptr())
+    torch.cuda.synchronize()
+    assert kvx.kvx_get_status(ctx) == 0 and int(n_live) == n - 1
+    is_parent(0)
+    held[0], held[-1] = held[-1].clone(), 0
+    assert torch.equal(refs, held)
+    kvx.kvx_free_pages(ctx, p, refs.data_ptr(), tables)
+    torch.cuda.synchronize()
+    assert kvx.kvx_get_status(ctx) == 0
+    assert int(table[:total].min()) == int(table[:total].max()) == -1 and int(table[total]) == -7
+    assert torch.equal(refs, (torch.arange(n, device="cuda") < n - 1).int())
     kvx.kvx_destroy(ctx)
