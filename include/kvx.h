@@ -498,7 +498,7 @@ typedef struct kvx_attn_cfg {
  * It keeps the addresses of page tables and slopes and a copy of the pool's pointers.  Its
  * workspace serves one launch at a time: launches of one plan must not overlap in time, and a
  * graph captured from a plan must be captured again after an update.  A request has at most
- * 2^30 tokens (KVX_ERR_CAPACITY above).
+ * 2^30 tokens, a step 2^31 - 256 rows of new tokens x query heads (KVX_ERR_CAPACITY above).
  * n_new and prefix are HOST arrays [n_req]; prefix may be NULL (all 0).  Rows of the step are
  * packed: request r's new tokens follow those of request r - 1 in q, out, lse, k and v. */
 typedef struct kvx_attn_plan kvx_attn_plan;

@@ -35,6 +35,9 @@ int64_t pages_of(int64_t tokens, int64_t page_size)
 
 // Positions of a request stay below this, so that sums of two of them fit in 32 bits.
 constexpr int32_t kMaxTokens = 1 << 30;
+// Rows of a step (new tokens x query heads): with the last block of the chunk kernel, of up to
+// 256 rows, they are counted in 32 bits.
+constexpr int64_t kMaxRows = INT32_MAX - 255;
 
 // The pool's own checks are those of a transfer without chunks.
 kvx_status validate_pool(const kvx_pool *pool, int level, bool have_gpu, char *msg, size_t len)
@@ -238,9 +241,9 @@ kvx_status validate_attn(const kvx_pool *pool, const kvx_request *reqs, int n_re
                         r);
         rows += n_new[r];
     }
-    if (rows * cfg->q_heads > INT32_MAX)
-        return fail(KVX_ERR_CAPACITY, msg, len, "%lld new tokens x %d heads exceed 2^31 rows",
-                    (long long)rows, cfg->q_heads);
+    if (rows * cfg->q_heads > kMaxRows)
+        return fail(KVX_ERR_CAPACITY, msg, len, "%lld new tokens x %d heads exceed 2^31 - 256 "
+                    "rows", (long long)rows, cfg->q_heads);
     if (level <= 1)
         return KVX_OK;
 
