@@ -513,8 +513,8 @@ size_t bitmap_bytes(int num_pages)
     return granules * kGranWords * 4 + (granules + kWarps + 1) * 4;
 }
 
-// Cut `units` pages of up to `page` bytes into slices so that every warp of the grid has one
-// job, or, past that, jobs of about 8 KiB; no slice below 1 KiB.
+// Cut `units` pages of up to `page` bytes into slices so that every copying warp of the grid
+// has one job, or, past that, jobs of about 8 KiB; no slice below 1 KiB.
 void choose_slices(const kvx_ctx *ctx, int64_t units, int64_t page, Args *a)
 {
     const int64_t warps = int64_t(ctx->num_sms) * (kWarps - kTableWarps);
@@ -661,8 +661,9 @@ kvx_status kvx_fork_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
         return st;
     a.table_warps = end.copy_begin ? kTableWarps : kWarps;
     const int64_t jobs = int64_t(end.copy_begin) * a.n_slabs * a.slices;
+    const int copy_warps = std::max(1, kWarps - a.table_warps);
     const int64_t ctas = std::min<int64_t>(
-        ctx->num_sms, std::max((jobs + kWarps - 1) / kWarps,
+        ctx->num_sms, std::max((jobs + copy_warps - 1) / copy_warps,
                                (int64_t(end.page_begin) + 32 * a.table_warps - 1) /
                                    (32 * a.table_warps)));
     return launch_batch(ctx, kvx_fork_kernel, a, &b, ctas, bitmap_bytes(pool->num_pages), jobs,

@@ -166,3 +166,26 @@ def test_as_many_entries_as_a_call_takes():
     assert int(table[:total].min()) == int(table[:total].max()) == -1 and int(table[total]) == -7
     assert torch.equal(refs, (torch.arange(n, device="cuda") < n - 1).int())
     kvx.kvx_destroy(ctx)
+
+
+@pytest.mark.parametrize("children,tokens", [(1, 9), (4, 9), (4, 1), (40, 15)])
+def test_copying_warps_of_a_fork(children, tokens):
+    """No warp of a fork has a second copy while SMs are left over: 12 warps of a CTA copy."""
+    ctx = kvx.kvx_create(0)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    bytes_ = torch.zeros((2, 32, 2 * children + 1, 16, 2048), dtype=torch.uint8, device="cuda")
+    p = kvx.Pool.from_tensor(bytes_, 16)
+    refs = torch.zeros(2 * children + 1, dtype=torch.int32, device="cuda")
+    refs[0] = 1
+    parent = torch.zeros(1, dtype=torch.int32, device="cuda")
+    child = torch.zeros((children, 1), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    kvx.kvx_fork_pages(ctx, p, refs.data_ptr(), kvx.forks_array(
+        [(parent.data_ptr(), c.data_ptr(), tokens, 16, False) for c in child]))
+    items, ctas, threads, _ = kvx.kvx_last_launch(ctx)
+    torch.cuda.synchronize()
+    assert threads == 512 and items >= children * 64
+    assert ctas == min(sms, -(-items // 12))
+    assert child[:, 0].cpu().tolist() == list(range(1, children + 1))
+    assert kvx.kvx_get_status(ctx) == 0
+    kvx.kvx_destroy(ctx)
