@@ -116,19 +116,42 @@ __device__ __forceinline__ float exp2_(float x)
     return y;
 }
 
-// tanh by its definition, 1 - 2 / (exp(2 x) + 1): off by a few 2^-24 of 1 whatever x, where
-// the hardware's approximate tanh is off by 2^-11.
-__device__ __forceinline__ float tanh_(float x)
-{
-    return 1.0f - __fdividef(2.0f, exp2_(x * (2.0f * kLog2e)) + 1.0f);
-}
-
 // tanh x = x P(x^2) for |x| <= 1/2: P of degree 3 with the least largest relative error there
 // (6e-7 in 32 bits; by weighted least squares iterated to it).  Scores rarely leave that range
 // under a cap, and it takes no special-function instruction.  kTanh[i] goes with x^(2 i).
 const int kTanhTerms = 4;
 __device__ constexpr float kTanh[kTanhTerms] = {0.999999464f, -0.333263189f, 0.131902963f,
                                                 -0.0444022268f};
+
+// tanh by its definition, 1 - 2 / (exp(2 x) + 1): off by a few 2^-24 of 1 whatever x, where
+// the hardware's approximate tanh is off by 2^-11.
+__device__ __forceinline__ float tanh_of_1(float x)
+{
+    return 1.0f - __fdividef(2.0f, exp2_(x * (2.0f * kLog2e)) + 1.0f);
+}
+
+// And off by a few 2^-24 of itself: a cap far above the scores, whose tanh is then small,
+// multiplies what that is off by.
+__device__ __forceinline__ float tanh_(float x)
+{
+    const float u = x * x;
+    float p = kTanh[kTanhTerms - 1];
+#pragma unroll
+    for (int n = kTanhTerms - 2; n >= 0; --n)
+        p = fmaf(p, u, kTanh[n]);
+    return fabsf(x) <= 0.5f ? x * p : tanh_of_1(x);
+}
+
+// Largest |z| up to which tanh(inner z) may be had from kTanh with the powers of `inner` in the
+// coefficients: 1/2 / inner, and less where a cap far above the scores makes `inner` so small
+// that they fall out of the normal numbers, x^6 and x^4 or all but 1 among them, and nothing
+// may be missed that they would add.
+__device__ __forceinline__ float tanh_reach(float inner)
+{
+    inner = fabsf(inner);
+    const float x = inner > 2e-6f ? 0.5f : inner > 1e-9f ? 0.015625f : 0.00048828125f;
+    return inner > 0.0f && inner < 1e4f ? fminf(x / inner, 1e18f) : 0.0f;
+}
 
 // What turns q . k into a score in units of log 2.
 struct Score {

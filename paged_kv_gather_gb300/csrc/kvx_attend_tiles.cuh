@@ -839,7 +839,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 const float factor = score.factor * row_factor;
                 // Under a cap, the terms of cap tanh(inner x) / x in x^2.
                 const float inner = score.inner * row_factor;
-                const bool series_fits = inner > 1e-4f && inner < 1e4f;
+                const float series_reach = tanh_reach(inner);
                 uint64_t series[kTanhTerms];
                 {
                     // Without a cap the first term alone is used, and is the factor itself.
@@ -925,11 +925,13 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                                     more = max3_abs(more, z[k + 2], z[k + 3]);
                                 }
                                 most = fmaxf(most, more);
-                                const bool small = series_fits && most * inner <= 0.5f;
-                                if (!__all_sync(0xffffffffu, small)) {
+                                // Past the series' reach tanh is good to 2^-22 of 1, which
+                                // the cap multiplies: less than what 32 bits make of products
+                                // that large.
+                                if (!__all_sync(0xffffffffu, most <= series_reach)) {
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
-                                        z[k] = score.cap * tanh_(z[k] * inner);
+                                        z[k] = score.cap * tanh_of_1(z[k] * inner);
                                     if (behind) {
 #pragma unroll
                                         for (int k = 0; k < 32; ++k)
