@@ -487,8 +487,9 @@ typedef struct kvx_attn_cfg {
  *     s_j = softcap * tanh(scale * k_scale * q.k_j / softcap) - slopes[h] * |p - j|,
  *     out = v_scale * sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j).
  * Every row sees its own position, so no row is empty.  Scores, the softmax statistics and
- * the sums are held in 32 bits; the weights are rounded to `type` for the product with V, and
- * the result once more to `type`.  The weight of a hidden key is exactly 0, but keys that some
+ * the sums are held in 32 bits; the weights are rounded to 16 bits for the product with V (to
+ * `type`, or to half precision over an e4m3 cache; in half precision they reach down to 2^-32
+ * of the largest), and the result once to `type`.  The weight of a hidden key is exactly 0, but keys that some
  * row of the request sees must be finite: pages, slots past n_tokens and positions that no
  * row sees are never used, whatever they hold (page-table entries for them may be anything).
  *

@@ -173,6 +173,7 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
     typedef Elem<TYPE> E;
     constexpr bool kEight = L::kEight;
     constexpr int kMath = kEight ? KVX_TYPE_HALF : TYPE;  // of the matrix products
+    constexpr float kRoom = Elem<kMath>::kRoom;
     constexpr int kSteps = D / 16, kRowsMax = 8 * NT;
     constexpr int kSlot = row_slot_floats<D, NT>();
     char *smem = attend_smem;
@@ -383,11 +384,11 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
                             z = -INFINITY;
                     }
                     s[n][x] = z;
-                    lift |= z > m[n][e] + 8.0f;
+                    lift |= z > m[n][e] + (kRoom + 8.0f);
                 }
-            // What is subtracted need not be the maximum: it may lag by up to 2^8, which
-            // neither a 32-bit sum nor a weight in either 16-bit type minds.  So lanes compare
-            // notes, and the output is rescaled, only past that.
+            // What is subtracted need not be the maximum (less kRoom): it may lag by up to
+            // 2^8, which neither a 32-bit sum nor a weight in either 16-bit type minds.  So
+            // lanes compare notes, and the output is rescaled, only past that.
             if (__any_sync(0xffffffffu, lift)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -397,7 +398,7 @@ kvx_attend_rows_kernel(const Attend a, const Work w)
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1)
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const float next = fmaxf(m[n][e], top);
+                        const float next = fmaxf(m[n][e], top - kRoom);
                         const float keep = next == -INFINITY ? 1.0f : exp2_(m[n][e] - next);
                         m[n][e] = next;
                         l[n][e] *= keep;

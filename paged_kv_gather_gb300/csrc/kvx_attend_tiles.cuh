@@ -977,11 +977,12 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                         tc_wait_st();
                     }
                     top *= unit;
-                    // The subtracted maximum may lag by up to 2^8; O is rescaled only past
-                    // that.  S of this step is complete, so P V of the last one is too.
-                    const bool lift = top > m + 8.0f;
+                    // The subtracted number may lag by up to 2^8 more than its room; O is
+                    // rescaled only past that.  S of this step is complete, so P V of the last
+                    // one is too.
+                    const bool lift = top > m + (P::kRoom + 8.0f);
                     if (__any_sync(0xffffffffu, lift)) {
-                        const float next = lift ? top : m;
+                        const float next = lift ? top - P::kRoom : m;
                         const float keep = lift ? exp2_(m - next) : 1.0f;
                         m = next;
                         l *= keep;

@@ -1,4 +1,7 @@
-"""kvx_attend where most is asked of 32 bits: caps far from the scores.  References are in 64 bits."""
+"""kvx_attend where most is asked of 32 bits: caps far from the scores, and many
+keys of small weight beside a large one.  References are in 64 bits."""
+import math
+
 import numpy as np
 import pytest
 
@@ -73,3 +76,40 @@ def test_caps_of_every_size(ctx, softcap, new, dtype, kv):
         lt = d + 2.0 ** -20 * (1 + np.abs(ref_lse)) + 2.0 ** -20 * reach
         assert (np.abs(got_lse[rows] - ref_lse) <= lt).all(), np.max(
             np.abs(got_lse[rows] - ref_lse) / lt)
+
+
+@pytest.mark.parametrize("dtype,kv", [("bf16", "fp8"), ("fp16", "fp8"), ("fp16", "fp16")])
+@pytest.mark.parametrize("new,requests,tokens", [(1, 160, 20000), (4, 160, 20000), (40, 160, 3000)])
+def test_many_small_weights_beside_a_large_one(ctx, new, requests, tokens, dtype, kv):
+    """One key 17.5 above all the others, whose values alone make up the result.
+
+    Half-precision weights are made 2^7 times their size, in steps of 2^-24 at the least: each
+    is off by at most 2^-32 of the largest, or by its own 2^-11.  With n such keys of values
+    up to V beside a sum of weights of at least 1, that is n 2^-32 V."""
+    heads, group, dim, gap = 2, 2, 64, 17.5
+    group = group if new < 40 else 4
+    cache = Cache([tokens], heads, dim, 16, kv, seed=1)
+    main = tokens - new      # seen by every row, in the first step of the walk
+    slots = (cache.tables[0].long()[torch.arange(tokens, device="cuda") // 16] * 16
+             + torch.arange(tokens, device="cuda") % 16)
+    top = 440.0 if kv == "fp8" else 1000.0
+    x = torch.zeros((2, tokens, heads, dim), device="cuda")
+    x[0, main] = 1.0
+    x[1] = top
+    x[1, main] = 0.0
+    x = x.to(TORCH[kv])
+    flat = cache.pool.view(torch.uint8).view(2, 2, cache.n_pages * 16, -1)
+    flat[:, LAYER, slots] = x.view(torch.uint8).view(2, tokens, -1)
+    value = float(x[1, main - 1, 0, 0])
+    q = torch.ones((requests * new, heads * group, dim), dtype=TORCH[dtype], device="cuda")
+    cfg = kvx.attn_config(heads * group, heads, dim, dtype, kv, scale=gap / dim)
+    reqs = kvx.requests_array([(cache.tables[0].data_ptr(), None, tokens)] * requests)
+    got, got_lse = attend(ctx, cache, reqs, [new] * requests, q, cfg)
+    n = np.tile(np.arange(tokens - new, tokens), requests)[:, None]  # keys beside the large one
+    tail = n * math.exp(-gap)
+    ref, ref_lse = (tail * value / (1 + tail))[..., None], gap + np.log1p(tail)
+    d = dim * 2.0 ** -24 * gap
+    tol = (2.02 * ROUNDOFF[dtype] + 2 * d + 2.0 ** -18) * ref + n[..., None] * 2.0 ** -32 * value
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), (np.max(err / tol), np.max(err / ref))
+    assert (np.abs(got_lse - ref_lse) <= d + 2.0 ** -18 * gap).all()
