@@ -19,8 +19,10 @@ namespace {
 // operand by a transposition of 8 x 8 blocks between lanes.
 //
 // An e4m3 cache is multiplied in half precision, which holds every code exactly, whatever the
-// type of q: q is first scaled by a power of two per row to at most 1, which is exact for
-// bfloat16 down to 2^-24 of the row's largest element.  The order of the 16 elements a matrix
+// type of q: q is first scaled by a power of two per row to at most 1.  That is exact for
+// elements down to 2^-17 of full scale in bfloat16 (8 bits above half's last, 2^-24), to 2^-14
+// in half; smaller ones are off by at most 2^-25 of it, which is what 32 bits make of products
+// with the row's largest element.  The order of the 16 elements a matrix
 // instruction sums over is free as long as both operands share it, and so is that of O's
 // columns; they are chosen so that a thread's operands are 16 consecutive bytes of a key.
 //

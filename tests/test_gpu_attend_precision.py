@@ -1,5 +1,6 @@
-"""kvx_attend where most is asked of 32 bits: caps far from the scores, and many
-keys of small weight beside a large one.  References are in 64 bits."""
+"""kvx_attend where most is asked of 32 bits: caps far from the scores, many keys
+of small weight beside a large one, rows of q that span many powers of two.  References are in
+64 bits."""
 import math
 
 import numpy as np
@@ -113,3 +114,45 @@ def test_many_small_weights_beside_a_large_one(ctx, new, requests, tokens, dtype
     err = np.abs(got - ref)
     assert (err <= tol).all(), (np.max(err / tol), np.max(err / ref))
     assert (np.abs(got_lse - ref_lse) <= d + 2.0 ** -18 * gap).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new", [1, 4, 60])
+def test_rows_of_q_that_span_many_powers_of_two(ctx, new, dtype):
+    """An e4m3 cache is multiplied in half precision: q, scaled to at most 1, keeps its elements
+    to 2^-25 of the row's largest.  Large elements meet zeros in K here, so that the small ones
+    make the scores; tolerance: that 2^-25 for every element, and the products' 32 bits."""
+    tokens, heads, group, dim, ks = [new, 900], 2, 3, 128, 2.0 ** 4
+    cache = Cache(tokens, heads, dim, 16, "fp8", scale=8.0, seed=8)
+    small = np.arange(dim) % 4 != 0
+    for r, t in enumerate(tokens):
+        cache.values[r][0, LAYER][:, :, ~small] = 0.0
+        at = (cache.tables[r].long()[torch.arange(t, device="cuda") // 16] * 16
+              + torch.arange(t, device="cuda") % 16)
+        x = torch.tensor(cache.values[r][0, LAYER], device="cuda").float().to(TORCH["fp8"])
+        flat = cache.pool.view(torch.uint8).view(2, 2, cache.n_pages * 16, -1)
+        flat[0, LAYER, at] = x.view(torch.uint8).view(t, -1)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    q = torch.randn((2 * new, heads * group, dim), device="cuda", generator=g)
+    power = torch.randint(-22, -12, q.shape, device="cuda", generator=g).float()
+    q = q * torch.where(torch.tensor(small, device="cuda"), torch.exp2(power),
+                        torch.ones((), device="cuda"))
+    q = q.to(TORCH[dtype])
+    scale = 2.0 ** 6
+    cfg = kvx.attn_config(heads * group, heads, dim, dtype, "fp8", scale=scale)
+    got, got_lse = attend(ctx, cache, cache.requests(), [new, new], q, cfg, ks, 1.0)
+    qd, u = q.double().cpu().numpy(), ROUNDOFF[dtype]
+    for r in range(2):
+        k, v = cache.values[r][0, LAYER] * ks, cache.values[r][1, LAYER]
+        rows = slice(r * new, (r + 1) * new)
+        ref, ref_lse, spread, reach = attend_reference(qd[rows], k, v, new, group, scale)
+        most = np.abs(qd[rows]).max(-1)                                  # of a row of q
+        size = np.abs(k).sum(-1).max(0)                                  # sum |k| per KV head
+        d = (dim * 2.0 ** -24 * reach
+             + 2.0 * 2.0 ** -25 * most * np.repeat(size, group)[None] * scale)
+        tol = 1.01 * u * (np.abs(ref) + spread) + (2 * d[..., None] + 2.0 ** -18) * spread
+        if dtype == "fp16":
+            tol += 2.0 ** -25 * (1 + tokens[r] * np.abs(v).max())
+        assert (np.abs(got[rows] - ref) <= tol).all(), np.max(np.abs(got[rows] - ref) / tol)
+        assert (np.abs(got_lse[rows] - ref_lse) <= d + 2.0 ** -20 * (1 + np.abs(ref_lse))).all()
