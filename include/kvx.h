@@ -193,7 +193,10 @@ typedef struct kvx_launch_cfg {
                              kernel, so events recorded after it keep their meaning.  Use it
                              only when this transfer touches no memory the previous kernel
                              writes and writes none it reads (for example consecutive
-                             per-layer loads).  A call made with it waits on the host for
+                             per-layer loads).  Overlapped transfers one behind the other
+                             may all run at once, beside a page upkeep, append or attention
+                             call right ahead of them, which lets its next kernel start
+                             early too: the condition holds against all of these.  A call made with it waits on the host for
                              its descriptor copy (a few microseconds) before it enqueues the
                              kernel.  Store, load and transform with the warp-segment
                              mapping; 0 elsewhere.  0 = off (default) */
@@ -489,14 +492,19 @@ typedef struct kvx_attn_cfg {
  * Every row sees its own position, so no row is empty.  Scores, the softmax statistics and
  * the sums are held in 32 bits; the weights are rounded to 16 bits for the product with V (to
  * `type`, or to half precision over an e4m3 cache; in half precision they reach down to 2^-32
- * of the largest), and the result once to `type`.  The weight of a hidden key is exactly 0, but keys that some
- * row of the request sees must be finite: pages, slots past n_tokens and positions that no
- * row sees are never used, whatever they hold (page-table entries for them may be anything).
+ * of the largest), and the result once to `type`.  The weight of a hidden key is exactly 0,
+ * but keys that some row of the request sees must be finite: pages, slots past n_tokens and
+ * positions that no row sees are never used, whatever they hold (page-table entries for them
+ * may be anything).  The same batch gives the same bits every time.  A request's bits depend
+ * on its batch: where its keys are cut for the SMs, and which of two kernels takes a few rows
+ * beside chunks, follow from all of it, and move results within the roundings above.
  *
  * A plan holds a step's batch on the device, for every layer of the step and any number of
  * launches: it is made once (kvx_attn_plan_create allocates), refilled for the next step with
  * kvx_attn_plan_update (which does not), and its launches may be captured into a CUDA graph.
- * It keeps the addresses of page tables and slopes and a copy of the pool's pointers.  Its
+ * It keeps the addresses of page tables and slopes and a copy of the pool's pointers, and
+ * holds 41 MB of device memory at head_dim 128, 21 at 64, mostly for parts of results (two of
+ * 256 rows per SM), whatever its batch: any later one may need them.  Its
  * workspace serves one launch at a time: launches of one plan must not overlap in time, and a
  * graph captured from a plan must be captured again after an update.  A request has at most
  * 2^30 tokens, a step 2^31 - 256 rows of new tokens x query heads (KVX_ERR_CAPACITY above).
@@ -519,8 +527,8 @@ void kvx_attn_plan_destroy(kvx_attn_plan *plan);
 
 /* Write the step's new K and V, [rows][kv_heads][head_dim] of `type` with k_stride and
  * v_stride elements from token to token (0 = packed), into layer `layer`'s pages.  For an
- * e4m3 cache the values are divided by k_scale / v_scale and rounded to the nearest code,
- * beyond +-448 to +-448 (NaN stays NaN); otherwise the bytes are copied and the scales are
+ * e4m3 cache the values are divided by k_scale / v_scale in 32 bits and the quotient rounded
+ * to the nearest code, beyond +-448 to +-448 (NaN stays NaN); otherwise the bytes are copied and the scales are
  * not used.  Pointers 16-byte aligned, strides multiples of 8 elements. */
 kvx_status kvx_append_tokens(const kvx_attn_plan *plan, int layer, const void *k, const void *v,
                              int64_t k_stride, int64_t v_stride, float k_scale, float v_scale,

@@ -58,9 +58,9 @@ struct Attend {
 
 // The schedule of one kernel.  The keys that each unit of rows visits, cut into tiles, are
 // laid end to end over all units, and every CTA takes an equal stretch of that line, whatever
-// the lengths (AttnStart); or units are dealt to the CTAs one by one, each a share of its own.  A unit that one CTA does not finish alone is joined from partial
-// results: CTA c keeps one it began and did not finish in slot 2 c + 1, and one it took over
-// from CTA c - 1 in slot 2 c.
+// the lengths (AttnStart); or units are dealt to the CTAs one by one, each a share of its own.
+// A unit that one CTA does not finish alone is joined from partial results: CTA c keeps one it
+// began and did not finish in slot 2 c + 1, and one it took over from CTA c - 1 in slot 2 c.
 struct Work {
     const AttnReq *reqs;       // of this kernel, those with rows
     const AttnStart *starts;   // [CTAs], and behind them the shares that follow those

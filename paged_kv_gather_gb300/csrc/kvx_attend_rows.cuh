@@ -22,14 +22,14 @@ namespace {
 // type of q: q is first scaled by a power of two per row to at most 1.  That is exact for
 // elements down to 2^-17 of full scale in bfloat16 (8 bits above half's last, 2^-24), to 2^-14
 // in half; smaller ones are off by at most 2^-25 of it, which is what 32 bits make of products
-// with the row's largest element.  The order of the 16 elements a matrix
-// instruction sums over is free as long as both operands share it, and so is that of O's
-// columns; they are chosen so that a thread's operands are 16 consecutive bytes of a key.
+// with the row's largest element.  The order of the 16 elements a matrix instruction sums over
+// is free as long as both operands share it, and so is that of O's columns; they are chosen so
+// that a thread's operands are 16 consecutive bytes of a key.
 //
 // Measured: 64 bf16 requests of 1k to 32k tokens, 8 KV heads, 321 us (2.2 GB, 6.9 TB/s; a copy
 // reaches 6.8); 64 e4m3 requests, 4 KV heads, 92 us (552 MB, 5.9 TB/s, where the heads' runs
 // of 128 bytes are what memory serves less well: neither more bytes in flight nor more warps
-// change it); one request of 32k tokens 28 us (134 MB), of 512 tokens 5.4 us, of which three
+// change it); one request of 32k tokens 26 us (134 MB), of 512 tokens 5.4 us, of which three
 // are a launch and the rest the chain page id, keys, products, join.
 const int kRowWarps = 8;
 const int kRowThreads = 32 * kRowWarps;

@@ -25,13 +25,19 @@ namespace {
 // call 128-byte swizzle.  K and q are read along it, V across it (its rows are the summed
 // index), so the same copy serves both.
 //
-// A step of 256 rows x 128 keys costs the tensor cores 2048 cycles and takes about 2540: each
-// tile's own chain (scores out, maximum, weights, the second half of P V, the next scores) is
-// 1490 + 1050 cycles, and tensor memory is full at D = 128, so no third tile fills the gap.
-// Measured: 2048 rows x 8 heads behind 32k tokens (2.13 TFLOP) 1.37 ms on its own and 1.45-1.5
-// ms in long runs under the power cap (cuBLAS sustains 1.70 PFLOP/s there); the tensor pipe is
-// active 68 % of the cycles.  A unit costs about 9000 cycles beside its steps (q in, first
-// scores, O out), which is what short prompts pay: 2k tokens 36 us, 8k 375 us.
+// A step of 256 rows x 128 keys costs the tensor cores 2048 cycles and takes 2950 (units 128
+// steps longer, at the clock sampled meanwhile; the tensor pipe is active 66-69 % of the
+// cycles): each tile's own chain (scores out, maximum, weights, the second half of P V, the next
+// scores) is 1490 + 1050 of them by counters in the kernel, and tensor memory is full at
+// D = 128, so no third tile fills the gap.  With options a step takes 3710 (bias), 5060 (cap),
+// 5300 (both) or 7820 cycles (scores past half the cap), with a cap the tensor pipe active 40 %
+// and the FMA pipe 37 % of them: S is read, shaped and written back one
+// block of 32 columns after the other, and read again for the weights.  Over an e4m3 cache,
+// converted by three warps, it takes 3620; at D = 64 2270, of which 1024 are products.
+// Measured: 2048 new tokens x 8 heads behind 32k tokens (2.13 TFLOP) 1.37 ms on its own and
+// 1.45-1.5 ms in long runs under the power cap (cuBLAS sustains 1.70 PFLOP/s there).  A unit
+// costs about 9000 cycles beside its steps (q in, first scores, O out), which is what short
+// prompts pay: 2k tokens 36 us, 8k 373 us.
 const int kTileThreads = 384;
 const int kTileRows = 128;
 const int kTileKeys = 128;
