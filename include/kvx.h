@@ -196,9 +196,9 @@ typedef struct kvx_launch_cfg {
                              per-layer loads).  Overlapped transfers one behind the other
                              may all run at once, beside a page upkeep, append or attention
                              call right ahead of them, which lets its next kernel start
-                             early too: the condition holds against all of these.  A call made with it waits on the host for
-                             its descriptor copy (a few microseconds) before it enqueues the
-                             kernel.  Store, load and transform with the warp-segment
+                             early too: the condition holds against all of these.  A call
+                             made with it waits on the host for its descriptor copy (a few
+                             microseconds) before it enqueues the kernel.  Store, load and transform with the warp-segment
                              mapping; 0 elsewhere.  0 = off (default) */
 } kvx_launch_cfg;
 
@@ -528,8 +528,8 @@ void kvx_attn_plan_destroy(kvx_attn_plan *plan);
 /* Write the step's new K and V, [rows][kv_heads][head_dim] of `type` with k_stride and
  * v_stride elements from token to token (0 = packed), into layer `layer`'s pages.  For an
  * e4m3 cache the values are divided by k_scale / v_scale in 32 bits and the quotient rounded
- * to the nearest code, beyond +-448 to +-448 (NaN stays NaN); otherwise the bytes are copied and the scales are
- * not used.  Pointers 16-byte aligned, strides multiples of 8 elements. */
+ * to the nearest code, beyond +-448 to +-448 (NaN stays NaN); otherwise the bytes are copied
+ * and the scales are not used.  Pointers 16-byte aligned, strides multiples of 8 elements. */
 kvx_status kvx_append_tokens(const kvx_attn_plan *plan, int layer, const void *k, const void *v,
                              int64_t k_stride, int64_t v_stride, float k_scale, float v_scale,
                              kvx_stream_t stream);

@@ -145,7 +145,7 @@ __device__ __forceinline__ float tanh_(float x)
 // Largest |z| up to which tanh(inner z) may be had from kTanh with the powers of `inner` in the
 // coefficients: 1/2 / inner, and less where a cap far above the scores makes `inner` so small
 // that they fall out of the normal numbers, x^6 and x^4 or all but 1 among them, and nothing
-// may be missed that they would add.
+// may be missed that they would add.  1e18: z^2 is finite.
 __device__ __forceinline__ float tanh_reach(float inner)
 {
     inner = fabsf(inner);

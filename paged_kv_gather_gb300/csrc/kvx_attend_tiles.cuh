@@ -356,7 +356,8 @@ __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes)
                  : "memory");
 }
 
-// Walks a CTA's share of the line, or the units dealt to it; every role of the CTA steps through the same units.
+// Walks a CTA's share of the line, or the units dealt to it; every role of the CTA steps through
+// the same units.
 struct Walk {
     const Attend &a;
     const Work &w;
