@@ -90,6 +90,8 @@ typedef enum kvx_status {
                                            nothing */
 #define KVX_DEV_PAGE_NOT_HELD 0x8u      /* a page table named a page nobody holds (its count
                                            is 0); that entry was skipped */
+#define KVX_DEV_BEAM_OUT_OF_RANGE 0x10u /* a beam continued one outside its group; the group
+                                           was skipped */
 
 typedef enum kvx_chunk_layout {
     KVX_CHUNK_LAYER_MAJOR = 0,
@@ -451,7 +453,36 @@ kvx_status kvx_compact_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
                              const kvx_table *tables, int n_tables, int32_t *n_live,
                              int32_t *remap, kvx_stream_t stream);
 
-/* The host checks of the three calls above (forks or tables may be NULL with a count of 0):
+/* A group of beams (the hypotheses of one prompt) that all hold n_tokens tokens. */
+#define KVX_MAX_BEAMS 32
+typedef struct kvx_beams {
+    int32_t *tables;         /* device array [width][table_stride]: page table of each beam */
+    int64_t table_stride;    /* entries from table to table, >= ceil(n_tokens / page_size) */
+    const int32_t *parents;  /* device array [width]: the beam, in [0, width), that each beam
+                                continues (kvx_select_beams writes them) */
+    int32_t width;           /* 1 .. KVX_MAX_BEAMS */
+    int32_t n_tokens;        /* >= 0 */
+} kvx_beams;
+
+/* Reorder: after a step of a beam search, make beam b of every group the continuation of beam
+ * parents[b], in the tables, the counts and the pages.  Full pages are taken over (a count goes
+ * up for every beam that takes a page and down for every beam that held it).  A partly filled
+ * last page is every beam's own (its count is 1, as kvx_fork_pages leaves it): the first of the
+ * beams that continue one parent keeps the parent's; of the others, in order, the i-th gets the
+ * last page of the i-th beam that nobody continues, with the parent's tokens copied into it in
+ * every layer, K and V.  So no free page is needed.  Slots behind the tokens, and table entries
+ * behind ceil(n_tokens / page_size), stay with the beam as they are.  A page that nobody holds
+ * afterwards has count 0.  `parents` is read on the device: nothing waits for the host.  Groups
+ * share no table (checked at validation level 2); they may share pages.  One or two kernel
+ * launches on `stream`, with descriptors as for the calls above (48 bytes per group). */
+kvx_status kvx_reorder_beams(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                             const kvx_beams *beams, int n_groups, kvx_stream_t stream);
+
+/* The host checks of kvx_reorder_beams. */
+kvx_status kvx_beams_validate(const kvx_pool *pool, const int32_t *refs, const kvx_beams *beams,
+                              int n_groups, int level, char *msg, size_t msg_len);
+
+/* The host checks of fork, free and compact (forks or tables may be NULL with a count of 0):
  * sizes and pointers at level 0 and 1, tables that meet at level 2. */
 kvx_status kvx_upkeep_validate(const kvx_pool *pool, const int32_t *refs,
                                const kvx_fork *forks, int n_forks, const kvx_table *tables,
@@ -463,15 +494,29 @@ kvx_status kvx_upkeep_validate(const kvx_pool *pool, const int32_t *refs,
 #define KVX_TYPE_HALF 0        /* IEEE half precision */
 #define KVX_TYPE_BFLOAT 1      /* bfloat16 */
 #define KVX_TYPE_FP_EIGHT 2    /* e4m3 (finite, 8 bits), cache only */
+#define KVX_TYPE_FP_FOUR 3     /* e2m1 (4 bits) in blocks with an e4m3 scale, cache only */
+#define KVX_TYPE_FLOAT 4       /* 32 bits, logits only */
+
+/* Bytes of a cache token of kv_type (a pool's token_bytes), 0 for a type that no cache has.
+ * For all but KVX_TYPE_FP_FOUR: kv_heads x head_dim x the type's bytes.
+ *
+ * KVX_TYPE_FP_FOUR holds a token as [kv_heads][head_dim / 2] bytes of codes (element 2 i in the
+ * low half of byte i, 2 i + 1 in the high half; a code is a sign and one of 0, 1/2, 1, 3/2, 2,
+ * 3, 4, 6), then [kv_heads][head_dim / 16] e4m3 scales, one for every 16 elements of a head, and
+ * pads that to a multiple of 16 bytes (the padding is neither written nor used): 4.5 bits per
+ * element.  An element is its code x its block's scale x k_scale (v_scale); the first product
+ * is exact in half precision, in which such a cache is multiplied. */
+int64_t kvx_token_bytes(int kv_heads, int head_dim, int kv_type);
 
 /* What stays the same for every layer and step of a model. */
 typedef struct kvx_attn_cfg {
     int32_t q_heads;       /* query heads, a multiple of kv_heads */
     int32_t kv_heads;      /* heads of the cache: token_bytes = kv_heads x head_dim x bytes of
-                              kv_type */
+                              kv_type (kvx_token_bytes) */
     int32_t head_dim;      /* 64 or 128 */
     int32_t type;          /* KVX_TYPE_HALF or KVX_TYPE_BFLOAT: q, new K and V, output */
-    int32_t kv_type;       /* the cache: the same as `type`, or KVX_TYPE_FP_EIGHT */
+    int32_t kv_type;       /* the cache: the same as `type`, KVX_TYPE_FP_EIGHT or
+                              KVX_TYPE_FP_FOUR */
     int32_t window;        /* > 0: a row at position i sees positions j with i - j < window;
                               0: no window */
     float scale;           /* factor of q.k; 0 = 1 / sqrt(head_dim) */
@@ -491,8 +536,8 @@ typedef struct kvx_attn_cfg {
  *     out = v_scale * sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j).
  * Every row sees its own position, so no row is empty.  Scores, the softmax statistics and
  * the sums are held in 32 bits; the weights are rounded to 16 bits for the product with V (to
- * `type`, or to half precision over an e4m3 cache; in half precision they reach down to 2^-32
- * of the largest), and the result once to `type`.  The weight of a hidden key is exactly 0,
+ * `type`, or to half precision over a cache of 8 or 4 bits; in half precision they reach down
+ * to 2^-32 of the largest), and the result once to `type`.  The weight of a hidden key is exactly 0,
  * but keys that some row of the request sees must be finite: pages, slots past n_tokens and
  * positions that no row sees are never used, whatever they hold (page-table entries for them
  * may be anything).  The same batch gives the same bits every time.  A request's bits depend
@@ -528,11 +573,43 @@ void kvx_attn_plan_destroy(kvx_attn_plan *plan);
 /* Write the step's new K and V, [rows][kv_heads][head_dim] of `type` with k_stride and
  * v_stride elements from token to token (0 = packed), into layer `layer`'s pages.  For an
  * e4m3 cache the values are divided by k_scale / v_scale in 32 bits and the quotient rounded
- * to the nearest code, beyond +-448 to +-448 (NaN stays NaN); otherwise the bytes are copied
- * and the scales are not used.  Pointers 16-byte aligned, strides multiples of 8 elements. */
+ * to the nearest code, beyond +-448 to +-448 (NaN stays NaN); a cache of `type` takes the bytes
+ * as they are and the scales are not used.  For a 4-bit cache a block's scale is the code of
+ * e4m3 nearest to its largest magnitude / (6 k_scale), at most 448, and an element becomes the
+ * code nearest to element / (scale x k_scale), ties to the even code, beyond +-6 to +-6 (k_scale
+ * and v_scale then lie between 2^-100 and 2^100); a block whose scale rounds to 0 is all 0, and one that holds a NaN gets the scale NaN, so that all of
+ * it reads as NaN.  Both factors are reciprocals in 32 bits: an element within 2^-22 of a border
+ * between two codes may go to either.  Pointers 16-byte aligned, strides multiples of 8
+ * elements. */
 kvx_status kvx_append_tokens(const kvx_attn_plan *plan, int layer, const void *k, const void *v,
                              int64_t k_stride, int64_t v_stride, float k_scale, float v_scale,
                              kvx_stream_t stream);
+
+/* Rotation of q and K by position. */
+typedef struct kvx_rope {
+    const float *freqs;        /* device array [rotary_dim / 2]: radians per position, finite */
+    const int32_t *positions;  /* device array [rows]: position of each new token (any number);
+                                  NULL: its place in its request */
+    int32_t rotary_dim;        /* elements of a head that are rotated, the first ones: a multiple
+                                  of 16 up to head_dim */
+    int32_t interleaved;       /* 0: element i is paired with i + rotary_dim / 2; 1: elements
+                                  2 i and 2 i + 1 are */
+    float magnitude;           /* factor of the cosines and sines (1 where there is none) */
+    int32_t reserved;          /* set to 0 */
+} kvx_rope;
+
+/* kvx_append_tokens with the position rotation on the way: pair i (x, y) of every head of K, and
+ * of q, becomes magnitude x (x cos a - y sin a, y cos a + x sin a) at the angle a = position x
+ * freqs[i], elements past rotary_dim stay as they are, and V is not rotated.  Rotated K goes into
+ * layer `layer`'s pages without another rounding before the cache's own, rotated q to q_out
+ * [rows][q_heads][head_dim] of `type`.  Angles are taken in whole turns of 64 bits, so that they
+ * are as exact at position 2^30 as at 1 (to 4e-9 while freqs are at most 1), products in 32 bits.
+ * q may be NULL (then q_out is not used) and q_out may be q itself with the same stride; no other
+ * output meets an input.  Strides, alignment and scales as for kvx_append_tokens. */
+kvx_status kvx_append_rotated(const kvx_attn_plan *plan, int layer, const kvx_rope *rope,
+                              const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                              const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                              float k_scale, float v_scale, kvx_stream_t stream);
 
 /* out [rows][q_heads][head_dim] = attention of q over layer `layer`, both of `type`, with
  * q_stride and out_stride elements from token to token (0 = packed).  lse: device array
@@ -547,6 +624,47 @@ kvx_status kvx_attend(const kvx_attn_plan *plan, int layer, const void *q, int64
 kvx_status kvx_attn_validate(const kvx_pool *pool, const kvx_request *reqs, int n_req,
                              const int32_t *n_new, const int32_t *prefix,
                              const kvx_attn_cfg *cfg, int level, char *msg, size_t msg_len);
+
+/* ---------------------------------------------------------------- beam search */
+
+#define KVX_MAX_PICKS 64
+#define KVX_MAX_VOCAB 524000
+
+/* What stays the same for every step of a beam search. */
+typedef struct kvx_select_cfg {
+    int32_t n_groups;      /* prompts, > 0 */
+    int32_t width;         /* beams of each, 1 .. KVX_MAX_BEAMS */
+    int32_t vocab;         /* tokens, 1 .. KVX_MAX_VOCAB */
+    int32_t picks;         /* continuations wanted of each group, 1 .. KVX_MAX_PICKS */
+    int32_t type;          /* of the logits: KVX_TYPE_HALF, KVX_TYPE_BFLOAT or KVX_TYPE_FLOAT */
+    int32_t done_token;    /* token given for a beam that is done */
+} kvx_select_cfg;
+
+/* Bytes of workspace that a call with this configuration needs (device memory, 16-byte aligned).
+ * The caller owns it; calls and captured graphs that may overlap in time need one each. */
+kvx_status kvx_select_workspace(kvx_ctx *ctx, const kvx_select_cfg *cfg, int64_t *bytes);
+
+/* Selection over beams and vocabulary: of every group's continuations (beam b, token t) with the
+ * sums of log probabilities
+ *     scores[b] + logits[b][t] - log sum_t' exp(logits[b][t'])
+ * the `picks` largest, in falling order: their beams in parents [n_groups][picks] (what
+ * kvx_reorder_beams takes), tokens and sums in tokens and out_scores of the same shape.  logits
+ * [n_groups * width][vocab] of cfg's type with logits_stride elements from beam to beam (0 =
+ * packed); scores [n_groups * width].  A beam with done[b] != 0 (device bytes, may be NULL) has
+ * finished: its one continuation is done_token with its own sum, and its logits are not read.
+ *
+ * Continuations are ordered by their sums in 64 bits, equal ones by beam and then by token; the
+ * sum of exponentials is taken in 32 bits within 512 x 8 or 512 x 32 logits and in 64 across
+ * those, so two sums closer than about 1e-7 may change places.  The same inputs give the same
+ * bits.  A logit of -infinity rules its token out; one that is NaN or +infinity counts as
+ * -infinity.  A beam whose sum is -infinity or NaN, or that has no logit left, has no
+ * continuation; where a group has fewer than `picks`, the rest are beam 0, token -1, -infinity.
+ * Logits, scores, parents, tokens and out_scores are aligned to their elements; out_scores may be
+ * scores where picks = width.  Two kernel launches on `stream`; they may be captured. */
+kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void *logits,
+                            int64_t logits_stride, const float *scores, const uint8_t *done,
+                            int32_t *parents, int32_t *tokens, float *out_scores, void *workspace,
+                            kvx_stream_t stream);
 
 /* Read the device status word (after synchronizing `stream`), clear it, and return
  * KVX_ERR_DEVICE_STATUS if any bit was set.  flags may be NULL. */

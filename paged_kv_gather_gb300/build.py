@@ -21,11 +21,13 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkvx.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-CUDA_UNITS = ("kvx.cu", "kvx_pages.cu", "kvx_attend.cu")
+CUDA_UNITS = ("kvx.cu", "kvx_pages.cu", "kvx_attend.cu", "kvx_attend_four.cu",
+              "kvx_rotate.cu", "kvx_beams.cu")
 HOST_UNITS = ("kvx_host.cpp", "kvx_cache_host.cpp", "kvx_partition.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in CUDA_UNITS + HOST_UNITS + (
     "kvx_kernels.cuh", "kvx_internal.h", "kvx_rules.h", "kvx_ctx.h", "kvx_cache.h",
-    "kvx_attend.cuh", "kvx_attend_rows.cuh", "kvx_attend_tiles.cuh")]
+    "kvx_attend.cuh", "kvx_attend_rows.cuh", "kvx_attend_tiles.cuh", "kvx_attend_four.cuh",
+    "kvx_attend_plan.h")]
 HEADER = os.path.join(ROOT, "include", "kvx.h")
 
 

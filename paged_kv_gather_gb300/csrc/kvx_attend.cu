@@ -11,102 +11,9 @@
 #include "kvx_attend.cuh"
 #include "kvx_attend_rows.cuh"
 #include "kvx_attend_tiles.cuh"
-#include "kvx_cache.h"
-#include "kvx_ctx.h"
-
-// The attention kernels by the rows (new tokens x heads that share a KV head) of a request:
-// up to 8, up to 16, more.
-enum { kRows = 0, kMoreRows = 1, kTiles = 2, kKinds = 3 };
-
-// What a unit costs beyond its tiles, and what each part of one costs that is cut, measured:
-// in bytes of K and V read meanwhile for the kernels of few rows, in tiles for the other
-// (half as many where a cap on the scores makes tiles take twice as long).
-const int64_t kUnitBytes = 128 << 10, kPartBytes = 48 << 10;
-const int64_t kUnitTiles = 4, kPartTiles = 2;
-
-// A launch more, in tiles' time.
-const int64_t kLaunchTiles = 3;
-
-// Up to this many units per SM are dealt out one by one (Scheduler::deal); past it the shares
-// of the line come out as even, and the descriptors long.
-const int kDealtPerSm = 16;
-
-// Scratch of the schedule.
-struct DealBlock {
-    int64_t tiles;
-    int32_t request, block;
-};
-struct DealCta {
-    int64_t load;
-    int32_t cta, at;  // its number, its latest share
-};
-
-struct kvx_attn_plan {
-    kvx_ctx *ctx = nullptr;
-    kvx_attn_cfg cfg = {};
-    int32_t page_size = 0, num_pages = 0, num_layers = 0;
-    int64_t token_bytes = 0;
-    char **pools = nullptr;    // host: [2 * layer + kv]
-    int capacity = 0;          // requests
-    int n_req = 0;
-    int64_t rows = 0;
-    int ctas[kKinds] = {};     // of each kernel's launch
-    bool cut[kKinds] = {};     // whether it cuts units
-    // Descriptors: [AttnReq of each kind, of all][AttnStart of each kind, the last one's with
-    // room for units dealt out]; a pinned image, and the device's copy.
-    char *host = nullptr, *dev = nullptr;
-    DealBlock *blocks = nullptr;       // [most_dealt()]
-    DealCta *heap = nullptr;           // [num_sms]
-    CUtensorMap *maps = nullptr;       // host: as pools, where the cache is copied by tensor copies
-    int32_t box = 0;                   // keys per copy, 0: it is not
-    unsigned int *counters = nullptr;  // [most_ctas()], zero between launches
-    float *partial = nullptr;          // serves one kind's launch after the other
-    cudaEvent_t copied = nullptr;      // the last update's copy
-
-    int most_ctas() const { return 2 * ctx->num_sms; }  // of a launch
-    int most_dealt() const { return kDealtPerSm * ctx->num_sms; }
-    size_t reqs_at(int k) const  // k = kKinds: all requests, for append
-    {
-        return size_t(k) * capacity * sizeof(AttnReq);
-    }
-    size_t starts_at(int k) const
-    {
-        return reqs_at(kKinds + 1) + size_t(k) * most_ctas() * sizeof(kvx::AttnStart);
-    }
-    size_t bytes() const
-    {
-        return starts_at(kTiles) +
-               std::max(most_ctas(), most_dealt()) * sizeof(kvx::AttnStart);
-    }
-};
+#include "kvx_attend_plan.h"
 
 namespace {
-
-struct Step {
-    const AttnReq *reqs;
-    unsigned int *status;
-    int32_t n_req;
-    int32_t rows;
-    int32_t page_size;
-    int32_t num_pages;
-    Divisor page;
-};
-
-// Request of a row: the last r with row_begin <= row that has rows.  Requests without new
-// tokens share their row_begin with the next one, and the last of equals is taken.
-__device__ __forceinline__ int request_of_row(const AttnReq *reqs, int n, int row, int lane)
-{
-    int lo = 0, hi = n;  // row_begin[lo] <= row < row_begin[hi]
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) >> 5;
-        const int idx = lo + lane * step;
-        const bool ok = idx < hi && __ldg(&reqs[idx].row_begin) <= row;
-        const unsigned m = __ballot_sync(0xffffffffu, ok);
-        lo += (31 - __clz(m)) * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
 
 // ------------------------------------------------------------------------------- append
 
@@ -198,33 +105,28 @@ kvx_append_kernel(const Append a)
 
 // ---------------------------------------------------------------------------------- host
 
-// Kernel of a kind, with its shared memory and the floats of a partial result.
-struct Kernel {
-    const void *fn;
-    int threads, ctas_per_sm;
-    size_t smem;
-    int slot_floats;
-    const void *join;  // of the parts of cut units, or NULL: the kernel joins them itself
-};
-
 template <int TYPE, int KV, int D>
 Kernel kernel_of(int kind)
 {
     if (kind == kRows)
         return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D, 1>),
                 kRowThreads, row_ctas_per_sm<KV, D, 1>(), row_smem<KV, D, 1>(),
-                row_slot_floats<D, 1>(), nullptr};
+                row_slot_floats<D, 1>(), nullptr, 0, 0, 0, row_smem<KV, D, 1>()};
     if (kind == kMoreRows)
         return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D, 2>),
                 kRowThreads, row_ctas_per_sm<KV, D, 2>(), row_smem<KV, D, 2>(),
-                row_slot_floats<D, 2>(), nullptr};
+                row_slot_floats<D, 2>(), nullptr, 0, 0, 0, row_smem<KV, D, 2>()};
     return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KV, D>), kTileThreads, 1,
             size_t(TileShape<KV, D>::kBytes), TileShape<KV, D>::kSlotFloats,
-            reinterpret_cast<const void *>(kvx_attend_join_kernel<TYPE, D>)};
+            reinterpret_cast<const void *>(kvx_attend_join_kernel<TYPE, D>), kJoinThreads,
+            kBlockRows / kJoinRows, 0, size_t(TileShape<KV, D>::kBytes)};
 }
 
-Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
+Kernel pick_kernel(const kvx_attn_plan *p, int kind)
 {
+    const kvx_attn_cfg &c = p->cfg;
+    if (c.kv_type == KVX_TYPE_FP_FOUR)
+        return kvx::four_kernel(c, p->token_bytes, kind);
     const bool half = c.type == KVX_TYPE_HALF, eight = c.kv_type == KVX_TYPE_FP_EIGHT;
     const int H = KVX_TYPE_HALF, B = KVX_TYPE_BFLOAT, F = KVX_TYPE_FP_EIGHT;
     if (c.head_dim == 64)
@@ -243,8 +145,8 @@ Kernel pick_kernel(const kvx_attn_cfg &c, int kind)
 struct Scheduler {
     const kvx_attn_plan *p;
     const AttnReq *reqs;
-    int n_req, kind, group, heads, block_rows, tile_keys;
-    int64_t unit_cost, part_cost, join_cost;   // beyond the tiles, in tiles
+    int n_req, kind, group, heads, block_rows, tile_keys;  // heads: units of a block of rows
+    int64_t unit_cost, part_cost, join_cost;               // beyond the tiles, in tiles
 
     Scheduler(const kvx_attn_plan *p_, int kind_, const AttnReq *reqs_, int n)
         : p(p_), reqs(reqs_), n_req(n), kind(kind_), group(p_->cfg.q_heads / p_->cfg.kv_heads),
@@ -257,8 +159,9 @@ struct Scheduler {
             part_cost = plain ? kPartTiles : kPartTiles / 2;
             join_cost = plain ? kLaunchTiles : kLaunchTiles / 2;
         } else {
-            const int64_t tile_bytes =
-                2 * int64_t(tile_keys) * p->cfg.head_dim * kvx::type_bytes(p->cfg.kv_type);
+            if (p->cfg.kv_type == KVX_TYPE_FP_FOUR)
+                kvx::four_units(p->cfg, p->token_bytes, &heads, &tile_keys);
+            const int64_t tile_bytes = 2 * tile_keys * p->token_bytes / heads;
             unit_cost = std::max<int64_t>(1, kUnitBytes / tile_bytes);
             part_cost = std::max<int64_t>(1, kPartBytes / tile_bytes);
             join_cost = 0;
@@ -400,7 +303,7 @@ struct Scheduler {
         *n_shares = 0;
         if (tiles == 0)
             return 0;
-        const int64_t slots = int64_t(p->ctx->num_sms) * pick_kernel(p->cfg, kind).ctas_per_sm;
+        const int64_t slots = int64_t(p->ctx->num_sms) * pick_kernel(p, kind).ctas_per_sm;
         const int64_t least = 2 * part_cost, whole = INT32_MAX;
         const int64_t shares = std::min(slots, std::max<int64_t>(1, tiles / least));
         int64_t cut_time, whole_time;
@@ -464,9 +367,14 @@ kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const
         kvx::AttnStart *starts = reinterpret_cast<kvx::AttnStart *>(p->host + p->starts_at(k));
         int64_t time;
         p->ctas[k] = Scheduler(p, k, lists[k], counts[k]).run(starts, &time, &shares);
-        p->cut[k] = false;
-        for (int c = 0; c < p->ctas[k]; ++c)
-            p->cut[k] |= starts[c].tile > 0;
+        int32_t *cuts = reinterpret_cast<int32_t *>(p->host + p->cuts_at(k));
+        p->cuts[k] = 0;
+        for (int c = 0; c + 1 < p->ctas[k]; ++c)
+            if (starts[c + 1].tile > 0 && starts[c + 1].first == c)
+                cuts[p->cuts[k]++] = c;
+        p->most_rows[k] = 0;
+        for (int i = 0; i < counts[k]; ++i)
+            p->most_rows[k] = std::max<int>(p->most_rows[k], lists[k][i].n_new * group);
     }
     if (n_req) {
         e = cudaMemcpyAsync(p->dev, p->host,
@@ -485,15 +393,15 @@ typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, 
 
 // Describe each layer's K and V as a matrix [slots][heads x head_dim] for tensor copies of
 // runs of keys: the largest power of two that divides the page size, up to a tile, so that a
-// run never crosses pages.  Runs below eight keys, an e4m3 cache (converted on the way) and
-// slots past the copies' 32-bit coordinates stay with plain copies (box 0).
+// run never crosses pages.  Runs below eight keys, a cache of 8 or 4 bits (converted on the way)
+// and slots past the copies' 32-bit coordinates stay with plain copies (box 0).
 kvx_status make_maps(kvx_attn_plan *p)
 {
     int box = 1;
     while (box < kTileKeys && p->page_size % (2 * box) == 0)
         box *= 2;
     const int64_t slots = int64_t(p->num_pages) * p->page_size;
-    if (p->cfg.kv_type == KVX_TYPE_FP_EIGHT || box < 8 || slots > INT32_MAX)
+    if (p->cfg.kv_type != p->cfg.type || box < 8 || slots > INT32_MAX)
         return KVX_OK;
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -521,51 +429,6 @@ kvx_status make_maps(kvx_attn_plan *p)
     }
     p->box = box;
     return KVX_OK;
-}
-
-// A launch that may start while the kernel ahead of it on the stream drains; the kernels
-// themselves wait for that one's completion before they touch memory.
-cudaError_t launch_early(const void *fn, dim3 ctas, int threads, size_t smem, cudaStream_t s,
-                         void **args)
-{
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = ctas;
-    lc.blockDim = dim3(unsigned(threads));
-    lc.dynamicSmemBytes = smem;
-    lc.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    return cudaLaunchKernelExC(&lc, fn, args);
-}
-
-kvx_status io_check(const kvx_attn_plan *p, int layer, const void *x, int64_t *stride,
-                    int64_t heads, const char *what)
-{
-    const int64_t packed = heads * p->cfg.head_dim;
-    if (layer < 0 || layer >= p->num_layers)
-        return kvx::set_err(p->ctx, KVX_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer,
-                            p->num_layers);
-    if (!x)
-        return kvx::set_err(p->ctx, KVX_ERR_INVALID_ARG, "%s is NULL", what);
-    if (*stride == 0)
-        *stride = packed;
-    if (*stride < packed)
-        return kvx::set_err(p->ctx, KVX_ERR_INVALID_ARG, "%s: stride %lld below %lld elements",
-                            what, (long long)*stride, (long long)packed);
-    if ((reinterpret_cast<uintptr_t>(x) & 15) || *stride % 8)
-        return kvx::set_err(p->ctx, KVX_ERR_ALIGNMENT, "%s not 16-byte aligned (stride %lld)",
-                            what, (long long)*stride);
-    *stride *= 2;  // bytes
-    return KVX_OK;
-}
-
-Step step_of(const kvx_attn_plan *p)
-{
-    return {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(kKinds)), p->ctx->status_dev, p->n_req,
-            int32_t(p->rows), p->page_size, p->num_pages, Divisor::of(p->page_size)};
 }
 
 }  // namespace
@@ -616,10 +479,11 @@ kvx_status kvx_attn_plan_create(kvx_ctx *ctx, const kvx_pool *pool, const kvx_re
     size_t partial = 0;
     cudaError_t e = cudaSuccess;
     for (int k = 0; k < kKinds && e == cudaSuccess; ++k) {
-        const Kernel kn = pick_kernel(p->cfg, k);
+        const Kernel kn = pick_kernel(p, k);
         partial = std::max(partial, 2 * size_t(ctx->num_sms) * kn.ctas_per_sm * kn.slot_floats *
                                         sizeof(float));
-        e = cudaFuncSetAttribute(kn.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kn.smem));
+        e = cudaFuncSetAttribute(kn.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(kn.most_smem));
     }
     if (e == cudaSuccess)
         e = cudaHostAlloc(reinterpret_cast<void **>(&p->host), p->bytes(), cudaHostAllocDefault);
@@ -704,15 +568,17 @@ kvx_status kvx_append_tokens(const kvx_attn_plan *p, int layer, const void *k, c
         return KVX_ERR_INVALID_ARG;
     if (p->rows == 0)
         return KVX_OK;
+    if (p->cfg.kv_type == KVX_TYPE_FP_FOUR)
+        return kvx::append_rotated(p, layer, nullptr, nullptr, 0, nullptr, 0, k, v, k_stride,
+                                   v_stride, k_scale, v_scale,
+                                   reinterpret_cast<cudaStream_t>(stream));
     kvx_status st = io_check(p, layer, k, &k_stride, p->cfg.kv_heads, "k");
     if (st == KVX_OK)
         st = io_check(p, layer, v, &v_stride, p->cfg.kv_heads, "v");
+    if (st == KVX_OK)
+        st = scales_check(p, k_scale, v_scale);
     if (st != KVX_OK)
         return st;
-    if (p->cfg.kv_type == KVX_TYPE_FP_EIGHT &&
-        !(k_scale > 0.0f && v_scale > 0.0f && std::isfinite(k_scale) && std::isfinite(v_scale)))
-        return kvx::set_err(p->ctx, KVX_ERR_INVALID_ARG, "k_scale %g, v_scale %g",
-                            double(k_scale), double(v_scale));
     kvx::DeviceGuard guard(p->ctx->device);
     if (!guard.ok)
         return kvx::set_err(p->ctx, KVX_ERR_CUDA, "cannot make device %d current",
@@ -766,9 +632,10 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
     for (int k = 0; k < kKinds; ++k) {
         if (p->ctas[k] == 0)
             continue;
-        const Kernel kn = pick_kernel(p->cfg, k);
+        const Kernel kn = pick_kernel(p, k);
         const Work w = {reinterpret_cast<const AttnReq *>(p->dev + p->reqs_at(k)),
                         reinterpret_cast<const kvx::AttnStart *>(p->dev + p->starts_at(k)),
+                        reinterpret_cast<const int32_t *>(p->dev + p->cuts_at(k)),
                         p->counters, p->partial};
         CUtensorMap none = {};
         CUtensorMap *maps[2] = {p->box ? p->maps + 2 * layer : &none,
@@ -778,9 +645,12 @@ kvx_status kvx_attend(const kvx_attn_plan *p, int layer, const void *q, int64_t 
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
         cudaError_t e = launch_early(kn.fn, dim3(unsigned(p->ctas[k])), kn.threads, kn.smem, s,
                                      args);
-        if (e == cudaSuccess && kn.join && p->cut[k])
-            e = launch_early(kn.join, dim3(unsigned(p->ctas[k] - 1), kBlockRows / kJoinRows),
-                             kJoinThreads, 0, s, args);
+        if (e == cudaSuccess && kn.join && p->cuts[k])
+            e = launch_early(kn.join,
+                             dim3(unsigned(p->cuts[k]),
+                                  unsigned(kn.join_slices ? kn.join_slices
+                                                          : kn.join_heads * p->most_rows[k])),
+                             kn.join_threads, 0, s, args);
         if (e != cudaSuccess)
             return kvx::cuda_err(p->ctx, e, "attention launch");
     }

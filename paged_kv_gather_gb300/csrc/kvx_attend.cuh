@@ -64,6 +64,7 @@ struct Attend {
 struct Work {
     const AttnReq *reqs;       // of this kernel, those with rows
     const AttnStart *starts;   // [CTAs], and behind them the shares that follow those
+    const int32_t *cuts;       // CTAs that begin a unit and do not finish it
     unsigned int *counters;    // [CTAs]: arrivals at the unit a CTA began, zero between launches
     float *partial;
 };
@@ -88,6 +89,11 @@ struct Keys {
 
     template <int T>
     __device__ __forceinline__ void set(const AttnReq &r, int window, int row_lo, int row_hi)
+    {
+        set(r, window, row_lo, row_hi, T);
+    }
+    __device__ __forceinline__ void set(const AttnReq &r, int window, int row_lo, int row_hi,
+                                        int T)
     {
         prefix = r.prefix;
         pmin = r.n_tokens - r.n_new + row_lo;
@@ -205,6 +211,30 @@ struct Elem<KVX_TYPE_BFLOAT> {
         return r;
     }
 };
+
+// Eight e2m1 codes (low half of the low byte first) as four pairs of half-precision numbers.
+__device__ __forceinline__ void half8_of_e2m1(unsigned eight, unsigned (&h)[4])
+{
+    asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; "
+        "cvt.rn.f16x2.e2m1x2 %1, b; cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d; }"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(eight));
+}
+
+// The low two e4m3 codes as a pair of half-precision numbers.
+__device__ __forceinline__ unsigned half2_of_e4m3(unsigned two)
+{
+    unsigned h;
+    asm("{ .reg .b16 x, y; mov.b32 {x, y}, %1; cvt.rn.f16x2.e4m3x2 %0, x; }" : "=r"(h) : "r"(two));
+    return h;
+}
+
+__device__ __forceinline__ unsigned mul_half2(unsigned a, unsigned b)
+{
+    unsigned r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
 // All of a kernel's dynamic shared memory; the matrix tiles in it start on 1024 bytes.
 extern __shared__ __align__(1024) char attend_smem[];

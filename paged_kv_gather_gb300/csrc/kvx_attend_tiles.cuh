@@ -17,8 +17,8 @@ namespace {
 // shared-memory slots (K0, V0, K1, V1, ...).  Where a tile of keys is whole and a page holds
 // eight keys or a power of two more, one of them fetches it with tensor copies, a run of keys
 // inside a page each: with 16-byte copies by the threads of all three, the only way for other
-// pages and ragged ends, the ring was what the kernel waited for.  An e4m3 cache is copied as
-// it is into a stage of its own and from there converted to half precision in the ring.
+// pages and ragged ends, the ring was what the kernel waited for.  A cache of 8 or 4 bits is
+// copied as it is into a stage of its own and from there converted to half precision in the ring.
 //
 // Shared-memory tiles are [D / 64][128 rows][64 elements] with the 16-byte chunks of a
 // 128-byte line permuted by the row's low three bits, the layout the matrix instructions
@@ -62,12 +62,16 @@ enum {
 
 template <int KV, int D>
 struct TileShape {
-    static const bool kEight = KV == KVX_TYPE_FP_EIGHT;
+    static const bool kFour = KV == KVX_TYPE_FP_FOUR;
+    static const bool kStaged = KV == KVX_TYPE_FP_EIGHT || kFour;  // and converted
     static const int kTile = kTileRows * D * 2;              // bytes of a q, K or V tile
-    static const int kSlots = (D == 128 ? 5 : 10) - kEight;
+    static const int kSlots = (D == 128 ? 5 : 10) - kStaged;
+    // A staged side: e4m3 elements, or 16-byte units of e2m1 codes and behind them, for each unit,
+    // the four bytes that its two scales lie in.
+    static const int kSide = !kStaged ? 0 : kFour ? kTileKeys * (D / 32) * 20 : kTile / 2;
     static const int kOffRing = 2 * kTile;
-    static const int kOffStage = kOffRing + kSlots * kTile;  // e4m3: [2][kTile / 2]
-    static const int kOffKeys = kOffStage + kEight * kTile;  // int64 [2][kTileKeys]
+    static const int kOffStage = kOffRing + kSlots * kTile;  // [2][kSide]
+    static const int kOffKeys = kOffStage + 2 * kSide;       // int64 [2][kTileKeys]
     static const int kOffBars = kOffKeys + 2 * kTileKeys * 8;
     static const int kOffMisc = kOffBars + 8 * kBars;        // int[2]
     static const int kBytes = kOffMisc + 16;
@@ -266,6 +270,14 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c)
     return r;
 }
 
+// Four bytes into shared memory, zeros if !valid.
+__device__ __forceinline__ void cp_async4(unsigned dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 4 : 0)
+                 : "memory");
+}
+
 struct Yes {
     static constexpr bool value = true;
 };
@@ -427,8 +439,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
 {
     typedef TileShape<KV, D> T;
     typedef Elem<TYPE> E;
-    constexpr bool kEight = KV == KVX_TYPE_FP_EIGHT;
-    constexpr int kMath = kEight ? KVX_TYPE_HALF : TYPE;
+    constexpr bool kFour = T::kFour, kStaged = T::kStaged;
+    constexpr int kMath = kStaged ? KVX_TYPE_HALF : TYPE;
     typedef Elem<kMath> P;
     char *smem = attend_smem;
     int *misc = reinterpret_cast<int *>(smem + T::kOffMisc);
@@ -572,7 +584,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         // ------------------------------------------------------------- K and V
         const int lt = threadIdx.x - (kTileThreads - kLoaders);
         int64_t *offs = reinterpret_cast<int64_t *>(smem + T::kOffKeys);  // [2][kTileKeys]
-        constexpr int kRow = D * (kEight ? 1 : 2), kChunks = kRow / 16;
+        constexpr int kRow = kFour ? D / 2 : kStaged ? D : D * 2, kChunks = kRow / 16;
         constexpr int kCopies = (kTileKeys * kChunks + kLoaders - 1) / kLoaders;  // per thread
         constexpr unsigned kPerTile = D / 64;  // tensor copies side by side
         unsigned slot = 0, turn = 0;
@@ -593,6 +605,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 turn ^= 1;
             }
         };
+        int scales_after = 0;
         // Copy this thread's chunks of 16 bytes of a tile, where each key lies at off[key].
         auto copy = [&](const char *base, const int64_t *off, unsigned dst) {
             int64_t o[kCopies];  // all at once: nothing moves across an asynchronous copy
@@ -605,16 +618,21 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             for (int b = 0; b < kCopies; ++b) {
                 const int x = lt + b * kLoaders, t = x / kChunks, c = x % kChunks;
                 if (x < kTileKeys * kChunks)
-                    cp_async16(dst + (kEight ? x * 16 : tile_at(t, c)),
+                    cp_async16(dst + (kStaged ? x * 16 : tile_at(t, c)),
                                base + (o[b] >= 0 ? o[b] : 0) + c * 16, o[b] >= 0);
+                // Each thread converts what it copied, so it copies the scales that it needs.
+                if (kFour && x < kTileKeys * kChunks)
+                    cp_async4(dst + kTileKeys * kRow + x * 4,
+                              base + (o[b] >= 0 ? o[b] + scales_after : 0) + c / 2 * 4,
+                              o[b] >= 0);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         unsigned key_phase = 0;
-        // e4m3: tile sides (K, V, K, V, ...) are copied one ahead of their conversion.
+        // Staged tile sides (K, V, K, V, ...) are copied one ahead of their conversion.
         bool staged = false;
         auto convert = [&]() {  // the staged side, number `filled` of the stream
-            const char *src = smem + T::kOffStage + (filled & 1) * (T::kTile / 2);
+            const char *src = smem + T::kOffStage + (filled & 1) * T::kSide;
             char *dst = smem + T::kOffRing + slot * T::kTile;
             uint4 in[kCopies];  // all at once: loads do not move up across stores
 #pragma unroll
@@ -626,7 +644,23 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
 #pragma unroll
             for (int b = 0; b < kCopies; ++b) {
                 const int x = lt + b * kLoaders, t = x / kChunks, c = x % kChunks;
-                if (x < kTileKeys * kChunks) {
+                if (x >= kTileKeys * kChunks)
+                    continue;
+                if constexpr (kFour) {
+                    // 32 elements of two blocks.
+                    const unsigned units = half2_of_e4m3(*reinterpret_cast<const uint16_t *>(
+                        src + kTileKeys * kRow + x * 4 + 2 * (c & 1)));
+                    const unsigned in4[4] = {in[b].x, in[b].y, in[b].z, in[b].w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const unsigned unit = __byte_perm(units, 0, y < 2 ? 0x1010 : 0x3232);
+                        unsigned h[4];
+                        half8_of_e2m1(in4[y], h);
+                        *reinterpret_cast<uint4 *>(dst + tile_at(t, 4 * c + y)) =
+                            make_uint4(mul_half2(h[0], unit), mul_half2(h[1], unit),
+                                       mul_half2(h[2], unit), mul_half2(h[3], unit));
+                    }
+                } else {
                     uint4 h0, h1;
                     half4_of_e4m3(in[b].x, h0.x, h0.y);
                     half4_of_e4m3(in[b].y, h0.z, h0.w);
@@ -652,6 +686,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
             }
             const int64_t head_at = int64_t(u.at.head) * kRow;
+            if (kFour)  // from a head's codes to its scales
+                scales_after = a.kv_heads * kRow - int(head_at) + u.at.head * (D / 16);
             // A lane per tensor copy of a tile: run of keys `lane / kPerTile` and 64-element
             // block of the head `lane % kPerTile`; its page is looked up a tile ahead.
             const int run = a.box ? int(unsigned(lane) / kPerTile) * a.box : kTileKeys;
@@ -660,7 +696,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 return i < u.todo && run < kTileKeys && u.keys.used(j)
                            ? u.r.table[a.page.div(j)] : -1;
             };
-            int next = kEight ? -1 : page_of(0);
+            int next = kStaged ? -1 : page_of(0);
             // Page of key lt + b * kLoaders of tile i.
             auto key_page = [&](int i, int b) {
                 const int t = lt + b * kLoaders;
@@ -671,7 +707,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             int later[2] = {-1, -1};
             for (int i = 0; ok && i < u.todo; ++i) {
                 const int j0 = u.key_of(i);
-                if (!kEight) {
+                if (!kStaged) {
                     const int page = next;
                     next = page_of(i + 1);
                     if (a.box && u.keys.whole<kTileKeys>(j0) &&
@@ -731,10 +767,10 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 key_phase ^= 1;
                 for (int side = 0; ok && side < 2; ++side) {
                     const char *base = side ? a.v : a.k;
-                    if (kEight) {
+                    if (kStaged) {
                         // The stage that this side takes was converted two sides ago.
                         copy(base, off, sm + T::kOffStage +
-                                            ((filled + staged) & 1) * (T::kTile / 2));
+                                            ((filled + staged) & 1) * T::kSide);
                         if (staged) {
                             asm volatile("cp.async.wait_group 1;" ::: "memory");
                             if ((ok = wait(kBarEmpty + slot, turn ^ 1)))
@@ -812,7 +848,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 }
 #pragma unroll
                 for (int t = 0; t < kRowChunks; ++t) {
-                    if (kEight) {  // scaled by a power of two into half precision
+                    if (kStaged) {  // scaled by a power of two into half precision
                         const typename E::T *e = reinterpret_cast<const typename E::T *>(&v[t]);
                         float q[8], top = 0.0f, down, up;
 #pragma unroll
@@ -1111,8 +1147,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The results of units that were cut: block (c, slice) joins, in order, the parts of the unit
-// that CTA c began and did not end, for 32 of its rows.  A launch of its own puts every SM to
+// The results of units that were cut: block (i, slice) joins, in order, the parts of the i-th of
+// them, that CTA c0 began and did not end, for 32 of its rows.  A launch of its own puts every SM to
 // this, where the last CTA of a unit would have read up to 150 parts of 128 KB alone (65 us
 // against 37 for 64 new tokens behind 32k), and spares all of them a fence and a counter.
 const int kJoinThreads = 256;
@@ -1125,12 +1161,10 @@ kvx_attend_join_kernel(const Attend a, const Work w)
     typedef Elem<TYPE> E;
     constexpr int kSlotFloats = kBlockRows * (D + 2);
     __shared__ uint2 out[kJoinRows][D / 4 + 1];
-    const int c0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = w.cuts[blockIdx.x], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const AttnStart next = w.starts[c0 + 1];
     const int c1 = w.starts[c0].last;
     wait_for_earlier_work();
-    if (next.tile == 0 || next.first != c0)
-        return;
     const AttnReq &r = next.req;
     const int row0 = next.block * kBlockRows, rows = min(kBlockRows, r.n_new * a.group - row0);
     const int row = blockIdx.y * kJoinRows + lane;

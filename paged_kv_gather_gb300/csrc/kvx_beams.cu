@@ -1,0 +1,445 @@
+// kvx_beams.cu -- selection of a beam search: the best continuations of every group over beams
+// and vocabulary.  The checks are in kvx_cache_host.cpp, the reordering in kvx_pages.cu.
+//
+// The logits are read once.  A row (a beam's logits) is cut into parts that a CTA holds in
+// registers: it takes the part's maximum and sum of exponentials, and its `picks` largest logits
+// (equal ones by token).  Those are found by way of each thread's largest: a threshold that
+// about `picks` of them reach is found by bisection, a barrier that counts per step; all of a
+// part's `picks` largest are at or above it, and only the few threads that reach it look through
+// their logits again.  A second kernel, a CTA per group, merges the parts' lists beam by beam and
+// the beams' by their sums in 64 bits.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "kvx_attend.cuh"
+#include "kvx_ctx.h"
+
+namespace {
+
+const int kSelThreads = 512;
+const int kSelWarps = kSelThreads / 32;
+// Threads that may reach the threshold: KVX_MAX_PICKS and some, so that bisection ends early.
+const int kSelSlack = 16;
+const int kMaxParts = 32;      // of a row: a lane each when they are merged
+const int kMergeWarps = KVX_MAX_BEAMS / 2;
+const int kMergeThreads = 32 * kMergeWarps;
+
+struct PartStats {
+    double sum;   // of exp(logit - max)
+    float max;
+    int32_t pad;
+};
+
+struct Select {
+    const char *logits;
+    int64_t stride;          // bytes from beam to beam
+    const float *scores;
+    const uint8_t *done;
+    int32_t *parents, *tokens;
+    float *out_scores;
+    PartStats *stats;        // [beams][parts]
+    uint64_t *keys;          // [beams][parts][picks], falling; 0: none
+    int32_t n_groups, width, vocab, picks, parts, done_token;
+};
+
+template <int TYPE>
+struct Logit {
+    typedef typename Elem<TYPE>::T T;
+    static __device__ __forceinline__ float load(T x) { return Elem<TYPE>::load(x); }
+};
+template <>
+struct Logit<KVX_TYPE_FLOAT> {
+    typedef float T;
+    static __device__ __forceinline__ float load(float x) { return x; }
+};
+
+// Unsigned numbers in the order of floats; larger than 0 for all but -NaN.
+__device__ __forceinline__ unsigned order_of(float x)
+{
+    const unsigned b = __float_as_uint(x);
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float float_of(unsigned order)
+{
+    return __uint_as_float(order >> 31 ? order & 0x7fffffffu : ~order);
+}
+
+// Keys fall with the logit, then with the token.
+__device__ __forceinline__ uint64_t key_of(float x, int token)
+{
+    return uint64_t(order_of(x)) << 32 | unsigned(~token);
+}
+
+__device__ __forceinline__ bool has_continuations(const Select &a, int beam)
+{
+    return a.scores[beam] > -INFINITY;  // not NaN either
+}
+
+template <int TYPE, int EACH>
+__global__ void __launch_bounds__(kSelThreads)
+kvx_select_parts_kernel(const Select a)
+{
+    typedef Logit<TYPE> L;
+    typedef typename L::T T;
+    constexpr int kVec = 16 / sizeof(T), kVecs = EACH / kVec;
+    constexpr int kList = (KVX_MAX_PICKS + kSelSlack) * EACH;
+    __shared__ uint64_t list[kList];
+    __shared__ unsigned most[kSelWarps], least[kSelWarps];
+    __shared__ double sums[kSelWarps];
+    __shared__ int found;
+    const int beam = blockIdx.x / a.parts, part = blockIdx.x - beam * a.parts;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_for_earlier_work();
+    if ((a.done && a.done[beam]) || !has_continuations(a, beam))
+        return;
+
+    // 16-byte units of the row, the first and last of them partly outside it.
+    const char *row = a.logits + beam * a.stride;
+    const int skew = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    const uint4 *units = reinterpret_cast<const uint4 *>(row - skew * sizeof(T));
+    auto token_of = [&](int i) {  // of the i-th unit's first logit
+        return ((part * kVecs + i) * kSelThreads + int(threadIdx.x)) * kVec - skew;
+    };
+    float x[EACH];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int t = token_of(i);
+        uint4 u;
+        T *e = reinterpret_cast<T *>(&u);
+        if (t >= 0 && t + kVec <= a.vocab) {
+            u = __ldcs(units + (t + skew) / kVec);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                x[i * kVec + k] = L::load(e[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                x[i * kVec + k] = t + k >= 0 && t + k < a.vocab
+                                      ? L::load(reinterpret_cast<const T *>(row)[t + k])
+                                      : -INFINITY;
+        }
+    }
+    float top = -INFINITY;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        // NaN and +infinity count as -infinity, -0 as 0.
+        x[i] = x[i] < INFINITY ? x[i] + 0.0f : -INFINITY;
+        if (x[i] > top) {
+            top = x[i];
+            at = i;
+        }
+    }
+    // Two lookups of `at`, not a select per logit.
+    const uint64_t mine =
+        top > -INFINITY ? key_of(top, token_of(at / kVec) + at % kVec) : 0;
+    const unsigned hi = __reduce_max_sync(0xffffffffu, unsigned(mine >> 32));
+    const unsigned lo = __reduce_min_sync(0xffffffffu, unsigned(mine >> 32));
+    if (lane == 0) {
+        most[warp] = hi;
+        least[warp] = lo;
+    }
+    if (threadIdx.x == 0)
+        found = 0;
+    const int some = __syncthreads_count(mine != 0);
+    unsigned all_hi = 0, all_lo = ~0u;
+#pragma unroll
+    for (int i = 0; i < kSelWarps; ++i) {
+        all_hi = max(all_hi, most[i]);
+        all_lo = min(all_lo, least[i]);
+    }
+    const float m = some ? float_of(all_hi) : -INFINITY;
+    float sum = 0.0f;
+    if (top > -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            sum += exp2_((x[i] - m) * kLog2e);
+    }
+    double s = sum;
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0)
+        sums[warp] = s;
+
+    // Between `picks` and a few more threads reach `bar`; all that have a logit, if those are few.
+    uint64_t bar = 1;
+    const int enough = a.picks + kSelSlack;
+    if (some > enough) {
+        // more than `enough` reach `below`, less than `picks` reach `above`
+        uint64_t below = max(uint64_t(all_lo) << 32, uint64_t(1));
+        uint64_t above = uint64_t(all_hi) + 1 << 32;
+        for (;;) {
+            bar = below + (above - below) / 2;
+            const int n = __syncthreads_count(mine >= bar);
+            if (n < a.picks)
+                above = bar;
+            else if (n > enough)
+                below = bar;
+            else
+                break;
+        }
+    }
+    if (mine >= bar) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const uint64_t key = key_of(x[i], token_of(i / kVec) + i % kVec);
+            if (x[i] > -INFINITY && key >= bar)
+                list[atomicAdd(&found, 1)] = key;
+        }
+    }
+    __syncthreads();
+    const int n = found;
+    uint64_t *out = a.keys + (int64_t(beam) * a.parts + part) * a.picks;
+    for (int i = threadIdx.x; i < n; i += kSelThreads) {
+        const uint64_t key = list[i];
+        int rank = 0;
+        for (int k = 0; k < n; ++k)
+            rank += list[k] > key;
+        if (rank < a.picks)
+            out[rank] = key;
+    }
+    for (int i = n + threadIdx.x; i < a.picks; i += kSelThreads)
+        out[i] = 0;
+    if (threadIdx.x == 0) {
+        double all = 0.0;
+#pragma unroll
+        for (int i = 0; i < kSelWarps; ++i)
+            all += sums[i];
+        a.stats[int64_t(beam) * a.parts + part] = {all, m, 0};
+    }
+}
+
+// Unsigned numbers in the order of doubles.
+__device__ __forceinline__ uint64_t order_of(double x)
+{
+    const uint64_t b = uint64_t(__double_as_longlong(x));
+    return b >> 63 ? ~b : b | 1ull << 63;
+}
+
+struct Continuation {
+    double sum;
+    int32_t beam, token;
+};
+
+// A warp per beam merges the falling lists of its parts, a lane holding the head of one list;
+// then all of the CTA ranks the beams' continuations.
+__global__ void __launch_bounds__(kMergeThreads)
+kvx_select_merge_kernel(const Select a)
+{
+    __shared__ Continuation all[KVX_MAX_BEAMS * KVX_MAX_PICKS];
+    __shared__ int count[KVX_MAX_BEAMS];
+    const int group = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_for_earlier_work();
+    for (int b = warp; b < a.width; b += kMergeWarps) {
+        const int beam = group * a.width + b;
+        Continuation *mine = all + b * a.picks;
+        int n = 0;
+        if (!has_continuations(a, beam)) {
+        } else if (a.done && a.done[beam]) {
+            if (lane == 0)
+                mine[0] = {double(a.scores[beam]), b, a.done_token};
+            n = 1;
+        } else {
+            const bool have = lane < a.parts;
+            const uint64_t *keys = a.keys + (int64_t(beam) * a.parts + lane) * a.picks;
+            uint64_t head = have ? keys[0] : 0, next = have && a.picks > 1 ? keys[1] : 0;
+            int at = 1;
+            PartStats part = {0.0, -INFINITY, 0};
+            if (have)
+                part = a.stats[int64_t(beam) * a.parts + lane];
+            const unsigned top =
+                __reduce_max_sync(0xffffffffu, order_of(part.max));
+            const double m = float_of(top);
+            double s = part.sum > 0.0 ? part.sum * exp(double(part.max) - m) : 0.0;
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, d);
+            const double so_far = a.scores[beam], norm = m + log(s);
+            for (; n < a.picks; ++n) {
+                // The largest head: high words first, then low words among those that have it.
+                const unsigned hi = __reduce_max_sync(0xffffffffu, unsigned(head >> 32));
+                if (hi == 0)
+                    break;
+                const bool among = unsigned(head >> 32) == hi;
+                const unsigned lo = __reduce_max_sync(0xffffffffu, among ? unsigned(head) : 0u);
+                if (among && unsigned(head) == lo) {
+                    mine[n] = {so_far + (double(float_of(hi)) - norm), b, int32_t(~lo)};
+                    head = next;
+                    ++at;
+                    next = at < a.picks ? keys[at] : 0;
+                }
+            }
+        }
+        if (lane == 0)
+            count[b] = n;
+    }
+    __syncthreads();
+
+    // Rank by counting; of many continuations, only of those that reach the sum that `picks`
+    // of them reach, found by bisection.
+    const int slots = a.width * a.picks;
+    auto valid = [&](int i) { return i - i / a.picks * a.picks < count[i / a.picks]; };
+    uint64_t bar = 0;
+    if (slots > 256) {
+        uint64_t below = 0, above = ~0ull;
+        for (int step = 0; step < 64; ++step) {
+            const uint64_t mid = below + (above - below) / 2;
+            int n = 0;
+            for (int i = threadIdx.x; i < (slots + kMergeThreads - 1) / kMergeThreads * kMergeThreads;
+                 i += kMergeThreads)
+                n += __syncthreads_count(i < slots && valid(i) && order_of(all[i].sum) >= mid);
+            if (n < a.picks)
+                above = mid;
+            else
+                below = mid;
+            if (n >= a.picks && n <= a.picks + kSelSlack)
+                break;
+        }
+        bar = below;
+    }
+    const int64_t out = int64_t(group) * a.picks;
+    for (int i = threadIdx.x; i < slots; i += kMergeThreads) {
+        if (!valid(i) || order_of(all[i].sum) < bar)
+            continue;
+        const Continuation mine = all[i];
+        // A beam's continuations are in order, so position settles equal sums.
+        int rank = 0;
+        for (int b = 0; b < a.width; ++b)
+            for (int k = 0; k < count[b]; ++k) {
+                const double other = all[b * a.picks + k].sum;
+                if (other > mine.sum || (other == mine.sum && b * a.picks + k < i))
+                    ++rank;
+                else if (other < mine.sum)
+                    break;
+            }
+        if (rank < a.picks) {
+            a.parents[out + rank] = mine.beam;
+            a.tokens[out + rank] = mine.token;
+            a.out_scores[out + rank] = float(mine.sum);
+        }
+    }
+    int total = 0;
+    for (int b = 0; b < a.width; ++b)
+        total += count[b];
+    for (int i = total + threadIdx.x; i < a.picks; i += kMergeThreads) {
+        a.parents[out + i] = 0;
+        a.tokens[out + i] = -1;
+        a.out_scores[out + i] = -INFINITY;
+    }
+}
+
+// Logits that a thread holds, 8 or 32: parts are small where there are few rows, so that a few
+// rows still fill the GPU.
+int each_of(const kvx_ctx *ctx, const kvx_select_cfg &c)
+{
+    const int64_t rows = int64_t(c.n_groups) * c.width;
+    const int64_t large = (c.vocab + 7 + 32 * kSelThreads - 1) / (32 * kSelThreads);
+    const int64_t small = (c.vocab + 7 + 8 * kSelThreads - 1) / (8 * kSelThreads);
+    return rows * large < 2 * ctx->num_sms && small <= kMaxParts ? 8 : 32;
+}
+
+int parts_of(const kvx_select_cfg &c, int each)
+{
+    return (c.vocab + 7 + each * kSelThreads - 1) / (each * kSelThreads);
+}
+
+template <int TYPE>
+const void *parts_kernel(int each)
+{
+    return each == 8 ? reinterpret_cast<const void *>(kvx_select_parts_kernel<TYPE, 8>)
+                     : reinterpret_cast<const void *>(kvx_select_parts_kernel<TYPE, 32>);
+}
+
+cudaError_t launch(const void *fn, int64_t ctas, int threads, cudaStream_t s, void **args)
+{
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(ctas));
+    lc.blockDim = dim3(unsigned(threads));
+    lc.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelExC(&lc, fn, args);
+}
+
+}  // namespace
+
+extern "C" {
+
+kvx_status kvx_select_workspace(kvx_ctx *ctx, const kvx_select_cfg *cfg, int64_t *bytes)
+{
+    if (!ctx || !bytes)
+        return KVX_ERR_INVALID_ARG;
+    *bytes = 0;
+    const kvx_status st = kvx::validate_select(cfg, ctx->err, sizeof ctx->err);
+    if (st != KVX_OK)
+        return st;
+    *bytes = int64_t(cfg->n_groups) * cfg->width * parts_of(*cfg, each_of(ctx, *cfg)) *
+             int64_t(sizeof(PartStats) + cfg->picks * sizeof(uint64_t));
+    return KVX_OK;
+}
+
+kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void *logits,
+                            int64_t logits_stride, const float *scores, const uint8_t *done,
+                            int32_t *parents, int32_t *tokens, float *out_scores, void *workspace,
+                            kvx_stream_t stream)
+{
+    if (!ctx)
+        return KVX_ERR_INVALID_ARG;
+    kvx::begin_call(ctx);
+    const kvx_status st = kvx::validate_select(cfg, ctx->err, sizeof ctx->err);
+    if (st != KVX_OK)
+        return st;
+    if (!logits || !scores || !parents || !tokens || !out_scores || !workspace)
+        return kvx::set_err(ctx, KVX_ERR_INVALID_ARG, "logits, scores, parents, tokens, "
+                            "out_scores or workspace is NULL");
+    const int item = cfg->type == KVX_TYPE_FLOAT ? 4 : 2;
+    auto bits = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
+    if (bits(logits) % item || (bits(scores) | bits(parents) | bits(tokens) | bits(out_scores)) & 3 ||
+        bits(workspace) & 15)
+        return kvx::set_err(ctx, KVX_ERR_ALIGNMENT, "logits, scores, parents, tokens or "
+                            "out_scores not aligned to their elements, or the workspace not to "
+                            "16 bytes");
+    if (logits_stride == 0)
+        logits_stride = cfg->vocab;
+    if (logits_stride < cfg->vocab)
+        return kvx::set_err(ctx, KVX_ERR_INVALID_ARG, "logits: stride %lld below %d elements",
+                            (long long)logits_stride, cfg->vocab);
+    if (out_scores == scores && cfg->picks != cfg->width)
+        return kvx::set_err(ctx, KVX_ERR_INVALID_ARG, "out_scores is scores, but picks %d is not "
+                            "width %d", cfg->picks, cfg->width);
+    kvx::DeviceGuard guard(ctx->device);
+    if (!guard.ok)
+        return kvx::set_err(ctx, KVX_ERR_CUDA, "cannot make device %d current", ctx->device);
+    const int each = each_of(ctx, *cfg), parts = parts_of(*cfg, each);
+    const int64_t beams = int64_t(cfg->n_groups) * cfg->width;
+    if (beams * parts > INT32_MAX)
+        return kvx::set_err(ctx, KVX_ERR_CAPACITY, "%lld beams of %d parts", (long long)beams,
+                            parts);
+    Select a = {static_cast<const char *>(logits), logits_stride * item, scores, done, parents,
+                tokens, out_scores, static_cast<PartStats *>(workspace),
+                reinterpret_cast<uint64_t *>(static_cast<PartStats *>(workspace) + beams * parts),
+                cfg->n_groups, cfg->width, cfg->vocab, cfg->picks, parts, cfg->done_token};
+    void *args[] = {&a};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const void *fn = cfg->type == KVX_TYPE_HALF     ? parts_kernel<KVX_TYPE_HALF>(each)
+                     : cfg->type == KVX_TYPE_BFLOAT ? parts_kernel<KVX_TYPE_BFLOAT>(each)
+                                                    : parts_kernel<KVX_TYPE_FLOAT>(each);
+    cudaError_t e = launch(fn, beams * parts, kSelThreads, s, args);
+    if (e == cudaSuccess)
+        e = launch(reinterpret_cast<const void *>(kvx_select_merge_kernel), cfg->n_groups,
+                   kMergeThreads, s, args);
+    if (e != cudaSuccess)
+        return kvx::cuda_err(ctx, e, "selection launch");
+    ctx->last_items = beams;
+    ctx->last_ctas = int32_t(beams * parts);
+    ctx->last_threads = kSelThreads;
+    return KVX_OK;
+}
+
+}  // extern "C"

@@ -36,6 +36,29 @@ struct TableEntry {
 };
 static_assert(sizeof(TableEntry) == 16, "descriptor layout");
 
+// Table columns that a CTA of the reordering rewrites.
+const int kBeamColumns = 128;
+
+// One group of beams.  The *_begin fields are running totals over the groups, and one entry
+// past the last holds the batch's.
+struct BeamEntry {
+    int32_t *tables;
+    int64_t stride;
+    const int32_t *parents;
+    int32_t width;
+    int32_t full;        // pages
+    int32_t tail;        // tokens in the page behind them
+    int32_t col_begin;   // table columns, in whole CTAs
+    int32_t copy_begin;  // last pages that may be copied
+    int32_t pad;
+};
+static_assert(sizeof(BeamEntry) == 48, "descriptor layout");
+
+kvx_status validate_beams(const kvx_pool *pool, const int32_t *refs, const kvx_beams *beams,
+                          int n, int level, bool have_gpu, char *msg, size_t len);
+kvx_status pack_beams(const kvx_pool *pool, const kvx_beams *beams, int n, BeamEntry *out,
+                      char *msg, size_t len);
+
 kvx_status validate_upkeep(const kvx_pool *pool, const int32_t *refs, const kvx_fork *forks,
                            int n_forks, const kvx_table *tables, int n_tables, int level,
                            bool have_gpu, char *msg, size_t len);
@@ -99,6 +122,7 @@ kvx_status validate_attn(const kvx_pool *pool, const kvx_request *reqs, int n_re
                          const int32_t *n_new, const int32_t *prefix, const kvx_attn_cfg *cfg,
                          int level, bool have_gpu, char *msg, size_t len);
 
-inline int type_bytes(int type) { return type == KVX_TYPE_FP_EIGHT ? 1 : 2; }
+kvx_status validate_rope(const kvx_rope *rope, int head_dim, char *msg, size_t len);
+kvx_status validate_select(const kvx_select_cfg *cfg, char *msg, size_t len);
 
 }  // namespace kvx

@@ -7,6 +7,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "kvx_cache.h"
@@ -182,6 +183,122 @@ kvx_status pack_tables(const kvx_table *tables, int n, TableEntry *out, char *ms
     return KVX_OK;
 }
 
+kvx_status validate_beams(const kvx_pool *pool, const int32_t *refs, const kvx_beams *beams,
+                          int n, int level, bool have_gpu, char *msg, size_t len)
+{
+    kvx_status st = validate_pool(pool, level, have_gpu, msg, len);
+    if (st != KVX_OK)
+        return st;
+    if (!refs || !aligned(refs, 4))
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "refs is NULL or not 4-byte aligned");
+    if (n < 0 || (n > 0 && !beams))
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "bad beam array (%d)", n);
+    for (int i = 0; i < n; ++i) {
+        const kvx_beams &b = beams[i];
+        if (b.width < 1 || b.width > KVX_MAX_BEAMS || b.n_tokens < 0)
+            return fail(KVX_ERR_INVALID_ARG, msg, len, "group %d: width %d, n_tokens %d", i,
+                        b.width, b.n_tokens);
+        const int64_t pages = pages_of(b.n_tokens, pool->page_size);
+        if (pages > pool->num_pages)
+            return fail(KVX_ERR_INVALID_ARG, msg, len, "group %d: %d tokens need more than the "
+                        "pool's %d pages", i, b.n_tokens, pool->num_pages);
+        if (!b.parents || (b.n_tokens > 0 && !b.tables))
+            return fail(KVX_ERR_INVALID_ARG, msg, len, "group %d: tables or parents is NULL", i);
+        if (!aligned(b.tables, 4) || !aligned(b.parents, 4))
+            return fail(KVX_ERR_ALIGNMENT, msg, len, "group %d: tables or parents not 4-byte "
+                        "aligned", i);
+        if (b.width > 1 && b.table_stride < pages)
+            return fail(KVX_ERR_INVALID_ARG, msg, len, "group %d: table_stride %lld below %lld "
+                        "entries", i, (long long)b.table_stride, (long long)pages);
+        // The last beam's table ends within the address space.
+        if (b.table_stride > INT64_MAX / 4 / KVX_MAX_BEAMS)
+            return fail(KVX_ERR_INVALID_ARG, msg, len, "group %d: table_stride %lld", i,
+                        (long long)b.table_stride);
+    }
+    if (level <= 1)
+        return KVX_OK;
+
+    // Level 2: no two groups write one table.  Tables of one group are table_stride apart.
+    try {
+        std::vector<std::pair<uintptr_t, int>> at;
+        for (int i = 0; i < n; ++i)
+            if (beams[i].n_tokens > 0)
+                for (int b = 0; b < beams[i].width; ++b)
+                    at.push_back({reinterpret_cast<uintptr_t>(beams[i].tables +
+                                                              b * beams[i].table_stride), i});
+        std::sort(at.begin(), at.end());
+        for (size_t k = 1; k < at.size(); ++k) {
+            const int g = at[k - 1].second;
+            if (at[k - 1].first + 4 * pages_of(beams[g].n_tokens, pool->page_size) > at[k].first)
+                return fail(KVX_ERR_OVERLAP, msg, len, "groups %d and %d: tables overlap", g,
+                            at[k].second);
+        }
+    } catch (const std::bad_alloc &) {
+        return fail(KVX_ERR_CAPACITY, msg, len, "out of host memory");
+    }
+    return KVX_OK;
+}
+
+kvx_status pack_beams(const kvx_pool *pool, const kvx_beams *beams, int n, BeamEntry *out,
+                      char *msg, size_t len)
+{
+    int64_t columns = 0, copies = 0;
+    for (int i = 0; i <= n; ++i) {
+        BeamEntry &e = out[i];
+        e = BeamEntry();
+        e.col_begin = int32_t(columns);
+        e.copy_begin = int32_t(copies);
+        if (i == n)
+            break;
+        const kvx_beams &b = beams[i];
+        e.tables = b.tables;
+        e.stride = b.table_stride;
+        e.parents = b.parents;
+        e.width = b.width;
+        e.full = b.n_tokens / pool->page_size;
+        e.tail = b.n_tokens % pool->page_size;
+        // Whole blocks of columns, so that none holds columns of two groups.
+        columns += (pages_of(b.n_tokens, pool->page_size) + kBeamColumns - 1) / kBeamColumns *
+                   kBeamColumns;
+        copies += e.tail ? e.width - 1 : 0;
+        if (columns > INT32_MAX)
+            return fail(KVX_ERR_CAPACITY, msg, len, "the tables hold more than 2^31 entries");
+    }
+    return KVX_OK;
+}
+
+kvx_status validate_rope(const kvx_rope *rope, int head_dim, char *msg, size_t len)
+{
+    if (!rope)
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "rope is NULL");
+    if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > head_dim)
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "rotary_dim %d: a multiple of 16 up to %d is "
+                    "supported", rope->rotary_dim, head_dim);
+    if ((rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->magnitude))
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "interleaved %d, magnitude %g",
+                    rope->interleaved, double(rope->magnitude));
+    if (!rope->freqs)
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "freqs is NULL");
+    if (!aligned(rope->freqs, 4) || !aligned(rope->positions, 4))
+        return fail(KVX_ERR_ALIGNMENT, msg, len, "freqs or positions not 4-byte aligned");
+    return KVX_OK;
+}
+
+kvx_status validate_select(const kvx_select_cfg *cfg, char *msg, size_t len)
+{
+    if (!cfg)
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "cfg is NULL");
+    if (cfg->n_groups < 1 || cfg->width < 1 || cfg->width > KVX_MAX_BEAMS || cfg->vocab < 1 ||
+        cfg->vocab > KVX_MAX_VOCAB || cfg->picks < 1 || cfg->picks > KVX_MAX_PICKS)
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "n_groups %d, width %d, vocab %d, picks %d",
+                    cfg->n_groups, cfg->width, cfg->vocab, cfg->picks);
+    if (cfg->type != KVX_TYPE_HALF && cfg->type != KVX_TYPE_BFLOAT && cfg->type != KVX_TYPE_FLOAT)
+        return fail(KVX_ERR_INVALID_ARG, msg, len, "type %d", cfg->type);
+    if (int64_t(cfg->n_groups) * cfg->width > INT32_MAX)
+        return fail(KVX_ERR_CAPACITY, msg, len, "more than 2^31 beams");
+    return KVX_OK;
+}
+
 void pack_slabs(const kvx_pool *pool, char **out)
 {
     for (int l = 0; l < pool->num_layers; ++l)
@@ -207,10 +324,11 @@ kvx_status validate_attn(const kvx_pool *pool, const kvx_request *reqs, int n_re
         return fail(KVX_ERR_INVALID_ARG, msg, len, "head_dim %d: 64 and 128 are supported",
                     cfg->head_dim);
     if ((cfg->type != KVX_TYPE_HALF && cfg->type != KVX_TYPE_BFLOAT) ||
-        (cfg->kv_type != cfg->type && cfg->kv_type != KVX_TYPE_FP_EIGHT))
+        (cfg->kv_type != cfg->type && cfg->kv_type != KVX_TYPE_FP_EIGHT &&
+         cfg->kv_type != KVX_TYPE_FP_FOUR))
         return fail(KVX_ERR_INVALID_ARG, msg, len, "type %d, kv_type %d", cfg->type,
                     cfg->kv_type);
-    if (pool->token_bytes != int64_t(cfg->kv_heads) * cfg->head_dim * type_bytes(cfg->kv_type))
+    if (pool->token_bytes != kvx_token_bytes(cfg->kv_heads, cfg->head_dim, cfg->kv_type))
         return fail(KVX_ERR_INVALID_ARG, msg, len, "token_bytes %lld is not %d heads x %d of "
                     "kv_type %d", (long long)pool->token_bytes, cfg->kv_heads, cfg->head_dim,
                     cfg->kv_type);
@@ -286,6 +404,30 @@ kvx_status kvx_upkeep_validate(const kvx_pool *pool, const int32_t *refs, const 
 {
     return kvx::validate_upkeep(pool, refs, forks, n_forks, tables, n_tables, level,
                                 level >= 2 && gpu_present(), msg, msg_len);
+}
+
+kvx_status kvx_beams_validate(const kvx_pool *pool, const int32_t *refs, const kvx_beams *beams,
+                              int n_groups, int level, char *msg, size_t msg_len)
+{
+    return kvx::validate_beams(pool, refs, beams, n_groups, level, level >= 2 && gpu_present(),
+                               msg, msg_len);
+}
+
+int64_t kvx_token_bytes(int kv_heads, int head_dim, int kv_type)
+{
+    if (kv_heads <= 0 || head_dim <= 0)
+        return 0;
+    const int64_t row = int64_t(kv_heads) * head_dim;
+    switch (kv_type) {
+    case KVX_TYPE_HALF:
+    case KVX_TYPE_BFLOAT:
+        return 2 * row;
+    case KVX_TYPE_FP_EIGHT:
+        return row;
+    case KVX_TYPE_FP_FOUR:
+        return head_dim % 16 ? 0 : (row / 2 + row / 16 + 15) / 16 * 16;
+    }
+    return 0;
 }
 
 kvx_status kvx_attn_validate(const kvx_pool *pool, const kvx_request *reqs, int n_req,

@@ -26,7 +26,9 @@
 #include "kvx_cache.h"
 #include "kvx_ctx.h"
 
+using kvx::BeamEntry;
 using kvx::ForkEntry;
+using kvx::kBeamColumns;
 using kvx::TableEntry;
 
 namespace {
@@ -66,6 +68,7 @@ struct Args {
     int32_t slices;          // jobs per (page, slab)
     int32_t wide;            // everything that is copied is 32-byte aligned
     int32_t table_warps;     // of each CTA, for tables; the others copy
+    int32_t copies;          // reorder: last pages that may be copied
 };
 
 // -------------------------------------------------------------------------------- device
@@ -505,6 +508,146 @@ kvx_compact_kernel(const Args a, const __grid_constant__ Inline in)
         }
 }
 
+// How the beams of one group go on, as every warp works it out for itself: lane b holds what
+// beam b continues.
+struct Heirs {
+    unsigned extra;    // beams that continue one an earlier beam continues too
+    unsigned dropped;  // beams that nobody continues
+    int parent;        // of beam `lane`
+    int count;         // beams that continue beam `lane`
+    bool ok;
+
+    __device__ __forceinline__ explicit Heirs(const BeamEntry &e)
+    {
+        const int lane = threadIdx.x & 31;
+        const unsigned all = e.width == 32 ? 0xffffffffu : (1u << e.width) - 1;
+        parent = lane < e.width ? __ldcg(e.parents + lane) : -1;
+        ok = !__any_sync(0xffffffffu, lane < e.width && unsigned(parent) >= unsigned(e.width));
+        const unsigned alike = __match_any_sync(0xffffffffu, parent);
+        extra = __ballot_sync(0xffffffffu, lane < e.width && (alike & ((1u << lane) - 1))) & all;
+        dropped = ~__reduce_or_sync(0xffffffffu,
+                                    ok && lane < e.width ? 1u << parent : 0u) & all;
+        count = 0;
+        for (int b = 0; b < e.width; ++b)
+            count += __shfl_sync(0xffffffffu, parent, b) == lane;
+    }
+    // The bit of rank i.
+    static __device__ __forceinline__ int nth(unsigned bits, int i)
+    {
+        for (; i > 0; --i)
+            bits &= bits - 1;
+        return __ffs(bits) - 1;
+    }
+};
+
+// Copies of partly filled last pages.  A job is the i-th extra beam of a group and a slice of a
+// slab, or a few slabs: `a.slices` > 0 slices of each, or -a.slices slabs.  Which beams are extra
+// is known here only, so there are jobs for all that may be (all but one of a group).
+__global__ void __launch_bounds__(kThreads, 1)
+kvx_reorder_copy_kernel(const Args a, const __grid_constant__ Inline in)
+{
+    __shared__ Inline staged;
+    const char *desc = descriptors(a, in, reinterpret_cast<char *>(&staged));
+    const BeamEntry *e = reinterpret_cast<const BeamEntry *>(desc + a.off_entries);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pieces = a.slices > 0 ? a.n_slabs * a.slices : (a.n_slabs - a.slices - 1) / -a.slices;
+    const int64_t jobs = int64_t(a.copies) * pieces;
+    __syncthreads();
+    wait_for_earlier_work();
+    for (int64_t job = int64_t(blockIdx.x) * kWarps + warp; job < jobs;
+         job += int64_t(gridDim.x) * kWarps) {
+        const int c = int(job / pieces), piece = int(job - int64_t(c) * pieces);
+        const int x = find_entry(e, a.n_entries, c, [](const BeamEntry &b) { return b.copy_begin; });
+        const Heirs h(e[x]);
+        const int i = c - e[x].copy_begin;
+        if (!h.ok || i >= __popc(h.extra))
+            continue;
+        const int parent = __shfl_sync(0xffffffffu, h.parent, Heirs::nth(h.extra, i));
+        const int giver = Heirs::nth(h.dropped, i);
+        const int from = __ldcg(e[x].tables + parent * e[x].stride + e[x].full);
+        const int to = __ldcg(e[x].tables + giver * e[x].stride + e[x].full);
+        if (unsigned(from) >= unsigned(a.num_pages) || unsigned(to) >= unsigned(a.num_pages)) {
+            if (lane == 0)
+                atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+            continue;
+        }
+        if (from == to)
+            continue;
+        if (a.slices > 0) {
+            copy_slice(a, desc, piece / a.slices, piece % a.slices, from, to, e[x].tail, lane);
+        } else {
+            for (int slab = piece * -a.slices; slab < min(a.n_slabs, (piece + 1) * -a.slices);
+                 ++slab)
+                copy_slice(a, desc, slab, 0, from, to, e[x].tail, lane);
+        }
+    }
+}
+
+// Tables and counts: a CTA takes kBeamColumns columns of a group, the entries of all its beams
+// at one logical page each, so nobody else reads what it writes.
+__global__ void __launch_bounds__(kBeamColumns)
+kvx_reorder_tables_kernel(const Args a, const __grid_constant__ Inline in)
+{
+    __shared__ int32_t held[KVX_MAX_BEAMS][kBeamColumns];
+    __shared__ int parents[KVX_MAX_BEAMS], givers[KVX_MAX_BEAMS], counts[KVX_MAX_BEAMS];
+    __shared__ int bad;
+    const char *desc = a.ext ? a.ext : reinterpret_cast<const char *>(&in);
+    const BeamEntry *entries = reinterpret_cast<const BeamEntry *>(desc + a.off_entries);
+    const int x = find_entry(entries, a.n_entries, int(blockIdx.x) * kBeamColumns,
+                             [](const BeamEntry &b) { return b.col_begin; });
+    const BeamEntry e = entries[x];
+    const int j = int(blockIdx.x) * kBeamColumns - e.col_begin + int(threadIdx.x);
+    wait_for_earlier_work();
+    const bool last = j == e.full && e.tail > 0, mine = j < e.full || last;
+    for (int b = 0; mine && b < e.width; ++b)
+        held[b][threadIdx.x] = __ldcg(e.tables + b * e.stride + j);
+    if (threadIdx.x < 32) {
+        const Heirs h(e);
+        const int lane = threadIdx.x;
+        if (lane == 0) {
+            bad = !h.ok;
+            if (bad && j == 0)
+                atomicOr(a.status, KVX_DEV_BEAM_OUT_OF_RANGE);
+        }
+        if (h.ok && lane < e.width) {
+            parents[lane] = h.parent;
+            counts[lane] = h.count;
+            givers[lane] = h.extra >> lane & 1
+                               ? Heirs::nth(h.dropped, __popc(h.extra & ((1u << lane) - 1)))
+                               : h.parent;
+        }
+    }
+    __syncthreads();
+    if (bad || !mine)
+        return;
+    const int t = threadIdx.x;
+    for (int b = 0; b < e.width; ++b) {
+        const int from = last ? givers[b] : parents[b];
+        if (from != b)
+            e.tables[b * e.stride + j] = held[from][t];
+    }
+    if (last)
+        return;
+    // Beams that share the page (a prompt's) change its count by nothing.
+    bool same = true;
+    for (int b = 1; b < e.width; ++b)
+        same &= held[b][t] == held[0][t];
+    unsigned wrong = 0;
+    for (int b = 0; b < e.width; ++b) {
+        const int p = held[b][t], d = counts[b] - 1;
+        if (unsigned(p) >= unsigned(a.num_pages)) {
+            wrong |= KVX_DEV_PAGE_OUT_OF_RANGE;
+        } else if (same ? b == 0 && __ldcg(a.refs + p) <= 0
+                        : d != 0 && atomicAdd(a.refs + p, d) <= 0) {
+            if (!same)  // not held: taken back
+                atomicSub(a.refs + p, d);
+            wrong |= KVX_DEV_PAGE_NOT_HELD;
+        }
+    }
+    if (wrong)
+        atomicOr(a.status, wrong);
+}
+
 // ---------------------------------------------------------------------------------- host
 
 size_t bitmap_bytes(int num_pages)
@@ -548,6 +691,23 @@ kvx_status begin_batch(kvx_ctx *ctx, size_t bytes, Batch *b)
     return st;
 }
 
+cudaError_t launch_one(void (*fn)(Args, Inline), Args &a, Batch *b, int64_t ctas, int threads,
+                       size_t smem, cudaStream_t s)
+{
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(ctas));
+    lc.blockDim = dim3(unsigned(threads));
+    lc.dynamicSmemBytes = smem;  // up to what prepare_upkeep asked for
+    lc.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    void *args[] = {&a, &b->in};
+    return cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(fn), args);
+}
+
 kvx_status launch_batch(kvx_ctx *ctx, void (*fn)(Args, Inline), Args a, Batch *b, int64_t ctas,
                         size_t smem, int64_t items, cudaStream_t s)
 {
@@ -559,18 +719,7 @@ kvx_status launch_batch(kvx_ctx *ctx, void (*fn)(Args, Inline), Args a, Batch *b
     }
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "descriptor copy");
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(unsigned(ctas));
-    lc.blockDim = dim3(kThreads);
-    lc.dynamicSmemBytes = smem;  // up to what prepare_upkeep asked for
-    lc.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    void *args[] = {&a, &b->in};
-    e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(fn), args);
+    e = launch_one(fn, a, b, ctas, kThreads, smem, s);
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "kernel launch");
     if (b->slot)
@@ -730,6 +879,74 @@ kvx_status kvx_compact_pages(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
                              int32_t *remap, kvx_stream_t stream)
 {
     return tables_call(ctx, pool, refs, tables, n_tables, n_live, remap, true, stream);
+}
+
+kvx_status kvx_reorder_beams(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
+                             const kvx_beams *beams, int n_groups, kvx_stream_t stream)
+{
+    if (!ctx)
+        return KVX_ERR_INVALID_ARG;
+    kvx::begin_call(ctx);
+    kvx_status st = kvx::validate_beams(pool, refs, beams, n_groups, ctx->validation, true,
+                                        ctx->err, sizeof ctx->err);
+    if (st != KVX_OK)
+        return st;
+    kvx::DeviceGuard guard(ctx->device);
+    if (!guard.ok)
+        return kvx::set_err(ctx, KVX_ERR_CUDA, "cannot make device %d current", ctx->device);
+    Args a = common_args(ctx, pool, refs, n_groups);
+    Batch b;
+    st = begin_batch(ctx, a.off_entries + (size_t(n_groups) + 1) * sizeof(BeamEntry), &b);
+    if (st != KVX_OK)
+        return st;
+    kvx::pack_slabs(pool, reinterpret_cast<char **>(b.host));
+    BeamEntry *e = reinterpret_cast<BeamEntry *>(b.host + a.off_entries);
+    st = kvx::pack_beams(pool, beams, n_groups, e, ctx->err, sizeof ctx->err);
+    if (st != KVX_OK)
+        return st;
+    const int64_t columns = e[n_groups].col_begin;
+    if (columns == 0)
+        return KVX_OK;
+    a.copies = e[n_groups].copy_begin;
+    int64_t longest = 0;
+    for (int i = 0; i < n_groups; ++i)
+        if (e[i + 1].copy_begin > e[i].copy_begin)
+            longest = std::max<int64_t>(longest, e[i].tail);
+    // Of the pages that may be copied, about half are.
+    const int64_t units = int64_t(a.copies) * a.n_slabs, warps = int64_t(ctx->num_sms) * kWarps;
+    choose_slices(ctx, std::max<int64_t>(1, units / 2),
+                  std::max<int64_t>(longest, 1) * pool->token_bytes, &a);
+    if (a.slices == 1 && units > 4 * warps)
+        a.slices = -int32_t(std::min<int64_t>(a.n_slabs, units / (2 * warps)));
+    const int64_t pieces = a.slices > 0 ? int64_t(a.n_slabs) * a.slices
+                                        : (a.n_slabs - a.slices - 1) / -a.slices;
+    if (pieces > INT32_MAX)
+        return kvx::set_err(ctx, KVX_ERR_CAPACITY, "%d slabs x %d slices exceed 2^31 copies",
+                            a.n_slabs, a.slices);
+    const int64_t jobs = a.copies * pieces;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
+    a.inline_bytes = b.slot ? 0 : int32_t((b.bytes + 15) / 16 * 16);
+    if (b.slot) {
+        a.ext = b.slot->dev;
+        err = kvx::stage(ctx, *b.slot, b.bytes, 0, 0, s);
+    }
+    if (err == cudaSuccess && jobs > 0)
+        err = launch_one(kvx_reorder_copy_kernel, a, &b,
+                         std::min<int64_t>(ctx->num_sms, (jobs + kWarps - 1) / kWarps), kThreads,
+                         0, s);
+    const int64_t ctas = columns / kBeamColumns;
+    if (err == cudaSuccess)
+        err = launch_one(kvx_reorder_tables_kernel, a, &b, ctas, kBeamColumns, 0, s);
+    if (err != cudaSuccess)
+        return kvx::cuda_err(ctx, err, "reorder launch");
+    if (b.slot)
+        return kvx::finish_call(ctx, *b.slot, s, jobs, ctas, kBeamColumns, b.bytes);
+    ctx->last_items = jobs;
+    ctx->last_ctas = int32_t(ctas);
+    ctx->last_threads = kBeamColumns;
+    ctx->last_desc_bytes = int64_t(b.bytes);
+    return KVX_OK;
 }
 
 }  // extern "C"

@@ -48,6 +48,8 @@ KVX_MAX_UPKEEP_PAGES = 1 << 20
 KVX_TYPE_HALF = 0
 KVX_TYPE_BFLOAT = 1
 KVX_TYPE_FP_EIGHT = 2
+KVX_TYPE_FP_FOUR = 3
+KVX_TYPE_FLOAT = 4
 
 KVX_CHUNK_LAYER_MAJOR = 0
 KVX_CHUNK_TOKEN_MAJOR = 1
@@ -132,6 +134,24 @@ class kvx_attn_cfg(ctypes.Structure):
                 ("slopes", ctypes.c_void_p)]
 
 
+class kvx_rope(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class kvx_select_cfg(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("picks", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("done_token", ctypes.c_int32)]
+
+
+class kvx_beams(ctypes.Structure):
+    _fields_ = [("tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("parents", ctypes.c_void_p), ("width", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int32)]
+
+
 CHUNK_DTYPE = np.dtype([("request", "<i4"), ("token_begin", "<i4"), ("n_tokens", "<i4"),
                         ("layer_begin", "<i4"), ("n_layers", "<i4"), ("layout", "<i4"),
                         ("ptr", "<u8")])
@@ -140,10 +160,13 @@ REQUEST_DTYPE = np.dtype([("page_table", "<u8"), ("page_table_host", "<u8"),
 TABLE_DTYPE = np.dtype([("pages", "<u8"), ("n_pages", "<i4"), ("reserved", "<i4")])
 FORK_DTYPE = np.dtype([("parent", "<u8"), ("child", "<u8"), ("shared_tokens", "<i4"),
                        ("child_tokens", "<i4"), ("copy", "<i4"), ("reserved", "<i4")])
+BEAMS_DTYPE = np.dtype([("tables", "<u8"), ("table_stride", "<i8"), ("parents", "<u8"),
+                        ("width", "<i4"), ("n_tokens", "<i4")])
 assert CHUNK_DTYPE.itemsize == ctypes.sizeof(kvx_chunk)
 assert REQUEST_DTYPE.itemsize == ctypes.sizeof(kvx_request)
 assert TABLE_DTYPE.itemsize == ctypes.sizeof(kvx_table)
 assert FORK_DTYPE.itemsize == ctypes.sizeof(kvx_fork)
+assert BEAMS_DTYPE.itemsize == ctypes.sizeof(kvx_beams)
 
 # ---------------------------------------------------------------------------- prototypes
 
@@ -241,6 +264,17 @@ _proto("kvx_attend", _c.c_int,
         _c.c_float, _c.c_float, _c.c_void_p])
 _proto("kvx_attn_validate", _c.c_int,
        [_P(kvx_pool), *_step, _P(kvx_attn_cfg), _c.c_int, _c.c_char_p, _c.c_size_t])
+_proto("kvx_token_bytes", _c.c_int64, [_c.c_int, _c.c_int, _c.c_int])
+_proto("kvx_append_rotated", _c.c_int,
+       [_c.c_void_p, _c.c_int, _P(kvx_rope), _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+        _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_float, _c.c_float, _c.c_void_p])
+_proto("kvx_reorder_beams", _c.c_int, [*_upkeep, _c.c_void_p])
+_proto("kvx_beams_validate", _c.c_int,
+       [_P(kvx_pool), _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int, _c.c_char_p, _c.c_size_t])
+_proto("kvx_select_workspace", _c.c_int, [_ctx_t, _P(kvx_select_cfg), _P(_c.c_int64)])
+_proto("kvx_select_beams", _c.c_int,
+       [_ctx_t, _P(kvx_select_cfg), _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p,
+        _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p])
 
 EXPORTED = ["kvx_create", "kvx_destroy", "kvx_set_validation", "kvx_default_launch_cfg",
             "kvx_store_chunks", "kvx_load_chunks", "kvx_exchange_chunks", "kvx_roundtrip_chunks",
@@ -254,7 +288,9 @@ EXPORTED = ["kvx_create", "kvx_destroy", "kvx_set_validation", "kvx_default_laun
             "kvx_partition_info", "kvx_partition_destroy", "kvx_test_roundtrip_timeout",
             "kvx_roundtrip_unit", "kvx_fork_pages", "kvx_free_pages", "kvx_compact_pages",
             "kvx_upkeep_validate", "kvx_attn_plan_create", "kvx_attn_plan_update",
-            "kvx_attn_plan_destroy", "kvx_append_tokens", "kvx_attend", "kvx_attn_validate"]
+            "kvx_attn_plan_destroy", "kvx_append_tokens", "kvx_attend", "kvx_attn_validate",
+            "kvx_token_bytes", "kvx_append_rotated", "kvx_reorder_beams", "kvx_beams_validate",
+            "kvx_select_workspace", "kvx_select_beams"]
 
 KVX_NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -385,15 +421,43 @@ def forks_array(entries) -> np.ndarray:
     return _Held(a)
 
 
-_TYPES = {"fp16": KVX_TYPE_HALF, "bf16": KVX_TYPE_BFLOAT, "fp8": KVX_TYPE_FP_EIGHT}
+def beams_array(entries) -> np.ndarray:
+    """entries: iterable of (tables_ptr, table_stride, parents_ptr, width, n_tokens)."""
+    entries = list(entries)
+    a = np.zeros(len(entries), BEAMS_DTYPE)
+    for i, e in enumerate(entries):
+        a[i] = tuple(e)
+    return _Held(a)
+
+
+_TYPES = {"fp16": KVX_TYPE_HALF, "bf16": KVX_TYPE_BFLOAT, "fp8": KVX_TYPE_FP_EIGHT,
+          "fp4": KVX_TYPE_FP_FOUR, "fp32": KVX_TYPE_FLOAT}
 
 
 def attn_config(q_heads: int, kv_heads: int, head_dim: int, dtype: str = "bf16",
                 kv_dtype: Optional[str] = None, window: int = 0, scale: float = 0.0,
                 softcap: float = 0.0, slopes: int = 0) -> kvx_attn_cfg:
-    """A kvx_attn_cfg; dtype "fp16" or "bf16", kv_dtype the same (default) or "fp8" (e4m3)."""
+    """A kvx_attn_cfg; dtype "fp16" or "bf16", kv_dtype the same (default), "fp8" (e4m3)
+    or "fp4" (e2m1 with an e4m3 scale per 16 elements)."""
     return kvx_attn_cfg(q_heads, kv_heads, head_dim, _TYPES[dtype], _TYPES[kv_dtype or dtype],
                         window, scale, softcap, slopes or None)
+
+
+def rope_config(freqs: int, rotary_dim: int, interleaved: bool = False, positions: int = 0,
+                magnitude: float = 1.0) -> kvx_rope:
+    """A kvx_rope; freqs [rotary_dim / 2] and positions [rows] are device addresses."""
+    return kvx_rope(freqs, positions or None, rotary_dim, int(interleaved), magnitude, 0)
+
+
+def select_config(n_groups: int, width: int, vocab: int, picks: int, dtype: str = "bf16",
+                  done_token: int = 0) -> kvx_select_cfg:
+    """A kvx_select_cfg; dtype "fp16", "bf16" or "fp32", of the logits."""
+    return kvx_select_cfg(n_groups, width, vocab, picks, _TYPES[dtype], done_token)
+
+
+def kvx_token_bytes(kv_heads: int, head_dim: int, kv_dtype: str) -> int:
+    """Bytes of a cache token (a pool's token_bytes) of kv_dtype, 0 if no cache has it."""
+    return _lib.kvx_token_bytes(kv_heads, head_dim, _TYPES[kv_dtype])
 
 
 def _arr_ptr(a: Optional[np.ndarray], dtype) -> Tuple[int, int]:
@@ -633,6 +697,36 @@ def kvx_upkeep_validate(pool: Pool, refs: int, forks=None, tables=None,
     return st, buf.value.decode()
 
 
+def kvx_reorder_beams(ctx, pool: Pool, refs: int, beams, stream: int = 0) -> None:
+    """Make every beam's pages those of the beam that it continues (beams_array)."""
+    p, n = _arr_ptr(beams, BEAMS_DTYPE)
+    _check(ctx, _lib.kvx_reorder_beams(ctx, ctypes.byref(pool.c), refs, p, n, stream))
+
+
+def kvx_beams_validate(pool: Pool, refs: int, beams, level: int = 1) -> Tuple[int, str]:
+    """Host checks of kvx_reorder_beams alone: (status, message)."""
+    p, n = _arr_ptr(beams, BEAMS_DTYPE)
+    buf = ctypes.create_string_buffer(512)
+    st = _lib.kvx_beams_validate(ctypes.byref(pool.c), refs or None, p, n, level, buf, len(buf))
+    return st, buf.value.decode()
+
+
+def kvx_select_workspace(ctx, cfg: kvx_select_cfg) -> int:
+    """Bytes of device memory that kvx_select_beams needs with this configuration."""
+    n = ctypes.c_int64()
+    _check(ctx, _lib.kvx_select_workspace(ctx, ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def kvx_select_beams(ctx, cfg: kvx_select_cfg, logits: int, scores: int, parents: int,
+                     tokens: int, out_scores: int, workspace: int, logits_stride: int = 0,
+                     done: int = 0, stream: int = 0) -> None:
+    """The best continuations of every group of beams over beams and vocabulary."""
+    _check(ctx, _lib.kvx_select_beams(ctx, ctypes.byref(cfg), logits, logits_stride, scores,
+                                      done or None, parents, tokens, out_scores, workspace,
+                                      stream))
+
+
 def _step_args(reqs, n_new, prefix):
     """reqs, n_req, n_new and prefix of a step, and the arrays that must outlive the call."""
     rp, nr = _arr_ptr(reqs, REQUEST_DTYPE)
@@ -669,6 +763,18 @@ def kvx_append_tokens(plan, layer: int, k: int, v: int, k_stride: int = 0, v_str
                       k_scale: float = 1.0, v_scale: float = 1.0, stream: int = 0) -> None:
     """Write the step's new K and V (device addresses, strides in elements) into the pages."""
     st = _lib.kvx_append_tokens(plan, layer, k, v, k_stride, v_stride, k_scale, v_scale, stream)
+    if st != KVX_OK:
+        raise KvxError(st, kvx_last_error(plan.ctx))
+
+
+def kvx_append_rotated(plan, layer: int, rope: kvx_rope, k: int, v: int, q: int = 0,
+                       q_out: int = 0, k_stride: int = 0, v_stride: int = 0, q_stride: int = 0,
+                       q_out_stride: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+                       stream: int = 0) -> None:
+    """kvx_append_tokens with K, and q into q_out, rotated by their positions on the way."""
+    st = _lib.kvx_append_rotated(plan, layer, ctypes.byref(rope), q or None, q_stride,
+                                 q_out or None, q_out_stride, k, v, k_stride, v_stride, k_scale,
+                                 v_scale, stream)
     if st != KVX_OK:
         raise KvxError(st, kvx_last_error(plan.ctx))
 
