@@ -26,7 +26,12 @@ const int kFourWarps = 8;
 const int kFourThreads = 32 * (kFourWarps + 1);
 const int kFourStages = 8;    // at most
 const int kFourKeys = 16;     // of a warp and step
-const int kFourLook = kFourKeys * kFourWarps / 32;  // tokens of a stage per producer lane
+const int kFourAhead = 3;     // stages that page ids are looked up before they are used
+
+template <int N>
+struct Looks {
+    static constexpr int value = N;
+};
 
 struct FourShape {
     int heads, groups;  // KV heads of a group, groups
@@ -74,7 +79,7 @@ __host__ __device__ constexpr int four_ctas_per_sm(int NT) { return NT == 1 ? 2 
 // Dynamic shared memory of a CTA, at most: beside 1 KB of its own and 1 KB of the system's.
 __host__ __device__ constexpr int four_room(int NT)
 {
-    return 224 * 1024 / four_ctas_per_sm(NT) - 2048;
+    return 226 * 1024 / four_ctas_per_sm(NT) - 2 * 1024;
 }
 
 template <int D, int NT>
@@ -91,18 +96,15 @@ inline size_t four_smem(const FourShape &f)
            kFourWarps / 2 * four_join_floats<D, NT>() * 4;
 }
 
-__device__ __forceinline__ unsigned lds_u16(unsigned addr)
+// As mma16816 in half precision; not volatile, so that products of K move among the conversions
+// of V.
+__device__ __forceinline__ void mma_half(float (&d)[4], const unsigned (&a)[4], unsigned b0,
+                                         unsigned b1)
 {
-    unsigned short r;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr) : "memory");
-    return r;
-}
-
-__device__ __forceinline__ unsigned lds_u8(unsigned addr)
-{
-    unsigned r;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
-    return r;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // `bytes` (a multiple of 16, addresses too) of global memory into shared memory; completes on a
@@ -179,115 +181,149 @@ kvx_attend_four_kernel(const Attend a, const Work w)
         unsigned filled = 0;
         while (at.tiles > 0) {
             enter();
-            // A lane's tokens of a stage are lane, lane + 32, ...; the first of a run inside a
-            // page fetches it.  Its page is looked up a stage ahead.
-            auto page_of = [&](int i, int b) {
-                const int t = lane + 32 * b, j = i < todo && t < f.keys ? key_of(i) + t : 0;
-                if (i >= todo || t >= f.keys || !keys.used(j))
-                    return -1;
-                const int nth = a.page.div(j);
-                return t == 0 || j == nth * a.page_size || !keys.used(j - 1) ? at.req.table[nth]
-                                                                             : -1;
-            };
             const int head0 = at.head * f.heads, heads = min(f.heads, a.kv_heads - head0);
-            int page[kFourLook];
-#pragma unroll
-            for (int b = 0; b < kFourLook; ++b)
-                page[b] = page_of(0, b);
-            for (int i = 0; i < todo; ++i) {
-                const int j0 = key_of(i);
-                int run[kFourLook], off[kFourLook];
-                unsigned bytes = 0;
-                const unsigned per_token =
-                    f.groups == 1 ? unsigned(a.token_bytes)
-                                  : unsigned(heads * (D / 2) +
-                                             ((head0 + heads) * (D / 16) + 15) / 16 * 16 -
-                                             head0 * (D / 16) / 16 * 16);
-                bool bad = false;
-#pragma unroll
-                for (int b = 0; b < kFourLook; ++b) {
-                    const int t = lane + 32 * b, j = j0 + t;
-                    run[b] = 0;
-                    if (t >= f.keys || !keys.used(j))
-                        continue;
-                    const int nth = a.page.div(j), in = j - nth * a.page_size;
-                    if (t > 0 && in > 0 && keys.used(j - 1))
-                        continue;
+            const int scale_lo = head0 * (D / 16) / 16 * 16;
+            const int scale_hi = ((head0 + heads) * (D / 16) + 15) / 16 * 16;
+            const unsigned per_token = f.groups == 1
+                                           ? unsigned(a.token_bytes)
+                                           : unsigned(heads * (D / 2) + scale_hi - scale_lo);
+            // A run of tokens inside a page and a stretch of used keys, from token t of a stage
+            // of keys from j0: its length, 0 if none begins there, its page of the table and its
+            // place in it.
+            auto run_at = [&](int j0, int t, bool whole, int &nth, int &in) {
+                const int j = j0 + t;
+                nth = a.page.div(j);
+                in = j - nth * a.page_size;
+                int n = t < f.keys && (t == 0 || in == 0) ? min(f.keys - t, a.page_size - in) : 0;
+                if (!whole) {
                     const int seen = j < keys.prefix && keys.prefix < keys.low
                                          ? keys.prefix : max(keys.prefix, keys.end);
-                    run[b] = min(min(f.keys - t, a.page_size - in), seen - j);
-                    off[b] = in;
-                    if (unsigned(page[b]) < unsigned(a.num_pages))
-                        bytes += 2 * run[b] * per_token;
-                    else
-                        bad = true;
+                    n = t < f.keys && keys.used(j) && (t == 0 || in == 0 || !keys.used(j - 1))
+                            ? min(min(f.keys - t, a.page_size - in), seen - j) : 0;
                 }
-                if (ok)
-                    ok = mbar_wait(empty(stage), phase ^ 1, &gave_up, a.status);
-                const unsigned dst = ring + stage * 2 * f.side;
-                if (__any_sync(0xffffffffu, bad)) {
-                    // Pages outside the pool: zeros, which nothing may be in flight beside.
-                    if (bad) {
-                        atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+                return n;
+            };
+            auto whole_at = [&](int j0) {
+                return j0 + f.keys <= keys.prefix || (j0 >= keys.low && j0 + f.keys <= keys.end);
+            };
+            // Pages outside the pool: zeros, which nothing may be in flight beside.
+            auto clear = [&](int t0, int n) {
+                for (int x = 0; x < 2 * n; ++x) {
+                    char *s = attend_smem + (stage * 2 + (x & 1)) * f.side;
+                    const int t = t0 + x / 2;
+                    for (int c = 0; c < f.code_row; c += 16)
+                        *reinterpret_cast<uint4 *>(s + t * f.code_row + c) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; f.groups > 1 && c < f.scale_row; c += 16)
+                        *reinterpret_cast<uint4 *>(s + f.scale_at + t * f.scale_row + c) =
+                            make_uint4(0, 0, 0, 0);
+                }
+            };
+            // A group's part of n tokens from `src`, token by token.
+            auto copy_group = [&](unsigned dst, int t, int n, int64_t src) {
+                for (int r = 0; r < 2 * n; ++r) {
+                    const char *s = (r & 1 ? a.v : a.k) + src + r / 2 * a.token_bytes;
+                    const unsigned d = dst + (r & 1) * f.side;
+                    bulk_copy(d + (t + r / 2) * f.code_row, s + head0 * (D / 2), heads * (D / 2),
+                              full(stage));
+                    bulk_copy(d + f.scale_at + (t + r / 2) * f.scale_row,
+                              s + a.kv_heads * (D / 2) + scale_lo, scale_hi - scale_lo,
+                              full(stage));
+                }
+            };
+            // One warp does this for eight that multiply, so instructions count: at 300 a stage
+            // it was what the kernel waited for.  A lane looks after tokens lane, lane + 32, ...
+            // of a stage, LOOK of them, and has their page ids kFourAhead stages early.
+            auto produce = [&](auto look) {
+                constexpr int LOOK = decltype(look)::value;
+                int ids[kFourAhead][LOOK];
+                auto look_up = [&](int i, int (&id)[LOOK]) {
+                    if (i >= todo)
+                        return;
+                    const int j0 = key_of(i);
+                    const bool whole = whole_at(j0);
 #pragma unroll
-                        for (int b = 0; b < kFourLook; ++b)
-                            if (run[b] && unsigned(page[b]) >= unsigned(a.num_pages))
-                                for (int x = 0; x < 2; ++x)
-                                    for (int t = lane + 32 * b; t < lane + 32 * b + run[b]; ++t) {
-                                        char *s = attend_smem + (stage * 2 + x) * f.side;
-                                        for (int c = 0; c < f.code_row; c += 16)
-                                            *reinterpret_cast<uint4 *>(s + t * f.code_row + c) =
-                                                make_uint4(0, 0, 0, 0);
-                                        for (int c = 0; f.groups > 1 && c < f.scale_row; c += 16)
-                                            *reinterpret_cast<uint4 *>(s + f.scale_at +
-                                                                       t * f.scale_row + c) =
-                                                make_uint4(0, 0, 0, 0);
-                                    }
+                    for (int b = 0; b < LOOK; ++b) {
+                        int nth, in;
+                        if (run_at(j0, lane + 32 * b, whole, nth, in))
+                            id[b] = at.req.table[nth];
                     }
-                    fence_async_shared();
-                    __syncwarp();
-                }
+                };
 #pragma unroll
-                for (int d = 16; d; d >>= 1)
-                    bytes += __shfl_xor_sync(0xffffffffu, bytes, d);
-                if (lane == 0 && ok) {
-                    if (bytes)
-                        mbar_expect(full(stage), bytes);
-                    else
-                        mbar_arrive(full(stage));
-                }
-                __syncwarp();
+                for (int q = 0; q < kFourAhead; ++q)
+                    look_up(q, ids[q]);
+#pragma unroll 1
+                for (int i = 0; i < todo; ++i) {
+                    const int j0 = key_of(i);
+                    const bool whole = whole_at(j0);
+                    int n[LOOK], in[LOOK], page[LOOK];
+                    bool bad = false;
 #pragma unroll
-                for (int b = 0; b < kFourLook; ++b) {
-                    if (!ok || !run[b] || unsigned(page[b]) >= unsigned(a.num_pages))
-                        continue;
-                    const int t = lane + 32 * b;
-                    const int64_t src = (int64_t(page[b]) * a.page_size + off[b]) * a.token_bytes;
-                    if (f.groups == 1) {
-                        const unsigned n = unsigned(run[b]) * unsigned(a.token_bytes);
-                        bulk_copy(dst + t * f.code_row, a.k + src, n, full(stage));
-                        bulk_copy(dst + f.side + t * f.code_row, a.v + src, n, full(stage));
-                        continue;
+                    for (int b = 0; b < LOOK; ++b) {
+                        int nth;
+                        n[b] = run_at(j0, lane + 32 * b, whole, nth, in[b]);
+                        page[b] = ids[0][b];
+                        bad |= n[b] && unsigned(page[b]) >= unsigned(a.num_pages);
                     }
-                    const int codes = a.kv_heads * (D / 2), lo = head0 * (D / 16) / 16 * 16;
-                    const int hi = ((head0 + heads) * (D / 16) + 15) / 16 * 16;
-                    for (int r = 0; r < run[b]; ++r)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const char *s = (x ? a.v : a.k) + src + r * a.token_bytes;
-                            const unsigned d = dst + x * f.side;
-                            bulk_copy(d + (t + r) * f.code_row, s + head0 * (D / 2),
-                                      heads * (D / 2), full(stage));
-                            bulk_copy(d + f.scale_at + (t + r) * f.scale_row, s + codes + lo,
-                                      hi - lo, full(stage));
+                    for (int q = 0; q + 1 < kFourAhead; ++q)
+#pragma unroll
+                        for (int b = 0; b < LOOK; ++b)
+                            ids[q][b] = ids[q + 1][b];
+                    look_up(i + kFourAhead, ids[kFourAhead - 1]);
+                    if (ok)
+                        ok = mbar_wait(empty(stage), phase ^ 1, &gave_up, a.status);
+                    unsigned bytes = 2 * unsigned(f.keys) * per_token;
+                    bad = __any_sync(0xffffffffu, bad);
+                    if (bad || !whole) {
+                        bytes = 0;
+#pragma unroll
+                        for (int b = 0; b < LOOK; ++b) {
+                            if (n[b] && unsigned(page[b]) >= unsigned(a.num_pages)) {
+                                atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+                                clear(lane + 32 * b, n[b]);
+                                n[b] = 0;
+                            }
+                            bytes += 2 * n[b] * per_token;
                         }
-                }
+                        bytes = __reduce_add_sync(0xffffffffu, bytes);
+                        fence_async_shared();
+                        __syncwarp();
+                    }
+                    if (!ok)
+                        continue;
+                    if (lane == 0) {
+                        if (bytes)
+                            mbar_expect(full(stage), bytes);
+                        else
+                            mbar_arrive(full(stage));
+                    }
+                    __syncwarp();
+                    const unsigned dst = ring + stage * 2 * f.side;
 #pragma unroll
-                for (int b = 0; b < kFourLook; ++b)
-                    page[b] = page_of(i + 1, b);
-                filled += ok;
-                advance();
-            }
+                    for (int b = 0; b < LOOK; ++b) {
+                        if (n[b] == 0)
+                            continue;
+                        const int t = lane + 32 * b;
+                        const int64_t src =
+                            (int64_t(page[b]) * a.page_size + in[b]) * a.token_bytes;
+                        if (f.groups == 1) {
+                            const unsigned size = unsigned(n[b]) * per_token;
+                            bulk_copy(dst + t * f.code_row, a.k + src, size, full(stage));
+                            bulk_copy(dst + f.side + t * f.code_row, a.v + src, size, full(stage));
+                        } else {
+                            copy_group(dst, t, n[b], src);
+                        }
+                    }
+                    ++filled;
+                    advance();
+                }
+            };
+            if (f.keys <= 32)
+                produce(Looks<1>());
+            else if (f.keys <= 64)
+                produce(Looks<2>());
+            else
+                produce(Looks<4>());
             next_unit();
         }
         if (!ok) {
@@ -315,6 +351,14 @@ kvx_attend_four_kernel(const Attend a, const Work w)
         const bool active = hh < f.heads && kv_head < a.kv_heads;
         // Byte of the group's first scale within a stage's 16-byte units of them.
         const int scale0 = f.groups == 1 ? 0 : at.head * f.heads * (D / 16) % 16;
+
+        // From a stage's start: codes and scales of K of key quad, of V of key 2 c.
+        const int t0 = sub * kFourKeys, in = hh * (D / 2), in_unit = scale0 + hh * (D / 16);
+        const int k_code = (t0 + quad) * f.code_row + in + c * (D / 8);
+        const int k_unit = f.scale_at + (t0 + quad) * f.scale_row + in_unit + c * (D / 64);
+        const int v_code = f.side + (t0 + 2 * c) * f.code_row + in + quad * (D / 16);
+        const int v_unit = f.side + f.scale_at + (t0 + 2 * c) * f.scale_row + in_unit +
+                           quad * (D / 16) / 8;
 
         // q as the second operand, in the order in which a thread reads K: step s of quad thread
         // c takes elements (D / 4) c + 4 s .. + 3.
@@ -367,17 +411,26 @@ kvx_attend_four_kernel(const Attend a, const Work w)
 #pragma unroll
             for (int t = 0; t < kSteps; ++t)
                 o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.0f;
-            m[n][0] = m[n][1] = -INFINITY;
+            m[n][0] = m[n][1] = 0.0f;
             l[n][0] = l[n][1] = 0.0f;
         }
+        // Rows (the same for the lanes that share them) of which no key has been seen; and the
+        // first keys of 16 that all rows see: from seen_lo to seen_hi, or up to seen_pre.
+        unsigned fresh = (1u << 2 * NT) - 1;
+        const int seen_hi = keys.pmin - kFourKeys + 1, seen_pre = keys.prefix - kFourKeys;
+        const int seen_lo = a.window ? keys.pmax - a.window + 1 : 0;
 
 #pragma unroll 1
         for (int i = 0; i < todo; ++i) {
             if (ok)
                 ok = mbar_wait(full(stage), phase, &gave_up, a.status);
-            const int t0 = sub * kFourKeys, j0 = key_of(i) + t0;
-            const unsigned ks = ring + stage * 2 * f.side, vs = ks + f.side;
+            const int j0 = key_of(i) + sub * kFourKeys;
             if (ok && active) {
+                // This stage's K and V, at the thread's own codes and scales of its first key.
+                const char *kc = attend_smem + stage * 2 * f.side + k_code;
+                const char *ku = attend_smem + stage * 2 * f.side + k_unit;
+                const char *vc = attend_smem + stage * 2 * f.side + v_code;
+                const char *vv = attend_smem + stage * 2 * f.side + v_unit;
                 // Scores: s[n][2 x + e] is key j0 + quad + 8 x, row 8 n + 2 c + e.
                 float s[NT][4], odd[NT][4];
 #pragma unroll
@@ -387,23 +440,35 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                 unsigned code[2][D / 32], unit[2][2];  // unit: of the first and second block
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int t = t0 + quad + 8 * x;
-                    const unsigned ka = ks + t * f.code_row + hh * (D / 2) + c * (D / 8);
-                    const unsigned sa = ks + f.scale_at + t * f.scale_row + scale0 +
-                                        hh * (D / 16) + c * (D / 64);
+                    const char *ka = kc + (x ? 8 * f.code_row : 0);
+                    const char *sa = ku + (x ? 8 * f.scale_row : 0);
                     if (D == 128) {
-                        const uint4 u = lds16(ka);
+                        const uint4 u = *reinterpret_cast<const uint4 *>(ka);
                         code[x][0] = u.x, code[x][1] = u.y;
                         code[x][D / 32 - 2] = u.z, code[x][D / 32 - 1] = u.w;
-                        const unsigned two = half2_of_e4m3(lds_u16(sa));
+                        const unsigned two =
+                            half2_of_e4m3(*reinterpret_cast<const uint16_t *>(sa));
                         unit[x][0] = __byte_perm(two, 0, 0x1010);
                         unit[x][1] = __byte_perm(two, 0, 0x3232);
                     } else {
-                        const uint2 u = lds8(ka);
+                        const uint2 u = *reinterpret_cast<const uint2 *>(ka);
                         code[x][0] = u.x, code[x][1] = u.y;
-                        unit[x][0] = half2_of_e4m3(lds_u8(sa) * 0x101);
+                        unit[x][0] = half2_of_e4m3(*reinterpret_cast<const uint8_t *>(sa) * 0x101u);
                         unit[x][1] = unit[x][0];
                     }
+                }
+                // V of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9: elements quad D / 8 and on.
+                unsigned v[4][D / 64], vu[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int t = (y & 1) + 8 * (y >> 1);
+                    if (D == 128) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(vc + t * f.code_row);
+                        v[y][0] = u.x, v[y][D / 64 - 1] = u.y;
+                    } else {
+                        v[y][0] = *reinterpret_cast<const unsigned *>(vc + t * f.code_row);
+                    }
+                    vu[y] = *reinterpret_cast<const uint8_t *>(vv + t * f.scale_row);
                 }
 #pragma unroll
                 for (int g = 0; g < D / 32; ++g) {
@@ -420,48 +485,60 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                         const unsigned k[4] = {h0[2 * y], h1[2 * y], h0[2 * y + 1], h1[2 * y + 1]};
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            mma16816<KVX_TYPE_HALF>(y ? odd[n] : s[n], k, qb[n][2 * g + y][0],
+                            mma_half(y ? odd[n] : s[n], k, qb[n][2 * g + y][0],
                                                     qb[n][2 * g + y][1]);
                     }
                 }
 
-                const bool all_seen = j0 + kFourKeys <= keys.prefix ||
-                                      (j0 + kFourKeys - 1 <= keys.pmin &&
-                                       (!a.window || j0 > keys.pmax - a.window));
-                bool lift = false;
+                // Scores less what is subtracted, m, which may lag behind the maximum, as in the
+                // other kernel.
+                const bool all_seen = (j0 <= seen_hi && j0 >= seen_lo) || j0 <= seen_pre;
+                float top = -INFINITY;
+                if (plain && all_seen) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int e = x & 1;
-                        float z = (s[n][x] + odd[n][x]) * factor[n][e];
-                        if (!plain) {
+                        for (int x = 0; x < 4; ++x)
+                            s[n][x] = fmaf(s[n][x] + odd[n][x], factor[n][x & 1], -m[n][x & 1]);
+                        top = max3(top, s[n][0], s[n][1]);
+                        top = max3(top, s[n][2], s[n][3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int e = x & 1, j = j0 + quad + 8 * (x >> 1);
+                            float z = (s[n][x] + odd[n][x]) * factor[n][e];
                             if (a.softcap > 0.0f)
                                 z = score.cap * tanh_(z);
-                            z -= slope[n][e] * fabsf(float(pos[n][e] - j0 - quad - 8 * (x >> 1)));
-                        }
-                        if (!all_seen) {
-                            const int j = j0 + quad + 8 * (x >> 1);
+                            z -= slope[n][e] * fabsf(float(pos[n][e] - j));
                             if (!(j < keys.prefix || (j <= pos[n][e] &&
                                                       (!a.window || pos[n][e] - j < a.window))))
                                 z = -INFINITY;
+                            s[n][x] = z - m[n][e];
+                            top = fmaxf(top, s[n][x]);
                         }
-                        s[n][x] = z;
-                        lift |= z > m[n][e] + (kRoom + 8.0f);
-                    }
-                // What is subtracted may lag behind the maximum, as in the other kernel.
-                if (__any_sync(0xffffffffu, lift)) {
+                }
+                if (__any_sync(0xffffffffu, top > kRoom + 8.0f || fresh)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float top = fmaxf(s[n][e], s[n][2 + e]);
+                            float most = fmaxf(s[n][e], s[n][2 + e]);
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1)
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                            const float next = fmaxf(m[n][e], top - kRoom);
-                            const float keep = next == -INFINITY ? 1.0f : exp2_(m[n][e] - next);
-                            m[n][e] = next;
+                                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                            // A row's first keys set m, down as well as up.
+                            const unsigned bit = 1u << (2 * n + e);
+                            const bool first = fresh & bit && most > -INFINITY;
+                            const float up = first         ? most - kRoom
+                                             : fresh & bit ? 0.0f : fmaxf(most - kRoom, 0.0f);
+                            const float keep = first ? 1.0f : exp2_(-up);
+                            fresh &= ~(first ? bit : 0u);
+                            m[n][e] += up;
+                            s[n][e] -= up;
+                            s[n][2 + e] -= up;
                             l[n][e] *= keep;
 #pragma unroll
                             for (int t = 0; t < kSteps; ++t) {
@@ -473,38 +550,24 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                 unsigned p[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float z[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const int e = x & 1;
-                        z[x] = exp2_(s[n][x] - (m[n][e] == -INFINITY ? 0.0f : m[n][e]));
-                        l[n][e] += z[x];
+                        s[n][x] = exp2_(s[n][x]);
+                        l[n][x & 1] += s[n][x];
                     }
-                    p[n][0] = transpose8x8(P::pack(z[0], z[1]));
-                    p[n][1] = transpose8x8(P::pack(z[2], z[3]));
+                    p[n][0] = transpose8x8(P::pack(s[n][0], s[n][1]));
+                    p[n][1] = transpose8x8(P::pack(s[n][2], s[n][3]));
                 }
 
-                // V of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9: elements quad D / 8 and on.  A key
-                // that no row sees has no weight; its scale is 0 too, whatever memory holds.
-                unsigned v[4][D / 64], vu[2];
+                // A key that no row sees has no weight; its scale is 0 too, whatever memory holds.
+                if (!all_seen) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int t = t0 + 2 * c + (y & 1) + 8 * (y >> 1);
-                    const unsigned va = vs + t * f.code_row + hh * (D / 2) + quad * (D / 16);
-                    if (D == 128) {
-                        const uint2 u = lds8(va);
-                        v[y][0] = u.x, v[y][D / 64 - 1] = u.y;
-                    } else {
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[y][0]) : "r"(va) : "memory");
-                    }
-                    unsigned one = lds_u8(vs + f.scale_at + t * f.scale_row + scale0 +
-                                          hh * (D / 16) + quad * (D / 16) / 8);
-                    if (!all_seen && !keys.used(key_of(i) + t))
-                        one = 0;
-                    vu[y >> 1] = y & 1 ? vu[y >> 1] | one << 8 : one;
+                    for (int y = 0; y < 4; ++y)
+                        if (!keys.used(j0 + 2 * c + (y & 1) + 8 * (y >> 1)))
+                            vu[y] = 0;
                 }
-                vu[0] = half2_of_e4m3(vu[0]);
-                vu[1] = half2_of_e4m3(vu[1]);
+                const unsigned va = half2_of_e4m3(vu[0] | vu[1] << 8);
+                const unsigned vb = half2_of_e4m3(vu[2] | vu[3] << 8);
 #pragma unroll
                 for (int g = 0; g < D / 64; ++g) {
                     unsigned h[4][4];
@@ -514,13 +577,13 @@ kvx_attend_four_kernel(const Attend a, const Work w)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const unsigned k[4] = {
-                            mul_half2(__byte_perm(h[0][x], h[1][x], 0x5410), vu[0]),
-                            mul_half2(__byte_perm(h[0][x], h[1][x], 0x7632), vu[0]),
-                            mul_half2(__byte_perm(h[2][x], h[3][x], 0x5410), vu[1]),
-                            mul_half2(__byte_perm(h[2][x], h[3][x], 0x7632), vu[1])};
+                            mul_half2(__byte_perm(h[0][x], h[1][x], 0x5410), va),
+                            mul_half2(__byte_perm(h[0][x], h[1][x], 0x7632), va),
+                            mul_half2(__byte_perm(h[2][x], h[3][x], 0x5410), vb),
+                            mul_half2(__byte_perm(h[2][x], h[3][x], 0x7632), vb)};
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            mma16816<KVX_TYPE_HALF>(o[n][4 * g + x], k, p[n][0], p[n][1]);
+                            mma_half(o[n][4 * g + x], k, p[n][0], p[n][1]);
                     }
                 }
             }
@@ -537,6 +600,12 @@ kvx_attend_four_kernel(const Attend a, const Work w)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+        // A row without keys here has no weight in what follows.
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                m[n][e] = fresh >> (2 * n + e) & 1 ? -1e30f : m[n][e];
         // Join the warps of a head by halves: the upper half hands its results to the lower.
         // Warps past the group's heads have no part in it.
         for (int half = f.split / 2; half > 0 && hh < f.heads; half >>= 1) {
@@ -569,8 +638,7 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                         const float2 other = *reinterpret_cast<const float2 *>(
                             area + kRowsMax * (D + 4) + 2 * row);
                         const float top = fmaxf(m[n][e], other.x);
-                        const float x = m[n][e] == -INFINITY ? 0.0f : exp2_(m[n][e] - top);
-                        const float y = other.x == -INFINITY ? 0.0f : exp2_(other.x - top);
+                        const float x = exp2_(m[n][e] - top), y = exp2_(other.x - top);
                         m[n][e] = top;
                         l[n][e] = l[n][e] * x + other.y * y;
 #pragma unroll
