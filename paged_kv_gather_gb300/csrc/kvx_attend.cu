@@ -126,7 +126,7 @@ Kernel pick_kernel(const kvx_attn_plan *p, int kind)
 {
     const kvx_attn_cfg &c = p->cfg;
     if (c.kv_type == KVX_TYPE_FP_FOUR)
-        return kvx::four_kernel(c, p->token_bytes, kind);
+        return kvx::four_kernel(c, p->token_bytes, kind, p->most_parts[kind]);
     const bool half = c.type == KVX_TYPE_HALF, eight = c.kv_type == KVX_TYPE_FP_EIGHT;
     const int H = KVX_TYPE_HALF, B = KVX_TYPE_BFLOAT, F = KVX_TYPE_FP_EIGHT;
     if (c.head_dim == 64)
@@ -158,9 +158,12 @@ struct Scheduler {
             unit_cost = plain ? kUnitTiles : kUnitTiles / 2;
             part_cost = plain ? kPartTiles : kPartTiles / 2;
             join_cost = plain ? kLaunchTiles : kLaunchTiles / 2;
+        } else if (p->cfg.kv_type == KVX_TYPE_FP_FOUR) {
+            kvx::four_units(p->cfg, p->token_bytes, &heads, &tile_keys);
+            unit_cost = kFourUnitTiles;
+            part_cost = kFourPartTiles;
+            join_cost = kFourJoinTiles;
         } else {
-            if (p->cfg.kv_type == KVX_TYPE_FP_FOUR)
-                kvx::four_units(p->cfg, p->token_bytes, &heads, &tile_keys);
             const int64_t tile_bytes = 2 * tile_keys * p->token_bytes / heads;
             unit_cost = std::max<int64_t>(1, kUnitBytes / tile_bytes);
             part_cost = std::max<int64_t>(1, kPartBytes / tile_bytes);
@@ -368,10 +371,12 @@ kvx_status fill_plan(kvx_attn_plan *p, const kvx_request *reqs, int n_req, const
         int64_t time;
         p->ctas[k] = Scheduler(p, k, lists[k], counts[k]).run(starts, &time, &shares);
         int32_t *cuts = reinterpret_cast<int32_t *>(p->host + p->cuts_at(k));
-        p->cuts[k] = 0;
+        p->cuts[k] = p->most_parts[k] = 0;
         for (int c = 0; c + 1 < p->ctas[k]; ++c)
-            if (starts[c + 1].tile > 0 && starts[c + 1].first == c)
+            if (starts[c + 1].tile > 0 && starts[c + 1].first == c) {
                 cuts[p->cuts[k]++] = c;
+                p->most_parts[k] = std::max(p->most_parts[k], starts[c].last - c + 1);
+            }
         p->most_rows[k] = 0;
         for (int i = 0; i < counts[k]; ++i)
             p->most_rows[k] = std::max<int>(p->most_rows[k], lists[k][i].n_new * group);

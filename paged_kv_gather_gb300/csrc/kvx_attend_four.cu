@@ -8,22 +8,23 @@
 namespace {
 
 template <int TYPE, int D, int NT>
-Kernel few_rows(const kvx_attn_cfg &c, int64_t token_bytes)
+Kernel few_rows(const kvx_attn_cfg &c, int64_t token_bytes, int most_parts)
 {
     const FourShape f = FourShape::of(c.kv_heads, D, int(token_bytes));
     return {reinterpret_cast<const void *>(kvx_attend_four_kernel<TYPE, D, NT>), kFourThreads,
             four_ctas_per_sm(NT), four_smem<D, NT>(f), four_slot_floats<D, NT>(),
             reinterpret_cast<const void *>(kvx_attend_four_join_kernel<TYPE, D, NT>),
-            32 * kFourJoinWarps, 0, f.heads, four_room(NT)};
+            32 * (most_parts > kFourManyParts ? kFourJoinWarps : kFourJoinFew), 0, f.heads,
+            four_room(NT)};
 }
 
 template <int TYPE, int D>
-Kernel kernel_of(const kvx_attn_cfg &c, int64_t token_bytes, int kind)
+Kernel kernel_of(const kvx_attn_cfg &c, int64_t token_bytes, int kind, int most_parts)
 {
     if (kind == kRows)
-        return few_rows<TYPE, D, 1>(c, token_bytes);
+        return few_rows<TYPE, D, 1>(c, token_bytes, most_parts);
     if (kind == kMoreRows)
-        return few_rows<TYPE, D, 2>(c, token_bytes);
+        return few_rows<TYPE, D, 2>(c, token_bytes, most_parts);
     return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KVX_TYPE_FP_FOUR, D>),
             kTileThreads, 1, size_t(TileShape<KVX_TYPE_FP_FOUR, D>::kBytes),
             TileShape<KVX_TYPE_FP_FOUR, D>::kSlotFloats,
@@ -33,14 +34,14 @@ Kernel kernel_of(const kvx_attn_cfg &c, int64_t token_bytes, int kind)
 
 }  // namespace
 
-Kernel kvx::four_kernel(const kvx_attn_cfg &c, int64_t token_bytes, int kind)
+Kernel kvx::four_kernel(const kvx_attn_cfg &c, int64_t token_bytes, int kind, int most_parts)
 {
     const bool half = c.type == KVX_TYPE_HALF;
     if (c.head_dim == 64)
-        return half ? kernel_of<KVX_TYPE_HALF, 64>(c, token_bytes, kind)
-                    : kernel_of<KVX_TYPE_BFLOAT, 64>(c, token_bytes, kind);
-    return half ? kernel_of<KVX_TYPE_HALF, 128>(c, token_bytes, kind)
-                : kernel_of<KVX_TYPE_BFLOAT, 128>(c, token_bytes, kind);
+        return half ? kernel_of<KVX_TYPE_HALF, 64>(c, token_bytes, kind, most_parts)
+                    : kernel_of<KVX_TYPE_BFLOAT, 64>(c, token_bytes, kind, most_parts);
+    return half ? kernel_of<KVX_TYPE_HALF, 128>(c, token_bytes, kind, most_parts)
+                : kernel_of<KVX_TYPE_BFLOAT, 128>(c, token_bytes, kind, most_parts);
 }
 
 void kvx::four_units(const kvx_attn_cfg &c, int64_t token_bytes, int *groups, int *keys)

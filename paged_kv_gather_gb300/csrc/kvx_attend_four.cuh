@@ -697,10 +697,12 @@ kvx_attend_four_kernel(const Attend a, const Work w)
 }
 
 // The results of units that were cut: block (i, head and row) joins the parts of one row of the
-// i-th of them, each of its warps every kFourJoinWarps-th part.  One request of 256k tokens has
-// a part in every CTA, 300 of 33 KB, which its last CTA would be reading alone for longer than
-// the attention takes.
-const int kFourJoinWarps = 8;
+// i-th of them, its warps every so many parts each, four of them in flight.  One request of 256k
+// tokens has a part in every CTA, 300 of 33 KB, which its last CTA would be reading alone for
+// longer than the attention takes: 32 warps to a row then, eight where there are few parts.
+const int kFourJoinWarps = 32;    // at most
+const int kFourJoinFew = 8;       // where no unit has more than kFourManyParts
+const int kFourManyParts = 24;
 
 template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(32 * kFourJoinWarps)
@@ -708,8 +710,10 @@ kvx_attend_four_join_kernel(const Attend a, const Work w)
 {
     typedef Elem<TYPE> E;
     constexpr int kSlot = four_slot_floats<D, NT>(), kRowsMax = 8 * NT, kEach = D / 32;
+    constexpr int kBatch = 4;
     __shared__ float sum[kFourJoinWarps][D], ml[kFourJoinWarps][2];
     const int c0 = w.cuts[blockIdx.x], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warps = blockDim.x >> 5;
     const AttnStart next = w.starts[c0 + 1];
     const int c1 = w.starts[c0].last;
     const FourShape f = FourShape::of(a.kv_heads, D, int(a.token_bytes));
@@ -719,25 +723,41 @@ kvx_attend_four_join_kernel(const Attend a, const Work w)
     const int kv_head = next.head * f.heads + hh;
     if (row >= r.n_new * a.group || kv_head >= a.kv_heads)
         return;
-    float m = -INFINITY, l = 0.0f, o[kEach] = {};
+    float m = -1e30f, l = 0.0f, o[kEach] = {};
     const int at = hh * kRowsMax + row;
-#pragma unroll 4
-    for (int c = c0 + warp; c <= c1; c += kFourJoinWarps) {
-        const float *part = w.partial + (2 * int64_t(c) + (c == c0)) * kSlot;
-        const float2 p = __ldcg(reinterpret_cast<const float2 *>(part + kFourWarps * kRowsMax * D) +
-                                at);
-        float v[kEach];
+    for (int b = c0 + warp; b <= c1; b += kBatch * warps) {
+        float2 p[kBatch];
+        float v[kBatch][kEach];
 #pragma unroll
-        for (int k = 0; k < kEach; ++k)
-            v[k] = __ldcg(part + at * D + 32 * k + lane);
-        const float top = fmaxf(m, p.x);
-        const float x = m == -INFINITY ? 0.0f : exp2_(m - top);
-        const float y = p.x == -INFINITY ? 0.0f : exp2_(p.x - top);
+        for (int y = 0; y < kBatch; ++y) {
+            const int c = b + y * warps;
+            const float *part = w.partial + (2 * int64_t(c) + (c == c0)) * kSlot;
+            p[y] = make_float2(-1e30f, 0.0f);
+            if (c <= c1)
+                p[y] = __ldcg(
+                    reinterpret_cast<const float2 *>(part + kFourWarps * kRowsMax * D) + at);
+#pragma unroll
+            for (int k = 0; k < kEach; ++k)
+                v[y][k] = c <= c1 ? __ldcg(part + at * D + 32 * k + lane) : 0.0f;
+        }
+        float top = m;
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y)
+            top = fmaxf(top, p[y].x);
+        const float keep = exp2_(m - top);
         m = top;
-        l = l * x + p.y * y;
+        l *= keep;
 #pragma unroll
         for (int k = 0; k < kEach; ++k)
-            o[k] = o[k] * x + v[k] * y;
+            o[k] *= keep;
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+            const float x = exp2_(p[y].x - top);
+            l += p[y].y * x;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k)
+                o[k] += v[y][k] * x;
+        }
     }
 #pragma unroll
     for (int k = 0; k < kEach; ++k)
@@ -749,13 +769,12 @@ kvx_attend_four_join_kernel(const Attend a, const Work w)
     __syncthreads();
     if (threadIdx.x >= D / 2)
         return;
-    float mm = -INFINITY, ll = 0.0f, lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kFourJoinWarps; ++k)
+    float mm = -1e30f, ll = 0.0f, lo = 0.0f, hi = 0.0f;
+    for (int k = 0; k < warps; ++k)
         mm = fmaxf(mm, ml[k][0]);
-#pragma unroll
-    for (int k = 0; k < kFourJoinWarps; ++k) {
-        const float y = ml[k][0] == -INFINITY ? 0.0f : exp2_(ml[k][0] - mm);
+#pragma unroll 4
+    for (int k = 0; k < warps; ++k) {
+        const float y = exp2_(ml[k][0] - mm);
         ll += ml[k][1] * y;
         lo += sum[k][2 * threadIdx.x] * y;
         hi += sum[k][2 * threadIdx.x + 1] * y;

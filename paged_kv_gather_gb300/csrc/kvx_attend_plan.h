@@ -25,6 +25,10 @@ const int64_t kUnitTiles = 4, kPartTiles = 2;
 // A launch more, in tiles' time.
 const int64_t kLaunchTiles = 3;
 
+// The same of the kernel of few rows over a 4-bit cache, whose parts are joined by a launch of
+// its own, in its tiles.
+const int64_t kFourUnitTiles = 4, kFourPartTiles = 1, kFourJoinTiles = 4;
+
 // Up to this many units per SM are dealt out one by one (Scheduler::deal); past it the shares
 // of the line come out as even, and the descriptors long.
 const int kDealtPerSm = 16;
@@ -63,7 +67,8 @@ struct kvx_attn_plan {
     int64_t rows = 0;
     int ctas[kKinds] = {};     // of each kernel's launch
     int cuts[kKinds] = {};     // units that it cuts
-    int most_rows[kKinds] = {};  // of a request: new tokens x heads that share a KV head
+    int most_parts[kKinds] = {};  // of one of them
+    int most_rows[kKinds] = {};   // of a request: new tokens x heads that share a KV head
     // Descriptors: [AttnReq of each kind, of all][CTAs of each kind that begin a unit that is
     // cut][AttnStart of each kind, the last one's with room for units dealt out]; a pinned image,
     // and the device's copy.
@@ -189,9 +194,9 @@ inline kvx_status scales_check(const kvx_attn_plan *p, float k_scale, float v_sc
 
 namespace kvx {
 
-// Of a 4-bit cache: the kernels of a kind (kvx_attend_four.cu), and how a unit of theirs is made
-// up, the groups of KV heads and the keys of a step.
-Kernel four_kernel(const kvx_attn_cfg &c, int64_t token_bytes, int kind);
+// Of a 4-bit cache: the kernels of a kind (kvx_attend_four.cu) for units cut into so many parts,
+// and how a unit of theirs is made up, the groups of KV heads and the keys of a step.
+Kernel four_kernel(const kvx_attn_cfg &c, int64_t token_bytes, int kind, int most_parts);
 void four_units(const kvx_attn_cfg &c, int64_t token_bytes, int *groups, int *keys);
 
 // kvx_append_rotated's launch; without rope and q, kvx_append_tokens into a 4-bit cache
