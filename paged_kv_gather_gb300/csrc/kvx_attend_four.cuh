@@ -25,7 +25,7 @@ namespace {
 const int kFourWarps = 8;
 const int kFourThreads = 32 * (kFourWarps + 1);
 const int kFourStages = 8;    // at most
-const int kFourKeys = 16;     // of a warp and step
+const int kFourKeys = 32;     // of a warp and step, two products' worth
 const int kFourAhead = 3;     // stages that page ids are looked up before they are used
 
 template <int N>
@@ -82,18 +82,24 @@ __host__ __device__ constexpr int four_room(int NT)
     return 226 * 1024 / four_ctas_per_sm(NT) - 2 * 1024;
 }
 
+// Shared memory in which warps of a head hand over their results.
+template <int D, int NT>
+__host__ __device__ inline int four_join_bytes(const FourShape &f)
+{
+    return f.heads * (f.split / 2) * four_join_floats<D, NT>() * 4;
+}
+
 template <int D, int NT>
 __host__ __device__ inline int four_stages(const FourShape &f)
 {
-    const int n = (four_room(NT) - kFourWarps / 2 * four_join_floats<D, NT>() * 4) / (2 * f.side);
+    const int n = (four_room(NT) - four_join_bytes<D, NT>(f)) / (2 * f.side);
     return n < kFourStages ? n : kFourStages;
 }
 
 template <int D, int NT>
 inline size_t four_smem(const FourShape &f)
 {
-    return size_t(four_stages<D, NT>(f)) * 2 * f.side +
-           kFourWarps / 2 * four_join_floats<D, NT>() * 4;
+    return size_t(four_stages<D, NT>(f)) * 2 * f.side + four_join_bytes<D, NT>(f);
 }
 
 // As mma16816 in half precision; not volatile, so that products of K move among the conversions
@@ -125,6 +131,7 @@ kvx_attend_four_kernel(const Attend a, const Work w)
     typedef Elem<KVX_TYPE_HALF> P;
     constexpr float kRoom = P::kRoom;
     constexpr int kSteps = D / 16, kRowsMax = 8 * NT, kMine = D / 8;  // elements of V per thread
+    constexpr int kHalves = kFourKeys / 16;
     constexpr int kJoin = four_join_floats<D, NT>(), kSlot = four_slot_floats<D, NT>();
     __shared__ __align__(8) uint64_t bars[2 * kFourStages];
     __shared__ int gave_up;
@@ -322,8 +329,10 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                 produce(Looks<1>());
             else if (f.keys <= 64)
                 produce(Looks<2>());
-            else
+            else if (f.keys <= 128)
                 produce(Looks<4>());
+            else
+                produce(Looks<8>());
             next_unit();
         }
         if (!ok) {
@@ -427,66 +436,54 @@ kvx_attend_four_kernel(const Attend a, const Work w)
             const int j0 = key_of(i) + sub * kFourKeys;
             if (ok && active) {
                 // This stage's K and V, at the thread's own codes and scales of its first key.
-                const char *kc = attend_smem + stage * 2 * f.side + k_code;
-                const char *ku = attend_smem + stage * 2 * f.side + k_unit;
-                const char *vc = attend_smem + stage * 2 * f.side + v_code;
-                const char *vv = attend_smem + stage * 2 * f.side + v_unit;
-                // Scores: s[n][2 x + e] is key j0 + quad + 8 x, row 8 n + 2 c + e.
-                float s[NT][4], odd[NT][4];
+                const char *base = attend_smem + stage * 2 * f.side;
+                // Scores of both halves: s[u][n][2 x + e] is key j0 + 16 u + quad + 8 x, row 8 n +
+                // 2 c + e.
+                float s[kHalves][NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = odd[n][0] = odd[n][1] = odd[n][2] =
-                        odd[n][3] = 0.0f;
-                unsigned code[2][D / 32], unit[2][2];  // unit: of the first and second block
+                for (int u = 0; u < kHalves; ++u) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const char *ka = kc + (x ? 8 * f.code_row : 0);
-                    const char *sa = ku + (x ? 8 * f.scale_row : 0);
-                    if (D == 128) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(ka);
-                        code[x][0] = u.x, code[x][1] = u.y;
-                        code[x][D / 32 - 2] = u.z, code[x][D / 32 - 1] = u.w;
-                        const unsigned two =
-                            half2_of_e4m3(*reinterpret_cast<const uint16_t *>(sa));
-                        unit[x][0] = __byte_perm(two, 0, 0x1010);
-                        unit[x][1] = __byte_perm(two, 0, 0x3232);
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(ka);
-                        code[x][0] = u.x, code[x][1] = u.y;
-                        unit[x][0] = half2_of_e4m3(*reinterpret_cast<const uint8_t *>(sa) * 0x101u);
-                        unit[x][1] = unit[x][0];
-                    }
-                }
-                // V of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9: elements quad D / 8 and on.
-                unsigned v[4][D / 64], vu[4];
+                    for (int n = 0; n < NT; ++n)
+                        s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.0f;
+                    unsigned code[2][D / 32], unit[2][2];  // unit: of the first and second block
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int t = (y & 1) + 8 * (y >> 1);
-                    if (D == 128) {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(vc + t * f.code_row);
-                        v[y][0] = u.x, v[y][D / 64 - 1] = u.y;
-                    } else {
-                        v[y][0] = *reinterpret_cast<const unsigned *>(vc + t * f.code_row);
-                    }
-                    vu[y] = *reinterpret_cast<const uint8_t *>(vv + t * f.scale_row);
-                }
-#pragma unroll
-                for (int g = 0; g < D / 32; ++g) {
-                    unsigned h0[4], h1[4];
-                    half8_of_e2m1(code[0][g], h0);
-                    half8_of_e2m1(code[1][g], h1);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        h0[y] = mul_half2(h0[y], unit[0][g / 2]);
-                        h1[y] = mul_half2(h1[y], unit[1][g / 2]);
+                    for (int x = 0; x < 2; ++x) {
+                        const char *ka = base + k_code + (16 * u + 8 * x) * f.code_row;
+                        const char *sa = base + k_unit + (16 * u + 8 * x) * f.scale_row;
+                        if (D == 128) {
+                            const uint4 w4 = *reinterpret_cast<const uint4 *>(ka);
+                            code[x][0] = w4.x, code[x][1] = w4.y;
+                            code[x][D / 32 - 2] = w4.z, code[x][D / 32 - 1] = w4.w;
+                            const unsigned two =
+                                half2_of_e4m3(*reinterpret_cast<const uint16_t *>(sa));
+                            unit[x][0] = __byte_perm(two, 0, 0x1010);
+                            unit[x][1] = __byte_perm(two, 0, 0x3232);
+                        } else {
+                            const uint2 w2 = *reinterpret_cast<const uint2 *>(ka);
+                            code[x][0] = w2.x, code[x][1] = w2.y;
+                            unit[x][0] =
+                                half2_of_e4m3(*reinterpret_cast<const uint8_t *>(sa) * 0x101u);
+                            unit[x][1] = unit[x][0];
+                        }
                     }
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const unsigned k[4] = {h0[2 * y], h1[2 * y], h0[2 * y + 1], h1[2 * y + 1]};
+                    for (int g = 0; g < D / 32; ++g) {
+                        unsigned h0[4], h1[4];
+                        half8_of_e2m1(code[0][g], h0);
+                        half8_of_e2m1(code[1][g], h1);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma_half(y ? odd[n] : s[n], k, qb[n][2 * g + y][0],
-                                                    qb[n][2 * g + y][1]);
+                        for (int y = 0; y < 4; ++y) {
+                            h0[y] = mul_half2(h0[y], unit[0][g / 2]);
+                            h1[y] = mul_half2(h1[y], unit[1][g / 2]);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const unsigned k[4] = {h0[2 * y], h1[2 * y], h0[2 * y + 1],
+                                                   h1[2 * y + 1]};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_half(s[u][n], k, qb[n][2 * g + y][0], qb[n][2 * g + y][1]);
+                        }
                     }
                 }
 
@@ -496,36 +493,44 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                 float top = -INFINITY;
                 if (plain && all_seen) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
+                    for (int u = 0; u < kHalves; ++u)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            s[n][x] = fmaf(s[n][x] + odd[n][x], factor[n][x & 1], -m[n][x & 1]);
-                        top = max3(top, s[n][0], s[n][1]);
-                        top = max3(top, s[n][2], s[n][3]);
-                    }
+                        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                s[u][n][x] = fmaf(s[u][n][x], factor[n][x & 1], -m[n][x & 1]);
+                            top = max3(top, s[u][n][0], s[u][n][1]);
+                            top = max3(top, s[u][n][2], s[u][n][3]);
+                        }
                 } else {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int u = 0; u < kHalves; ++u)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int e = x & 1, j = j0 + quad + 8 * (x >> 1);
-                            float z = (s[n][x] + odd[n][x]) * factor[n][e];
-                            if (a.softcap > 0.0f)
-                                z = score.cap * tanh_(z);
-                            z -= slope[n][e] * fabsf(float(pos[n][e] - j));
-                            if (!(j < keys.prefix || (j <= pos[n][e] &&
-                                                      (!a.window || pos[n][e] - j < a.window))))
-                                z = -INFINITY;
-                            s[n][x] = z - m[n][e];
-                            top = fmaxf(top, s[n][x]);
-                        }
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const int e = x & 1, j = j0 + 16 * u + quad + 8 * (x >> 1);
+                                float z = s[u][n][x] * factor[n][e];
+                                if (a.softcap > 0.0f)
+                                    z = score.cap * tanh_(z);
+                                z -= slope[n][e] * fabsf(float(pos[n][e] - j));
+                                if (!(j < keys.prefix ||
+                                      (j <= pos[n][e] &&
+                                       (!a.window || pos[n][e] - j < a.window))))
+                                    z = -INFINITY;
+                                s[u][n][x] = z - m[n][e];
+                                top = fmaxf(top, s[u][n][x]);
+                            }
                 }
                 if (__any_sync(0xffffffffu, top > kRoom + 8.0f || fresh)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float most = fmaxf(s[n][e], s[n][2 + e]);
+                            float most = -INFINITY;
+#pragma unroll
+                            for (int u = 0; u < kHalves; ++u)
+                                most = max3(most, s[u][n][e], s[u][n][2 + e]);
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1)
                                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
@@ -537,8 +542,11 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                             const float keep = first ? 1.0f : exp2_(-up);
                             fresh &= ~(first ? bit : 0u);
                             m[n][e] += up;
-                            s[n][e] -= up;
-                            s[n][2 + e] -= up;
+#pragma unroll
+                            for (int u = 0; u < kHalves; ++u) {
+                                s[u][n][e] -= up;
+                                s[u][n][2 + e] -= up;
+                            }
                             l[n][e] *= keep;
 #pragma unroll
                             for (int t = 0; t < kSteps; ++t) {
@@ -547,43 +555,63 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                             }
                         }
                 }
-                unsigned p[NT][2];
+                unsigned p[kHalves][NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int u = 0; u < kHalves; ++u)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        s[n][x] = exp2_(s[n][x]);
-                        l[n][x & 1] += s[n][x];
+                    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            s[u][n][x] = exp2_(s[u][n][x]);
+                            l[n][x & 1] += s[u][n][x];
+                        }
+                        p[u][n][0] = transpose8x8(P::pack(s[u][n][0], s[u][n][1]));
+                        p[u][n][1] = transpose8x8(P::pack(s[u][n][2], s[u][n][3]));
                     }
-                    p[n][0] = transpose8x8(P::pack(s[n][0], s[n][1]));
-                    p[n][1] = transpose8x8(P::pack(s[n][2], s[n][3]));
-                }
 
-                // A key that no row sees has no weight; its scale is 0 too, whatever memory holds.
-                if (!all_seen) {
+                // V of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9: elements quad D / 8 and on.  A key
+                // that no row sees has no weight; its scale is 0 too, whatever memory holds.
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        if (!keys.used(j0 + 2 * c + (y & 1) + 8 * (y >> 1)))
-                            vu[y] = 0;
-                }
-                const unsigned va = half2_of_e4m3(vu[0] | vu[1] << 8);
-                const unsigned vb = half2_of_e4m3(vu[2] | vu[3] << 8);
+                for (int u = 0; u < kHalves; ++u) {
+                    unsigned v[4][D / 64], vu[4];
 #pragma unroll
-                for (int g = 0; g < D / 64; ++g) {
-                    unsigned h[4][4];
+                    for (int y = 0; y < 4; ++y) {
+                        const int t = 16 * u + (y & 1) + 8 * (y >> 1);
+                        const char *va = base + v_code + t * f.code_row;
+                        if (D == 128) {
+                            const uint2 w2 = *reinterpret_cast<const uint2 *>(va);
+                            v[y][0] = w2.x, v[y][D / 64 - 1] = w2.y;
+                        } else {
+                            v[y][0] = *reinterpret_cast<const unsigned *>(va);
+                        }
+                        vu[y] = *reinterpret_cast<const uint8_t *>(base + v_unit +
+                                                                   t * f.scale_row);
+                    }
+                    if (!all_seen) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        half8_of_e2m1(v[y][g], h[y]);
+                        for (int y = 0; y < 4; ++y)
+                            if (!keys.used(j0 + 16 * u + 2 * c + (y & 1) + 8 * (y >> 1)))
+                                vu[y] = 0;
+                    }
+                    const unsigned unit0 = half2_of_e4m3(vu[0] | vu[1] << 8);
+                    const unsigned unit1 = half2_of_e4m3(vu[2] | vu[3] << 8);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const unsigned k[4] = {
-                            mul_half2(__byte_perm(h[0][x], h[1][x], 0x5410), va),
-                            mul_half2(__byte_perm(h[0][x], h[1][x], 0x7632), va),
-                            mul_half2(__byte_perm(h[2][x], h[3][x], 0x5410), vb),
-                            mul_half2(__byte_perm(h[2][x], h[3][x], 0x7632), vb)};
+                    for (int g = 0; g < D / 64; ++g) {
+                        unsigned h[4][4];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma_half(o[n][4 * g + x], k, p[n][0], p[n][1]);
+                        for (int y = 0; y < 4; ++y)
+                            half8_of_e2m1(v[y][g], h[y]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const unsigned k[4] = {
+                                mul_half2(__byte_perm(h[0][x], h[1][x], 0x5410), unit0),
+                                mul_half2(__byte_perm(h[0][x], h[1][x], 0x7632), unit0),
+                                mul_half2(__byte_perm(h[2][x], h[3][x], 0x5410), unit1),
+                                mul_half2(__byte_perm(h[2][x], h[3][x], 0x7632), unit1)};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_half(o[n][4 * g + x], k, p[u][n][0], p[u][n][1]);
+                        }
                     }
                 }
             }

@@ -27,7 +27,7 @@ const int64_t kLaunchTiles = 3;
 
 // The same of the kernel of few rows over a 4-bit cache, whose parts are joined by a launch of
 // its own, in its tiles.
-const int64_t kFourUnitTiles = 4, kFourPartTiles = 1, kFourJoinTiles = 4;
+const int64_t kFourUnitTiles = 2, kFourPartTiles = 1, kFourJoinTiles = 2;
 
 // Up to this many units per SM are dealt out one by one (Scheduler::deal); past it the shares
 // of the line come out as even, and the descriptors long.
