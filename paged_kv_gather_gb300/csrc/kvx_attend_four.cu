@@ -11,8 +11,10 @@ template <int TYPE, int D, int NT>
 Kernel few_rows(const kvx_attn_cfg &c, int64_t token_bytes, int most_parts)
 {
     const FourShape f = FourShape::of(c.kv_heads, D, int(token_bytes));
-    return {reinterpret_cast<const void *>(kvx_attend_four_kernel<TYPE, D, NT>), kFourThreads,
-            four_ctas_per_sm(NT), four_smem<D, NT>(f), four_slot_floats<D, NT>(),
+    const bool plain = !(c.softcap > 0.0f) && !c.slopes;
+    return {plain ? reinterpret_cast<const void *>(kvx_attend_four_kernel<TYPE, D, NT, true>)
+                  : reinterpret_cast<const void *>(kvx_attend_four_kernel<TYPE, D, NT, false>),
+            kFourThreads, four_ctas_per_sm(NT), four_smem<D, NT>(f), four_slot_floats<D, NT>(),
             reinterpret_cast<const void *>(kvx_attend_four_join_kernel<TYPE, D, NT>),
             32 * (most_parts > kFourManyParts ? kFourJoinWarps : kFourJoinFew), 0, f.heads,
             four_room(NT)};

@@ -123,7 +123,9 @@ __device__ __forceinline__ void bulk_copy(unsigned dst, const void *src, unsigne
                  : "memory");
 }
 
-template <int TYPE, int D, int NT>
+// PLAIN: neither a cap nor a bias, whose code keeps the rest from staying in the instruction
+// caches.
+template <int TYPE, int D, int NT, bool PLAIN>
 __global__ void __launch_bounds__(kFourThreads, four_ctas_per_sm(NT))
 kvx_attend_four_kernel(const Attend a, const Work w)
 {
@@ -350,7 +352,6 @@ kvx_attend_four_kernel(const Attend a, const Work w)
     const int quad = lane >> 2, c = lane & 3;
     const int hh = warp / f.split, sub = warp - hh * f.split;  // head of the group, share of keys
     const Score score(a);
-    const bool plain = !(a.softcap > 0.0f) && !a.slopes;
     float *join = reinterpret_cast<float *>(attend_smem + stages * 2 * f.side);
     wait_for_earlier_work();
     while (at.tiles > 0) {
@@ -491,7 +492,7 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                 // other kernel.
                 const bool all_seen = (j0 <= seen_hi && j0 >= seen_lo) || j0 <= seen_pre;
                 float top = -INFINITY;
-                if (plain && all_seen) {
+                if (PLAIN && all_seen) {
 #pragma unroll
                     for (int u = 0; u < kHalves; ++u)
 #pragma unroll
@@ -511,9 +512,11 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                             for (int x = 0; x < 4; ++x) {
                                 const int e = x & 1, j = j0 + 16 * u + quad + 8 * (x >> 1);
                                 float z = s[u][n][x] * factor[n][e];
-                                if (a.softcap > 0.0f)
-                                    z = score.cap * tanh_(z);
-                                z -= slope[n][e] * fabsf(float(pos[n][e] - j));
+                                if (!PLAIN) {
+                                    if (a.softcap > 0.0f)
+                                        z = score.cap * tanh_(z);
+                                    z -= slope[n][e] * fabsf(float(pos[n][e] - j));
+                                }
                                 if (!(j < keys.prefix ||
                                       (j <= pos[n][e] &&
                                        (!a.window || pos[n][e] - j < a.window))))
