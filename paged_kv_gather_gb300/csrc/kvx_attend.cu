@@ -116,7 +116,8 @@ Kernel kernel_of(int kind)
         return {reinterpret_cast<const void *>(kvx_attend_rows_kernel<TYPE, KV, D, 2>),
                 kRowThreads, row_ctas_per_sm<KV, D, 2>(), row_smem<KV, D, 2>(),
                 row_slot_floats<D, 2>(), nullptr, 0, 0, 0, row_smem<KV, D, 2>()};
-    return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KV, D>), kTileThreads, 1,
+    return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KV, D>),
+            TileShape<KV, D>::kThreads, 1,
             size_t(TileShape<KV, D>::kBytes), TileShape<KV, D>::kSlotFloats,
             reinterpret_cast<const void *>(kvx_attend_join_kernel<TYPE, D>), kJoinThreads,
             kBlockRows / kJoinRows, 0, size_t(TileShape<KV, D>::kBytes)};

@@ -38,12 +38,9 @@ namespace {
 // 1.45-1.5 ms in long runs under the power cap (cuBLAS sustains 1.70 PFLOP/s there).  A unit
 // costs about 9000 cycles beside its steps (q in, first scores, O out), which is what short
 // prompts pay: 2k tokens 36 us, 8k 373 us.
-const int kTileThreads = 384;
 const int kTileRows = 128;
 const int kTileKeys = 128;
 const int kBlockRows = 2 * kTileRows;
-const int kLoaders = 96;
-const int kLoaderWarps = kLoaders / 32;
 const int kLoaderLag = 2;          // slots filled by 16-byte copies before the first is announced
 
 // Barriers, by index: of the two tiles of rows first, then the loaders', the ring's, the end's.
@@ -57,21 +54,31 @@ enum {
     kBarFull = 11,
     kBarEmpty = 21,
     kBarEnd = 31,
-    kBars = 32
+    kBarStage = 32, // stages of a 4-bit cache are filled
+    kBarFree = 35,  // and converted
+    kBars = 38
 };
+const int kFourStaged = 3;  // of them
 
 template <int KV, int D>
 struct TileShape {
     static const bool kFour = KV == KVX_TYPE_FP_FOUR;
     static const bool kStaged = KV == KVX_TYPE_FP_EIGHT || kFour;  // and converted
+    // Eight warps of weights, one that issues products, and the loaders: of a 4-bit cache one that
+    // copies and three each that convert K and V, which leaves the weights their registers by
+    // handing over some of their own (kFewRegs and kManyRegs sum up to what the launch has).
+    static const int kThreads = kFour ? 512 : 384;
+    static const int kLoaderWarps = kThreads / 32 - 9, kLoaders = 32 * kLoaderWarps;
+    static const int kConverters = 3;
+    static const int kFewRegs = 104, kManyRegs = 152;
     static const int kTile = kTileRows * D * 2;              // bytes of a q, K or V tile
     static const int kSlots = (D == 128 ? 5 : 10) - kStaged;
-    // A staged side: e4m3 elements, or 16-byte units of e2m1 codes and behind them, for each unit,
-    // the four bytes that its two scales lie in.
-    static const int kSide = !kStaged ? 0 : kFour ? kTileKeys * (D / 32) * 20 : kTile / 2;
+    // A staged side: e4m3 elements, or e2m1 codes and behind those of all keys their scales.
+    static const int kSide = !kStaged ? 0 : kFour ? kTileKeys * (D / 2 + D / 16) : kTile / 2;
+    static const int kStages = kFour ? kFourStaged : 2;
     static const int kOffRing = 2 * kTile;
-    static const int kOffStage = kOffRing + kSlots * kTile;  // [2][kSide]
-    static const int kOffKeys = kOffStage + 2 * kSide;       // int64 [2][kTileKeys]
+    static const int kOffStage = kOffRing + kSlots * kTile;  // [kStages][kSide]
+    static const int kOffKeys = kOffStage + kStages * kSide; // int64 [2][kTileKeys]
     static const int kOffBars = kOffKeys + 2 * kTileKeys * 8;
     static const int kOffMisc = kOffBars + 8 * kBars;        // int[2]
     static const int kBytes = kOffMisc + 16;
@@ -270,11 +277,12 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c)
     return r;
 }
 
-// Four bytes into shared memory, zeros if !valid.
-__device__ __forceinline__ void cp_async4(unsigned dst, const void *src, bool valid)
+// N = 4 or 8 bytes into shared memory, zeros if !valid.
+template <int N>
+__device__ __forceinline__ void cp_async_few(unsigned dst, const void *src, bool valid)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(valid ? 4 : 0)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
+                 "r"(valid ? N : 0)
                  : "memory");
 }
 
@@ -433,13 +441,14 @@ struct Walk {
 };
 
 template <int TYPE, int KV, int D>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(TileShape<KV, D>::kThreads, 1)
 kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map)
 {
     typedef TileShape<KV, D> T;
     typedef Elem<TYPE> E;
     constexpr bool kFour = T::kFour, kStaged = T::kStaged;
+    constexpr int kLoaders = T::kLoaders, kLoaderWarps = T::kLoaderWarps;
     constexpr int kMath = kStaged ? KVX_TYPE_HALF : TYPE;
     typedef Elem<kMath> P;
     char *smem = attend_smem;
@@ -469,8 +478,12 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
         mbar_init(bar(kBarKeys), kLoaders);
         mbar_init(bar(kBarEnd), 1);
         for (int i = 0; i < T::kSlots; ++i) {
-            mbar_init(bar(kBarFull + i), kLoaderWarps);
+            mbar_init(bar(kBarFull + i), kFour ? T::kConverters : kLoaderWarps);
             mbar_init(bar(kBarEmpty + i), 1);
+        }
+        for (int i = 0; kFour && i < T::kStages; ++i) {
+            mbar_init(bar(kBarStage + i), 32);
+            mbar_init(bar(kBarFree + i), T::kConverters);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -480,6 +493,12 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
     const unsigned tmem = tmem_base;
     const AttnStart begin = w.starts[blockIdx.x];
     bool waited = false;  // for earlier work: the first unit's arithmetic goes before it
+    if constexpr (kFour) {
+        if (warp < 8)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T::kManyRegs));
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T::kFewRegs));
+    }
 
     if (warp == 8) {
         // ------------------------------------------------------------- matrix products
@@ -580,11 +599,134 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
             }
         }
         __syncwarp();
+    } else if (kFour && warp == 9) {
+        // ------------------------------------------------------------- K and V in 4 bits: copies
+        // Sides of tiles (K, V, K, V, ...) come into stages as they are.  Converters and copies in
+        // warps of their own, and K's apart from V's: in turn by the same warps, both showed.
+        constexpr int kRow = D / 2, kChunks = kRow / 16, kKeys = kTileKeys / 32;  // keys per lane
+        unsigned copied = 0;  // sides
+        bool ok = true;
+        for (Walk u(a, w, begin); ok && !u.done(); u.next()) {
+            if (!waited)
+                wait_for_earlier_work();
+            waited = true;
+            for (int i = lane; i < u.rows * (D / 64); i += 32) {
+                const int packed = u.row0 + i / (D / 64), tok = packed / a.group;
+                const char *q = a.q + int64_t(u.r.row_begin + tok) * a.q_stride +
+                                (u.at.head * a.group + packed - tok * a.group) * (D * 2) +
+                                i % (D / 64) * 128;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+            }
+            const int codes_at = u.at.head * kRow, units_at = a.kv_heads * kRow + u.at.head * (D / 16);
+            // Pages of keys lane, lane + 32, ... of a tile, looked up a tile ahead.
+            int next[kKeys];
+            auto look_up = [&](int i) {
+                const int j0 = i < u.todo ? u.key_of(i) + lane : 0;
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k)
+                    next[k] = i < u.todo && u.keys.used(j0 + 32 * k)
+                                  ? u.r.table[a.page.div(j0 + 32 * k)] : -1;
+            };
+            look_up(0);
+            for (int i = 0; ok && i < u.todo; ++i) {
+                const int j0 = u.key_of(i) + lane;
+                int64_t off[kKeys];  // of the keys' tokens; -1: not used
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k) {
+                    const int j = j0 + 32 * k;
+                    off[k] = -1;
+                    if (unsigned(next[k]) < unsigned(a.num_pages))
+                        off[k] = (int64_t(next[k]) * a.page_size + j -
+                                  a.page.div(j) * a.page_size) * a.token_bytes;
+                    else if (u.keys.used(j))
+                        atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+                }
+                look_up(i + 1);
+                for (int side = 0; side < 2; ++side) {
+                    const unsigned s = copied % kFourStaged;
+                    if (!(ok = wait(kBarFree + s, (copied / kFourStaged & 1) ^ 1)))
+                        break;
+                    const unsigned dst = sm + T::kOffStage + s * T::kSide;
+                    const char *base = side ? a.v : a.k;
+#pragma unroll
+                    for (int b = 0; b < kKeys * kChunks; ++b) {
+                        // 16-byte unit 32 b + lane of the codes: of key (32 b + lane) / kChunks.
+                        const int64_t o = __shfl_sync(0xffffffffu, off[b / kChunks],
+                                                      (b % kChunks * 32 + lane) / kChunks);
+                        cp_async16(dst + (32 * b + lane) * 16,
+                                   base + (o >= 0 ? o : 0) + codes_at + lane % kChunks * 16, o >= 0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kKeys; ++k)
+                        cp_async_few<D / 16>(dst + kTileKeys * kRow + (lane + 32 * k) * (D / 16),
+                                             base + (off[k] >= 0 ? off[k] : 0) + units_at,
+                                             off[k] >= 0);
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(
+                                     bar(kBarStage + s))
+                                 : "memory");
+                    ++copied;
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (kFour && warp > 9) {
+        // ------------------------------------------------------------- K and V in 4 bits: halves
+        constexpr int kRow = D / 2, kChunks = kRow / 16, kThreads = 32 * T::kConverters;
+        constexpr int kAll = kTileKeys * kChunks, kStep = kThreads / kChunks;  // keys
+        static_assert(kStep % 8 == 0, "a thread's rows are swizzled alike");
+        const int side = (warp - 10) / T::kConverters;
+        const int ct = threadIdx.x - 32 * (10 + side * T::kConverters);
+        const int t0 = ct / kChunks, c = ct % kChunks;
+        int to[4];  // 16-byte units 4 c .. + 3 of row t0
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            to[y] = tile_at(t0, 4 * c + y);
+        unsigned n = side;  // of the sides
+        bool ok = true;
+        for (Walk u(a, w, begin); ok && !u.done(); u.next()) {
+            if (!waited)
+                wait_for_earlier_work();
+            waited = true;
+            for (int i = 0; i < u.todo; ++i, n += 2) {
+                const unsigned s = n % kFourStaged, slot = n % T::kSlots;
+                if (!(ok = wait(kBarStage + s, n / kFourStaged & 1)) ||
+                    !(ok = wait(kBarEmpty + slot, (n / T::kSlots & 1) ^ 1)))
+                    break;
+                const char *src = smem + T::kOffStage + s * T::kSide + ct * 16;
+                const char *units = smem + T::kOffStage + s * T::kSide + kTileKeys * kRow + ct * 2;
+                char *dst = smem + T::kOffRing + slot * T::kTile;
+#pragma unroll
+                for (int b = 0; b < (kAll + kThreads - 1) / kThreads; ++b) {
+                    if ((b + 1) * kThreads > kAll && ct + b * kThreads >= kAll)
+                        break;
+                    // 32 elements of two blocks.
+                    const uint4 in = *reinterpret_cast<const uint4 *>(src + b * kThreads * 16);
+                    const unsigned two = half2_of_e4m3(
+                        *reinterpret_cast<const uint16_t *>(units + b * kThreads * 2));
+                    const unsigned w4[4] = {in.x, in.y, in.z, in.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const unsigned unit = __byte_perm(two, 0, y < 2 ? 0x1010 : 0x3232);
+                        unsigned h[4];
+                        half8_of_e2m1(w4[y], h);
+                        *reinterpret_cast<uint4 *>(dst + to[y] + b * kStep * 128) =
+                            make_uint4(mul_half2(h[0], unit), mul_half2(h[1], unit),
+                                       mul_half2(h[2], unit), mul_half2(h[3], unit));
+                    }
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(kBarFull + slot));
+                    mbar_arrive(bar(kBarFree + s));
+                }
+            }
+        }
     } else if (warp > 8) {
         // ------------------------------------------------------------- K and V
-        const int lt = threadIdx.x - (kTileThreads - kLoaders);
+        const int lt = threadIdx.x - (T::kThreads - kLoaders);
         int64_t *offs = reinterpret_cast<int64_t *>(smem + T::kOffKeys);  // [2][kTileKeys]
-        constexpr int kRow = kFour ? D / 2 : kStaged ? D : D * 2, kChunks = kRow / 16;
+        constexpr int kRow = kStaged ? D : D * 2, kChunks = kRow / 16;
         constexpr int kCopies = (kTileKeys * kChunks + kLoaders - 1) / kLoaders;  // per thread
         constexpr unsigned kPerTile = D / 64;  // tensor copies side by side
         unsigned slot = 0, turn = 0;
@@ -605,7 +747,6 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 turn ^= 1;
             }
         };
-        int scales_after = 0;
         // Copy this thread's chunks of 16 bytes of a tile, where each key lies at off[key].
         auto copy = [&](const char *base, const int64_t *off, unsigned dst) {
             int64_t o[kCopies];  // all at once: nothing moves across an asynchronous copy
@@ -620,16 +761,11 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 if (x < kTileKeys * kChunks)
                     cp_async16(dst + (kStaged ? x * 16 : tile_at(t, c)),
                                base + (o[b] >= 0 ? o[b] : 0) + c * 16, o[b] >= 0);
-                // Each thread converts what it copied, so it copies the scales that it needs.
-                if (kFour && x < kTileKeys * kChunks)
-                    cp_async4(dst + kTileKeys * kRow + x * 4,
-                              base + (o[b] >= 0 ? o[b] + scales_after : 0) + c / 2 * 4,
-                              o[b] >= 0);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         unsigned key_phase = 0;
-        // Staged tile sides (K, V, K, V, ...) are copied one ahead of their conversion.
+        // e4m3: tile sides (K, V, K, V, ...) are copied one ahead of their conversion.
         bool staged = false;
         auto convert = [&]() {  // the staged side, number `filled` of the stream
             const char *src = smem + T::kOffStage + (filled & 1) * T::kSide;
@@ -644,23 +780,7 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
 #pragma unroll
             for (int b = 0; b < kCopies; ++b) {
                 const int x = lt + b * kLoaders, t = x / kChunks, c = x % kChunks;
-                if (x >= kTileKeys * kChunks)
-                    continue;
-                if constexpr (kFour) {
-                    // 32 elements of two blocks.
-                    const unsigned units = half2_of_e4m3(*reinterpret_cast<const uint16_t *>(
-                        src + kTileKeys * kRow + x * 4 + 2 * (c & 1)));
-                    const unsigned in4[4] = {in[b].x, in[b].y, in[b].z, in[b].w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const unsigned unit = __byte_perm(units, 0, y < 2 ? 0x1010 : 0x3232);
-                        unsigned h[4];
-                        half8_of_e2m1(in4[y], h);
-                        *reinterpret_cast<uint4 *>(dst + tile_at(t, 4 * c + y)) =
-                            make_uint4(mul_half2(h[0], unit), mul_half2(h[1], unit),
-                                       mul_half2(h[2], unit), mul_half2(h[3], unit));
-                    }
-                } else {
+                if (x < kTileKeys * kChunks) {
                     uint4 h0, h1;
                     half4_of_e4m3(in[b].x, h0.x, h0.y);
                     half4_of_e4m3(in[b].y, h0.z, h0.w);
@@ -686,8 +806,6 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
             }
             const int64_t head_at = int64_t(u.at.head) * kRow;
-            if (kFour)  // from a head's codes to its scales
-                scales_after = a.kv_heads * kRow - int(head_at) + u.at.head * (D / 16);
             // A lane per tensor copy of a tile: run of keys `lane / kPerTile` and 64-element
             // block of the head `lane % kPerTile`; its page is looked up a tile ahead.
             const int run = a.box ? int(unsigned(lane) / kPerTile) * a.box : kTileKeys;
