@@ -3,10 +3,9 @@
 //
 // The logits are read once.  A row (a beam's logits) is cut into parts that a CTA holds in
 // registers: it takes the part's maximum and sum of exponentials, and its `picks` largest logits
-// (equal ones by token).  Those are found by way of each thread's largest: a threshold that
-// about `picks` of them reach is found by bisection, a barrier that counts per step; all of a
-// part's `picks` largest are at or above it, and only the few threads that reach it look through
-// their logits again.  A second kernel, a CTA per group, merges the parts' lists beam by beam and
+// (equal ones by token).  Those all reach the `picks`-th largest of what 64 groups of threads have
+// as their largest, and hardly more than twice as many logits do: only the few threads that reach
+// it look through their logits again, and rank what they find by counting.  A second kernel, a CTA per group, merges the parts' lists beam by beam and
 // the beams' by their sums in 64 bits.
 #include <cuda_runtime.h>
 
@@ -19,8 +18,9 @@ namespace {
 
 const int kSelThreads = 512;
 const int kSelWarps = kSelThreads / 32;
-// Threads that may reach the threshold: KVX_MAX_PICKS and some, so that bisection ends early.
-const int kSelSlack = 16;
+const int kSelGroups = 64;     // of threads, KVX_MAX_PICKS at least
+// Threads beyond `picks` that may have candidates, before ties are looked into.
+const int kSelSlack = 64;
 const int kMaxParts = 32;      // of a row: a lane each when they are merged
 const int kMergeWarps = KVX_MAX_BEAMS / 2;
 const int kMergeThreads = 32 * kMergeWarps;
@@ -47,11 +47,13 @@ template <int TYPE>
 struct Logit {
     typedef typename Elem<TYPE>::T T;
     static __device__ __forceinline__ float load(T x) { return Elem<TYPE>::load(x); }
+    static __device__ __forceinline__ T store(float x) { return T(x); }
 };
 template <>
 struct Logit<KVX_TYPE_FLOAT> {
     typedef float T;
     static __device__ __forceinline__ float load(float x) { return x; }
+    static __device__ __forceinline__ float store(float x) { return x; }
 };
 
 // Unsigned numbers in the order of floats; larger than 0 for all but -NaN.
@@ -66,10 +68,10 @@ __device__ __forceinline__ float float_of(unsigned order)
     return __uint_as_float(order >> 31 ? order & 0x7fffffffu : ~order);
 }
 
-// Keys fall with the logit, then with the token.
+// Keys fall with the logit (-0 is 0), then with the token.
 __device__ __forceinline__ uint64_t key_of(float x, int token)
 {
-    return uint64_t(order_of(x)) << 32 | unsigned(~token);
+    return uint64_t(order_of(x + 0.0f)) << 32 | unsigned(~token);
 }
 
 __device__ __forceinline__ bool has_continuations(const Select &a, int beam)
@@ -77,18 +79,33 @@ __device__ __forceinline__ bool has_continuations(const Select &a, int beam)
     return a.scores[beam] > -INFINITY;  // not NaN either
 }
 
+// The larger of each of two logits, and the largest of a unit of 16 bytes; NaN is passed over.
+template <int TYPE>
+__device__ __forceinline__ unsigned max_pair(unsigned a, unsigned b)
+{
+    unsigned r;
+    if (TYPE == KVX_TYPE_HALF)
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else if (TYPE == KVX_TYPE_BFLOAT)
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    return r;
+}
+
 template <int TYPE, int EACH>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, EACH * sizeof(typename Logit<TYPE>::T) > 64 ? 2 : 3)
 kvx_select_parts_kernel(const Select a)
 {
     typedef Logit<TYPE> L;
     typedef typename L::T T;
     constexpr int kVec = 16 / sizeof(T), kVecs = EACH / kVec;
-    constexpr int kList = (KVX_MAX_PICKS + kSelSlack) * EACH;
-    __shared__ uint64_t list[kList];
-    __shared__ unsigned most[kSelWarps], least[kSelWarps];
+    constexpr int kEnough = KVX_MAX_PICKS + kSelSlack;  // threads that may have candidates
+    __shared__ uint64_t list[kEnough * EACH];
+    __shared__ __align__(16) float tops[kSelGroups];
     __shared__ double sums[kSelWarps];
-    __shared__ int found;
+    __shared__ float reach[2];  // the largest logit, the `picks`-th largest of `tops`
+    __shared__ int found, odd;
     const int beam = blockIdx.x / a.parts, part = blockIdx.x - beam * a.parts;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier_work();
@@ -102,92 +119,121 @@ kvx_select_parts_kernel(const Select a)
     auto token_of = [&](int i) {  // of the i-th unit's first logit
         return ((part * kVecs + i) * kSelThreads + int(threadIdx.x)) * kVec - skew;
     };
-    float x[EACH];
+    uint4 u[kVecs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int t = token_of(i);
-        uint4 u;
-        T *e = reinterpret_cast<T *>(&u);
         if (t >= 0 && t + kVec <= a.vocab) {
-            u = __ldcs(units + (t + skew) / kVec);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                x[i * kVec + k] = L::load(e[k]);
+            u[i] = __ldcs(units + (t + skew) / kVec);
         } else {
+            T *e = reinterpret_cast<T *>(&u[i]);
 #pragma unroll
             for (int k = 0; k < kVec; ++k)
-                x[i * kVec + k] = t + k >= 0 && t + k < a.vocab
-                                      ? L::load(reinterpret_cast<const T *>(row)[t + k])
-                                      : -INFINITY;
+                e[k] = t + k >= 0 && t + k < a.vocab ? reinterpret_cast<const T *>(row)[t + k]
+                                                     : L::store(-INFINITY);
         }
     }
-    float top = -INFINITY;
-    int at = 0;
+    auto logit = [&](int i) {
+        return L::load(reinterpret_cast<const T *>(&u[i / kVec])[i % kVec]);
+    };
+
+    float top, m, bar;
+    int reached;
+    for (bool again = false;; again = true) {
+        unsigned pair = u[0].x;
 #pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        // NaN and +infinity count as -infinity, -0 as 0.
-        x[i] = x[i] < INFINITY ? x[i] + 0.0f : -INFINITY;
-        if (x[i] > top) {
-            top = x[i];
-            at = i;
+        for (int i = 0; i < kVecs; ++i)
+            pair = max_pair<TYPE>(max_pair<TYPE>(pair, max_pair<TYPE>(u[i].x, u[i].y)),
+                                  max_pair<TYPE>(u[i].z, u[i].w));
+        const T *two = reinterpret_cast<const T *>(&pair);
+        top = fmaxf(L::load(two[0]), L::load(two[4 / sizeof(T) - 1]));
+        // The `picks`-th largest of 64 groups' largest: so many logits at least reach it.
+        float group = top;
+#pragma unroll
+        for (int d = 1; d < 32 * kSelWarps / kSelGroups; d <<= 1)
+            group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, d));
+        if (lane % (32 * kSelWarps / kSelGroups) == 0)
+            tops[threadIdx.x / (32 * kSelWarps / kSelGroups)] = group;
+        if (threadIdx.x == 0)
+            found = odd = 0;
+        __syncthreads();
+        if (threadIdx.x < kSelGroups) {
+            const float mine = tops[threadIdx.x];
+            int rank = 0;
+#pragma unroll
+            for (int k = 0; k < kSelGroups; k += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(tops + k);
+                rank += (f.x > mine || (f.x == mine && k < int(threadIdx.x))) +
+                        (f.y > mine || (f.y == mine && k + 1 < int(threadIdx.x))) +
+                        (f.z > mine || (f.z == mine && k + 2 < int(threadIdx.x))) +
+                        (f.w > mine || (f.w == mine && k + 3 < int(threadIdx.x)));
+            }
+            if (rank == 0)
+                reach[0] = mine;
+            if (rank == a.picks - 1)
+                reach[1] = mine;
         }
-    }
-    // Two lookups of `at`, not a select per logit.
-    const uint64_t mine =
-        top > -INFINITY ? key_of(top, token_of(at / kVec) + at % kVec) : 0;
-    const unsigned hi = __reduce_max_sync(0xffffffffu, unsigned(mine >> 32));
-    const unsigned lo = __reduce_min_sync(0xffffffffu, unsigned(mine >> 32));
-    if (lane == 0) {
-        most[warp] = hi;
-        least[warp] = lo;
-    }
-    if (threadIdx.x == 0)
-        found = 0;
-    const int some = __syncthreads_count(mine != 0);
-    unsigned all_hi = 0, all_lo = ~0u;
+        __syncthreads();
+        m = reach[0];
+        bar = reach[1];
+        // A thread without a logit has no part in the sum (and -infinity less itself is NaN).
+        float sum = 0.0f;
+        if (top > -INFINITY) {
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) {
-        all_hi = max(all_hi, most[i]);
-        all_lo = min(all_lo, least[i]);
-    }
-    const float m = some ? float_of(all_hi) : -INFINITY;
-    float sum = 0.0f;
-    if (top > -INFINITY) {
+            for (int i = 0; i < EACH; ++i)
+                sum += exp2_((logit(i) - m) * kLog2e);
+        }
+        // NaN, or +infinity, which the sum is NaN with too: taken out, once.
+        if (!again && !(sum < INFINITY))
+            odd = 1;
+        double s = sum;
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (lane == 0)
+            sums[warp] = s;
+        reached = __syncthreads_count(top >= bar && top > -INFINITY);
+        if (again || !odd)
+            break;
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < EACH; ++i)
-            sum += exp2_((x[i] - m) * kLog2e);
+            if (!(logit(i) < INFINITY))
+                reinterpret_cast<T *>(&u[i / kVec])[i % kVec] = L::store(-INFINITY);
     }
-    double s = sum;
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-        s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0)
-        sums[warp] = s;
 
-    // Between `picks` and a few more threads reach `bar`; all that have a logit, if those are few.
-    uint64_t bar = 1;
-    const int enough = a.picks + kSelSlack;
-    if (some > enough) {
-        // more than `enough` reach `below`, less than `picks` reach `above`
-        uint64_t below = max(uint64_t(all_lo) << 32, uint64_t(1));
-        uint64_t above = uint64_t(all_hi) + 1 << 32;
+    // Candidates: the logits that reach the bar.  Where ties make those too many threads', the
+    // tokens decide, by bisection over the threads' largest keys.
+    uint64_t low = top >= bar && top > -INFINITY ? 0 : ~0ull;  // of this thread's candidates
+    if (reached > a.picks + kSelSlack) {
+        uint64_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            if (mine == 0 && logit(i) == top && top > -INFINITY)
+                mine = key_of(top, token_of(i / kVec) + i % kVec);
+        // more than enough reach `below`, less than `picks` reach `above`
+        uint64_t below = 1, above = key_of(m, 0) + 1, mid;
         for (;;) {
-            bar = below + (above - below) / 2;
-            const int n = __syncthreads_count(mine >= bar);
+            mid = below + (above - below) / 2;
+            const int n = __syncthreads_count(mine >= mid);
             if (n < a.picks)
-                above = bar;
-            else if (n > enough)
-                below = bar;
+                above = mid;
+            else if (n > a.picks + kSelSlack)
+                below = mid;
             else
                 break;
         }
+        low = mine >= mid ? mid : ~0ull;
     }
-    if (mine >= bar) {
+    if (low != ~0ull) {
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
-            const uint64_t key = key_of(x[i], token_of(i / kVec) + i % kVec);
-            if (x[i] > -INFINITY && key >= bar)
-                list[atomicAdd(&found, 1)] = key;
+            const float x = logit(i);
+            if (x >= bar && x > -INFINITY) {
+                const uint64_t key = key_of(x, token_of(i / kVec) + i % kVec);
+                if (key >= low)
+                    list[atomicAdd(&found, 1)] = key;
+            }
         }
     }
     __syncthreads();
@@ -212,16 +258,43 @@ kvx_select_parts_kernel(const Select a)
     }
 }
 
-// Unsigned numbers in the order of doubles.
+// Unsigned numbers in the order of doubles, and back.
 __device__ __forceinline__ uint64_t order_of(double x)
 {
     const uint64_t b = uint64_t(__double_as_longlong(x));
     return b >> 63 ? ~b : b | 1ull << 63;
 }
 
+__device__ __forceinline__ double double_of(uint64_t order)
+{
+    return __longlong_as_double(int64_t(order >> 63 ? order & ~(1ull << 63) : ~order));
+}
+
+// log s to about 1e-9, for normal s >= 1: s = 2^e f with f in [3/4, 3/2), and
+// log f = 2 artanh z by its power series, z = (f - 1) / (f + 1) with its rounding carried along.
+// 64-bit arithmetic is slow here: a library logarithm per beam was a third of the merge.
+__device__ __forceinline__ double log_of(double s)
+{
+    const uint64_t b = uint64_t(__double_as_longlong(s));
+    const bool half = (b >> 51 & 1) != 0;  // f of the mantissa is 3/2 or more
+    const int e = int(b >> 52) - 1023 + half;
+    const double f = __longlong_as_double(int64_t((b & 0xfffffffffffffull) |
+                                                  uint64_t(1023 - half) << 52));
+    const double num = f - 1.0, den = f + 1.0;
+    const float n0 = float(num), n1 = float(num - n0), d0 = float(den), d1 = float(den - d0);
+    const float z = n0 / d0, z1 = (fmaf(-z, d0, n0) + (n1 - z * d1)) / d0, y = z * z;
+    float p = 1.0f / 13;
+    p = fmaf(p, y, 1.0f / 11);
+    p = fmaf(p, y, 1.0f / 9);
+    p = fmaf(p, y, 1.0f / 7);
+    p = fmaf(p, y, 1.0f / 5);
+    p = fmaf(p, y, 1.0f / 3);
+    return e * 0.69314718055994530942 + (2.0 * z + double(2.0f * fmaf(z * y, p, z1)));
+}
+
 struct Continuation {
-    double sum;
-    int32_t beam, token;
+    uint64_t sum;  // order_of the sum
+    int32_t token, pad;
 };
 
 // A warp per beam merges the falling lists of its parts, a lane holding the head of one list;
@@ -240,7 +313,7 @@ kvx_select_merge_kernel(const Select a)
         if (!has_continuations(a, beam)) {
         } else if (a.done && a.done[beam]) {
             if (lane == 0)
-                mine[0] = {double(a.scores[beam]), b, a.done_token};
+                mine[0] = {order_of(double(a.scores[beam])), a.done_token, 0};
             n = 1;
         } else {
             const bool have = lane < a.parts;
@@ -250,14 +323,15 @@ kvx_select_merge_kernel(const Select a)
             PartStats part = {0.0, -INFINITY, 0};
             if (have)
                 part = a.stats[int64_t(beam) * a.parts + lane];
-            const unsigned top =
-                __reduce_max_sync(0xffffffffu, order_of(part.max));
-            const double m = float_of(top);
-            double s = part.sum > 0.0 ? part.sum * exp(double(part.max) - m) : 0.0;
+            const float m = float_of(__reduce_max_sync(0xffffffffu, order_of(part.max)));
+            // exp(max - m): what the difference is rounded by goes in to first order.
+            const double away = part.sum > 0.0 ? double(part.max) - m : 0.0;
+            const float near = float(away);
+            double s = part.sum * (double(expf(near)) * (1.0 + (away - near)));
 #pragma unroll
             for (int d = 16; d; d >>= 1)
                 s += __shfl_xor_sync(0xffffffffu, s, d);
-            const double so_far = a.scores[beam], norm = m + log(s);
+            const double so_far = a.scores[beam], norm = m + log_of(s);
             for (; n < a.picks; ++n) {
                 // The largest head: high words first, then low words among those that have it.
                 const unsigned hi = __reduce_max_sync(0xffffffffu, unsigned(head >> 32));
@@ -266,7 +340,7 @@ kvx_select_merge_kernel(const Select a)
                 const bool among = unsigned(head >> 32) == hi;
                 const unsigned lo = __reduce_max_sync(0xffffffffu, among ? unsigned(head) : 0u);
                 if (among && unsigned(head) == lo) {
-                    mine[n] = {so_far + (double(float_of(hi)) - norm), b, int32_t(~lo)};
+                    mine[n] = {order_of(so_far + (double(float_of(hi)) - norm)), int32_t(~lo), 0};
                     head = next;
                     ++at;
                     next = at < a.picks ? keys[at] : 0;
@@ -283,14 +357,14 @@ kvx_select_merge_kernel(const Select a)
     const int slots = a.width * a.picks;
     auto valid = [&](int i) { return i - i / a.picks * a.picks < count[i / a.picks]; };
     uint64_t bar = 0;
-    if (slots > 256) {
+    if (slots > kMergeThreads) {
         uint64_t below = 0, above = ~0ull;
         for (int step = 0; step < 64; ++step) {
             const uint64_t mid = below + (above - below) / 2;
             int n = 0;
             for (int i = threadIdx.x; i < (slots + kMergeThreads - 1) / kMergeThreads * kMergeThreads;
                  i += kMergeThreads)
-                n += __syncthreads_count(i < slots && valid(i) && order_of(all[i].sum) >= mid);
+                n += __syncthreads_count(i < slots && valid(i) && all[i].sum >= mid);
             if (n < a.picks)
                 above = mid;
             else
@@ -302,23 +376,29 @@ kvx_select_merge_kernel(const Select a)
     }
     const int64_t out = int64_t(group) * a.picks;
     for (int i = threadIdx.x; i < slots; i += kMergeThreads) {
-        if (!valid(i) || order_of(all[i].sum) < bar)
+        if (!valid(i) || all[i].sum < bar)
             continue;
         const Continuation mine = all[i];
-        // A beam's continuations are in order, so position settles equal sums.
+        // A beam's continuations are in order, and position settles equal sums: of each other
+        // beam, as many are ahead as a search finds.
         int rank = 0;
-        for (int b = 0; b < a.width; ++b)
-            for (int k = 0; k < count[b]; ++k) {
-                const double other = all[b * a.picks + k].sum;
-                if (other > mine.sum || (other == mine.sum && b * a.picks + k < i))
-                    ++rank;
-                else if (other < mine.sum)
-                    break;
+        for (int b = 0; b < a.width; ++b) {
+            const Continuation *other = all + b * a.picks;
+            int lo = 0, hi = count[b];
+            while (lo < hi) {
+                const int k = (lo + hi) / 2;
+                const uint64_t sum = other[k].sum;
+                if (sum > mine.sum || (sum == mine.sum && b * a.picks + k < i))
+                    lo = k + 1;
+                else
+                    hi = k;
             }
+            rank += lo;
+        }
         if (rank < a.picks) {
-            a.parents[out + rank] = mine.beam;
+            a.parents[out + rank] = i / a.picks;
             a.tokens[out + rank] = mine.token;
-            a.out_scores[out + rank] = float(mine.sum);
+            a.out_scores[out + rank] = float(double_of(mine.sum));
         }
     }
     int total = 0;
