@@ -26,9 +26,8 @@ const int kMergeWarps = KVX_MAX_BEAMS / 2;
 const int kMergeThreads = 32 * kMergeWarps;
 
 struct PartStats {
-    double sum;   // of exp(logit - max)
-    float max;
-    int32_t pad;
+    float sum, more;  // of exp(logit - max), in two numbers
+    float max, pad;
 };
 
 struct Select {
@@ -48,12 +47,18 @@ struct Logit {
     typedef typename Elem<TYPE>::T T;
     static __device__ __forceinline__ float load(T x) { return Elem<TYPE>::load(x); }
     static __device__ __forceinline__ T store(float x) { return T(x); }
+    static __device__ __forceinline__ float larger(unsigned pair)
+    {
+        const T *x = reinterpret_cast<const T *>(&pair);
+        return fmaxf(load(x[0]), load(x[1]));
+    }
 };
 template <>
 struct Logit<KVX_TYPE_FLOAT> {
     typedef float T;
     static __device__ __forceinline__ float load(float x) { return x; }
     static __device__ __forceinline__ float store(float x) { return x; }
+    static __device__ __forceinline__ float larger(unsigned one) { return __uint_as_float(one); }
 };
 
 // Unsigned numbers in the order of floats; larger than 0 for all but -NaN.
@@ -93,6 +98,26 @@ __device__ __forceinline__ unsigned max_pair(unsigned a, unsigned b)
     return r;
 }
 
+template <int TYPE>
+__device__ __forceinline__ unsigned max_unit(const uint4 &u)
+{
+    return max_pair<TYPE>(max_pair<TYPE>(u.x, u.y), max_pair<TYPE>(u.z, u.w));
+}
+
+// The sum over a warp of what hi + lo holds, to about 2^-45 of it: 64-bit additions are slow here.
+__device__ __forceinline__ float2 warp_sum(float hi, float lo)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, hi, d);
+        lo += __shfl_xor_sync(0xffffffffu, lo, d);
+        const float s = hi + other, part = s - hi;  // and what that sum is rounded by
+        lo += (hi - (s - part)) + (other - part);
+        hi = s;
+    }
+    return make_float2(hi, lo);
+}
+
 template <int TYPE, int EACH>
 __global__ void __launch_bounds__(kSelThreads, EACH * sizeof(typename Logit<TYPE>::T) > 64 ? 2 : 3)
 kvx_select_parts_kernel(const Select a)
@@ -103,9 +128,9 @@ kvx_select_parts_kernel(const Select a)
     constexpr int kEnough = KVX_MAX_PICKS + kSelSlack;  // threads that may have candidates
     __shared__ uint64_t list[kEnough * EACH];
     __shared__ __align__(16) float tops[kSelGroups];
-    __shared__ double sums[kSelWarps];
-    __shared__ float reach[2];  // the largest logit, the `picks`-th largest of `tops`
-    __shared__ int found, odd;
+    __shared__ float2 sums[kSelWarps];
+    __shared__ float reach;  // the `picks`-th largest of `tops`
+    __shared__ int found, reached, odd;
     const int beam = blockIdx.x / a.parts, part = blockIdx.x - beam * a.parts;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier_work();
@@ -120,17 +145,24 @@ kvx_select_parts_kernel(const Select a)
         return ((part * kVecs + i) * kSelThreads + int(threadIdx.x)) * kVec - skew;
     };
     uint4 u[kVecs];
+    const int first = part * kVecs * kSelThreads * kVec - skew;  // token of the part
+    if (first >= 0 && first + kVecs * kSelThreads * kVec <= a.vocab) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const int t = token_of(i);
-        if (t >= 0 && t + kVec <= a.vocab) {
-            u[i] = __ldcs(units + (t + skew) / kVec);
-        } else {
-            T *e = reinterpret_cast<T *>(&u[i]);
+        for (int i = 0; i < kVecs; ++i)
+            u[i] = __ldcs(units + (part * kVecs + i) * kSelThreads + threadIdx.x);
+    } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                e[k] = t + k >= 0 && t + k < a.vocab ? reinterpret_cast<const T *>(row)[t + k]
-                                                     : L::store(-INFINITY);
+        for (int i = 0; i < kVecs; ++i) {
+            const int t = token_of(i);
+            if (t >= 0 && t + kVec <= a.vocab) {
+                u[i] = __ldcs(units + (t + skew) / kVec);
+            } else {
+                T *e = reinterpret_cast<T *>(&u[i]);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k)
+                    e[k] = t + k >= 0 && t + k < a.vocab ? reinterpret_cast<const T *>(row)[t + k]
+                                                         : L::store(-INFINITY);
+            }
         }
     }
     auto logit = [&](int i) {
@@ -138,61 +170,62 @@ kvx_select_parts_kernel(const Select a)
     };
 
     float top, m, bar;
-    int reached;
+    constexpr int kLanes = kSelThreads / kSelGroups;  // of a group
     for (bool again = false;; again = true) {
         unsigned pair = u[0].x;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
-            pair = max_pair<TYPE>(max_pair<TYPE>(pair, max_pair<TYPE>(u[i].x, u[i].y)),
-                                  max_pair<TYPE>(u[i].z, u[i].w));
-        const T *two = reinterpret_cast<const T *>(&pair);
-        top = fmaxf(L::load(two[0]), L::load(two[4 / sizeof(T) - 1]));
-        // The `picks`-th largest of 64 groups' largest: so many logits at least reach it.
+            pair = max_pair<TYPE>(pair, max_unit<TYPE>(u[i]));
+        top = L::larger(pair);
         float group = top;
 #pragma unroll
-        for (int d = 1; d < 32 * kSelWarps / kSelGroups; d <<= 1)
+        for (int d = 1; d < kLanes; d <<= 1)
             group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, d));
-        if (lane % (32 * kSelWarps / kSelGroups) == 0)
-            tops[threadIdx.x / (32 * kSelWarps / kSelGroups)] = group;
+        const int mine = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
+        if (sub == 0)
+            tops[mine] = group;
         if (threadIdx.x == 0)
-            found = odd = 0;
+            found = reached = odd = 0;
         __syncthreads();
-        if (threadIdx.x < kSelGroups) {
-            const float mine = tops[threadIdx.x];
-            int rank = 0;
+        // The largest of all, and the rank of the own group's largest, by its threads together.
+        // At least `picks` logits reach the one of rank `picks` - 1.
+        int rank = 0;
+        m = group;
 #pragma unroll
-            for (int k = 0; k < kSelGroups; k += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(tops + k);
-                rank += (f.x > mine || (f.x == mine && k < int(threadIdx.x))) +
-                        (f.y > mine || (f.y == mine && k + 1 < int(threadIdx.x))) +
-                        (f.z > mine || (f.z == mine && k + 2 < int(threadIdx.x))) +
-                        (f.w > mine || (f.w == mine && k + 3 < int(threadIdx.x)));
-            }
-            if (rank == 0)
-                reach[0] = mine;
-            if (rank == a.picks - 1)
-                reach[1] = mine;
+        for (int k = 0; k < kSelGroups / kLanes; ++k) {
+            const float f = tops[k * kLanes + sub];
+            m = fmaxf(m, f);
+            rank += f > group || (f == group && k * kLanes + sub < mine);
         }
-        __syncthreads();
-        m = reach[0];
-        bar = reach[1];
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) {
+            rank += __shfl_xor_sync(0xffffffffu, rank, d);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        }
+        if (sub == 0 && rank == a.picks - 1)
+            reach = group;
         // A thread without a logit has no part in the sum (and -infinity less itself is NaN).
         float sum = 0.0f;
         if (top > -INFINITY) {
+            const uint64_t less = pair_of(-m, -m), log2e = pair_of(kLog2e, kLog2e);
+            uint64_t both[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < EACH; ++i)
-                sum += exp2_((logit(i) - m) * kLog2e);
+            for (int i = 0; i < EACH; i += 2) {
+                const float2 x =
+                    halves_of(mul_pair(add_pair(pair_of(logit(i), logit(i + 1)), less), log2e));
+                both[i >> 1 & 1] = add_pair(both[i >> 1 & 1], pair_of(exp2_(x.x), exp2_(x.y)));
+            }
+            const float2 x = halves_of(add_pair(both[0], both[1]));
+            sum = x.x + x.y;
         }
         // NaN, or +infinity, which the sum is NaN with too: taken out, once.
         if (!again && !(sum < INFINITY))
             odd = 1;
-        double s = sum;
-#pragma unroll
-        for (int d = 16; d; d >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, d);
+        const float2 s = warp_sum(sum, 0.0f);
         if (lane == 0)
             sums[warp] = s;
-        reached = __syncthreads_count(top >= bar && top > -INFINITY);
+        __syncthreads();
+        bar = reach;
         if (again || !odd)
             break;
         __syncthreads();
@@ -202,14 +235,32 @@ kvx_select_parts_kernel(const Select a)
                 reinterpret_cast<T *>(&u[i / kVec])[i % kVec] = L::store(-INFINITY);
     }
 
-    // Candidates: the logits that reach the bar.  Where ties make those too many threads', the
-    // tokens decide, by bisection over the threads' largest keys.
-    uint64_t low = top >= bar && top > -INFINITY ? 0 : ~0ull;  // of this thread's candidates
-    if (reached > a.picks + kSelSlack) {
+    // Candidates: the logits that reach the bar.
+    auto collect = [&](uint64_t low) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            if (L::larger(max_unit<TYPE>(u[i])) < bar)
+                continue;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                const float x = logit(i * kVec + k);
+                const uint64_t key = key_of(x, token_of(i) + k);
+                if (x >= bar && x > -INFINITY && key >= low)
+                    list[atomicAdd(&found, 1)] = key;
+            }
+        }
+    };
+    const int enough = a.picks + kSelSlack;
+    const bool has = top >= bar && top > -INFINITY;
+    if (has && atomicAdd(&reached, 1) < enough)
+        collect(0);
+    __syncthreads();
+    if (reached > enough) {
+        // Ties make them too many: the tokens decide, by bisection over the threads' largest keys.
         uint64_t mine = 0;
 #pragma unroll
         for (int i = 0; i < EACH; ++i)
-            if (mine == 0 && logit(i) == top && top > -INFINITY)
+            if (mine == 0 && has && logit(i) == top)
                 mine = key_of(top, token_of(i / kVec) + i % kVec);
         // more than enough reach `below`, less than `picks` reach `above`
         uint64_t below = 1, above = key_of(m, 0) + 1, mid;
@@ -218,43 +269,39 @@ kvx_select_parts_kernel(const Select a)
             const int n = __syncthreads_count(mine >= mid);
             if (n < a.picks)
                 above = mid;
-            else if (n > a.picks + kSelSlack)
+            else if (n > enough)
                 below = mid;
             else
                 break;
         }
-        low = mine >= mid ? mid : ~0ull;
+        if (threadIdx.x == 0)
+            found = 0;
+        __syncthreads();
+        if (mine >= mid)
+            collect(mid);
+        __syncthreads();
     }
-    if (low != ~0ull) {
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            const float x = logit(i);
-            if (x >= bar && x > -INFINITY) {
-                const uint64_t key = key_of(x, token_of(i / kVec) + i % kVec);
-                if (key >= low)
-                    list[atomicAdd(&found, 1)] = key;
-            }
-        }
-    }
-    __syncthreads();
     const int n = found;
     uint64_t *out = a.keys + (int64_t(beam) * a.parts + part) * a.picks;
-    for (int i = threadIdx.x; i < n; i += kSelThreads) {
-        const uint64_t key = list[i];
+    for (int i = threadIdx.x / kLanes; i < (n + kSelGroups - 1) / kSelGroups * kSelGroups;
+         i += kSelGroups) {
+        const uint64_t key = i < n ? list[i] : 0;
         int rank = 0;
-        for (int k = 0; k < n; ++k)
+        for (int k = threadIdx.x % kLanes; k < n; k += kLanes)
             rank += list[k] > key;
-        if (rank < a.picks)
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1)
+            rank += __shfl_xor_sync(0xffffffffu, rank, d);
+        if (i < n && rank < a.picks && threadIdx.x % kLanes == 0)
             out[rank] = key;
     }
     for (int i = n + threadIdx.x; i < a.picks; i += kSelThreads)
         out[i] = 0;
-    if (threadIdx.x == 0) {
-        double all = 0.0;
-#pragma unroll
-        for (int i = 0; i < kSelWarps; ++i)
-            all += sums[i];
-        a.stats[int64_t(beam) * a.parts + part] = {all, m, 0};
+    if (warp == 0) {
+        const float2 s = lane < kSelWarps ? sums[lane] : make_float2(0.0f, 0.0f);
+        const float2 all = warp_sum(s.x, s.y);
+        if (lane == 0)
+            a.stats[int64_t(beam) * a.parts + part] = {all.x, all.y, m, 0.0f};
     }
 }
 
@@ -318,33 +365,48 @@ kvx_select_merge_kernel(const Select a)
         } else {
             const bool have = lane < a.parts;
             const uint64_t *keys = a.keys + (int64_t(beam) * a.parts + lane) * a.picks;
-            uint64_t head = have ? keys[0] : 0, next = have && a.picks > 1 ? keys[1] : 0;
-            int at = 1;
-            PartStats part = {0.0, -INFINITY, 0};
+            // The next four of the lane's list: later ones are hardly ever needed.
+            uint64_t q[4];
+            int at = 0;
+            auto refill = [&]() {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[i] = have && at + i < a.picks ? keys[at + i] : 0;
+                at += 4;
+            };
+            refill();
+            PartStats part = {0.0f, 0.0f, -INFINITY, 0.0f};
             if (have)
                 part = a.stats[int64_t(beam) * a.parts + lane];
             const float m = float_of(__reduce_max_sync(0xffffffffu, order_of(part.max)));
             // exp(max - m): what the difference is rounded by goes in to first order.
-            const double away = part.sum > 0.0 ? double(part.max) - m : 0.0;
+            const double away = part.sum > 0.0f ? double(part.max) - m : 0.0;
             const float near = float(away);
-            double s = part.sum * (double(expf(near)) * (1.0 + (away - near)));
-#pragma unroll
-            for (int d = 16; d; d >>= 1)
-                s += __shfl_xor_sync(0xffffffffu, s, d);
-            const double so_far = a.scores[beam], norm = m + log_of(s);
+            const double mine_s = (double(part.sum) + part.more) *
+                                  (double(expf(near)) * (1.0 + (away - near)));
+            const float s_hi = float(mine_s);
+            const float2 s = warp_sum(s_hi, float(mine_s - s_hi));
             for (; n < a.picks; ++n) {
                 // The largest head: high words first, then low words among those that have it.
-                const unsigned hi = __reduce_max_sync(0xffffffffu, unsigned(head >> 32));
+                const unsigned hi = __reduce_max_sync(0xffffffffu, unsigned(q[0] >> 32));
                 if (hi == 0)
                     break;
-                const bool among = unsigned(head >> 32) == hi;
-                const unsigned lo = __reduce_max_sync(0xffffffffu, among ? unsigned(head) : 0u);
-                if (among && unsigned(head) == lo) {
-                    mine[n] = {order_of(so_far + (double(float_of(hi)) - norm)), int32_t(~lo), 0};
-                    head = next;
-                    ++at;
-                    next = at < a.picks ? keys[at] : 0;
+                const bool among = unsigned(q[0] >> 32) == hi;
+                const unsigned lo = __reduce_max_sync(0xffffffffu, among ? unsigned(q[0]) : 0u);
+                if (among && unsigned(q[0]) == lo) {
+                    mine[n].sum = q[0];
+                    q[0] = q[1], q[1] = q[2], q[2] = q[3], q[3] = 0;
+                    if (q[0] == 0)
+                        refill();
                 }
+            }
+            __syncwarp();
+            const double so_far = a.scores[beam];
+            const double norm = m + log_of(double(s.x) + s.y);
+            for (int i = lane; i < n; i += 32) {
+                const uint64_t key = mine[i].sum;
+                mine[i] = {order_of(so_far + (double(float_of(unsigned(key >> 32))) - norm)),
+                           int32_t(~unsigned(key)), 0};
             }
         }
         if (lane == 0)
