@@ -20,7 +20,7 @@ const int kSelThreads = 512;
 const int kSelWarps = kSelThreads / 32;
 const int kSelGroups = 64;     // of threads, KVX_MAX_PICKS at least
 // Threads beyond `picks` that may have candidates, before ties are looked into.
-const int kSelSlack = 64;
+const int kSelSlack = 16;
 const int kMaxParts = 32;      // of a row: a lane each when they are merged
 const int kMergeWarps = KVX_MAX_BEAMS / 2;
 const int kMergeThreads = 32 * kMergeWarps;
@@ -207,16 +207,18 @@ kvx_select_parts_kernel(const Select a)
         // A thread without a logit has no part in the sum (and -infinity less itself is NaN).
         float sum = 0.0f;
         if (top > -INFINITY) {
-            const uint64_t less = pair_of(-m, -m), log2e = pair_of(kLog2e, kLog2e);
+            // The exponents x log2 e - round(m log2 e) come out of one operation; what the
+            // rounding moves them by is the same for all and goes into the sum at the end.
+            const float base = m * kLog2e, off = fmaf(m, kLog2e, -base);
+            const uint64_t less = pair_of(-base, -base), log2e = pair_of(kLog2e, kLog2e);
             uint64_t both[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < EACH; i += 2) {
-                const float2 x =
-                    halves_of(mul_pair(add_pair(pair_of(logit(i), logit(i + 1)), less), log2e));
+                const float2 x = halves_of(fma_pair(pair_of(logit(i), logit(i + 1)), log2e, less));
                 both[i >> 1 & 1] = add_pair(both[i >> 1 & 1], pair_of(exp2_(x.x), exp2_(x.y)));
             }
             const float2 x = halves_of(add_pair(both[0], both[1]));
-            sum = x.x + x.y;
+            sum = (x.x + x.y) * fmaf(off, -kLn2, 1.0f);
         }
         // NaN, or +infinity, which the sum is NaN with too: taken out, once.
         if (!again && !(sum < INFINITY))
@@ -473,14 +475,16 @@ kvx_select_merge_kernel(const Select a)
     }
 }
 
-// Logits that a thread holds, 8 or 32: parts are small where there are few rows, so that a few
-// rows still fill the GPU.
+// Logits that a thread holds: 128 bytes of them, so that what a part costs besides its logits
+// (half of the instructions at 64) is met seldom; 8 where there are few rows, so that they still
+// fill the GPU.
 int each_of(const kvx_ctx *ctx, const kvx_select_cfg &c)
 {
+    const int most = c.type == KVX_TYPE_FLOAT ? 32 : 64;
     const int64_t rows = int64_t(c.n_groups) * c.width;
-    const int64_t large = (c.vocab + 7 + 32 * kSelThreads - 1) / (32 * kSelThreads);
+    const int64_t large = (c.vocab + 7 + most * kSelThreads - 1) / (most * kSelThreads);
     const int64_t small = (c.vocab + 7 + 8 * kSelThreads - 1) / (8 * kSelThreads);
-    return rows * large < 2 * ctx->num_sms && small <= kMaxParts ? 8 : 32;
+    return rows * large < 2 * ctx->num_sms && small <= kMaxParts ? 8 : most;
 }
 
 int parts_of(const kvx_select_cfg &c, int each)
@@ -492,7 +496,8 @@ template <int TYPE>
 const void *parts_kernel(int each)
 {
     return each == 8 ? reinterpret_cast<const void *>(kvx_select_parts_kernel<TYPE, 8>)
-                     : reinterpret_cast<const void *>(kvx_select_parts_kernel<TYPE, 32>);
+                     : reinterpret_cast<const void *>(
+                           kvx_select_parts_kernel<TYPE, TYPE == KVX_TYPE_FLOAT ? 32 : 64>);
 }
 
 cudaError_t launch(const void *fn, int64_t ctas, int threads, cudaStream_t s, void **args)
