@@ -106,33 +106,17 @@ kvx_append_rotated_kernel(const Rotate a)
     typedef Elem<TYPE> E;
     typedef typename E::T T;
     constexpr int kLanes = D / 16;
-    __shared__ float2 turn[D / 2];
+    __shared__ float2 turn[D / 2 + D / 16];  // a gap after each eight, for the banks
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x;
-    const AttnReq q = a.step.reqs[request_of_row(a.step.reqs, a.step.n_req, row, lane)];
-    const int pos = q.n_tokens - q.n_new + row - q.row_begin, nth = a.step.page.div(pos);
-    wait_for_earlier_work();
-    const int page = q.table[nth];
-    if (a.rotary) {
-        const int at = a.positions ? a.positions[row] : pos;
-        for (int i = threadIdx.x; i < a.rotary / 2; i += blockDim.x) {
-            const float2 t = cos_sin(turns_of(a.freqs[i]) * uint64_t(int64_t(at)));
-            turn[i] = make_float2(t.x * a.magnitude, t.y * a.magnitude);
-        }
-        __syncthreads();
-    }
-    const bool held = unsigned(page) < unsigned(a.step.num_pages);
-    if (!held && threadIdx.x == 0)
-        atomicOr(a.step.status, KVX_DEV_PAGE_OUT_OF_RANGE);
-    const int64_t slot = int64_t(held ? page : 0) * a.step.page_size + pos - nth * a.step.page_size;
-
     const int pairs = a.rotary / 16;  // lanes of a head that rotate
     const int jobs = (a.q_heads + 2 * a.kv_heads) * kLanes;
-    // Whole warps stay together for the shuffles.
-    for (int job0 = threadIdx.x - lane; job0 < jobs; job0 += blockDim.x) {
-        const int job = min(job0 + lane, jobs - 1);
-        const bool mine = job0 + lane < jobs;
-        int head = job / kLanes, j = job % kLanes, kind = 0;
+    // What a job reads: its head, kind (0 q, 1 K, 2 V) and units of eight elements, which may lie
+    // apart where they rotate.
+    auto job_of = [&](int job, int &head, int &kind, int &u0, int &u1) {
+        const int j = job % kLanes;
+        head = job / kLanes;
+        kind = 0;
         if (head >= a.q_heads) {
             head -= a.q_heads;
             kind = 1;
@@ -141,12 +125,48 @@ kvx_append_rotated_kernel(const Rotate a)
                 kind = 2;
             }
         }
+        const bool apart = kind < 2 && j < pairs && !a.interleaved;
+        u0 = apart ? j : 2 * j;
+        u1 = apart ? j + pairs : 2 * j + 1;
+    };
+    auto load = [&](int job0, uint4 (&in)[2]) {
+        int head, kind, u0, u1;
+        job_of(min(job0 + lane, jobs - 1), head, kind, u0, u1);
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.src[kind] + row * a.stride[kind] +
+                                                           head * (D * 2));
+        in[0] = src[u0];
+        in[1] = src[u1];
+    };
+    // Whole warps stay together, for the shuffles.  The data is on its way before anything else.
+    const int job_first = threadIdx.x - lane;
+    wait_for_earlier_work();
+    uint4 in[2];
+    load(job_first, in);
+    const AttnReq q = a.step.reqs[request_of_row(a.step.reqs, a.step.n_req, row, lane)];
+    const int pos = q.n_tokens - q.n_new + row - q.row_begin, nth = a.step.page.div(pos);
+    const int page = q.table[nth];
+    if (a.rotary) {
+        const int at = a.positions ? a.positions[row] : pos;
+        for (int i = threadIdx.x; i < a.rotary / 2; i += blockDim.x) {
+            const float2 t = cos_sin(turns_of(a.freqs[i]) * uint64_t(int64_t(at)));
+            turn[i + i / 8] = make_float2(t.x * a.magnitude, t.y * a.magnitude);
+        }
+        __syncthreads();
+    }
+    const bool held = unsigned(page) < unsigned(a.step.num_pages);
+    if (!held && threadIdx.x == 0)
+        atomicOr(a.step.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+    const int64_t slot = int64_t(held ? page : 0) * a.step.page_size + pos - nth * a.step.page_size;
+
+    for (int job0 = job_first; job0 < jobs; job0 += blockDim.x) {
+        uint4 later[2] = {in[0], in[1]};
+        if (job0 + int(blockDim.x) < jobs)
+            load(job0 + blockDim.x, later);
+        const bool mine = job0 + lane < jobs;
+        const int j = min(job0 + lane, jobs - 1) % kLanes;
+        int head, kind, u0, u1;
+        job_of(min(job0 + lane, jobs - 1), head, kind, u0, u1);
         const bool turned = kind < 2 && j < pairs, apart = turned && !a.interleaved;
-        // The head's units of eight elements: kind < 2 and below 2 pairs they may lie apart.
-        const int u0 = apart ? j : 2 * j, u1 = apart ? j + pairs : 2 * j + 1;
-        const char *src = a.src[kind] + row * a.stride[kind] + head * (D * 2);
-        uint4 in[2] = {reinterpret_cast<const uint4 *>(src)[u0],
-                       reinterpret_cast<const uint4 *>(src)[u1]};
         float x[2][8];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -156,7 +176,7 @@ kvx_append_rotated_kernel(const Rotate a)
         if (apart) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float2 t = turn[8 * u0 + k];
+                const float2 t = turn[9 * u0 + k];
                 const float p = x[0][k], r = x[1][k];
                 x[0][k] = p * t.x - r * t.y;
                 x[1][k] = r * t.x + p * t.y;
@@ -166,7 +186,8 @@ kvx_append_rotated_kernel(const Rotate a)
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
-                    const float2 t = turn[4 * (i ? u1 : u0) + k / 2];
+                    const int pair = 4 * (i ? u1 : u0) + k / 2;
+                    const float2 t = turn[pair + pair / 8];
                     const float p = x[i][k], r = x[i][k + 1];
                     x[i][k] = p * t.x - r * t.y;
                     x[i][k + 1] = r * t.x + p * t.y;
@@ -202,12 +223,15 @@ kvx_append_rotated_kernel(const Rotate a)
             top[0] = both[0];
             top[1] = both[1];
         }
+        const uint4 out[2] = {in[0], in[1]};
+        in[0] = later[0];
+        in[1] = later[1];
         if (!mine)
             continue;
         if (kind == 0) {
             char *dst = a.q_out + row * a.q_out_stride + head * (D * 2);
-            reinterpret_cast<uint4 *>(dst)[u0] = in[0];
-            reinterpret_cast<uint4 *>(dst)[u1] = in[1];
+            reinterpret_cast<uint4 *>(dst)[u0] = out[0];
+            reinterpret_cast<uint4 *>(dst)[u1] = out[1];
             continue;
         }
         if (!held)
@@ -216,8 +240,8 @@ kvx_append_rotated_kernel(const Rotate a)
         const float scale = a.scale[kind - 1];
         if (KV == TYPE) {
             uint4 *dst = reinterpret_cast<uint4 *>(token + head * (D * 2));
-            dst[u0] = in[0];
-            dst[u1] = in[1];
+            dst[u0] = out[0];
+            dst[u1] = out[1];
         } else if (KV == KVX_TYPE_FP_EIGHT) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -324,7 +348,8 @@ kvx_status kvx::append_rotated(const kvx_attn_plan *p, int layer, const kvx_rope
                          : half ? pick_append<KVX_TYPE_HALF, 128>(p->cfg.kv_type)
                                 : pick_append<KVX_TYPE_BFLOAT, 128>(p->cfg.kv_type);
     const int64_t jobs = (int64_t(a.q_heads) + 2 * a.kv_heads) * (p->cfg.head_dim / 16);
-    const int threads = int(std::min<int64_t>(kRotateThreads, (jobs + 31) / 32 * 32));
+    const int64_t rounds = (jobs + kRotateThreads - 1) / kRotateThreads;  // shared out evenly
+    const int threads = int((jobs + 32 * rounds - 1) / (32 * rounds) * 32);
     void *args[] = {&a};
     const cudaError_t e = launch_early(fn, dim3(unsigned(p->rows)), threads, 0, s, args);
     return e == cudaSuccess ? KVX_OK : kvx::cuda_err(p->ctx, e, "append launch");
