@@ -69,6 +69,7 @@ struct Args {
     int32_t wide;            // everything that is copied is 32-byte aligned
     int32_t table_warps;     // of each CTA, for tables; the others copy
     int32_t copies;          // reorder: last pages that may be copied
+    int32_t splits;          // and CTAs for each
 };
 
 // -------------------------------------------------------------------------------- device
@@ -514,7 +515,6 @@ struct Heirs {
     unsigned extra;    // beams that continue one an earlier beam continues too
     unsigned dropped;  // beams that nobody continues
     int parent;        // of beam `lane`
-    int count;         // beams that continue beam `lane`
     bool ok;
 
     __device__ __forceinline__ explicit Heirs(const BeamEntry &e)
@@ -527,9 +527,14 @@ struct Heirs {
         extra = __ballot_sync(0xffffffffu, lane < e.width && (alike & ((1u << lane) - 1))) & all;
         dropped = ~__reduce_or_sync(0xffffffffu,
                                     ok && lane < e.width ? 1u << parent : 0u) & all;
-        count = 0;
-        for (int b = 0; b < e.width; ++b)
-            count += __shfl_sync(0xffffffffu, parent, b) == lane;
+    }
+    // Beams that continue beam `lane`.
+    __device__ __forceinline__ int count(int width) const
+    {
+        int n = 0;
+        for (int b = 0; b < width; ++b)
+            n += __shfl_sync(0xffffffffu, parent, b) == int(threadIdx.x & 31);
+        return n;
     }
     // The bit of rank i.
     static __device__ __forceinline__ int nth(unsigned bits, int i)
@@ -540,51 +545,45 @@ struct Heirs {
     }
 };
 
-// Copies of partly filled last pages.  A job is the i-th extra beam of a group and a slice of a
-// slab, or a few slabs: `a.slices` > 0 slices of each, or -a.slices slabs.  Which beams are extra
-// is known here only, so there are jobs for all that may be (all but one of a group).
+// Copies of partly filled last pages: `a.splits` CTAs to each that there may be (all beams but one
+// of a group; which are copied is known here only), whose warps take its slices of slabs in turn.
+// Each warp finds out once what it copies.
 __global__ void __launch_bounds__(kThreads, 1)
 kvx_reorder_copy_kernel(const Args a, const __grid_constant__ Inline in)
 {
     __shared__ Inline staged;
     const char *desc = descriptors(a, in, reinterpret_cast<char *>(&staged));
-    const BeamEntry *e = reinterpret_cast<const BeamEntry *>(desc + a.off_entries);
+    const BeamEntry *entries = reinterpret_cast<const BeamEntry *>(desc + a.off_entries);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int pieces = a.slices > 0 ? a.n_slabs * a.slices : (a.n_slabs - a.slices - 1) / -a.slices;
-    const int64_t jobs = int64_t(a.copies) * pieces;
     __syncthreads();
+    const int c = int(blockIdx.x / unsigned(a.splits)), split = int(blockIdx.x) - c * a.splits;
+    const int x = find_entry(entries, a.n_entries, c, [](const BeamEntry &b) { return b.copy_begin; });
+    const BeamEntry e = entries[x];
     wait_for_earlier_work();
-    for (int64_t job = int64_t(blockIdx.x) * kWarps + warp; job < jobs;
-         job += int64_t(gridDim.x) * kWarps) {
-        const int c = int(job / pieces), piece = int(job - int64_t(c) * pieces);
-        const int x = find_entry(e, a.n_entries, c, [](const BeamEntry &b) { return b.copy_begin; });
-        const Heirs h(e[x]);
-        const int i = c - e[x].copy_begin;
-        if (!h.ok || i >= __popc(h.extra))
-            continue;
-        const int parent = __shfl_sync(0xffffffffu, h.parent, Heirs::nth(h.extra, i));
-        const int giver = Heirs::nth(h.dropped, i);
-        const int from = __ldcg(e[x].tables + parent * e[x].stride + e[x].full);
-        const int to = __ldcg(e[x].tables + giver * e[x].stride + e[x].full);
-        if (unsigned(from) >= unsigned(a.num_pages) || unsigned(to) >= unsigned(a.num_pages)) {
-            if (lane == 0)
-                atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
-            continue;
-        }
-        if (from == to)
-            continue;
-        if (a.slices > 0) {
-            copy_slice(a, desc, piece / a.slices, piece % a.slices, from, to, e[x].tail, lane);
-        } else {
-            for (int slab = piece * -a.slices; slab < min(a.n_slabs, (piece + 1) * -a.slices);
-                 ++slab)
-                copy_slice(a, desc, slab, 0, from, to, e[x].tail, lane);
-        }
+    const int last = lane < e.width ? __ldcg(e.tables + lane * e.stride + e.full) : -1;
+    const Heirs h(e);
+    const int i = c - e.copy_begin;
+    if (!h.ok || i >= __popc(h.extra))
+        return;
+    const int parent = __shfl_sync(0xffffffffu, h.parent, Heirs::nth(h.extra, i));
+    const int from = __shfl_sync(0xffffffffu, last, parent);
+    const int to = __shfl_sync(0xffffffffu, last, Heirs::nth(h.dropped, i));
+    if (unsigned(from) >= unsigned(a.num_pages) || unsigned(to) >= unsigned(a.num_pages)) {
+        if (threadIdx.x == 0)
+            atomicOr(a.status, KVX_DEV_PAGE_OUT_OF_RANGE);
+        return;
     }
+    if (from == to)
+        return;
+    const int pieces = a.n_slabs * a.slices;
+    for (int piece = split * kWarps + warp; piece < pieces; piece += a.splits * kWarps)
+        copy_slice(a, desc, piece / a.slices, piece % a.slices, from, to, e.tail, lane);
 }
 
 // Tables and counts: a CTA takes kBeamColumns columns of a group, the entries of all its beams
-// at one logical page each, so nobody else reads what it writes.
+// at one logical page each, so nobody else reads what it writes but the copies, which read the
+// last column.  It starts when every CTA of those has seen all earlier work done, so only that
+// column waits for them.
 __global__ void __launch_bounds__(kBeamColumns)
 kvx_reorder_tables_kernel(const Args a, const __grid_constant__ Inline in)
 {
@@ -597,55 +596,67 @@ kvx_reorder_tables_kernel(const Args a, const __grid_constant__ Inline in)
                              [](const BeamEntry &b) { return b.col_begin; });
     const BeamEntry e = entries[x];
     const int j = int(blockIdx.x) * kBeamColumns - e.col_begin + int(threadIdx.x);
-    wait_for_earlier_work();
+    const int t = threadIdx.x;
+    if (a.copies == 0)  // no copies ahead
+        wait_for_earlier_work();
     const bool last = j == e.full && e.tail > 0, mine = j < e.full || last;
-    for (int b = 0; mine && b < e.width; ++b)
-        held[b][threadIdx.x] = __ldcg(e.tables + b * e.stride + j);
-    if (threadIdx.x < 32) {
+    for (int b0 = 0; mine && b0 < e.width; b0 += 8) {
+        int32_t p[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            p[b] = b0 + b < e.width ? __ldcg(e.tables + (b0 + b) * e.stride + j) : 0;
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            if (b0 + b < e.width)
+                held[b0 + b][t] = p[b];
+    }
+    if (t < 32) {
         const Heirs h(e);
-        const int lane = threadIdx.x;
-        if (lane == 0) {
+        const int n = h.count(e.width);
+        if (t == 0) {
             bad = !h.ok;
             if (bad && j == 0)
                 atomicOr(a.status, KVX_DEV_BEAM_OUT_OF_RANGE);
         }
-        if (h.ok && lane < e.width) {
-            parents[lane] = h.parent;
-            counts[lane] = h.count;
-            givers[lane] = h.extra >> lane & 1
-                               ? Heirs::nth(h.dropped, __popc(h.extra & ((1u << lane) - 1)))
-                               : h.parent;
+        if (h.ok && t < e.width) {
+            parents[t] = h.parent;
+            counts[t] = n;
+            givers[t] = h.extra >> t & 1
+                            ? Heirs::nth(h.dropped, __popc(h.extra & ((1u << t) - 1)))
+                            : h.parent;
         }
     }
     __syncthreads();
-    if (bad || !mine)
-        return;
-    const int t = threadIdx.x;
-    for (int b = 0; b < e.width; ++b) {
-        const int from = last ? givers[b] : parents[b];
-        if (from != b)
-            e.tables[b * e.stride + j] = held[from][t];
-    }
-    if (last)
-        return;
-    // Beams that share the page (a prompt's) change its count by nothing.
-    bool same = true;
-    for (int b = 1; b < e.width; ++b)
-        same &= held[b][t] == held[0][t];
-    unsigned wrong = 0;
-    for (int b = 0; b < e.width; ++b) {
-        const int p = held[b][t], d = counts[b] - 1;
-        if (unsigned(p) >= unsigned(a.num_pages)) {
-            wrong |= KVX_DEV_PAGE_OUT_OF_RANGE;
-        } else if (same ? b == 0 && __ldcg(a.refs + p) <= 0
-                        : d != 0 && atomicAdd(a.refs + p, d) <= 0) {
-            if (!same)  // not held: taken back
-                atomicSub(a.refs + p, d);
-            wrong |= KVX_DEV_PAGE_NOT_HELD;
+    if (mine && !last && !bad) {
+        // Beams that share the page (a prompt's) change neither their entries nor its count.
+        bool same = true;
+        for (int b = 1; b < e.width; ++b)
+            same &= held[b][t] == held[0][t];
+        for (int b = 0; !same && b < e.width; ++b)
+            if (parents[b] != b)
+                e.tables[b * e.stride + j] = held[parents[b]][t];
+        unsigned wrong = 0;
+        for (int b = 0; b < (same ? 1 : e.width); ++b) {
+            const int p = held[b][t], d = counts[b] - 1;
+            if (unsigned(p) >= unsigned(a.num_pages)) {
+                wrong |= KVX_DEV_PAGE_OUT_OF_RANGE;
+            } else if (same) {
+                if (__ldcg(a.refs + p) <= 0)
+                    wrong |= KVX_DEV_PAGE_NOT_HELD;
+            } else if (d != 0 && atomicAdd(a.refs + p, d) <= 0) {
+                atomicSub(a.refs + p, d);  // not held: taken back
+                wrong |= KVX_DEV_PAGE_NOT_HELD;
+            }
         }
+        if (wrong)
+            atomicOr(a.status, wrong);
     }
-    if (wrong)
-        atomicOr(a.status, wrong);
+    if (a.copies > 0)
+        wait_for_earlier_work();
+    if (last && !bad)
+        for (int b = 0; b < e.width; ++b)
+            if (givers[b] != b)
+                e.tables[b * e.stride + j] = held[givers[b]][t];
 }
 
 // ---------------------------------------------------------------------------------- host
@@ -912,17 +923,16 @@ kvx_status kvx_reorder_beams(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
     for (int i = 0; i < n_groups; ++i)
         if (e[i + 1].copy_begin > e[i].copy_begin)
             longest = std::max<int64_t>(longest, e[i].tail);
-    // Of the pages that may be copied, about half are.
-    const int64_t units = int64_t(a.copies) * a.n_slabs, warps = int64_t(ctx->num_sms) * kWarps;
-    choose_slices(ctx, std::max<int64_t>(1, units / 2),
+    // Of the pages that may be copied, about half are; their slices go round all warps of the GPU
+    // about once.
+    choose_slices(ctx, std::max<int64_t>(1, int64_t(a.copies) * a.n_slabs / 2),
                   std::max<int64_t>(longest, 1) * pool->token_bytes, &a);
-    if (a.slices == 1 && units > 4 * warps)
-        a.slices = -int32_t(std::min<int64_t>(a.n_slabs, units / (2 * warps)));
-    const int64_t pieces = a.slices > 0 ? int64_t(a.n_slabs) * a.slices
-                                        : (a.n_slabs - a.slices - 1) / -a.slices;
-    if (pieces > INT32_MAX)
-        return kvx::set_err(ctx, KVX_ERR_CAPACITY, "%d slabs x %d slices exceed 2^31 copies",
-                            a.n_slabs, a.slices);
+    const int64_t pieces = int64_t(a.n_slabs) * a.slices;
+    const int64_t ahead = 2 * (int64_t(ctx->num_sms) + 1) / std::max(1, a.copies);
+    a.splits = int32_t(std::max<int64_t>(1, std::min((pieces + kWarps - 1) / kWarps, ahead)));
+    if (pieces > INT32_MAX || int64_t(a.copies) * a.splits > INT32_MAX)
+        return kvx::set_err(ctx, KVX_ERR_CAPACITY, "%d slabs x %d slices of %d pages exceed 2^31 "
+                            "copies", a.n_slabs, a.slices, a.copies);
     const int64_t jobs = a.copies * pieces;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
@@ -931,10 +941,9 @@ kvx_status kvx_reorder_beams(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
         a.ext = b.slot->dev;
         err = kvx::stage(ctx, *b.slot, b.bytes, 0, 0, s);
     }
-    if (err == cudaSuccess && jobs > 0)
-        err = launch_one(kvx_reorder_copy_kernel, a, &b,
-                         std::min<int64_t>(ctx->num_sms, (jobs + kWarps - 1) / kWarps), kThreads,
-                         0, s);
+    if (err == cudaSuccess && a.copies > 0)
+        err = launch_one(kvx_reorder_copy_kernel, a, &b, int64_t(a.copies) * a.splits, kThreads, 0,
+                         s);
     const int64_t ctas = columns / kBeamColumns;
     if (err == cudaSuccess)
         err = launch_one(kvx_reorder_tables_kernel, a, &b, ctas, kBeamColumns, 0, s);
