@@ -548,7 +548,7 @@ struct Heirs {
 // Copies of partly filled last pages: `a.splits` CTAs to each that there may be (all beams but one
 // of a group; which are copied is known here only), whose warps take its slices of slabs in turn.
 // Each warp finds out once what it copies.
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
 kvx_reorder_copy_kernel(const Args a, const __grid_constant__ Inline in)
 {
     __shared__ Inline staged;
@@ -928,7 +928,7 @@ kvx_status kvx_reorder_beams(kvx_ctx *ctx, const kvx_pool *pool, int32_t *refs,
     choose_slices(ctx, std::max<int64_t>(1, int64_t(a.copies) * a.n_slabs / 2),
                   std::max<int64_t>(longest, 1) * pool->token_bytes, &a);
     const int64_t pieces = int64_t(a.n_slabs) * a.slices;
-    const int64_t ahead = 2 * (int64_t(ctx->num_sms) + 1) / std::max(1, a.copies);
+    const int64_t ahead = 4 * int64_t(ctx->num_sms) / std::max(1, a.copies);
     a.splits = int32_t(std::max<int64_t>(1, std::min((pieces + kWarps - 1) / kWarps, ahead)));
     if (pieces > INT32_MAX || int64_t(a.copies) * a.splits > INT32_MAX)
         return kvx::set_err(ctx, KVX_ERR_CAPACITY, "%d slabs x %d slices of %d pages exceed 2^31 "
