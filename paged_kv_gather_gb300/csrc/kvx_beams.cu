@@ -177,6 +177,7 @@ kvx_select_parts_kernel(const Select a)
         for (int i = 0; i < kVecs; ++i)
             pair = max_pair<TYPE>(pair, max_unit<TYPE>(u[i]));
         top = L::larger(pair);
+        top = top > -INFINITY ? top : -INFINITY;  // nor NaN, where there is nothing else
         float group = top;
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1)
