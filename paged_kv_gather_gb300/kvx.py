@@ -42,8 +42,12 @@ KVX_DEV_PAGE_OUT_OF_RANGE = 0x1
 KVX_DEV_WAIT_TIMEOUT = 0x2
 KVX_DEV_NO_FREE_PAGE = 0x4
 KVX_DEV_PAGE_NOT_HELD = 0x8
+KVX_DEV_BEAM_OUT_OF_RANGE = 0x10
 
 KVX_MAX_UPKEEP_PAGES = 1 << 20
+KVX_MAX_BEAMS = 32
+KVX_MAX_PICKS = 64
+KVX_MAX_VOCAB = 524000
 
 KVX_TYPE_HALF = 0
 KVX_TYPE_BFLOAT = 1
