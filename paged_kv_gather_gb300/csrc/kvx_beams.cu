@@ -16,7 +16,7 @@
 
 namespace {
 
-const int kSelThreads = 512;
+const int kSelThreads = 256;
 const int kSelWarps = kSelThreads / 32;
 const int kSelGroups = 64;     // of threads, KVX_MAX_PICKS at least
 // Threads beyond `picks` that may have candidates, before ties are looked into.
@@ -119,7 +119,7 @@ __device__ __forceinline__ float2 warp_sum(float hi, float lo)
 }
 
 template <int TYPE, int EACH>
-__global__ void __launch_bounds__(kSelThreads, EACH * sizeof(typename Logit<TYPE>::T) > 64 ? 2 : 3)
+__global__ void __launch_bounds__(kSelThreads, EACH * sizeof(typename Logit<TYPE>::T) > 128 ? 2 : 4)
 kvx_select_parts_kernel(const Select a)
 {
     typedef Logit<TYPE> L;
@@ -247,9 +247,11 @@ kvx_select_parts_kernel(const Select a)
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
                 const float x = logit(i * kVec + k);
-                const uint64_t key = key_of(x, token_of(i) + k);
-                if (x >= bar && x > -INFINITY && key >= low)
-                    list[atomicAdd(&found, 1)] = key;
+                if (x >= bar && x > -INFINITY) {
+                    const uint64_t key = key_of(x, token_of(i) + k);
+                    if (key >= low)
+                        list[atomicAdd(&found, 1)] = key;
+                }
             }
         }
     };
@@ -476,16 +478,16 @@ kvx_select_merge_kernel(const Select a)
     }
 }
 
-// Logits that a thread holds: 128 bytes of them, so that what a part costs besides its logits
-// (half of the instructions at 64) is met seldom; 8 where there are few rows, so that they still
-// fill the GPU.
+// Logits that a thread holds: 64, so that what a part costs besides its logits (half of the
+// instructions at 32) is met seldom; 8 where there are few rows, so that they still fill the GPU.
+const int kEachMost = 64;
+
 int each_of(const kvx_ctx *ctx, const kvx_select_cfg &c)
 {
-    const int most = c.type == KVX_TYPE_FLOAT ? 32 : 64;
     const int64_t rows = int64_t(c.n_groups) * c.width;
-    const int64_t large = (c.vocab + 7 + most * kSelThreads - 1) / (most * kSelThreads);
+    const int64_t large = (c.vocab + 7 + kEachMost * kSelThreads - 1) / (kEachMost * kSelThreads);
     const int64_t small = (c.vocab + 7 + 8 * kSelThreads - 1) / (8 * kSelThreads);
-    return rows * large < 2 * ctx->num_sms && small <= kMaxParts ? 8 : most;
+    return rows * large < 2 * ctx->num_sms && small <= kMaxParts ? 8 : kEachMost;
 }
 
 int parts_of(const kvx_select_cfg &c, int each)
@@ -498,7 +500,7 @@ const void *parts_kernel(int each)
 {
     return each == 8 ? reinterpret_cast<const void *>(kvx_select_parts_kernel<TYPE, 8>)
                      : reinterpret_cast<const void *>(
-                           kvx_select_parts_kernel<TYPE, TYPE == KVX_TYPE_FLOAT ? 32 : 64>);
+                           kvx_select_parts_kernel<TYPE, kEachMost>);
 }
 
 cudaError_t launch(const void *fn, int64_t ctas, int threads, cudaStream_t s, void **args)
