@@ -19,8 +19,9 @@ namespace {
 const int kSelThreads = 256;
 const int kSelWarps = kSelThreads / 32;
 const int kSelGroups = 64;     // of threads, KVX_MAX_PICKS at least
-// Threads beyond `picks` that may have candidates, before ties are looked into.
-const int kSelSlack = 16;
+const int kSelRows = 96;       // threads of a part that have candidates, and ...
+const int kSelList = 512;      // ... candidates, before ties are looked into
+const int kMergeList = 512;    // continuations that are ranked, before ties are looked into
 const int kMaxParts = 32;      // of a row: a lane each when they are merged
 const int kMergeWarps = KVX_MAX_BEAMS / 2;
 const int kMergeThreads = 32 * kMergeWarps;
@@ -125,8 +126,10 @@ kvx_select_parts_kernel(const Select a)
     typedef Logit<TYPE> L;
     typedef typename L::T T;
     constexpr int kVec = 16 / sizeof(T), kVecs = EACH / kVec;
-    constexpr int kEnough = KVX_MAX_PICKS + kSelSlack;  // threads that may have candidates
-    __shared__ uint64_t list[kEnough * EACH];
+    constexpr int kPer = 4 / sizeof(T), kWords = EACH / kPer;  // logits of a word, words of a thread
+    __shared__ uint64_t list[kSelList];
+    __shared__ uint4 rows[kSelRows][kVecs];
+    __shared__ int owner[kSelRows];
     __shared__ __align__(16) float tops[kSelGroups];
     __shared__ float2 sums[kSelWarps];
     __shared__ float reach;  // the `picks`-th largest of `tops`
@@ -238,70 +241,91 @@ kvx_select_parts_kernel(const Select a)
                 reinterpret_cast<T *>(&u[i / kVec])[i % kVec] = L::store(-INFINITY);
     }
 
-    // Candidates: the logits that reach the bar.
-    auto collect = [&](uint64_t low) {
+    // Candidates: the logits that reach the bar.  The few threads that have some put all their
+    // logits where the CTA looks through them together: each on its own, one divergent pass per
+    // warp, took half of the kernel's time.
+    if (top >= bar && top > -INFINITY) {
+        const int at = atomicAdd(&reached, 1);
+        if (at < kSelRows) {
+            owner[at] = threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if (L::larger(max_unit<TYPE>(u[i])) < bar)
-                continue;
+            for (int i = 0; i < kVecs; ++i)
+                rows[at][i] = u[i];
+        }
+    }
+    __syncthreads();
+    const int all_rows = reached;
+    for (int i = threadIdx.x; i < min(all_rows, kSelRows) * kWords; i += kSelThreads) {
+        const int r = i / kWords, w = i % kWords;
+        const unsigned word = reinterpret_cast<const unsigned *>(rows[r])[w];
+        if (L::larger(word) < bar)
+            continue;
+        const int token = ((part * kVecs + w / 4) * kSelThreads + owner[r]) * kVec - skew +
+                          w % 4 * kPer;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                const float x = logit(i * kVec + k);
-                if (x >= bar && x > -INFINITY) {
-                    const uint64_t key = key_of(x, token_of(i) + k);
-                    if (key >= low)
-                        list[atomicAdd(&found, 1)] = key;
-                }
+        for (int k = 0; k < kPer; ++k) {
+            const float x = L::load(reinterpret_cast<const T *>(&word)[k]);
+            if (x >= bar && x > -INFINITY) {
+                const int at = atomicAdd(&found, 1);
+                if (at < kSelList)
+                    list[at] = key_of(x, token + k);
             }
         }
-    };
-    const int enough = a.picks + kSelSlack;
-    const bool has = top >= bar && top > -INFINITY;
-    if (has && atomicAdd(&reached, 1) < enough)
-        collect(0);
+    }
     __syncthreads();
-    if (reached > enough) {
-        // Ties make them too many: the tokens decide, by bisection over the threads' largest keys.
-        uint64_t mine = 0;
-#pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            if (mine == 0 && has && logit(i) == top)
-                mine = key_of(top, token_of(i / kVec) + i % kVec);
-        // more than enough reach `below`, less than `picks` reach `above`
-        uint64_t below = 1, above = key_of(m, 0) + 1, mid;
-        for (;;) {
-            mid = below + (above - below) / 2;
-            const int n = __syncthreads_count(mine >= mid);
-            if (n < a.picks)
-                above = mid;
-            else if (n > enough)
-                below = mid;
-            else
-                break;
-        }
-        if (threadIdx.x == 0)
-            found = 0;
-        __syncthreads();
-        if (mine >= mid)
-            collect(mid);
-        __syncthreads();
-    }
-    const int n = found;
+    const int n = all_rows > kSelRows ? kSelList + 1 : found;
     uint64_t *out = a.keys + (int64_t(beam) * a.parts + part) * a.picks;
-    for (int i = threadIdx.x / kLanes; i < (n + kSelGroups - 1) / kSelGroups * kSelGroups;
-         i += kSelGroups) {
-        const uint64_t key = i < n ? list[i] : 0;
-        int rank = 0;
-        for (int k = threadIdx.x % kLanes; k < n; k += kLanes)
-            rank += list[k] > key;
+    if (n <= kSelList) {
+        for (int i = threadIdx.x / kLanes; i < (n + kSelGroups - 1) / kSelGroups * kSelGroups;
+             i += kSelGroups) {
+            const uint64_t key = i < n ? list[i] : 0;
+            int rank = 0;
+            for (int k = threadIdx.x % kLanes; k < n; k += kLanes)
+                rank += list[k] > key;
 #pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1)
-            rank += __shfl_xor_sync(0xffffffffu, rank, d);
-        if (i < n && rank < a.picks && threadIdx.x % kLanes == 0)
-            out[rank] = key;
+            for (int d = 1; d < kLanes; d <<= 1)
+                rank += __shfl_xor_sync(0xffffffffu, rank, d);
+            if (i < n && rank < a.picks && threadIdx.x % kLanes == 0)
+                out[rank] = key;
+        }
+        for (int i = n + threadIdx.x; i < a.picks; i += kSelThreads)
+            out[i] = 0;
+    } else {
+        // Ties make them too many: one after the other, the largest of what the threads have left.
+        uint64_t last = ~0ull;  // of this thread's, the one taken last
+        uint64_t next = ~0ull;
+        for (int r = 0; r < a.picks; ++r) {
+            if (next == last) {
+                // Read again: with registers of its own this would cost the usual case some.
+                next = 0;
+#pragma unroll 1
+                for (int i = 0; i < EACH; ++i) {
+                    const int token = token_of(i / kVec) + i % kVec;
+                    if (token < 0 || token >= a.vocab)
+                        continue;
+                    const float x = L::load(reinterpret_cast<const T *>(row)[token]);
+                    const uint64_t key = key_of(x, token);
+                    if (x >= bar && x > -INFINITY && x < INFINITY && key < last && key > next)
+                        next = key;
+                }
+            }
+            const unsigned hi = __reduce_max_sync(0xffffffffu, unsigned(next >> 32));
+            const unsigned lo = __reduce_max_sync(
+                0xffffffffu, unsigned(next >> 32) == hi ? unsigned(next) : 0u);
+            if (lane == 0)
+                list[warp] = uint64_t(hi) << 32 | lo;
+            __syncthreads();
+            uint64_t best = 0;
+#pragma unroll
+            for (int i = 0; i < kSelWarps; ++i)
+                best = max(best, list[i]);
+            if (next == best)
+                last = best;
+            if (threadIdx.x == 0)
+                out[r] = best;
+            __syncthreads();
+        }
     }
-    for (int i = n + threadIdx.x; i < a.picks; i += kSelThreads)
-        out[i] = 0;
     if (warp == 0) {
         const float2 s = lane < kSelWarps ? sums[lane] : make_float2(0.0f, 0.0f);
         const float2 all = warp_sum(s.x, s.y);
@@ -346,135 +370,159 @@ __device__ __forceinline__ double log_of(double s)
 
 struct Continuation {
     uint64_t sum;  // order_of the sum
-    int32_t token, pad;
+    int32_t token, beam;
 };
 
-// A warp per beam merges the falling lists of its parts, a lane holding the head of one list;
-// then all of the CTA ranks the beams' continuations.
+// Norms first, a warp per beam: score + logit - norm is a continuation's sum.  Then the largest
+// `picks` sums of all the beams' lists in the way of the parts' kernel: those that reach the
+// `picks`-th largest of what 64 groups of threads have, ranked by counting.
 __global__ void __launch_bounds__(kMergeThreads)
 kvx_select_merge_kernel(const Select a)
 {
-    __shared__ Continuation all[KVX_MAX_BEAMS * KVX_MAX_PICKS];
-    __shared__ int count[KVX_MAX_BEAMS];
+    __shared__ Continuation list[kMergeList];
+    __shared__ uint64_t tops[kSelGroups], bar;
+    __shared__ double norms[KVX_MAX_BEAMS], so_far[KVX_MAX_BEAMS];
+    __shared__ int state[KVX_MAX_BEAMS];  // 0: no continuations, 1: lists, 2: itself
+    __shared__ int found;
+    constexpr int kLanes = kMergeThreads / kSelGroups;
     const int group = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier_work();
     for (int b = warp; b < a.width; b += kMergeWarps) {
         const int beam = group * a.width + b;
-        Continuation *mine = all + b * a.picks;
-        int n = 0;
-        if (!has_continuations(a, beam)) {
-        } else if (a.done && a.done[beam]) {
-            if (lane == 0)
-                mine[0] = {order_of(double(a.scores[beam])), a.done_token, 0};
-            n = 1;
-        } else {
-            const bool have = lane < a.parts;
-            const uint64_t *keys = a.keys + (int64_t(beam) * a.parts + lane) * a.picks;
-            // The next four of the lane's list: later ones are hardly ever needed.
-            uint64_t q[4];
-            int at = 0;
-            auto refill = [&]() {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    q[i] = have && at + i < a.picks ? keys[at + i] : 0;
-                at += 4;
-            };
-            refill();
-            PartStats part = {0.0f, 0.0f, -INFINITY, 0.0f};
-            if (have)
-                part = a.stats[int64_t(beam) * a.parts + lane];
-            const float m = float_of(__reduce_max_sync(0xffffffffu, order_of(part.max)));
-            // exp(max - m): what the difference is rounded by goes in to first order.
-            const double away = part.sum > 0.0f ? double(part.max) - m : 0.0;
-            const float near = float(away);
-            const double mine_s = (double(part.sum) + part.more) *
-                                  (double(expf(near)) * (1.0 + (away - near)));
-            const float s_hi = float(mine_s);
-            const float2 s = warp_sum(s_hi, float(mine_s - s_hi));
-            for (; n < a.picks; ++n) {
-                // The largest head: high words first, then low words among those that have it.
-                const unsigned hi = __reduce_max_sync(0xffffffffu, unsigned(q[0] >> 32));
-                if (hi == 0)
-                    break;
-                const bool among = unsigned(q[0] >> 32) == hi;
-                const unsigned lo = __reduce_max_sync(0xffffffffu, among ? unsigned(q[0]) : 0u);
-                if (among && unsigned(q[0]) == lo) {
-                    mine[n].sum = q[0];
-                    q[0] = q[1], q[1] = q[2], q[2] = q[3], q[3] = 0;
-                    if (q[0] == 0)
-                        refill();
-                }
-            }
-            __syncwarp();
-            const double so_far = a.scores[beam];
-            const double norm = m + log_of(double(s.x) + s.y);
-            for (int i = lane; i < n; i += 32) {
-                const uint64_t key = mine[i].sum;
-                mine[i] = {order_of(so_far + (double(float_of(unsigned(key >> 32))) - norm)),
-                           int32_t(~unsigned(key)), 0};
-            }
+        const int kind = !has_continuations(a, beam) ? 0 : a.done && a.done[beam] ? 2 : 1;
+        PartStats part = {0.0f, 0.0f, -INFINITY, 0.0f};
+        if (kind == 1 && lane < a.parts)
+            part = a.stats[int64_t(beam) * a.parts + lane];
+        const float m = float_of(__reduce_max_sync(0xffffffffu, order_of(part.max)));
+        // exp(max - m): what the difference is rounded by goes in to first order.
+        const double away = part.sum > 0.0f ? double(part.max) - m : 0.0;
+        const float near = float(away);
+        const double mine = (double(part.sum) + part.more) *
+                            (double(expf(near)) * (1.0 + (away - near)));
+        const float hi = float(mine);
+        const float2 s = warp_sum(hi, float(mine - hi));
+        if (lane == 0) {
+            state[b] = kind;
+            so_far[b] = a.scores[beam];
+            norms[b] = m + log_of(double(s.x) + s.y);
         }
-        if (lane == 0)
-            count[b] = n;
     }
+    if (threadIdx.x == 0)
+        found = 0;
     __syncthreads();
 
-    // Rank by counting; of many continuations, only of those that reach the sum that `picks`
-    // of them reach, found by bisection.
-    const int slots = a.width * a.picks;
-    auto valid = [&](int i) { return i - i / a.picks * a.picks < count[i / a.picks]; };
-    uint64_t bar = 0;
-    if (slots > kMergeThreads) {
-        uint64_t below = 0, above = ~0ull;
-        for (int step = 0; step < 64; ++step) {
-            const uint64_t mid = below + (above - below) / 2;
-            int n = 0;
-            for (int i = threadIdx.x; i < (slots + kMergeThreads - 1) / kMergeThreads * kMergeThreads;
-                 i += kMergeThreads)
-                n += __syncthreads_count(i < slots && valid(i) && all[i].sum >= mid);
-            if (n < a.picks)
-                above = mid;
-            else
-                below = mid;
-            if (n >= a.picks && n <= a.picks + kSelSlack)
-                break;
+    // Candidate i: of beam b, key i - b per_beam of its parts' lists.  0: none.
+    const int per_beam = a.parts * a.picks, all = a.width * per_beam;
+    const uint64_t *keys = a.keys + int64_t(group) * all;
+    auto sum_of = [&](int i, int &b, int32_t &token) -> uint64_t {
+        b = i / per_beam;
+        if (state[b] == 2) {
+            token = a.done_token;
+            return i == b * per_beam ? order_of(so_far[b]) : 0;
         }
-        bar = below;
+        const uint64_t key = state[b] ? keys[i] : 0;
+        token = int32_t(~unsigned(key));
+        return key ? order_of(so_far[b] + (double(float_of(unsigned(key >> 32))) - norms[b])) : 0;
+    };
+    int b;
+    int32_t token;
+    uint64_t top = 0;
+    for (int i = threadIdx.x; i < all; i += kMergeThreads)
+        top = max(top, sum_of(i, b, token));
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1)
+        top = max(top, uint64_t(__shfl_xor_sync(0xffffffffu, top, d)));
+    const int mine = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
+    if (sub == 0)
+        tops[mine] = top;
+    __syncthreads();
+    int rank = 0;
+#pragma unroll
+    for (int k = 0; k < kSelGroups / kLanes; ++k) {
+        const uint64_t other = tops[k * kLanes + sub];
+        rank += other > top || (other == top && k * kLanes + sub < mine);
     }
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1)
+        rank += __shfl_xor_sync(0xffffffffu, rank, d);
+    if (sub == 0 && rank == a.picks - 1)
+        bar = top;
+    __syncthreads();
+    for (int i = threadIdx.x; i < all; i += kMergeThreads) {
+        const uint64_t sum = sum_of(i, b, token);
+        if (sum && sum >= bar) {
+            const int at = atomicAdd(&found, 1);
+            if (at < kMergeList)
+                list[at] = {sum, token, b};
+        }
+    }
+    __syncthreads();
     const int64_t out = int64_t(group) * a.picks;
-    for (int i = threadIdx.x; i < slots; i += kMergeThreads) {
-        if (!valid(i) || all[i].sum < bar)
-            continue;
-        const Continuation mine = all[i];
-        // A beam's continuations are in order, and position settles equal sums: of each other
-        // beam, as many are ahead as a search finds.
-        int rank = 0;
-        for (int b = 0; b < a.width; ++b) {
-            const Continuation *other = all + b * a.picks;
-            int lo = 0, hi = count[b];
-            while (lo < hi) {
-                const int k = (lo + hi) / 2;
-                const uint64_t sum = other[k].sum;
-                if (sum > mine.sum || (sum == mine.sum && b * a.picks + k < i))
-                    lo = k + 1;
-                else
-                    hi = k;
-            }
-            rank += lo;
+    auto write = [&](int r, const Continuation &c) {
+        a.parents[out + r] = c.beam;
+        a.tokens[out + r] = c.token;
+        a.out_scores[out + r] = float(double_of(c.sum));
+    };
+    // Larger sums first, equal ones by beam and then by token.
+    auto ahead = [](const Continuation &x, const Continuation &y) {
+        return x.sum != y.sum ? x.sum > y.sum
+                              : x.beam != y.beam ? x.beam < y.beam : x.token < y.token;
+    };
+    const int n = found;
+    if (n <= kMergeList) {
+        for (int i = mine; i < (n + kSelGroups - 1) / kSelGroups * kSelGroups; i += kSelGroups) {
+            int r = 0;
+            for (int k = sub; i < n && k < n; k += kLanes)
+                r += ahead(list[k], list[i]);
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1)
+                r += __shfl_xor_sync(0xffffffffu, r, d);
+            if (i < n && r < a.picks && sub == 0)
+                write(r, list[i]);
         }
-        if (rank < a.picks) {
-            a.parents[out + rank] = i / a.picks;
-            a.tokens[out + rank] = mine.token;
-            a.out_scores[out + rank] = float(double_of(mine.sum));
+        for (int i = n + threadIdx.x; i < a.picks; i += kMergeThreads) {
+            a.parents[out + i] = 0;
+            a.tokens[out + i] = -1;
+            a.out_scores[out + i] = -INFINITY;
         }
+        return;
     }
-    int total = 0;
-    for (int b = 0; b < a.width; ++b)
-        total += count[b];
-    for (int i = total + threadIdx.x; i < a.picks; i += kMergeThreads) {
-        a.parents[out + i] = 0;
-        a.tokens[out + i] = -1;
-        a.out_scores[out + i] = -INFINITY;
+    // Ties make them too many (and at least `picks`): one after the other, the first of what the
+    // threads have left.
+    Continuation last = {~0ull, -1, -1}, next = last;
+    bool stale = true;
+    for (int r = 0; r < a.picks; ++r) {
+        if (stale) {
+            next = {0, 0, INT32_MAX};
+            for (int i = threadIdx.x; i < all; i += kMergeThreads) {
+                Continuation c;
+                c.sum = sum_of(i, c.beam, c.token);
+                if (c.sum && c.sum >= bar && ahead(last, c) && ahead(c, next))
+                    next = c;
+            }
+        }
+        Continuation best = next;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const Continuation c = {__shfl_xor_sync(0xffffffffu, best.sum, d),
+                                    __shfl_xor_sync(0xffffffffu, best.token, d),
+                                    __shfl_xor_sync(0xffffffffu, best.beam, d)};
+            if (ahead(c, best))
+                best = c;
+        }
+        if (lane == 0)
+            list[warp] = best;
+        __syncthreads();
+        best = list[0];
+        for (int i = 1; i < kMergeWarps; ++i)
+            if (ahead(list[i], best))
+                best = list[i];
+        stale = next.beam == best.beam && next.token == best.token && next.sum == best.sum;
+        if (stale)
+            last = best;
+        if (threadIdx.x == 0)
+            write(r, best);
+        __syncthreads();
     }
 }
 
