@@ -537,8 +537,8 @@ typedef struct kvx_attn_cfg {
  * Every row sees its own position, so no row is empty.  Scores, the softmax statistics and
  * the sums are held in 32 bits; the weights are rounded to 16 bits for the product with V (to
  * `type`, or to half precision over a cache of 8 or 4 bits; in half precision they reach down
- * to 2^-32 of the largest), and the result once to `type`.  The weight of a hidden key is exactly 0,
- * but keys that some row of the request sees must be finite: pages, slots past n_tokens and
+ * to 2^-32 of the largest), and the result once to `type`.  The weight of a hidden key is
+ * exactly 0, but keys that some row of the request sees must be finite: pages, slots past n_tokens and
  * positions that no row sees are never used, whatever they hold (page-table entries for them
  * may be anything).  The same batch gives the same bits every time.  A request's bits depend
  * on its batch: where its keys are cut for the SMs, and which of two kernels takes a few rows
@@ -577,10 +577,10 @@ void kvx_attn_plan_destroy(kvx_attn_plan *plan);
  * as they are and the scales are not used.  For a 4-bit cache a block's scale is the code of
  * e4m3 nearest to its largest magnitude / (6 k_scale), at most 448, and an element becomes the
  * code nearest to element / (scale x k_scale), ties to the even code, beyond +-6 to +-6 (k_scale
- * and v_scale then lie between 2^-100 and 2^100); a block whose scale rounds to 0 is all 0, and one that holds a NaN gets the scale NaN, so that all of
- * it reads as NaN.  Both factors are reciprocals in 32 bits: an element within 2^-22 of a border
- * between two codes may go to either.  Pointers 16-byte aligned, strides multiples of 8
- * elements. */
+ * and v_scale then lie between 2^-100 and 2^100); a block whose scale rounds to 0 is all 0, and
+ * one that holds a NaN gets the scale NaN, so that all of it reads as NaN.  Both factors are
+ * reciprocals in 32 bits: an element within 2^-22 of a border between two codes may go to either.
+ * Pointers 16-byte aligned, strides multiples of 8 elements. */
 kvx_status kvx_append_tokens(const kvx_attn_plan *plan, int layer, const void *k, const void *v,
                              int64_t k_stride, int64_t v_stride, float k_scale, float v_scale,
                              kvx_stream_t stream);
@@ -654,8 +654,8 @@ kvx_status kvx_select_workspace(kvx_ctx *ctx, const kvx_select_cfg *cfg, int64_t
  * finished: its one continuation is done_token with its own sum, and its logits are not read.
  *
  * Continuations are ordered by their sums in 64 bits, equal ones by beam and then by token; the
- * sum of exponentials is taken in 32 bits within 512 x 8 or 512 x 32 logits and in 64 across
- * those, so two sums closer than about 1e-7 may change places.  The same inputs give the same
+ * sum of exponentials is taken in 32 bits within a thread's 8 or 64 logits and in two numbers of
+ * 32 bits across those, so two sums closer than about 1e-7 may change places.  The same inputs give the same
  * bits.  A logit of -infinity rules its token out; one that is NaN or +infinity counts as
  * -infinity.  A beam whose sum is -infinity or NaN, or that has no logit left, has no
  * continuation; where a group has fewer than `picks`, the rest are beam 0, token -1, -infinity.

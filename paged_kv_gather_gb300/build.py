@@ -1,7 +1,8 @@
 """Build libkvx.so (the C-ABI library) in-tree for sm_103a with nvcc.
 
 One object per translation unit, compiled in parallel: the transfer kernels (kvx.cu), page
-upkeep (kvx_pages.cu) and attention (kvx_attend.cu) by nvcc, the host logic (kvx_host.cpp,
+upkeep (kvx_pages.cu), attention (kvx_attend.cu, over a 4-bit cache kvx_attend_four.cu), rotated
+append (kvx_rotate.cu) and beam selection (kvx_beams.cu) by nvcc, the host logic (kvx_host.cpp,
 kvx_cache_host.cpp) and the SM partitioning (kvx_partition.cpp) by the host C++ compiler.
 The CUDA runtime is
 linked statically so the library loads on machines without a GPU (its host logic and

@@ -28,7 +28,8 @@ Kernel kernel_of(const kvx_attn_cfg &c, int64_t token_bytes, int kind, int most_
     if (kind == kMoreRows)
         return few_rows<TYPE, D, 2>(c, token_bytes, most_parts);
     return {reinterpret_cast<const void *>(kvx_attend_tiles_kernel<TYPE, KVX_TYPE_FP_FOUR, D>),
-            TileShape<KVX_TYPE_FP_FOUR, D>::kThreads, 1, size_t(TileShape<KVX_TYPE_FP_FOUR, D>::kBytes),
+            TileShape<KVX_TYPE_FP_FOUR, D>::kThreads, 1,
+            size_t(TileShape<KVX_TYPE_FP_FOUR, D>::kBytes),
             TileShape<KVX_TYPE_FP_FOUR, D>::kSlotFloats,
             reinterpret_cast<const void *>(kvx_attend_join_kernel<TYPE, D>), kJoinThreads,
             kBlockRows / kJoinRows, 0, size_t(TileShape<KVX_TYPE_FP_FOUR, D>::kBytes)};

@@ -33,7 +33,9 @@ namespace {
 // 5300 (both) or 7820 cycles (scores past half the cap), with a cap the tensor pipe active 40 %
 // and the FMA pipe 37 % of them: S is read, shaped and written back one
 // block of 32 columns after the other, and read again for the weights.  Over an e4m3 cache,
-// converted by three warps, it takes 3620; at D = 64 2270, of which 1024 are products.
+// converted by three warps, it takes 3620, over a 4-bit one, converted by six, 3500 (2048 tokens x
+// 4 heads behind 32k 763 us, tensor pipe active 61 %; 700 with no conversion at all); at D = 64
+// 2270, of which 1024 are products.
 // Measured: 2048 new tokens x 8 heads behind 32k tokens (2.13 TFLOP) 1.37 ms on its own and
 // 1.45-1.5 ms in long runs under the power cap (cuBLAS sustains 1.70 PFLOP/s there).  A unit
 // costs about 9000 cycles beside its steps (q in, first scores, O out), which is what short
@@ -581,7 +583,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                                 i % (D / 64) * 128;
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
             }
-            const int codes_at = u.at.head * kRow, units_at = a.kv_heads * kRow + u.at.head * (D / 16);
+            const int codes_at = u.at.head * kRow;
+            const int units_at = a.kv_heads * kRow + u.at.head * (D / 16);
             // Pages of keys lane, lane + 32, ... of a tile, looked up a tile ahead.
             int next[kKeys];
             auto look_up = [&](int i) {
@@ -618,7 +621,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                         const int64_t o = __shfl_sync(0xffffffffu, off[b / kChunks],
                                                       (b % kChunks * 32 + lane) / kChunks);
                         cp_async16(dst + (32 * b + lane) * 16,
-                                   base + (o >= 0 ? o : 0) + codes_at + lane % kChunks * 16, o >= 0);
+                                   base + (o >= 0 ? o : 0) + codes_at + lane % kChunks * 16,
+                                   o >= 0);
                     }
 #pragma unroll
                     for (int k = 0; k < kKeys; ++k)

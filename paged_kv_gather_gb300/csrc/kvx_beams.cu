@@ -4,9 +4,14 @@
 // The logits are read once.  A row (a beam's logits) is cut into parts that a CTA holds in
 // registers: it takes the part's maximum and sum of exponentials, and its `picks` largest logits
 // (equal ones by token).  Those all reach the `picks`-th largest of what 64 groups of threads have
-// as their largest, and hardly more than twice as many logits do: only the few threads that reach
-// it look through their logits again, and rank what they find by counting.  A second kernel, a CTA per group, merges the parts' lists beam by beam and
-// the beams' by their sums in 64 bits.
+// as their largest, and hardly more than twice as many logits do: the CTA looks through the few
+// threads' logits that reach it and ranks what it finds by counting.  A second kernel, a CTA per
+// group, does the same with the parts' lists, by their sums in 64 bits.
+//
+// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 47 us, 118 MB:
+// parts 37 (3.2 TB/s; 29 without candidates, 24 without exponentials either: 14 instructions a
+// logit, and the chain load, maximum, bar, sum), merge 10.  One group of 4 beams
+// over 32k 7.6 us, two launches and their chains.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -126,7 +131,8 @@ kvx_select_parts_kernel(const Select a)
     typedef Logit<TYPE> L;
     typedef typename L::T T;
     constexpr int kVec = 16 / sizeof(T), kVecs = EACH / kVec;
-    constexpr int kPer = 4 / sizeof(T), kWords = EACH / kPer;  // logits of a word, words of a thread
+    constexpr int kPer = 4 / sizeof(T);   // logits of a word
+    constexpr int kWords = EACH / kPer;  // words of a thread
     __shared__ uint64_t list[kSelList];
     __shared__ uint4 rows[kSelRows][kVecs];
     __shared__ int owner[kSelRows];
@@ -598,8 +604,8 @@ kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void 
                             "out_scores or workspace is NULL");
     const int item = cfg->type == KVX_TYPE_FLOAT ? 4 : 2;
     auto bits = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
-    if (bits(logits) % item || (bits(scores) | bits(parents) | bits(tokens) | bits(out_scores)) & 3 ||
-        bits(workspace) & 15)
+    const uintptr_t words = bits(scores) | bits(parents) | bits(tokens) | bits(out_scores);
+    if (bits(logits) % item || words & 3 || bits(workspace) & 15)
         return kvx::set_err(ctx, KVX_ERR_ALIGNMENT, "logits, scores, parents, tokens or "
                             "out_scores not aligned to their elements, or the workspace not to "
                             "16 bytes");

