@@ -533,15 +533,17 @@ kvx_select_merge_kernel(const Select a)
 }
 
 // Logits that a thread holds: 64, so that what a part costs besides its logits (half of the
-// instructions at 32) is met seldom; 8 where there are few rows, so that they still fill the GPU.
-const int kEachMost = 64;
+// instructions at 32) is met seldom, and the merge has few lists; 8 where even those of one group
+// leave the GPU nearly empty (4 beams over 32k 7.5 us instead of 8.3; but 8 beams 11.4 instead of
+// 9.8, and 16 groups of 8 20.6 instead of 10.6).
+const int kEachMost = 64, kFewParts = 16;
 
-int each_of(const kvx_ctx *ctx, const kvx_select_cfg &c)
+int each_of(const kvx_select_cfg &c)
 {
     const int64_t rows = int64_t(c.n_groups) * c.width;
     const int64_t large = (c.vocab + 7 + kEachMost * kSelThreads - 1) / (kEachMost * kSelThreads);
     const int64_t small = (c.vocab + 7 + 8 * kSelThreads - 1) / (8 * kSelThreads);
-    return rows * large < 2 * ctx->num_sms && small <= kMaxParts ? 8 : kEachMost;
+    return rows * large < kFewParts && small <= kMaxParts ? 8 : kEachMost;
 }
 
 int parts_of(const kvx_select_cfg &c, int each)
@@ -583,7 +585,7 @@ kvx_status kvx_select_workspace(kvx_ctx *ctx, const kvx_select_cfg *cfg, int64_t
     const kvx_status st = kvx::validate_select(cfg, ctx->err, sizeof ctx->err);
     if (st != KVX_OK)
         return st;
-    *bytes = int64_t(cfg->n_groups) * cfg->width * parts_of(*cfg, each_of(ctx, *cfg)) *
+    *bytes = int64_t(cfg->n_groups) * cfg->width * parts_of(*cfg, each_of(*cfg)) *
              int64_t(sizeof(PartStats) + cfg->picks * sizeof(uint64_t));
     return KVX_OK;
 }
@@ -620,7 +622,7 @@ kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void 
     kvx::DeviceGuard guard(ctx->device);
     if (!guard.ok)
         return kvx::set_err(ctx, KVX_ERR_CUDA, "cannot make device %d current", ctx->device);
-    const int each = each_of(ctx, *cfg), parts = parts_of(*cfg, each);
+    const int each = each_of(*cfg), parts = parts_of(*cfg, each);
     const int64_t beams = int64_t(cfg->n_groups) * cfg->width;
     if (beams * parts > INT32_MAX)
         return kvx::set_err(ctx, KVX_ERR_CAPACITY, "%lld beams of %d parts", (long long)beams,
