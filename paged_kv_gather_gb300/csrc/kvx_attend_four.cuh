@@ -566,7 +566,10 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                             }
                         }
                 }
-                unsigned p[kHalves][NT][2];
+                // Weights as the second operand, for half-precision outputs in two numbers: rounded
+                // once, weights of short contexts alone would be as far off as the output's type.
+                constexpr int kParts = TYPE == KVX_TYPE_HALF ? 2 : 1;
+                unsigned p[kParts][kHalves][NT][2];
 #pragma unroll
                 for (int u = 0; u < kHalves; ++u)
 #pragma unroll
@@ -576,8 +579,17 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                             s[u][n][x] = exp2_(s[u][n][x]);
                             l[n][x & 1] += s[u][n][x];
                         }
-                        p[u][n][0] = transpose8x8(P::pack(s[u][n][0], s[u][n][1]));
-                        p[u][n][1] = transpose8x8(P::pack(s[u][n][2], s[u][n][3]));
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const float lo = s[u][n][2 * b], hi = s[u][n][2 * b + 1];
+                            const unsigned w = P::pack(lo, hi);
+                            p[0][u][n][b] = transpose8x8(w);
+                            if constexpr (kParts == 2) {
+                                const __half *h = reinterpret_cast<const __half *>(&w);
+                                p[1][u][n][b] = transpose8x8(
+                                    P::pack(lo - P::load(h[0]), hi - P::load(h[1])));
+                            }
+                        }
                     }
 
                 // V of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9: elements quad D / 8 and on.  A key
@@ -621,7 +633,9 @@ kvx_attend_four_kernel(const Attend a, const Work w)
                                 mul_half2(__byte_perm(h[2][x], h[3][x], 0x7632), unit1)};
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                mma_half(o[n][4 * g + x], k, p[u][n][0], p[u][n][1]);
+#pragma unroll
+                                for (int y = 0; y < kParts; ++y)
+                                    mma_half(o[n][4 * g + x], k, p[y][u][n][0], p[y][u][n][1]);
                         }
                     }
                 }
