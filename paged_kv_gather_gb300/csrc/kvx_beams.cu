@@ -393,6 +393,17 @@ kvx_select_merge_kernel(const Select a)
     constexpr int kLanes = kMergeThreads / kSelGroups;
     const int group = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier_work();
+    // Candidate i: of beam b, key i - b per_beam of its parts' lists.  A thread's first few stay
+    // in registers and are on their way before the norms.
+    constexpr int kKept = 2;
+    const int per_beam = a.parts * a.picks, all = a.width * per_beam;
+    const uint64_t *keys = a.keys + int64_t(group) * all;
+    uint64_t kept[kKept];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int i = threadIdx.x + k * kMergeThreads;
+        kept[k] = i < all ? keys[i] : 0;
+    }
     for (int b = warp; b < a.width; b += kMergeWarps) {
         const int beam = group * a.width + b;
         const int kind = !has_continuations(a, beam) ? 0 : a.done && a.done[beam] ? 2 : 1;
@@ -417,24 +428,29 @@ kvx_select_merge_kernel(const Select a)
         found = 0;
     __syncthreads();
 
-    // Candidate i: of beam b, key i - b per_beam of its parts' lists.  0: none.
-    const int per_beam = a.parts * a.picks, all = a.width * per_beam;
-    const uint64_t *keys = a.keys + int64_t(group) * all;
-    auto sum_of = [&](int i, int &b, int32_t &token) -> uint64_t {
+    // The sum of candidate i with this key, as an ordered number; 0: there is none.
+    auto sum_of = [&](int i, uint64_t key, int &b, int32_t &token) -> uint64_t {
         b = i / per_beam;
         if (state[b] == 2) {
             token = a.done_token;
             return i == b * per_beam ? order_of(so_far[b]) : 0;
         }
-        const uint64_t key = state[b] ? keys[i] : 0;
         token = int32_t(~unsigned(key));
-        return key ? order_of(so_far[b] + (double(float_of(unsigned(key >> 32))) - norms[b])) : 0;
+        return state[b] && key
+                   ? order_of(so_far[b] + (double(float_of(unsigned(key >> 32))) - norms[b])) : 0;
     };
+    uint64_t sums[kKept];
     int b;
     int32_t token;
     uint64_t top = 0;
-    for (int i = threadIdx.x; i < all; i += kMergeThreads)
-        top = max(top, sum_of(i, b, token));
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int i = threadIdx.x + k * kMergeThreads;
+        sums[k] = i < all ? sum_of(i, kept[k], b, token) : 0;
+        top = max(top, sums[k]);
+    }
+    for (int i = threadIdx.x + kKept * kMergeThreads; i < all; i += kMergeThreads)
+        top = max(top, sum_of(i, keys[i], b, token));
 #pragma unroll
     for (int d = 1; d < kLanes; d <<= 1)
         top = max(top, uint64_t(__shfl_xor_sync(0xffffffffu, top, d)));
@@ -454,13 +470,21 @@ kvx_select_merge_kernel(const Select a)
     if (sub == 0 && rank == a.picks - 1)
         bar = top;
     __syncthreads();
-    for (int i = threadIdx.x; i < all; i += kMergeThreads) {
-        const uint64_t sum = sum_of(i, b, token);
-        if (sum && sum >= bar) {
-            const int at = atomicAdd(&found, 1);
-            if (at < kMergeList)
-                list[at] = {sum, token, b};
+    auto take = [&](uint64_t sum, int32_t token, int b) {
+        const int at = atomicAdd(&found, 1);
+        if (at < kMergeList)
+            list[at] = {sum, token, b};
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+        if (sums[k] && sums[k] >= bar) {
+            sum_of(threadIdx.x + k * kMergeThreads, kept[k], b, token);
+            take(sums[k], token, b);
         }
+    for (int i = threadIdx.x + kKept * kMergeThreads; i < all; i += kMergeThreads) {
+        const uint64_t sum = sum_of(i, keys[i], b, token);
+        if (sum && sum >= bar)
+            take(sum, token, b);
     }
     __syncthreads();
     const int64_t out = int64_t(group) * a.picks;
@@ -502,7 +526,7 @@ kvx_select_merge_kernel(const Select a)
             next = {0, 0, INT32_MAX};
             for (int i = threadIdx.x; i < all; i += kMergeThreads) {
                 Continuation c;
-                c.sum = sum_of(i, c.beam, c.token);
+                c.sum = sum_of(i, keys[i], c.beam, c.token);
                 if (c.sum && c.sum >= bar && ahead(last, c) && ahead(c, next))
                     next = c;
             }
