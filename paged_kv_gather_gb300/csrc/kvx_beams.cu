@@ -8,10 +8,9 @@
 // threads' logits that reach it and ranks what it finds by counting.  A second kernel, a CTA per
 // group, does the same with the parts' lists, by their sums in 64 bits.
 //
-// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 47 us, 118 MB:
+// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 45 us, 118 MB:
 // parts 37 (3.2 TB/s; 29 without candidates, 24 without exponentials either: 14 instructions a
-// logit, and the chain load, maximum, bar, sum), merge 10.  One group of 4 beams
-// over 32k 7.6 us, two launches and their chains.
+// logit, and the chain load, maximum, bar, sum), merge 8.  One group of 4 beams over 32k 7.1 us, two launches and their chains.
 #include <cuda_runtime.h>
 
 #include <algorithm>
