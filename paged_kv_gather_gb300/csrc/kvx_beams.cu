@@ -10,7 +10,8 @@
 //
 // Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 45 us, 118 MB:
 // parts 37 (3.2 TB/s; 29 without candidates, 24 without exponentials either: 14 instructions a
-// logit, and the chain load, maximum, bar, sum), merge 8.  One group of 4 beams over 32k 7.1 us, two launches and their chains.
+// logit, and the chain load, maximum, bar, sum), merge 8.  One group of 4 beams
+// over 32k 7.1 us, two launches and their chains.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -217,9 +218,12 @@ kvx_select_parts_kernel(const Select a)
         float sum = 0.0f;
         if (top > -INFINITY) {
             // The exponents x log2 e - round(m log2 e) come out of one operation; what the
-            // rounding moves them by is the same for all and goes into the sum at the end.
-            const float base = m * kLog2e, off = fmaf(m, kLog2e, -base);
-            const uint64_t less = pair_of(-base, -base), log2e = pair_of(kLog2e, kLog2e);
+            // rounding moves them by is the same for all and goes into the sum at the end.  A
+            // part of mask values alone may have them as large as the type goes: past 2^30 logits
+            // are alike or at least 64 apart, and 2^(x - m) does as well, without overflow.
+            const float unit = fabsf(m) > 0x1p30f ? 1.0f : kLog2e;
+            const float base = m * unit, off = fmaf(m, unit, -base);
+            const uint64_t less = pair_of(-base, -base), log2e = pair_of(unit, unit);
             uint64_t both[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < EACH; i += 2) {
@@ -227,7 +231,8 @@ kvx_select_parts_kernel(const Select a)
                 both[i >> 1 & 1] = add_pair(both[i >> 1 & 1], pair_of(exp2_(x.x), exp2_(x.y)));
             }
             const float2 x = halves_of(add_pair(both[0], both[1]));
-            sum = (x.x + x.y) * fmaf(off, -kLn2, 1.0f);
+            // The rounding, 64 at most, to first order where the second is below 2^-25.
+            sum = (x.x + x.y) * (fabsf(off) < 0x1p-12f ? fmaf(off, -kLn2, 1.0f) : exp2f(-off));
         }
         // NaN, or +infinity, which the sum is NaN with too: taken out, once.
         if (!again && !(sum < INFINITY))
@@ -413,8 +418,9 @@ kvx_select_merge_kernel(const Select a)
         // exp(max - m): what the difference is rounded by goes in to first order.
         const double away = part.sum > 0.0f ? double(part.max) - m : 0.0;
         const float near = float(away);
-        const double mine = (double(part.sum) + part.more) *
-                            (double(expf(near)) * (1.0 + (away - near)));
+        const double mine = near < -200.0f ? 0.0  // and what follows may be 0 times infinity
+                                           : (double(part.sum) + part.more) *
+                                                 (double(expf(near)) * (1.0 + (away - near)));
         const float hi = float(mine);
         const float2 s = warp_sum(hi, float(mine - hi));
         if (lane == 0) {

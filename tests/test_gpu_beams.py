@@ -195,6 +195,31 @@ def test_masks_infinities_and_nan(ctx, dtype, vocab):
     assert tokens[0].tolist() == [3, 9, 20]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("mask", [-1e6, -1e9, -1e12, "lowest"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_mask_values_of_whole_parts(ctx, dtype, mask, groups):
+    """Finite mask values everywhere but at a few tokens: whatever of a row a CTA takes, some have
+    nothing else.  One beam of each group has nothing but mask values, one the largest of all."""
+    vocab = 40000
+    value = torch.finfo(TORCH[dtype]).min if mask == "lowest" else mask
+    x, s = make(groups, 4, vocab, dtype, 8)
+    y = torch.full_like(x, value)
+    y[:, 17000:17100] = x[:, 17000:17100]
+    y[1::4] = value
+    y[3::4, 50] = -value
+    check_selection(select(ctx, y, s, 8, dtype), y, s, 8)
+
+
+@pytest.mark.parametrize("at", [3e4, -3e4, 1e6, -1e6, 3e7, -1e9])
+def test_logits_far_from_zero(ctx, at):
+    """All logits around `at`.  Near 2^20 the sum's correction is an exponential of its own, 2^-22
+    off: within what a beam's sum is compared by, 2^-22 and 2^-24 of its size (about 10)."""
+    x, s = make(2, 3, 30000, "fp32", 9)
+    x = x.double().add(at).float()
+    check_selection(select(ctx, x, s, 6, "fp32"), x, s, 6)
+
+
 def test_done_beams(ctx):
     x, s = make(4, 5, 3001, "bf16", 6)
     done = torch.zeros((4, 5), dtype=torch.uint8, device="cuda")
