@@ -536,11 +536,11 @@ typedef struct kvx_attn_cfg {
  *     out = v_scale * sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j).
  * Every row sees its own position, so no row is empty.  Scores, the softmax statistics and
  * the sums are held in 32 bits; the weights are rounded to 16 bits for the product with V (to
- * `type`, or to half precision over a cache of 8 or 4 bits; in half precision they reach down
- * to 2^-32 of the largest), and the result once to `type`.  The weight of a hidden key is
- * exactly 0, but keys that some row of the request sees must be finite: pages, slots past n_tokens and
- * positions that no row sees are never used, whatever they hold (page-table entries for them
- * may be anything).  The same batch gives the same bits every time.  A request's bits depend
+ * `type`, or to half precision over a cache of 8 or 4 bits, some finer; in half precision they
+ * reach down to 2^-32 of the largest), and the result once to `type`.  The weight of a hidden key
+ * is exactly 0, but keys that some row of the request sees must be finite: pages, slots past
+ * n_tokens and positions that no row sees are never used, whatever they hold (page-table entries
+ * for them may be anything).  The same batch gives the same bits every time.  A request's bits depend
  * on its batch: where its keys are cut for the SMs, and which of two kernels takes a few rows
  * beside chunks, follow from all of it, and move results within the roundings above.
  *
