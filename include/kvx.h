@@ -540,9 +540,9 @@ typedef struct kvx_attn_cfg {
  * reach down to 2^-32 of the largest), and the result once to `type`.  The weight of a hidden key
  * is exactly 0, but keys that some row of the request sees must be finite: pages, slots past
  * n_tokens and positions that no row sees are never used, whatever they hold (page-table entries
- * for them may be anything).  The same batch gives the same bits every time.  A request's bits depend
- * on its batch: where its keys are cut for the SMs, and which of two kernels takes a few rows
- * beside chunks, follow from all of it, and move results within the roundings above.
+ * for them may be anything).  The same batch gives the same bits every time.  A request's bits
+ * depend on its batch: where its keys are cut for the SMs, and which of two kernels takes a few
+ * rows beside chunks, follow from all of it, and move results within the roundings above.
  *
  * A plan holds a step's batch on the device, for every layer of the step and any number of
  * launches: it is made once (kvx_attn_plan_create allocates), refilled for the next step with
@@ -655,9 +655,10 @@ kvx_status kvx_select_workspace(kvx_ctx *ctx, const kvx_select_cfg *cfg, int64_t
  *
  * Continuations are ordered by their sums in 64 bits, equal ones by beam and then by token; the
  * sum of exponentials is taken in 32 bits within a thread's 8 or 64 logits and in two numbers of
- * 32 bits across those, so two sums closer than about 1e-7 may change places.  The same inputs give the same
- * bits.  A logit of -infinity rules its token out; one that is NaN or +infinity counts as
- * -infinity.  A beam whose sum is -infinity or NaN, or that has no logit left, has no
+ * 32 bits across those, so two beams' sums closer than about 1e-7 (5e-7 where logits are in the
+ * thousands) may change places.  The same inputs give the same bits.  A logit of -infinity rules
+ * its token out, one of the type's lowest value or another mask value counts as it is; one that is
+ * NaN or +infinity counts as -infinity.  A beam whose sum is -infinity or NaN, or that has no logit left, has no
  * continuation; where a group has fewer than `picks`, the rest are beam 0, token -1, -infinity.
  * Logits, scores, parents, tokens and out_scores are aligned to their elements; out_scores may be
  * scores where picks = width.  Two kernel launches on `stream`; they may be captured. */
