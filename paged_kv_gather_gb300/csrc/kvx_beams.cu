@@ -8,8 +8,8 @@
 // threads' logits that reach it and ranks what it finds by counting.  A second kernel, a CTA per
 // group, does the same with the parts' lists, by their sums in 64 bits.
 //
-// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 45 us, 118 MB:
-// parts 37 (3.2 TB/s; 29 without candidates, 24 without exponentials either: 14 instructions a
+// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 44 us, 118 MB:
+// parts 36 (3.3 TB/s; 28 without candidates, 24 without exponentials either: 14 instructions a
 // logit, and the chain load, maximum, bar, sum), merge 8.  One group of 4 beams
 // over 32k 7.1 us, two launches and their chains.
 #include <cuda_runtime.h>
@@ -124,6 +124,16 @@ __device__ __forceinline__ float2 warp_sum(float hi, float lo)
     return make_float2(hi, lo);
 }
 
+// A warp's sum of numbers in [0, 64.1] as integers, which are added in one operation each and in
+// any order: in 2^-15, and what that leaves in 2^-38.
+__device__ __forceinline__ int2 sum_of_warp(float x)
+{
+    constexpr float kUnit = 384.0f, kRest = 1.5f / 32768;  // numbers near these are that far apart
+    const float whole = x + kUnit, rest = x - (whole - kUnit) + kRest;
+    return make_int2(__reduce_add_sync(0xffffffffu, __float_as_int(whole) - __float_as_int(kUnit)),
+                     __reduce_add_sync(0xffffffffu, __float_as_int(rest) - __float_as_int(kRest)));
+}
+
 template <int TYPE, int EACH>
 __global__ void __launch_bounds__(kSelThreads, EACH * sizeof(typename Logit<TYPE>::T) > 128 ? 2 : 4)
 kvx_select_parts_kernel(const Select a)
@@ -136,9 +146,9 @@ kvx_select_parts_kernel(const Select a)
     __shared__ uint64_t list[kSelList];
     __shared__ uint4 rows[kSelRows][kVecs];
     __shared__ int owner[kSelRows];
-    __shared__ __align__(16) float tops[kSelGroups];
-    __shared__ float2 sums[kSelWarps];
-    __shared__ float reach;  // the `picks`-th largest of `tops`
+    __shared__ uint4 tops[kSelGroups / 4], maxima[kSelWarps / 4];  // order_of, of groups and warps
+    __shared__ int2 sums[kSelWarps];
+    __shared__ unsigned reach;  // the largest that `picks` of `tops` reach
     __shared__ int found, reached, odd;
     const int beam = blockIdx.x / a.parts, part = blockIdx.x - beam * a.parts;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -192,28 +202,38 @@ kvx_select_parts_kernel(const Select a)
         for (int d = 1; d < kLanes; d <<= 1)
             group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, d));
         const int mine = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
+        const unsigned own = order_of(group);
+        const unsigned most = __reduce_max_sync(0xffffffffu, own);
         if (sub == 0)
-            tops[mine] = group;
+            reinterpret_cast<unsigned *>(tops)[mine] = own;
+        if (lane == 0)
+            reinterpret_cast<unsigned *>(maxima)[warp] = most;
         if (threadIdx.x == 0)
-            found = reached = odd = 0;
+            found = reached = odd = 0, reach = 0;
         __syncthreads();
-        // The largest of all, and the rank of the own group's largest, by its threads together.
-        // At least `picks` logits reach the one of rank `picks` - 1.
+        // The largest of all, and how many groups' largest reach the own, by its threads together.
+        unsigned all = 0;
+#pragma unroll
+        for (int k = 0; k < kSelWarps / 4; ++k) {
+            const uint4 f = maxima[k];
+            all = max(all, max(max(f.x, f.y), max(f.z, f.w)));
+        }
+        m = float_of(all);
         int rank = 0;
-        m = group;
 #pragma unroll
-        for (int k = 0; k < kSelGroups / kLanes; ++k) {
-            const float f = tops[k * kLanes + sub];
-            m = fmaxf(m, f);
-            rank += f > group || (f == group && k * kLanes + sub < mine);
+        for (int k = 0; k < kSelGroups / 4 / kLanes; ++k) {
+            const uint4 f = tops[k * kLanes + sub];
+            rank += f.x >= own;
+            rank += f.y >= own;
+            rank += f.z >= own;
+            rank += f.w >= own;
         }
 #pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) {
+        for (int d = 1; d < kLanes; d <<= 1)
             rank += __shfl_xor_sync(0xffffffffu, rank, d);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        }
-        if (sub == 0 && rank == a.picks - 1)
-            reach = group;
+        const unsigned reaches = __reduce_max_sync(0xffffffffu, rank >= a.picks ? own : 0u);
+        if (lane == 0)
+            atomicMax(&reach, reaches);
         // A thread without a logit has no part in the sum (and -infinity less itself is NaN).
         float sum = 0.0f;
         if (top > -INFINITY) {
@@ -237,11 +257,11 @@ kvx_select_parts_kernel(const Select a)
         // NaN, or +infinity, which the sum is NaN with too: taken out, once.
         if (!again && !(sum < INFINITY))
             odd = 1;
-        const float2 s = warp_sum(sum, 0.0f);
+        const int2 s = sum_of_warp(sum);
         if (lane == 0)
             sums[warp] = s;
         __syncthreads();
-        bar = reach;
+        bar = float_of(reach);
         if (again || !odd)
             break;
         __syncthreads();
@@ -337,10 +357,13 @@ kvx_select_parts_kernel(const Select a)
         }
     }
     if (warp == 0) {
-        const float2 s = lane < kSelWarps ? sums[lane] : make_float2(0.0f, 0.0f);
-        const float2 all = warp_sum(s.x, s.y);
+        const int2 s = lane < kSelWarps ? sums[lane] : make_int2(0, 0);
+        const int whole = __reduce_add_sync(0xffffffffu, s.x);  // up to 2^29
+        const int rest = __reduce_add_sync(0xffffffffu, s.y);
         if (lane == 0)
-            a.stats[int64_t(beam) * a.parts + part] = {all.x, all.y, m, 0.0f};
+            a.stats[int64_t(beam) * a.parts + part] = {
+                float(whole & ~31) * 0x1p-15f,
+                fmaf(float(rest), 0x1p-38f, float(whole & 31) * 0x1p-15f), m, 0.0f};
     }
 }
 
