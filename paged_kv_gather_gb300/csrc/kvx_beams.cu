@@ -9,9 +9,8 @@
 // group, does the same with the parts' lists, by their sums in 64 bits.
 //
 // Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 44 us, 118 MB:
-// parts 36 (3.3 TB/s; 28 without candidates, 24 without exponentials either: 14 instructions a
-// logit, and the chain load, maximum, bar, sum), merge 8.  One group of 4 beams
-// over 32k 7.1 us, two launches and their chains.
+// parts 36 (3.3 TB/s; a fifth of it candidates, an eighth exponentials, and the chain load,
+// maximum, bar, sum), merge 8.  One group of 4 beams over 32k 7.1 us, two launches and their chains.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -305,7 +304,19 @@ kvx_select_parts_kernel(const Select a)
     __syncthreads();
     const int n = all_rows > kSelRows ? kSelList + 1 : found;
     uint64_t *out = a.keys + (int64_t(beam) * a.parts + part) * a.picks;
-    if (n <= kSelList) {
+    if (n <= kSelGroups) {  // as usual: the other warps are done
+        if (threadIdx.x < n) {
+            const uint64_t key = list[threadIdx.x];
+            int rank = 0;
+#pragma unroll 4
+            for (int k = 0; k < n; ++k)
+                rank += list[k] > key;
+            if (rank < a.picks)
+                out[rank] = key;
+        } else if (threadIdx.x < a.picks) {
+            out[threadIdx.x] = 0;
+        }
+    } else if (n <= kSelList) {
         for (int i = threadIdx.x / kLanes; i < (n + kSelGroups - 1) / kSelGroups * kSelGroups;
              i += kSelGroups) {
             const uint64_t key = i < n ? list[i] : 0;
@@ -318,8 +329,6 @@ kvx_select_parts_kernel(const Select a)
             if (i < n && rank < a.picks && threadIdx.x % kLanes == 0)
                 out[rank] = key;
         }
-        for (int i = n + threadIdx.x; i < a.picks; i += kSelThreads)
-            out[i] = 0;
     } else {
         // Ties make them too many: one after the other, the largest of what the threads have left.
         uint64_t last = ~0ull;  // of this thread's, the one taken last
