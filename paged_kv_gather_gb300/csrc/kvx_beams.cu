@@ -8,9 +8,9 @@
 // threads' logits that reach it and ranks what it finds by counting.  A second kernel, a CTA per
 // group, does the same with the parts' lists, by their sums in 64 bits.
 //
-// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 44 us, 118 MB:
-// parts 36 (3.3 TB/s; a fifth of it candidates, an eighth exponentials, and the chain load,
-// maximum, bar, sum), merge 8.  One group of 4 beams over 32k 7.1 us, two launches and their chains.
+// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 42 us, 118 MB:
+// parts 35 (3.4 TB/s; a fifth of it candidates, an eighth exponentials, and the chain load,
+// maximum, bar, sum), merge 7.  One group of 4 beams over 32k 6.5 us, two launches and their chains.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -84,9 +84,13 @@ __device__ __forceinline__ uint64_t key_of(float x, int token)
     return uint64_t(order_of(x + 0.0f)) << 32 | unsigned(~token);
 }
 
-__device__ __forceinline__ bool has_continuations(const Select &a, int beam)
+// What continues a beam: 0 nothing (not where its score is NaN either), 1 its logits, 2 itself.
+// Both are asked for at once.
+__device__ __forceinline__ int kind_of(const Select &a, int beam)
 {
-    return a.scores[beam] > -INFINITY;  // not NaN either
+    const float score = __ldcg(a.scores + beam);
+    const int done = a.done ? __ldcg(a.done + beam) : 0;
+    return !(score > -INFINITY) ? 0 : done ? 2 : 1;
 }
 
 // The larger of each of two logits, and the largest of a unit of 16 bytes; NaN is passed over.
@@ -152,7 +156,7 @@ kvx_select_parts_kernel(const Select a)
     const int beam = blockIdx.x / a.parts, part = blockIdx.x - beam * a.parts;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier_work();
-    if ((a.done && a.done[beam]) || !has_continuations(a, beam))
+    if (kind_of(a, beam) != 1)
         return;
 
     // 16-byte units of the row, the first and last of them partly outside it.
@@ -442,10 +446,11 @@ kvx_select_merge_kernel(const Select a)
     }
     for (int b = warp; b < a.width; b += kMergeWarps) {
         const int beam = group * a.width + b;
-        const int kind = !has_continuations(a, beam) ? 0 : a.done && a.done[beam] ? 2 : 1;
-        PartStats part = {0.0f, 0.0f, -INFINITY, 0.0f};
-        if (kind == 1 && lane < a.parts)
-            part = a.stats[int64_t(beam) * a.parts + lane];
+        // Without logits that count there is nothing there, but it is asked for at once too.
+        PartStats part = a.stats[int64_t(beam) * a.parts + min(lane, a.parts - 1)];
+        const int kind = kind_of(a, beam);
+        if (kind != 1 || lane >= a.parts)
+            part = {0.0f, 0.0f, -INFINITY, 0.0f};
         const float m = float_of(__reduce_max_sync(0xffffffffu, order_of(part.max)));
         // exp(max - m): what the difference is rounded by goes in to first order.
         const double away = part.sum > 0.0f ? double(part.max) - m : 0.0;
