@@ -419,15 +419,18 @@ struct Continuation {
     int32_t token, beam;
 };
 
-// Norms first, a warp per beam: score + logit - norm is a continuation's sum.  Then the largest
-// `picks` sums of all the beams' lists in the way of the parts' kernel: those that reach the
-// `picks`-th largest of what 64 groups of threads have, ranked by counting.
+// Norms first, a warp per beam.  A continuation's sum is (logit - m) + (score - log s) with the
+// beam's largest logit m and s the sum of exp(logit - m): m + log s in one number would round
+// log s away where m is a large mask value, and a beam of mask values alone has nothing else.  Then
+// the largest `picks` sums of all the beams' lists in the way of the parts' kernel: those that reach
+// the `picks`-th largest of what 64 groups of threads have, ranked by counting.
 __global__ void __launch_bounds__(kMergeThreads)
 kvx_select_merge_kernel(const Select a)
 {
     __shared__ Continuation list[kMergeList];
     __shared__ uint64_t tops[kSelGroups], bar;
-    __shared__ double norms[KVX_MAX_BEAMS], so_far[KVX_MAX_BEAMS];
+    __shared__ double bases[KVX_MAX_BEAMS];   // score - log s; the score alone of a beam that is done
+    __shared__ float largest[KVX_MAX_BEAMS];  // m
     __shared__ int state[KVX_MAX_BEAMS];  // 0: no continuations, 1: lists, 2: itself
     __shared__ int found;
     constexpr int kLanes = kMergeThreads / kSelGroups;
@@ -462,8 +465,8 @@ kvx_select_merge_kernel(const Select a)
         const float2 s = warp_sum(hi, float(mine - hi));
         if (lane == 0) {
             state[b] = kind;
-            so_far[b] = a.scores[beam];
-            norms[b] = m + log_of(double(s.x) + s.y);
+            largest[b] = m;
+            bases[b] = a.scores[beam] - (kind == 1 ? log_of(double(s.x) + s.y) : 0.0);
         }
     }
     if (threadIdx.x == 0)
@@ -475,11 +478,11 @@ kvx_select_merge_kernel(const Select a)
         b = i / per_beam;
         if (state[b] == 2) {
             token = a.done_token;
-            return i == b * per_beam ? order_of(so_far[b]) : 0;
+            return i == b * per_beam ? order_of(bases[b]) : 0;
         }
         token = int32_t(~unsigned(key));
         return state[b] && key
-                   ? order_of(so_far[b] + (double(float_of(unsigned(key >> 32))) - norms[b])) : 0;
+                   ? order_of(bases[b] + (double(float_of(unsigned(key >> 32))) - largest[b])) : 0;
     };
     uint64_t sums[kKept];
     int b;
