@@ -29,6 +29,7 @@ const int kMergeList = 512;    // continuations that are ranked, before ties are
 const int kMaxParts = 32;      // of a row: a lane each when they are merged
 const int kMergeWarps = KVX_MAX_BEAMS / 2;
 const int kMergeThreads = 32 * kMergeWarps;
+static_assert(kMergeList == kMergeThreads, "a candidate per thread fits the list");
 
 struct PartStats {
     float sum, more;  // of exp(logit - max), in two numbers
@@ -424,6 +425,15 @@ struct Continuation {
 // log s away where m is a large mask value, and a beam of mask values alone has nothing else.  Then
 // the largest `picks` sums of all the beams' lists in the way of the parts' kernel: those that reach
 // the `picks`-th largest of what 64 groups of threads have, ranked by counting.
+//
+// FEW: the list holds all candidates, each thread has one, and they stay in order, in as few warps
+// as there can be, because their sums are 64-bit arithmetic.  More of them are spread: a thread's
+// k-th is one of 64 in a row, another place in every row.  Lists are sorted, and a group of threads
+// that had the same ranks of all of them would have a largest far below what it should be (16 beams,
+// 32 picks: 380 candidates reached such a bar, 40 reach this one; 32 beams, 64 picks: 5000 and 180;
+// one group of 16 beams over 500k with 32 picks 448 us and 61).  Rows turn by 64 / the golden ratio,
+// which spreads the places that a group has had evenly, however many rows.
+template <bool FEW>
 __global__ void __launch_bounds__(kMergeThreads)
 kvx_select_merge_kernel(const Select a)
 {
@@ -438,13 +448,20 @@ kvx_select_merge_kernel(const Select a)
     wait_for_earlier_work();
     // Candidate i: of beam b, key i - b per_beam of its parts' lists.  A thread's first few stay
     // in registers and are on their way before the norms.
-    constexpr int kKept = 2;
+    constexpr int kKept = FEW ? 1 : 2, kTurn = 39;
+    const int mine = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
     const int per_beam = a.parts * a.picks, all = a.width * per_beam;
+    const int rounds = FEW ? 1 : (all + kMergeThreads - 1) / kMergeThreads;
+    auto candidate = [&](int k) {
+        const int r = k * kLanes + sub;
+        return FEW ? int(threadIdx.x)
+                   : r * kSelGroups + ((mine + kTurn * r) & (kSelGroups - 1));
+    };
     const uint64_t *keys = a.keys + int64_t(group) * all;
     uint64_t kept[kKept];
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
-        const int i = threadIdx.x + k * kMergeThreads;
+        const int i = candidate(k);
         kept[k] = i < all ? keys[i] : 0;
     }
     for (int b = warp; b < a.width; b += kMergeWarps) {
@@ -458,11 +475,11 @@ kvx_select_merge_kernel(const Select a)
         // exp(max - m): what the difference is rounded by goes in to first order.
         const double away = part.sum > 0.0f ? double(part.max) - m : 0.0;
         const float near = float(away);
-        const double mine = near < -200.0f ? 0.0  // and what follows may be 0 times infinity
-                                           : (double(part.sum) + part.more) *
-                                                 (double(expf(near)) * (1.0 + (away - near)));
-        const float hi = float(mine);
-        const float2 s = warp_sum(hi, float(mine - hi));
+        const double scaled = near < -200.0f ? 0.0  // and what follows may be 0 times infinity
+                                             : (double(part.sum) + part.more) *
+                                                   (double(expf(near)) * (1.0 + (away - near)));
+        const float hi = float(scaled);
+        const float2 s = warp_sum(hi, float(scaled - hi));
         if (lane == 0) {
             state[b] = kind;
             largest[b] = m;
@@ -490,16 +507,18 @@ kvx_select_merge_kernel(const Select a)
     uint64_t top = 0;
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
-        const int i = threadIdx.x + k * kMergeThreads;
+        const int i = candidate(k);
         sums[k] = i < all ? sum_of(i, kept[k], b, token) : 0;
         top = max(top, sums[k]);
     }
-    for (int i = threadIdx.x + kKept * kMergeThreads; i < all; i += kMergeThreads)
-        top = max(top, sum_of(i, keys[i], b, token));
+    for (int k = kKept; k < rounds; ++k) {
+        const int i = candidate(k);
+        if (i < all)
+            top = max(top, sum_of(i, keys[i], b, token));
+    }
 #pragma unroll
     for (int d = 1; d < kLanes; d <<= 1)
         top = max(top, uint64_t(__shfl_xor_sync(0xffffffffu, top, d)));
-    const int mine = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
     if (sub == 0)
         tops[mine] = top;
     __syncthreads();
@@ -523,11 +542,12 @@ kvx_select_merge_kernel(const Select a)
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
         if (sums[k] && sums[k] >= bar) {
-            sum_of(threadIdx.x + k * kMergeThreads, kept[k], b, token);
+            sum_of(candidate(k), kept[k], b, token);
             take(sums[k], token, b);
         }
-    for (int i = threadIdx.x + kKept * kMergeThreads; i < all; i += kMergeThreads) {
-        const uint64_t sum = sum_of(i, keys[i], b, token);
+    for (int k = kKept; k < rounds; ++k) {
+        const int i = candidate(k);
+        const uint64_t sum = i < all ? sum_of(i, keys[i], b, token) : 0;
         if (sum && sum >= bar)
             take(sum, token, b);
     }
@@ -544,7 +564,7 @@ kvx_select_merge_kernel(const Select a)
                               : x.beam != y.beam ? x.beam < y.beam : x.token < y.token;
     };
     const int n = found;
-    if (n <= kMergeList) {
+    if (FEW || n <= kMergeList) {
         for (int i = mine; i < (n + kSelGroups - 1) / kSelGroups * kSelGroups; i += kSelGroups) {
             int r = 0;
             for (int k = sub; i < n && k < n; k += kLanes)
@@ -562,8 +582,8 @@ kvx_select_merge_kernel(const Select a)
         }
         return;
     }
-    // Ties make them too many (and at least `picks`): one after the other, the first of what the
-    // threads have left.
+    // Equal sums make them too many (and at least `picks`): one after the other, the first of what
+    // the threads have left.
     Continuation last = {~0ull, -1, -1}, next = last;
     bool stale = true;
     for (int r = 0; r < a.picks; ++r) {
@@ -707,8 +727,10 @@ kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void 
                                                     : parts_kernel<KVX_TYPE_FLOAT>(each);
     cudaError_t e = launch(fn, beams * parts, kSelThreads, s, args);
     if (e == cudaSuccess)
-        e = launch(reinterpret_cast<const void *>(kvx_select_merge_kernel), cfg->n_groups,
-                   kMergeThreads, s, args);
+        e = launch(cfg->width * parts * cfg->picks <= kMergeList
+                       ? reinterpret_cast<const void *>(kvx_select_merge_kernel<true>)
+                       : reinterpret_cast<const void *>(kvx_select_merge_kernel<false>),
+                   cfg->n_groups, kMergeThreads, s, args);
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "selection launch");
     ctx->last_items = beams;
