@@ -3,10 +3,12 @@
 //
 // The logits are read once.  A row (a beam's logits) is cut into parts that a CTA holds in
 // registers: it takes the part's maximum and sum of exponentials, and its `picks` largest logits
-// (equal ones by token).  Those all reach the `picks`-th largest of what 64 groups of threads have
-// as their largest, and hardly more than twice as many logits do: the CTA looks through the few
-// threads' logits that reach it and ranks what it finds by counting.  A second kernel, a CTA per
-// group, does the same with the parts' lists, by their sums in 64 bits.
+// (equal ones by token).  Those all reach the `picks`-th largest of what 64 or 128 groups of threads
+// have as their largest, and without ties hardly more than 1.4 times as many logits do: the CTA
+// looks through the few threads' logits that reach it and ranks what it finds by counting.  A second
+// kernel, a CTA per group, does the same with the parts' lists, by their sums in 64 bits.  Where
+// ties make candidates too many for a list (a row of one value, a part of one mask value), the
+// largest are taken one after the other, which takes a part several us for each.
 //
 // Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 42 us, 118 MB:
 // parts 35 (3.4 TB/s; a fifth of it candidates, an eighth exponentials, and the chain load,
@@ -22,9 +24,8 @@ namespace {
 
 const int kSelThreads = 256;
 const int kSelWarps = kSelThreads / 32;
-const int kSelGroups = 64;     // of threads, KVX_MAX_PICKS at least
-const int kSelRows = 96;       // threads of a part that have candidates, and ...
-const int kSelList = 512;      // ... candidates, before ties are looked into
+const int kSelGroups = 64;     // of threads of the merge, KVX_MAX_PICKS at least
+const int kSelList = 512;      // candidates of a part that are ranked, before ties are looked into
 const int kMergeList = 512;    // continuations that are ranked, before ties are looked into
 const int kMaxParts = 32;      // of a row: a lane each when they are merged
 const int kMergeWarps = KVX_MAX_BEAMS / 2;
@@ -138,7 +139,7 @@ __device__ __forceinline__ int2 sum_of_warp(float x)
                      __reduce_add_sync(0xffffffffu, __float_as_int(rest) - __float_as_int(kRest)));
 }
 
-template <int TYPE, int EACH>
+template <int TYPE, int EACH, int GROUPS>
 __global__ void __launch_bounds__(kSelThreads, EACH * sizeof(typename Logit<TYPE>::T) > 128 ? 2 : 4)
 kvx_select_parts_kernel(const Select a)
 {
@@ -147,10 +148,11 @@ kvx_select_parts_kernel(const Select a)
     constexpr int kVec = 16 / sizeof(T), kVecs = EACH / kVec;
     constexpr int kPer = 4 / sizeof(T);   // logits of a word
     constexpr int kWords = EACH / kPer;  // words of a thread
+    constexpr int kRows = GROUPS == 64 ? 96 : 128;  // threads that have candidates, at most
     __shared__ uint64_t list[kSelList];
-    __shared__ uint4 rows[kSelRows][kVecs];
-    __shared__ int owner[kSelRows];
-    __shared__ uint4 tops[kSelGroups / 4], maxima[kSelWarps / 4];  // order_of, of groups and warps
+    __shared__ uint4 rows[kRows][kVecs];
+    __shared__ int owner[kRows];
+    __shared__ uint4 tops[GROUPS / 4], maxima[kSelWarps / 4];  // order_of, of groups and warps
     __shared__ int2 sums[kSelWarps];
     __shared__ unsigned reach;  // the largest that `picks` of `tops` reach
     __shared__ int found, reached, odd;
@@ -193,7 +195,7 @@ kvx_select_parts_kernel(const Select a)
     };
 
     float top, m, bar;
-    constexpr int kLanes = kSelThreads / kSelGroups;  // of a group
+    constexpr int kLanes = kSelThreads / GROUPS;  // of a group
     for (bool again = false;; again = true) {
         unsigned pair = u[0].x;
 #pragma unroll
@@ -225,7 +227,7 @@ kvx_select_parts_kernel(const Select a)
         m = float_of(all);
         int rank = 0;
 #pragma unroll
-        for (int k = 0; k < kSelGroups / 4 / kLanes; ++k) {
+        for (int k = 0; k < GROUPS / 4 / kLanes; ++k) {
             const uint4 f = tops[k * kLanes + sub];
             rank += f.x >= own;
             rank += f.y >= own;
@@ -280,7 +282,7 @@ kvx_select_parts_kernel(const Select a)
     // warp, took half of the kernel's time.
     if (top >= bar && top > -INFINITY) {
         const int at = atomicAdd(&reached, 1);
-        if (at < kSelRows) {
+        if (at < kRows) {
             owner[at] = threadIdx.x;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
@@ -289,7 +291,7 @@ kvx_select_parts_kernel(const Select a)
     }
     __syncthreads();
     const int all_rows = reached;
-    for (int i = threadIdx.x; i < min(all_rows, kSelRows) * kWords; i += kSelThreads) {
+    for (int i = threadIdx.x; i < min(all_rows, kRows) * kWords; i += kSelThreads) {
         const int r = i / kWords, w = i % kWords;
         const unsigned word = reinterpret_cast<const unsigned *>(rows[r])[w];
         if (L::larger(word) < bar)
@@ -307,9 +309,10 @@ kvx_select_parts_kernel(const Select a)
         }
     }
     __syncthreads();
-    const int n = all_rows > kSelRows ? kSelList + 1 : found;
+    const int n = all_rows > kRows ? kSelList + 1 : found;
     uint64_t *out = a.keys + (int64_t(beam) * a.parts + part) * a.picks;
-    if (n <= kSelGroups) {  // as usual: the other warps are done
+    constexpr int kRanked = 64, kSpread = kSelThreads / kRanked;  // candidates, threads to each
+    if (n <= kRanked) {  // as usual: the other warps are done
         if (threadIdx.x < n) {
             const uint64_t key = list[threadIdx.x];
             int rank = 0;
@@ -322,16 +325,16 @@ kvx_select_parts_kernel(const Select a)
             out[threadIdx.x] = 0;
         }
     } else if (n <= kSelList) {
-        for (int i = threadIdx.x / kLanes; i < (n + kSelGroups - 1) / kSelGroups * kSelGroups;
-             i += kSelGroups) {
+        for (int i = threadIdx.x / kSpread; i < (n + kRanked - 1) / kRanked * kRanked;
+             i += kRanked) {
             const uint64_t key = i < n ? list[i] : 0;
             int rank = 0;
-            for (int k = threadIdx.x % kLanes; k < n; k += kLanes)
+            for (int k = threadIdx.x % kSpread; k < n; k += kSpread)
                 rank += list[k] > key;
 #pragma unroll
-            for (int d = 1; d < kLanes; d <<= 1)
+            for (int d = 1; d < kSpread; d <<= 1)
                 rank += __shfl_xor_sync(0xffffffffu, rank, d);
-            if (i < n && rank < a.picks && threadIdx.x % kLanes == 0)
+            if (i < n && rank < a.picks && threadIdx.x % kSpread == 0)
                 out[rank] = key;
         }
     } else {
@@ -640,12 +643,25 @@ int parts_of(const kvx_select_cfg &c, int each)
     return (c.vocab + 7 + each * kSelThreads - 1) / (each * kSelThreads);
 }
 
-template <int TYPE>
-const void *parts_kernel(int each)
+// Up to this many picks a part's threads make 64 groups, past it 128: the nearer the picks are to
+// the groups, the more logits reach the bar.  With 64 of 64 it is the smallest of the groups'
+// largest, 300 logits of 175 threads reach it, and they are taken one after the other; with 64 of
+// 128 it is 90 logits.  64 groups of 8 beams over 128k, 64 and 128 groups: 37.5 and 40.4 us with 4
+// picks, 44.5 and 45.4 with 16, 52.4 and 50.4 with 24, 60.5 and 56 with 32, 2700 and 96 with 64.
+const int kFewPicks = 16;
+
+template <int TYPE, int EACH>
+const void *parts_kernel(int picks)
 {
-    return each == 8 ? reinterpret_cast<const void *>(kvx_select_parts_kernel<TYPE, 8>)
-                     : reinterpret_cast<const void *>(
-                           kvx_select_parts_kernel<TYPE, kEachMost>);
+    return picks > kFewPicks
+               ? reinterpret_cast<const void *>(kvx_select_parts_kernel<TYPE, EACH, 128>)
+               : reinterpret_cast<const void *>(kvx_select_parts_kernel<TYPE, EACH, 64>);
+}
+
+template <int TYPE>
+const void *parts_kernel(int each, int picks)
+{
+    return each == 8 ? parts_kernel<TYPE, 8>(picks) : parts_kernel<TYPE, kEachMost>(picks);
 }
 
 cudaError_t launch(const void *fn, int64_t ctas, int threads, cudaStream_t s, void **args)
@@ -722,9 +738,9 @@ kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void 
                 cfg->n_groups, cfg->width, cfg->vocab, cfg->picks, parts, cfg->done_token};
     void *args[] = {&a};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const void *fn = cfg->type == KVX_TYPE_HALF     ? parts_kernel<KVX_TYPE_HALF>(each)
-                     : cfg->type == KVX_TYPE_BFLOAT ? parts_kernel<KVX_TYPE_BFLOAT>(each)
-                                                    : parts_kernel<KVX_TYPE_FLOAT>(each);
+    const void *fn = cfg->type == KVX_TYPE_HALF     ? parts_kernel<KVX_TYPE_HALF>(each, cfg->picks)
+                     : cfg->type == KVX_TYPE_BFLOAT ? parts_kernel<KVX_TYPE_BFLOAT>(each, cfg->picks)
+                                                    : parts_kernel<KVX_TYPE_FLOAT>(each, cfg->picks);
     cudaError_t e = launch(fn, beams * parts, kSelThreads, s, args);
     if (e == cudaSuccess)
         e = launch(cfg->width * parts * cfg->picks <= kMergeList

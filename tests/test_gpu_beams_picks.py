@@ -54,3 +54,22 @@ def test_merging_many_lists(ctx, width, vocab):  # noqa: F811
     check_selection(select(ctx, x, s, 32, "bf16"), x, s, 32)
     few, many = (device_time(ctx, x, s, picks, "bf16") for picks in (16, 32))
     assert many < 4 * few, (few, many)
+
+
+@pytest.mark.parametrize("groups,width,vocab,dtype", [(16, 8, 128256, "bf16"),
+                                                      (16, 8, 128256, "fp16"),
+                                                      (1, 2, 128256, "fp32")])
+def test_as_many_picks_as_there_may_be(ctx, groups, width, vocab, dtype):  # noqa: F811
+    """A part's own bar, and what reaches it, at KVX_MAX_PICKS."""
+    x, s = make(groups, width, vocab, dtype, 12)
+    check_selection(select(ctx, x, s, 64, dtype), x, s, 64)
+    few, many = (device_time(ctx, x, s, picks, dtype) for picks in (32, 64))
+    assert many < 4 * few, (few, many)
+
+
+@pytest.mark.parametrize("picks", [16, 17, 31, 32, 33, 47, 63])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_picks_around_every_choice(ctx, picks, dtype):  # noqa: F811
+    for groups, width, vocab in ((1, 4, 3000), (3, 7, 40001), (20, 2, 17000)):
+        x, s = make(groups, width, vocab, dtype, picks)
+        check_selection(select(ctx, x, s, picks, dtype), x, s, picks)
