@@ -1015,9 +1015,10 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
                         // Where rows see no key after their own, -|i - j| is j - i.
                         const bool behind = a.slopes && u.keys.prefix <= u.keys.pmin + 1;
                         // Scores from products, two at a time: a factor or the cap's series, and a
-                        // bias that grows by `step` from pair to pair (its rounding grows with the
-                        // bias, that is, with how little such keys weigh).  Each combination is
-                        // code of its own: as one with conditions, all of it is executed.
+                        // bias that grows by `step` from pair to pair (each addition rounds it by
+                        // at most 2^-24 of what it is at the block's first key: near keys are off
+                        // by up to 19 x 2^-24 x 32 slopes).  Each combination is code of its own:
+                        // as one with conditions, all of it is executed.
                         auto shape = [&](float(&z)[32], float away, auto capped, auto biased) {
                             const float z0 = slope * away, two = 2.0f * slope;
                             uint64_t bias = pair_of(z0, z0 + slope);
