@@ -196,12 +196,13 @@ typedef struct kvx_launch_cfg {
                              only when this transfer touches no memory the previous kernel
                              writes and writes none it reads (for example consecutive
                              per-layer loads).  Overlapped transfers one behind the other
-                             may all run at once, beside a page upkeep, append or attention
-                             call right ahead of them, which lets its next kernel start
-                             early too: the condition holds against all of these.  A call
-                             made with it waits on the host for its descriptor copy (a few
-                             microseconds) before it enqueues the kernel.  Store, load and transform with the warp-segment
-                             mapping; 0 elsewhere.  0 = off (default) */
+                             may all run at once, beside a page upkeep, append, attention or
+                             beam search call right ahead of them, which lets its next kernel
+                             start early too: the condition holds against all of these.  A
+                             call made with it waits on the host for its descriptor copy (a
+                             few microseconds) before it enqueues the kernel.  Store, load and
+                             transform with the warp-segment mapping; 0 elsewhere.  0 = off
+                             (default) */
 } kvx_launch_cfg;
 
 typedef struct kvx_ctx kvx_ctx;
@@ -333,8 +334,9 @@ kvx_status kvx_transform_hbm(kvx_ctx *ctx, int dir, const kvx_pool *pool,
 /* ---------------------------------------------------------------- prepared plans */
 
 /* A store, load or transform (op = KVX_OP_STORE .. KVX_OP_SCATTER_HBM) validated and
- * packed once (cfg as for the call it prepares).  kvx_plan_create allocates device memory of its own for the descriptors,
- * copies them there on `stream` and waits for the copy.  kvx_plan_launch then only
+ * packed once (cfg as for the call it prepares).  kvx_plan_create allocates device memory of
+ * its own for the descriptors, copies them there on `stream` and waits for the copy.
+ * kvx_plan_launch then only
  * enqueues the kernel: no validation, no host packing, no descriptor copy, no slot wait,
  * so repeated transfers (the same per-layer batches every prefill, for instance) cost one
  * launch each, and a sequence of launches can be captured into a CUDA graph.  The plan

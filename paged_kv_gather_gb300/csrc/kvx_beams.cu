@@ -25,7 +25,6 @@ namespace {
 const int kSelThreads = 256;
 const int kSelWarps = kSelThreads / 32;
 const int kSelGroups = 64;     // of threads of the merge, KVX_MAX_PICKS at least
-const int kSelList = 512;      // candidates of a part that are ranked, before ties are looked into
 const int kMergeList = 512;    // continuations that are ranked, before ties are looked into
 const int kMaxParts = 32;      // of a row: a lane each when they are merged
 const int kMergeWarps = KVX_MAX_BEAMS / 2;
@@ -148,8 +147,11 @@ kvx_select_parts_kernel(const Select a)
     constexpr int kVec = 16 / sizeof(T), kVecs = EACH / kVec;
     constexpr int kPer = 4 / sizeof(T);   // logits of a word
     constexpr int kWords = EACH / kPer;  // words of a thread
-    constexpr int kRows = GROUPS == 64 ? 96 : 128;  // threads that have candidates, at most
-    __shared__ uint64_t list[kSelList];
+    // Threads that have candidates, and candidates, at most, before ties are looked into.  Where
+    // few tokens are left, or there are few, all of them may be candidates: those of fewer groups
+    // than there are picks, eight to a thread.
+    constexpr int kRows = GROUPS == 64 ? 96 : 128, kList = GROUPS == 64 ? 512 : 1024;
+    __shared__ uint64_t list[kList];
     __shared__ uint4 rows[kRows][kVecs];
     __shared__ int owner[kRows];
     __shared__ uint4 tops[GROUPS / 4], maxima[kSelWarps / 4];  // order_of, of groups and warps
@@ -303,13 +305,13 @@ kvx_select_parts_kernel(const Select a)
             const float x = L::load(reinterpret_cast<const T *>(&word)[k]);
             if (x >= bar && x > -INFINITY) {
                 const int at = atomicAdd(&found, 1);
-                if (at < kSelList)
+                if (at < kList)
                     list[at] = key_of(x, token + k);
             }
         }
     }
     __syncthreads();
-    const int n = all_rows > kRows ? kSelList + 1 : found;
+    const int n = all_rows > kRows ? kList + 1 : found;
     uint64_t *out = a.keys + (int64_t(beam) * a.parts + part) * a.picks;
     constexpr int kRanked = 64, kSpread = kSelThreads / kRanked;  // candidates, threads to each
     if (n <= kRanked) {  // as usual: the other warps are done
@@ -324,7 +326,7 @@ kvx_select_parts_kernel(const Select a)
         } else if (threadIdx.x < a.picks) {
             out[threadIdx.x] = 0;
         }
-    } else if (n <= kSelList) {
+    } else if (n <= kList) {
         for (int i = threadIdx.x / kSpread; i < (n + kRanked - 1) / kRanked * kRanked;
              i += kRanked) {
             const uint64_t key = i < n ? list[i] : 0;

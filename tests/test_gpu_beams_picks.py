@@ -73,3 +73,15 @@ def test_picks_around_every_choice(ctx, picks, dtype):  # noqa: F811
     for groups, width, vocab in ((1, 4, 3000), (3, 7, 40001), (20, 2, 17000)):
         x, s = make(groups, width, vocab, dtype, picks)
         check_selection(select(ctx, x, s, picks, dtype), x, s, picks)
+
+
+@pytest.mark.parametrize("vocab,live", [(1000, 1000), (128256, 1000), (50257, 600)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_few_tokens_left(ctx, vocab, live, dtype):  # noqa: F811
+    """Fewer groups of threads have a logit than there are picks: all that is left are candidates,
+    up to 1000 instead of some 50, each compared with all."""
+    x, s = make(1, 32, vocab, dtype, 13)
+    x[:, live:] = -float("inf")
+    check_selection(select(ctx, x, s, 64, dtype), x, s, 64)
+    few, many = (device_time(ctx, x, s, picks, dtype) for picks in (32, 64))
+    assert many < 6 * few, (few, many)
