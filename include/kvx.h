@@ -655,15 +655,19 @@ kvx_status kvx_select_workspace(kvx_ctx *ctx, const kvx_select_cfg *cfg, int64_t
  * packed); scores [n_groups * width].  A beam with done[b] != 0 (device bytes, may be NULL) has
  * finished: its one continuation is done_token with its own sum, and its logits are not read.
  *
- * Continuations are ordered by their sums in 64 bits, equal ones by beam and then by token; the
- * sum of exponentials is taken in 32 bits within a thread's 8 or 64 logits and in two numbers of
- * 32 bits across those, so two beams' sums closer than about 1e-7 (5e-7 where logits are in the
- * thousands) may change places.  The same inputs give the same bits.  A logit of -infinity rules
- * its token out, one of the type's lowest value or another mask value counts as it is; one that is
- * NaN or +infinity counts as -infinity.  A beam whose sum is -infinity or NaN, or that has no logit left, has no
- * continuation; where a group has fewer than `picks`, the rest are beam 0, token -1, -infinity.
- * Logits, scores, parents, tokens and out_scores are aligned to their elements; out_scores may be
- * scores where picks = width.  Two kernel launches on `stream`; they may be captured. */
+ * Continuations are ordered by their sums in 64 bits, taken relative to a beam's largest logit,
+ * equal ones by beam and then by token; the sum of exponentials is taken in 32 bits within a
+ * thread's 8 or 64 logits and in two numbers of 32 bits across those, so two beams' sums closer
+ * than about 1e-7 (5e-7 where logits are in the thousands) may change places.  The same inputs give
+ * the same bits.  A logit of -infinity rules its token out; one of the type's lowest value or
+ * another mask value counts as it is (of V equal logits each has log probability -log V, whatever
+ * their value, and a beam of nothing else continues at that); one that is NaN or +infinity counts
+ * as -infinity.  Many equal logits among a beam's largest, as of a mask value where few others are
+ * left, take up to 16 times as long as -infinity in their place.  A beam whose sum is -infinity or
+ * NaN, or that has no logit left, has no continuation; where a group has fewer than `picks`, the
+ * rest are beam 0, token -1, -infinity.  Logits, scores, parents, tokens and out_scores are aligned
+ * to their elements; out_scores may be scores where picks = width.  Two kernel launches on
+ * `stream`; they may be captured. */
 kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void *logits,
                             int64_t logits_stride, const float *scores, const uint8_t *done,
                             int32_t *parents, int32_t *tokens, float *out_scores, void *workspace,

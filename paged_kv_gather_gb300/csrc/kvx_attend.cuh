@@ -1,5 +1,6 @@
 // kvx_attend.cuh -- what the attention kernels share: element types, a step's schedule,
-// visibility of keys, and the scores' arithmetic.  Included by kvx_attend.cu only.
+// visibility of keys, and the scores' arithmetic.  Included by the units that
+// attend, append or select.
 #pragma once
 
 #include <cuda.h>

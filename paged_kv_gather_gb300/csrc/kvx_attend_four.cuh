@@ -433,7 +433,7 @@ kvx_attend_four_kernel(const Attend a, const Work w)
             l[n][0] = l[n][1] = 0.0f;
         }
         // Rows (the same for the lanes that share them) of which no key has been seen; and the
-        // first keys of 16 that all rows see: from seen_lo to seen_hi, or up to seen_pre.
+        // first keys of 32 that all rows see: from seen_lo to seen_hi, or up to seen_pre.
         unsigned fresh = (1u << 2 * NT) - 1;
         const int seen_hi = keys.pmin - kFourKeys + 1, seen_pre = keys.prefix - kFourKeys;
         const int seen_lo = a.window ? keys.pmax - a.window + 1 : 0;

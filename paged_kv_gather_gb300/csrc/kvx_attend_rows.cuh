@@ -1,6 +1,7 @@
 // kvx_attend_rows.cuh -- attention of at most 16 rows per KV head (single new tokens, a few
 // drafted ones): the cache is read once and each byte of it meets few rows, so what bounds the
-// kernel is reading K and V.  Included by kvx_attend.cu only.
+// kernel is reading K and V.  Included by kvx_attend.cu, and by kvx_attend_four.cuh
+// for what the kernels of few rows share.
 #pragma once
 
 #include "kvx_attend.cuh"

@@ -1,6 +1,6 @@
 // kvx_attend_tiles.cuh -- attention of more than 16 rows per KV head (prefill chunks, many
 // drafted tokens): every key meets enough rows that the tensor cores bound the kernel.
-// Included by kvx_attend.cu only.
+// Included by kvx_attend.cu, and by kvx_attend_four.cuh for a 4-bit cache.
 #pragma once
 
 #include "kvx_attend.cuh"
@@ -1235,8 +1235,8 @@ kvx_attend_tiles_kernel(const Attend a, const Work w, const __grid_constant__ CU
 }
 
 // The results of units that were cut: block (i, slice) joins, in order, the parts of the i-th of
-// them, that CTA c0 began and did not end, for 32 of its rows.  A launch of its own puts every SM to
-// this, where the last CTA of a unit would have read up to 150 parts of 128 KB alone (65 us
+// them, that CTA c0 began and did not end, for 32 of its rows.  A launch of its own puts every SM
+// to this, where the last CTA of a unit would have read up to 150 parts of 128 KB alone (65 us
 // against 37 for 64 new tokens behind 32k), and spares all of them a fence and a counter.
 const int kJoinThreads = 256;
 const int kJoinRows = 32;

@@ -3,16 +3,18 @@
 //
 // The logits are read once.  A row (a beam's logits) is cut into parts that a CTA holds in
 // registers: it takes the part's maximum and sum of exponentials, and its `picks` largest logits
-// (equal ones by token).  Those all reach the `picks`-th largest of what 64 or 128 groups of threads
-// have as their largest, and without ties hardly more than 1.4 times as many logits do: the CTA
-// looks through the few threads' logits that reach it and ranks what it finds by counting.  A second
-// kernel, a CTA per group, does the same with the parts' lists, by their sums in 64 bits.  Where
-// ties make candidates too many for a list (a row of one value, a part of one mask value), the
-// largest are taken one after the other, which takes a part several us for each.
+// (equal ones by token).  Those all reach the `picks`-th largest of what 64 or 128 groups of
+// threads have as their largest, and without ties hardly more than 1.4 times as many logits do: the
+// CTA looks through the few threads' logits that reach it and ranks what it finds by counting.  A
+// second kernel, a CTA per group, does the same with the parts' lists, by their sums in 64 bits.
+// Where ties make candidates too many for a list (a row of one value, parts of one finite mask
+// value), the largest are taken one after the other, which takes a part several us for each: 64
+// groups of 8 beams with -1e9 for all but 1000 tokens of 128k, 16 picks, 613 us, with -infinity 37.
 //
-// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 42 us, 118 MB:
-// parts 35 (3.4 TB/s; a fifth of it candidates, an eighth exponentials, and the chain load,
-// maximum, bar, sum), merge 7.  One group of 4 beams over 32k 6.5 us, two launches and their chains.
+// Measured: 64 groups of 8 beams over 128k bf16 logits (a tenth of the beams done) 43 us, 118 MB:
+// parts 35 (3.4 TB/s, issuing in 57 % of the cycles, DRAM 42 %: no unit's limit but the chain
+// load, maximum, bar, sum, candidates, with a barrier after each), merge 7 (half of it the 64-bit
+// pipe).  One group of 4 beams over 32k 6.8 us, two launches and their chains.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -427,24 +429,24 @@ struct Continuation {
 
 // Norms first, a warp per beam.  A continuation's sum is (logit - m) + (score - log s) with the
 // beam's largest logit m and s the sum of exp(logit - m): m + log s in one number would round
-// log s away where m is a large mask value, and a beam of mask values alone has nothing else.  Then
-// the largest `picks` sums of all the beams' lists in the way of the parts' kernel: those that reach
-// the `picks`-th largest of what 64 groups of threads have, ranked by counting.
+// log s away where m is a large mask value, and a beam of mask values alone has nothing else.
+// Then the largest `picks` sums of all the beams' lists in the way of the parts' kernel: those that
+// reach the `picks`-th largest of what 64 groups of threads have, ranked by counting.
 //
 // FEW: the list holds all candidates, each thread has one, and they stay in order, in as few warps
 // as there can be, because their sums are 64-bit arithmetic.  More of them are spread: a thread's
 // k-th is one of 64 in a row, another place in every row.  Lists are sorted, and a group of threads
-// that had the same ranks of all of them would have a largest far below what it should be (16 beams,
-// 32 picks: 380 candidates reached such a bar, 40 reach this one; 32 beams, 64 picks: 5000 and 180;
-// one group of 16 beams over 500k with 32 picks 448 us and 61).  Rows turn by 64 / the golden ratio,
-// which spreads the places that a group has had evenly, however many rows.
+// that had the same ranks of all of them would have a largest far below what it should be (16
+// beams, 32 picks: 380 candidates reached such a bar, 40 reach this one; 32 beams, 64 picks: 5000
+// and 180; one group of 16 beams over 500k with 32 picks 448 us and 61).  Rows turn by 64 / the
+// golden ratio, which spreads the places that a group has had evenly, however many rows.
 template <bool FEW>
 __global__ void __launch_bounds__(kMergeThreads)
 kvx_select_merge_kernel(const Select a)
 {
     __shared__ Continuation list[kMergeList];
     __shared__ uint64_t tops[kSelGroups], bar;
-    __shared__ double bases[KVX_MAX_BEAMS];   // score - log s; the score alone of a beam that is done
+    __shared__ double bases[KVX_MAX_BEAMS];   // score - log s, of a beam that is done the score
     __shared__ float largest[KVX_MAX_BEAMS];  // m
     __shared__ int state[KVX_MAX_BEAMS];  // 0: no continuations, 1: lists, 2: itself
     __shared__ int found;
@@ -628,8 +630,11 @@ kvx_select_merge_kernel(const Select a)
 
 // Logits that a thread holds: 64, so that what a part costs besides its logits (half of the
 // instructions at 32) is met seldom, and the merge has few lists; 8 where even those of one group
-// leave the GPU nearly empty (4 beams over 32k 7.5 us instead of 8.3; but 8 beams 11.4 instead of
-// 9.8, and 16 groups of 8 20.6 instead of 10.6).
+// leave the GPU nearly empty, and a row has at most 32 parts then, a lane each in the merge.  With
+// 64 and 8, one group over 32k, as many picks as beams: 4 beams of fp32 7.1 and 6.6 us, of bf16 7.1
+// and 7.1, 5 7.4 and 7.5, 7 8.3 and 9.3; over 50k 1 beam 7.3 and 6.3, 3 with 6 picks 7.7 and 7.1.
+// Past the rule: 8 beams over 32k with 16 picks 10.4 and 13.1, 2 groups of 4 7.3 and 6.9, 8 groups
+// 7.3 and 8.3, 16 groups of 8 11.9 and 19.5.  Between 10 and 16 parts it is either, by up to 1 us.
 const int kEachMost = 64, kFewParts = 16;
 
 int each_of(const kvx_select_cfg &c)
@@ -740,9 +745,10 @@ kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void 
                 cfg->n_groups, cfg->width, cfg->vocab, cfg->picks, parts, cfg->done_token};
     void *args[] = {&a};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const void *fn = cfg->type == KVX_TYPE_HALF     ? parts_kernel<KVX_TYPE_HALF>(each, cfg->picks)
-                     : cfg->type == KVX_TYPE_BFLOAT ? parts_kernel<KVX_TYPE_BFLOAT>(each, cfg->picks)
-                                                    : parts_kernel<KVX_TYPE_FLOAT>(each, cfg->picks);
+    const int picks = cfg->picks;
+    const void *fn = cfg->type == KVX_TYPE_HALF     ? parts_kernel<KVX_TYPE_HALF>(each, picks)
+                     : cfg->type == KVX_TYPE_BFLOAT ? parts_kernel<KVX_TYPE_BFLOAT>(each, picks)
+                                                    : parts_kernel<KVX_TYPE_FLOAT>(each, picks);
     cudaError_t e = launch(fn, beams * parts, kSelThreads, s, args);
     if (e == cudaSuccess)
         e = launch(cfg->width * parts * cfg->picks <= kMergeList
