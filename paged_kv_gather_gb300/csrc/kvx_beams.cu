@@ -433,14 +433,17 @@ struct Continuation {
 // Then the largest `picks` sums of all the beams' lists in the way of the parts' kernel: those that
 // reach the `picks`-th largest of what 64 groups of threads have, ranked by counting.
 //
-// FEW: the list holds all candidates, each thread has one, and they stay in order, in as few warps
-// as there can be, because their sums are 64-bit arithmetic.  More of them are spread: a thread's
-// k-th is one of 64 in a row, another place in every row.  Lists are sorted, and a group of threads
-// that had the same ranks of all of them would have a largest far below what it should be (16
-// beams, 32 picks: 380 candidates reached such a bar, 40 reach this one; 32 beams, 64 picks: 5000
-// and 180; one group of 16 beams over 500k with 32 picks 448 us and 61).  Rows turn by 64 / the
-// golden ratio, which spreads the places that a group has had evenly, however many rows.
-template <bool FEW>
+// KEPT: candidates of a thread that stay in registers, and are on their way before the norms: all
+// of them up to 4 (one group of 8 beams over 500k with 8 picks, 1984 candidates, 13.1 us; 14.4 with
+// 2 kept; with 4 that are not there, of 1024, 10.9 instead of 10.5).  With one each the list holds
+// all of them, and they stay in order, in as few warps as there can be, because their sums are
+// 64-bit arithmetic.  More of them are spread: a thread's k-th is one of 64 in a row, another place
+// in every row.  Lists are sorted, and a group of threads that had the same ranks of all of them
+// would have a largest far below what it should be (16 beams, 32 picks: 380 candidates reached such
+// a bar, 40 reach this one; 32 beams, 64 picks: 5000 and 180; one group of 16 beams over 500k with
+// 32 picks 448 us and 60).  Rows turn by 64 / the golden ratio, which spreads the places that a
+// group has had evenly, however many rows.
+template <int KEPT>
 __global__ void __launch_bounds__(kMergeThreads)
 kvx_select_merge_kernel(const Select a)
 {
@@ -453,21 +456,21 @@ kvx_select_merge_kernel(const Select a)
     constexpr int kLanes = kMergeThreads / kSelGroups;
     const int group = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier_work();
-    // Candidate i: of beam b, key i - b per_beam of its parts' lists.  A thread's first few stay
-    // in registers and are on their way before the norms.
-    constexpr int kKept = FEW ? 1 : 2, kTurn = 39;
+    // Candidate i: of beam b, key i - b per_beam of its parts' lists.
+    constexpr bool kFew = KEPT == 1;
+    constexpr int kTurn = 39;
     const int mine = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
     const int per_beam = a.parts * a.picks, all = a.width * per_beam;
-    const int rounds = FEW ? 1 : (all + kMergeThreads - 1) / kMergeThreads;
+    const int rounds = kFew ? 1 : (all + kMergeThreads - 1) / kMergeThreads;
     auto candidate = [&](int k) {
         const int r = k * kLanes + sub;
-        return FEW ? int(threadIdx.x)
+        return kFew ? int(threadIdx.x)
                    : r * kSelGroups + ((mine + kTurn * r) & (kSelGroups - 1));
     };
     const uint64_t *keys = a.keys + int64_t(group) * all;
-    uint64_t kept[kKept];
+    uint64_t kept[KEPT];
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) {
+    for (int k = 0; k < KEPT; ++k) {
         const int i = candidate(k);
         kept[k] = i < all ? keys[i] : 0;
     }
@@ -508,17 +511,17 @@ kvx_select_merge_kernel(const Select a)
         return state[b] && key
                    ? order_of(bases[b] + (double(float_of(unsigned(key >> 32))) - largest[b])) : 0;
     };
-    uint64_t sums[kKept];
+    uint64_t sums[KEPT];
     int b;
     int32_t token;
     uint64_t top = 0;
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) {
+    for (int k = 0; k < KEPT; ++k) {
         const int i = candidate(k);
         sums[k] = i < all ? sum_of(i, kept[k], b, token) : 0;
         top = max(top, sums[k]);
     }
-    for (int k = kKept; k < rounds; ++k) {
+    for (int k = KEPT; k < rounds; ++k) {
         const int i = candidate(k);
         if (i < all)
             top = max(top, sum_of(i, keys[i], b, token));
@@ -547,12 +550,12 @@ kvx_select_merge_kernel(const Select a)
             list[at] = {sum, token, b};
     };
 #pragma unroll
-    for (int k = 0; k < kKept; ++k)
+    for (int k = 0; k < KEPT; ++k)
         if (sums[k] && sums[k] >= bar) {
             sum_of(candidate(k), kept[k], b, token);
             take(sums[k], token, b);
         }
-    for (int k = kKept; k < rounds; ++k) {
+    for (int k = KEPT; k < rounds; ++k) {
         const int i = candidate(k);
         const uint64_t sum = i < all ? sum_of(i, keys[i], b, token) : 0;
         if (sum && sum >= bar)
@@ -571,7 +574,7 @@ kvx_select_merge_kernel(const Select a)
                               : x.beam != y.beam ? x.beam < y.beam : x.token < y.token;
     };
     const int n = found;
-    if (FEW || n <= kMergeList) {
+    if (kFew || n <= kMergeList) {
         for (int i = mine; i < (n + kSelGroups - 1) / kSelGroups * kSelGroups; i += kSelGroups) {
             int r = 0;
             for (int k = sub; i < n && k < n; k += kLanes)
@@ -671,6 +674,14 @@ const void *parts_kernel(int each, int picks)
     return each == 8 ? parts_kernel<TYPE, 8>(picks) : parts_kernel<TYPE, kEachMost>(picks);
 }
 
+const void *merge_kernel(int candidates)  // of a group
+{
+    return candidates <= kMergeThreads ? reinterpret_cast<const void *>(kvx_select_merge_kernel<1>)
+           : candidates <= 2 * kMergeThreads
+               ? reinterpret_cast<const void *>(kvx_select_merge_kernel<2>)
+               : reinterpret_cast<const void *>(kvx_select_merge_kernel<4>);
+}
+
 cudaError_t launch(const void *fn, int64_t ctas, int threads, cudaStream_t s, void **args)
 {
     cudaLaunchConfig_t lc = {};
@@ -751,10 +762,7 @@ kvx_status kvx_select_beams(kvx_ctx *ctx, const kvx_select_cfg *cfg, const void 
                                                     : parts_kernel<KVX_TYPE_FLOAT>(each, picks);
     cudaError_t e = launch(fn, beams * parts, kSelThreads, s, args);
     if (e == cudaSuccess)
-        e = launch(cfg->width * parts * cfg->picks <= kMergeList
-                       ? reinterpret_cast<const void *>(kvx_select_merge_kernel<true>)
-                       : reinterpret_cast<const void *>(kvx_select_merge_kernel<false>),
-                   cfg->n_groups, kMergeThreads, s, args);
+        e = launch(merge_kernel(cfg->width * parts * picks), cfg->n_groups, kMergeThreads, s, args);
     if (e != cudaSuccess)
         return kvx::cuda_err(ctx, e, "selection launch");
     ctx->last_items = beams;
